@@ -357,6 +357,145 @@ moe_status moe_nvfp4_profile_events(void* const* events, int32_t n);
  * around it include.  Process-wide, not thread-safe; for benchmarks only. */
 moe_status moe_nvfp4_profile_spans(void* device_spans);
 
+/* ---------------------------------------------------------------- training objectives
+ *
+ * The losses of a routed model whose experts stay frozen in NVFP4 while its
+ * router and its head learn, each with its gradient.  Conventions beyond those
+ * above:
+ *   - logits are fp32, bf16 or f16 (moe_dtype), rows of `ld` elements (ld >= the
+ *     row length, any alignment of a row: a pointer needs its element's only).
+ *     A gradient has its logits' type and its own row stride, is rounded once
+ *     from fp32, and may be the logits' buffer itself (same pointer and stride);
+ *     any other overlap is not allowed.
+ *   - Logits may be -inf or the type's lowest value (masked entries: probability
+ *     0, gradient 0).  A row without a finite logit is left out: loss, log-
+ *     probability and gradient 0.  NaN and +inf reach their row's loss and
+ *     gradient, and no other row.
+ *   - A row of a row-wise loss depends on that row alone; where every row starts
+ *     on a 16-byte boundary its bits do not depend on the other rows or on N. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+
+/* A matrix of logits. */
+typedef struct {
+  const void* data;
+  int64_t ld;    /* row stride in elements */
+  int32_t rows;  /* N (or T): 0 <= rows <= 2^26 */
+  int32_t cols;  /* V (or E) */
+  int32_t dtype; /* moe_dtype */
+} moe_logits;
+
+/* Log-probability of one chosen token per row under softmax(logits / temperature):
+ * logp[i] = logits[i][actions[i]] / temperature - log sum_j exp(logits[i][j] /
+ * temperature).  actions: int32 (ids_int64 = 0) or int64 [N]; a row whose action is
+ * outside [0, V) is left out (logp 0).  1 <= V <= 2^18; temperature > 0. */
+moe_status moe_nvfp4_token_logp(const moe_logits* z, const void* actions, int32_t ids_int64,
+                                float temperature, float* logp, moe_stream_t stream);
+
+/* Settings of the policy loss. */
+typedef struct {
+  float clip_low;    /* the ratio is clipped to [1 - clip_low, 1 + clip_high], */
+  float clip_high;   /* 0 <= clip_low <= 1, clip_high >= 0                      */
+  float kl_coef;     /* b; not 0 needs ref_logp */
+  float temperature; /* of the softmax, > 0 */
+} moe_policy_opts;
+
+/* Clipped policy loss with a KL term, per row: with lp as moe_nvfp4_token_logp,
+ * r = exp(lp - old_logp), x = ref_logp - lp,
+ *   row_loss = -min(r * adv, clip(r) * adv) + b * (exp(x) - x - 1).
+ * logits, actions: as moe_nvfp4_token_logp (a left-out row has row_loss 0).
+ * old_logp, adv [N] fp32; ref_logp [N] fp32 or NULL (no KL term).  Writes
+ * row_loss [N] and logp [N]. */
+moe_status moe_nvfp4_policy_loss(const moe_logits* z, const void* actions, int32_t ids_int64,
+                                 const float* old_logp, const float* adv, const float* ref_logp,
+                                 const moe_policy_opts* opts, float* row_loss, float* logp,
+                                 moe_stream_t stream);
+
+/* The same, and the gradient of sum_i row_weight[i] * row_loss[i] with respect to
+ * the logits: dlogits [N][V], row stride ld_grad.  row_weight [N] fp32 (NULL: 1) is
+ * the upstream gradient of each row's loss; a row of weight 0 is left out (loss,
+ * logp and gradient 0, its logits are not read).  Where the clipped branch is the
+ * smaller one it is a constant.  old_logp, adv and ref_logp are constants. */
+moe_status moe_nvfp4_policy_loss_grad(const moe_logits* z, const void* actions,
+                                      int32_t ids_int64, const float* old_logp, const float* adv,
+                                      const float* ref_logp, const float* row_weight,
+                                      const moe_policy_opts* opts, float* row_loss, float* logp,
+                                      void* dlogits, int64_t ld_grad, moe_stream_t stream);
+
+/* A teacher's top logits: K slots per row. */
+typedef struct {
+  const void* ids;    /* int32 or int64 [N][K]; outside [0, V): an empty slot.  A token
+                         in several slots counts once per slot. */
+  const void* logits; /* [N][K] of `dtype` */
+  const float* lse;   /* [N] log-sum-exp of the teacher's whole row over the temperature,
+                         or NULL */
+  int32_t K;          /* 1 <= K <= 256 */
+  int32_t ids_int64;
+  int32_t dtype;      /* moe_dtype */
+} moe_teacher;
+
+/* KL divergence to a teacher known by its top logits t, per row:
+ *   row_loss = temperature^2 * sum_k q_k (log q_k - log p[ids_k]),
+ * p = softmax(logits / temperature).  Without teacher lse q is the softmax of
+ * t / temperature over the row's slots; with it q_k = exp(t_k / temperature - lse),
+ * the teacher's probabilities over the whole vocabulary (the mass outside the slots
+ * is left out).  A row without a teacher (every slot empty, or q = 0) is left out. */
+moe_status moe_nvfp4_distill_loss(const moe_logits* z, const moe_teacher* teacher,
+                                  float temperature, float* row_loss, moe_stream_t stream);
+
+/* The same, and the gradient of sum_i row_weight[i] * row_loss[i]:
+ *   dlogits[j] = row_weight * temperature * (p_j * sum_k q_k - sum_{k: ids_k = j} q_k).
+ * row_weight, dlogits, ld_grad: as moe_nvfp4_policy_loss_grad. */
+moe_status moe_nvfp4_distill_loss_grad(const moe_logits* z, const moe_teacher* teacher,
+                                       const float* row_weight, float temperature,
+                                       float* row_loss, void* dlogits, int64_t ld_grad,
+                                       moe_stream_t stream);
+
+/* Router logits, what the router chose, and which rows count: for the router losses. */
+typedef struct {
+  moe_logits logits;          /* [T][E], 1 <= E <= 1024, T*K <= 2^26 */
+  const void* topk_ids;       /* int32 or int64 [T][K], 1 <= K <= min(32, E); -1 = empty
+                                 slot; other ids outside [0, E) are treated as empty and
+                                 reported by moe_nvfp4_read_status(ws) */
+  const uint8_t* token_mask;  /* [T], 0: the row is left out; or NULL: all count */
+  const int32_t* seq_offsets; /* [S+1] ascending: sequence s is rows [o[s], o[s+1]); rows
+                                 outside all sequences are left out; or NULL: S = 1, all
+                                 rows */
+  int32_t K;
+  int32_t S;                  /* 1 <= S <= 2^20, S*E <= 2^30 */
+  int32_t ids_int64;
+  float balance_coef;
+  float z_coef;
+} moe_router_batch;
+
+/* Workspace of moe_nvfp4_router_loss; 0 for invalid arguments.  Host only. */
+size_t moe_nvfp4_router_loss_workspace_bytes(int32_t T, int32_t E, int32_t S);
+
+/* Balance loss, z loss and per-expert counts.  With p = softmax(logits[t]) over all E
+ * experts, n_s the rows of sequence s that count, n = sum_s n_s:
+ *   counts [S][E] int32    how often those rows chose each expert
+ *   tokens [S+1] int32     n_s, then n
+ *   losses[0] = balance_coef / n * sum_s sum_e f_se * sum_{t in s} p_te,
+ *               f_se = E * counts_se / (K * n_s)  (balance_coef when the load is even)
+ *   losses[1] = z_coef / n * sum_t (log sum_e exp logits[t][e])^2
+ * (0 when n = 0).  Sums are taken in a fixed order: equal inputs give equal bits.
+ * ws: moe_nvfp4_router_loss_workspace_bytes(T, E, S) bytes, 256-byte aligned, one per
+ * stream; its contents before the call do not matter.  T == 0 writes zeros. */
+moe_status moe_nvfp4_router_loss(const moe_router_batch* b, float* losses, int32_t* counts,
+                                 int32_t* tokens, void* ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+
+/* Gradient of loss_grad[0] * losses[0] + loss_grad[1] * losses[1] with respect to the
+ * logits (counts are constants), given moe_nvfp4_router_loss's counts and tokens of the
+ * same batch, plus, where topk_w and d_topk_w [T][K] fp32 are given (both or neither),
+ * the gradient that reaches the logits through the routing scores topk_w of
+ * moe_nvfp4_route_topk: topk_w_k (d_topk_w_k - sum_j topk_w_j d_topk_w_j) at topk_ids_k.
+ * loss_grad: device [2] fp32, or NULL: 1.  Rows that are left out get 0.
+ * dlogits [T][E], row stride ld_grad. */
+moe_status moe_nvfp4_router_loss_grad(const moe_router_batch* b, const int32_t* counts,
+                                      const int32_t* tokens, const float* loss_grad,
+                                      const float* topk_w, const float* d_topk_w, void* dlogits,
+                                      int64_t ld_grad, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,6 +51,27 @@ class moe_forward_opts(C.Structure):
     _fields_ = [("ids_int64", C.c_int32), ("swiglu_limit", C.c_float)]
 
 
+class moe_logits(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("ld", C.c_int64), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("dtype", C.c_int32)]
+
+
+class moe_policy_opts(C.Structure):
+    _fields_ = [("clip_low", C.c_float), ("clip_high", C.c_float), ("kl_coef", C.c_float),
+                ("temperature", C.c_float)]
+
+
+class moe_teacher(C.Structure):
+    _fields_ = [("ids", C.c_void_p), ("logits", C.c_void_p), ("lse", C.c_void_p),
+                ("K", C.c_int32), ("ids_int64", C.c_int32), ("dtype", C.c_int32)]
+
+
+class moe_router_batch(C.Structure):
+    _fields_ = [("logits", moe_logits), ("topk_ids", C.c_void_p), ("token_mask", C.c_void_p),
+                ("seq_offsets", C.c_void_p), ("K", C.c_int32), ("S", C.c_int32),
+                ("ids_int64", C.c_int32), ("balance_coef", C.c_float), ("z_coef", C.c_float)]
+
+
 class moe_ws_layout(C.Structure):
     _fields_ = [(n, C.c_int64 if n == "rows_cap" else C.c_size_t) for n in _LAYOUT_FIELDS]
 
@@ -102,7 +123,22 @@ def lib():
         L.moe_nvfp4_forward_w4a16_ex.argtypes = [C.POINTER(moe_dims),
                                                  C.POINTER(moe_nvfp4_weights), i32, i32, vp, vp,
                                                  vp, vp, vp, sz, C.POINTER(moe_forward_opts), vp]
-        for f in ["moe_nvfp4_selftest_wait_timeout",
+        f32, i64, zp = C.c_float, C.c_int64, C.POINTER(moe_logits)
+        po, tp, rb = C.POINTER(moe_policy_opts), C.POINTER(moe_teacher), C.POINTER(moe_router_batch)
+        L.moe_nvfp4_token_logp.argtypes = [zp, vp, i32, f32, vp, vp]
+        L.moe_nvfp4_policy_loss.argtypes = [zp, vp, i32, vp, vp, vp, po, vp, vp, vp]
+        L.moe_nvfp4_policy_loss_grad.argtypes = [zp, vp, i32, vp, vp, vp, vp, po, vp, vp, vp, i64,
+                                                 vp]
+        L.moe_nvfp4_distill_loss.argtypes = [zp, tp, f32, vp, vp]
+        L.moe_nvfp4_distill_loss_grad.argtypes = [zp, tp, vp, f32, vp, vp, i64, vp]
+        L.moe_nvfp4_router_loss_workspace_bytes.restype = sz
+        L.moe_nvfp4_router_loss_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_nvfp4_router_loss.argtypes = [rb, vp, vp, vp, vp, sz, vp]
+        L.moe_nvfp4_router_loss_grad.argtypes = [rb, vp, vp, vp, vp, vp, vp, i64, vp]
+        for f in ["moe_nvfp4_token_logp", "moe_nvfp4_policy_loss", "moe_nvfp4_policy_loss_grad",
+                  "moe_nvfp4_distill_loss", "moe_nvfp4_distill_loss_grad",
+                  "moe_nvfp4_router_loss", "moe_nvfp4_router_loss_grad",
+                  "moe_nvfp4_selftest_wait_timeout",
                   "moe_nvfp4_route_topk", "moe_nvfp4_forward_ex", "moe_nvfp4_forward_w4a16_ex",
                   "moe_nvfp4_prepare_weights_per_tensor", "moe_nvfp4_quantize_tokens_static",
                   "moe_nvfp4_forward_per_tensor",
@@ -459,3 +495,232 @@ def ws_view(ws, layout, name, dtype, shape):
         n *= s
     nbytes = n * torch.empty((), dtype=dtype).element_size()
     return ws[off:off + nbytes].view(dtype).view(*shape)
+
+
+# ------------------------------------------------------------------ training objectives
+#
+# Losses and gradients of the routed model's trained parts (formulas and row rules
+# in include/moe_nvfp4.h).  Logits may be views of row-strided storage; every other
+# tensor is contiguous.  Outputs passed in are written and returned, else allocated
+# on the stream of the call.  With `stream`, the inputs must be ready on that stream.
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_IDS64 = {torch.int32: 0, torch.int64: 1}
+
+
+def _matrix(t, name):
+    """moe_logits of a 2-D CUDA tensor whose rows are contiguous."""
+    dt = _DTYPE.get(t.dtype)
+    if dt is None or t.dim() != 2:
+        raise ValueError(f"{name}: a 2-D float32, bfloat16 or float16 tensor")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor of the current CUDA device (no CPU path exists)")
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if (one != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return moe_logits(t.data_ptr(), ld if rows > 1 else cols, rows, cols, dt)
+
+
+def _arg(t, name, shape, dtypes, like):
+    """Pointer of a contiguous tensor of the given shape and type, on `like`'s device."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)} of {[str(d) for d in dtypes]}, got "
+                         f"{tuple(t.shape)} of {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name}: expected a tensor on {like.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+_F32, _I32, _ID = (torch.float32,), (torch.int32,), (torch.int32, torch.int64)
+_FLOAT, _MASK = tuple(_DTYPE), (torch.bool, torch.uint8)
+
+
+def _out(t, name, shape, dtype, like, stream):
+    """An output tensor: `t` if given, else a new one that belongs to `stream`."""
+    if t is not None:
+        _arg(t, name, shape, (dtype,), like)
+        return t
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _dlogits(t, logits, stream):
+    """The gradient's tensor and its row stride; rows may be strided like the logits'."""
+    if t is None:
+        t = _out(None, "dlogits", logits.shape, logits.dtype, logits, stream)
+    elif t.shape != logits.shape or t.dtype != logits.dtype:
+        raise ValueError("dlogits: must have the logits' shape and type")
+    return t, _matrix(t, "dlogits").ld
+
+
+def _raw(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def token_logp(logits, actions, temperature=1.0, logp=None, stream=None):
+    """Log-probability [N] fp32 of one chosen token per row of logits [N, V];
+    actions int32 or int64 [N], outside [0, V): the row is left out (0)."""
+    z = _matrix(logits, "logits")
+    n = logits.shape[:1]
+    a = _arg(actions, "actions", n, _ID, logits)
+    logp = _out(logp, "logp", n, torch.float32, logits, stream)
+    _check(lib().moe_nvfp4_token_logp(z, a, _IDS64[actions.dtype], temperature, logp.data_ptr(),
+                                      _raw(stream)), "moe_nvfp4_token_logp")
+    return logp
+
+
+def _policy_args(logits, actions, old_logp, advantages, ref_logp):
+    n = logits.shape[:1]
+    return (_matrix(logits, "logits"), _arg(actions, "actions", n, _ID, logits),
+            _IDS64[actions.dtype], _arg(old_logp, "old_logp", n, _F32, logits),
+            _arg(advantages, "advantages", n, _F32, logits),
+            _arg(ref_logp, "ref_logp", n, _F32, logits))
+
+
+def policy_loss(logits, actions, old_logp, advantages, ref_logp=None, clip_low=0.2, clip_high=0.2,
+                kl_coef=0.0, temperature=1.0, row_loss=None, logp=None, stream=None):
+    """Clipped policy loss with a KL term: (row_loss [N], logp [N]) fp32."""
+    args = _policy_args(logits, actions, old_logp, advantages, ref_logp)
+    n = logits.shape[:1]
+    row_loss = _out(row_loss, "row_loss", n, torch.float32, logits, stream)
+    logp = _out(logp, "logp", n, torch.float32, logits, stream)
+    _check(lib().moe_nvfp4_policy_loss(*args, moe_policy_opts(clip_low, clip_high, kl_coef,
+                                                              temperature),
+                                       row_loss.data_ptr(), logp.data_ptr(), _raw(stream)),
+           "moe_nvfp4_policy_loss")
+    return row_loss, logp
+
+
+def policy_loss_grad(logits, actions, old_logp, advantages, row_weight=None, ref_logp=None,
+                     clip_low=0.2, clip_high=0.2, kl_coef=0.0, temperature=1.0, row_loss=None,
+                     logp=None, dlogits=None, stream=None):
+    """policy_loss and the gradient of sum(row_weight * row_loss) (weights None: 1):
+    (row_loss, logp, dlogits).  dlogits may be the logits tensor itself."""
+    args = _policy_args(logits, actions, old_logp, advantages, ref_logp)
+    n = logits.shape[:1]
+    w = _arg(row_weight, "row_weight", n, _F32, logits)
+    row_loss = _out(row_loss, "row_loss", n, torch.float32, logits, stream)
+    logp = _out(logp, "logp", n, torch.float32, logits, stream)
+    dlogits, ld = _dlogits(dlogits, logits, stream)
+    _check(lib().moe_nvfp4_policy_loss_grad(*args, w, moe_policy_opts(clip_low, clip_high, kl_coef,
+                                                                      temperature),
+                                            row_loss.data_ptr(), logp.data_ptr(),
+                                            dlogits.data_ptr(), ld, _raw(stream)),
+           "moe_nvfp4_policy_loss_grad")
+    return row_loss, logp, dlogits
+
+
+def _teacher(logits, ids, t_logits, lse):
+    if ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
+        raise ValueError("teacher_ids: one row of slots per row of logits")
+    return moe_teacher(_arg(ids, "teacher_ids", ids.shape, _ID, logits),
+                       _arg(t_logits, "teacher_logits", ids.shape, _FLOAT, logits),
+                       _arg(lse, "teacher_lse", logits.shape[:1], _F32, logits),
+                       ids.shape[1], _IDS64[ids.dtype], _DTYPE[t_logits.dtype])
+
+
+def distill_loss(logits, teacher_ids, teacher_logits, teacher_lse=None, temperature=1.0,
+                 row_loss=None, stream=None):
+    """KL divergence [N] fp32 of softmax(logits / temperature) from a teacher's top
+    logits: teacher_ids int32 / int64 [N, K] (outside [0, V): empty slot) and
+    teacher_logits [N, K]; teacher_lse [N]: the teacher's whole row's, at the same
+    temperature (else the slots are renormalised)."""
+    z = _matrix(logits, "logits")
+    t = _teacher(logits, teacher_ids, teacher_logits, teacher_lse)
+    row_loss = _out(row_loss, "row_loss", logits.shape[:1], torch.float32, logits, stream)
+    _check(lib().moe_nvfp4_distill_loss(z, t, temperature, row_loss.data_ptr(), _raw(stream)),
+           "moe_nvfp4_distill_loss")
+    return row_loss
+
+
+def distill_loss_grad(logits, teacher_ids, teacher_logits, row_weight=None, teacher_lse=None,
+                      temperature=1.0, row_loss=None, dlogits=None, stream=None):
+    """distill_loss and the gradient of sum(row_weight * row_loss) (weights None: 1):
+    (row_loss, dlogits).  dlogits may be the logits tensor itself."""
+    z = _matrix(logits, "logits")
+    t = _teacher(logits, teacher_ids, teacher_logits, teacher_lse)
+    n = logits.shape[:1]
+    w = _arg(row_weight, "row_weight", n, _F32, logits)
+    row_loss = _out(row_loss, "row_loss", n, torch.float32, logits, stream)
+    dlogits, ld = _dlogits(dlogits, logits, stream)
+    _check(lib().moe_nvfp4_distill_loss_grad(z, t, w, temperature, row_loss.data_ptr(),
+                                             dlogits.data_ptr(), ld, _raw(stream)),
+           "moe_nvfp4_distill_loss_grad")
+    return row_loss, dlogits
+
+
+def _router_batch(logits, topk_ids, balance_coef, z_coef, seq_offsets, token_mask):
+    z = _matrix(logits, "logits")
+    T = logits.shape[0]
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError("topk_ids: one row of expert ids per row of logits")
+    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2):
+        raise ValueError("seq_offsets: S + 1 row numbers")
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    return moe_router_batch(
+        z, _arg(topk_ids, "topk_ids", topk_ids.shape, _ID, logits),
+        _arg(token_mask, "token_mask", logits.shape[:1], _MASK, logits),
+        None if seq_offsets is None else _arg(seq_offsets, "seq_offsets", seq_offsets.shape, _I32,
+                                              logits),
+        topk_ids.shape[1], S, _IDS64[topk_ids.dtype], balance_coef, z_coef)
+
+
+def moe_nvfp4_router_loss_workspace_bytes(T, E, S=1):
+    return int(lib().moe_nvfp4_router_loss_workspace_bytes(T, E, S))
+
+
+def router_loss_workspace(T_max, E, S=1, device="cuda"):
+    """A workspace for router_loss with up to T_max rows and S sequences."""
+    n = moe_nvfp4_router_loss_workspace_bytes(T_max, E, S)
+    if n == 0:
+        raise MoeError(2, "moe_nvfp4_router_loss_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def router_loss(logits, topk_ids, balance_coef, z_coef=0.0, seq_offsets=None, token_mask=None,
+                ws=None, losses=None, counts=None, tokens=None, stream=None):
+    """Balance and z loss of router logits [T, E] and the load of the chosen experts
+    topk_ids [T, K]: (losses [2] fp32, counts [S, E] int32, tokens [S + 1] int32: rows
+    that count per sequence, then in all).  seq_offsets int32 [S + 1] on the device;
+    token_mask bool [T], False: left out."""
+    b = _router_batch(logits, topk_ids, balance_coef, z_coef, seq_offsets, token_mask)
+    T, E = logits.shape
+    losses = _out(losses, "losses", (2,), torch.float32, logits, stream)
+    counts = _out(counts, "counts", (b.S, E), torch.int32, logits, stream)
+    tokens = _out(tokens, "tokens", (b.S + 1,), torch.int32, logits, stream)
+    if ws is None:
+        n = moe_nvfp4_router_loss_workspace_bytes(T, E, b.S)
+        ws = _out(None, "ws", (n,), torch.uint8, logits, stream)
+    else:
+        _arg(ws, "ws", ws.shape, (torch.uint8,), logits)
+    _check(lib().moe_nvfp4_router_loss(b, losses.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
+                                       ws.data_ptr(), ws.numel(), _raw(stream)),
+           "moe_nvfp4_router_loss")
+    return losses, counts, tokens
+
+
+def router_loss_grad(logits, topk_ids, counts, tokens, balance_coef, z_coef=0.0, seq_offsets=None,
+                     token_mask=None, loss_grad=None, topk_w=None, d_topk_w=None, dlogits=None,
+                     stream=None):
+    """Gradient [T, E] of router_loss with respect to the logits, given its counts and
+    tokens; loss_grad [2]: upstream gradients of the two losses (None: 1).  With topk_w
+    and d_topk_w [T, K] (route_topk's scores and their upstream gradients) the scores'
+    gradient is added."""
+    b = _router_batch(logits, topk_ids, balance_coef, z_coef, seq_offsets, token_mask)
+    E = logits.shape[1]
+    dlogits, ld = _dlogits(dlogits, logits, stream)
+    _check(lib().moe_nvfp4_router_loss_grad(
+        b, _arg(counts, "counts", (b.S, E), _I32, logits),
+        _arg(tokens, "tokens", (b.S + 1,), _I32, logits),
+        _arg(loss_grad, "loss_grad", (2,), _F32, logits),
+        _arg(topk_w, "topk_w", topk_ids.shape, _F32, logits),
+        _arg(d_topk_w, "d_topk_w", topk_ids.shape, _F32, logits),
+        dlogits.data_ptr(), ld, _raw(stream)), "moe_nvfp4_router_loss_grad")
+    return dlogits

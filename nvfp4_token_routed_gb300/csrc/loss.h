@@ -1,0 +1,88 @@
+// loss.h -- launch arguments of the training objectives (token_loss.cu,
+// router_loss.cu), shared with their host entry points (loss_api.cu).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace moe {
+
+// Logits types, as moe_dtype in include/moe_nvfp4.h.
+enum LossDtype { kF32 = 0, kBf16 = 1, kF16 = 2 };
+
+// Objectives over a row of vocabulary logits.
+enum TokenLossMode { kTokenLogp = 0, kPolicy = 1, kDistill = 2 };
+
+constexpr int kMaxTeacher = 256;     // teacher slots per row
+constexpr int kMaxVocab = 1 << 18;   // logits per row
+
+struct TokenLossArgs {
+  int N, V;
+  int64_t ld, ld_grad;      // row strides in elements
+  const void* logits;       // [N][V]
+  void* dlogits;            // [N][V], or null: losses only
+  const float* row_weight;  // [N] upstream gradient of each row's loss, or null: 1
+  float* row_loss;          // [N] (not kTokenLogp)
+  float* logp;              // [N] (not kDistill)
+  float tau, inv_tau;       // temperature and its reciprocal
+  float c2;                 // log2(e) / tau: exp(x / tau) = 2^(x c2)
+  int ids64;                // actions / teacher ids are int64
+  // kTokenLogp, kPolicy
+  const void* actions;      // [N]
+  const float* old_logp;
+  const float* adv;
+  const float* ref_logp;    // or null
+  float clip_lo, clip_hi;   // bounds of the probability ratio
+  float kl_coef;
+  // kDistill
+  int k;
+  const void* t_ids;        // [N][k]
+  const void* t_logits;     // [N][k]
+  int t_dtype;
+  const float* t_lse;       // [N] log-sum-exp of the teacher's whole row over tau, or null
+};
+
+cudaError_t launch_token_loss(const TokenLossArgs& a, int mode, int dtype, cudaStream_t s);
+
+struct RouterLossArgs {
+  int T, E, K, S;
+  int64_t ld, ld_grad;
+  const void* logits;         // [T][E]
+  const void* ids;            // [T][K]
+  int ids64;
+  const uint8_t* mask;        // [T], 0 = row left out; or null
+  const int32_t* offsets;     // [S+1] first row of each sequence; or null (S == 1, all rows)
+  float balance_coef, z_coef;
+  float* losses;              // [2] balance, z
+  int32_t* counts;            // [S][E]
+  int32_t* tokens;            // [S+1] live rows per sequence, then their sum
+  void* ws;
+  // gradient
+  const float* loss_grad;     // [2] upstream gradients of losses, or null: 1
+  const float* topk_w;        // [T][K] routing scores and
+  const float* d_topk_w;      // [T][K] their upstream gradients, or null
+  void* dlogits;              // [T][E]
+};
+
+size_t router_loss_ws_bytes(int T, int E, int S);
+cudaError_t launch_router_loss(const RouterLossArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_router_loss_grad(const RouterLossArgs& a, int dtype, cudaStream_t s);
+
+// One logit as float.
+template <int DT>
+struct LogitType;
+template <>
+struct LogitType<kF32> {
+  using type = float;
+};
+template <>
+struct LogitType<kBf16> {
+  using type = uint16_t;
+};
+template <>
+struct LogitType<kF16> {
+  using type = uint16_t;
+};
+
+}  // namespace moe

@@ -253,6 +253,7 @@ T* at(void* ws, size_t off) {
 
 namespace moe {
 int route_kernel_launches(int64_t TK);  // routing + gather launches; next to those kernels
+int device_status(int* sms_out) { return check_device(sms_out); }
 }  // namespace moe
 
 extern "C" {
