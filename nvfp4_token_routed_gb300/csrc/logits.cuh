@@ -32,6 +32,86 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 values in one 64-bit register: Blackwell adds and multiplies them in one
+// instruction.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 16 bytes of logits: 4 fp32 or 8 16-bit values, handled in pairs.
+template <int DT>
+struct Vec {
+  static constexpr int kElems = DT == kF32 ? 4 : 8;
+  static constexpr int kPairs = kElems / 2;
+  // The bits of -inf, four bytes of them.
+  static constexpr uint32_t kNegInf = DT == kF32 ? 0xFF800000u : DT == kBf16 ? 0xFF80FF80u
+                                                                            : 0xFC00FC00u;
+  uint4 v;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+  }
+  __device__ __forceinline__ void set_word(int i, uint32_t w) {
+    (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = w;
+  }
+  __device__ __forceinline__ void fill(uint32_t w) { v = make_uint4(w, w, w, w); }
+  __device__ __forceinline__ f32x2 pair(int i) const {
+    if constexpr (DT == kF32)
+      return pack2(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+    const uint32_t w = word(i);
+    if constexpr (DT == kBf16)
+      return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pack2(f.x, f.y);
+  }
+  __device__ __forceinline__ void set_pair(int i, f32x2 p) {
+    const float2 f = unpack2(p);
+    if constexpr (DT == kF32) {
+      set_word(2 * i, __float_as_uint(f.x));
+      set_word(2 * i + 1, __float_as_uint(f.y));
+    } else if constexpr (DT == kBf16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      set_word(i, *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      const __half2 h = __floats2half2_rn(f.x, f.y);
+      set_word(i, *reinterpret_cast<const uint32_t*>(&h));
+    }
+  }
+  // Words of elementwise maxima (a NaN gives way to the other operand).
+  static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+    if constexpr (DT == kF32)
+      return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    uint32_t r;
+    if constexpr (DT == kBf16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    if constexpr (DT == kF16) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float max_of_word(uint32_t w) {
+    if constexpr (DT == kF32) return __uint_as_float(w);
+    if constexpr (DT == kBf16)
+      return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return fmaxf(f.x, f.y);
+  }
+};
+
 // A softmax's running pair: the largest logit m and s = sum 2^((z - m) c).
 // Scaling by the distance to m before exponentiating keeps every term in [0, 1]
 // for any finite logits; a set without a finite logit has m = -inf, s = 0; a
@@ -40,19 +120,14 @@ struct MaxSum {
   float m, s;
 };
 __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.0f : m; }
-__device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  const float r = finite_ref(m);
-  return {m, a.s * ex2((a.m - r) * c) + b.s * ex2((b.m - r) * c)};
-}
-__device__ __forceinline__ MaxSum warp_merge(MaxSum v, float c) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const MaxSum o = {__shfl_xor_sync(0xFFFFFFFFu, v.m, off),
-                      __shfl_xor_sync(0xFFFFFFFFu, v.s, off)};
-    v = merge(v, o, c);
-  }
-  return v;
+// Pairs of lanes 0..n-1 merged in every lane, n a power of two; the order of the
+// additions does not depend on the lane.
+__device__ __forceinline__ MaxSum warp_merge(MaxSum v, float c, int n) {
+  float m = v.m;
+  for (int off = n / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+  float s = v.s * ex2((v.m - finite_ref(m)) * c);
+  for (int off = n / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  return {m, s};
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

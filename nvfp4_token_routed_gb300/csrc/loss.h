@@ -12,7 +12,7 @@ namespace moe {
 enum LossDtype { kF32 = 0, kBf16 = 1, kF16 = 2 };
 
 // Objectives over a row of vocabulary logits.
-enum TokenLossMode { kTokenLogp = 0, kPolicy = 1, kDistill = 2 };
+enum TokenLossMode { kPolicy = 0, kDistill = 1 };  // kPolicy without adv: logp alone
 
 constexpr int kMaxTeacher = 256;     // teacher slots per row
 constexpr int kMaxVocab = 1 << 18;   // logits per row
@@ -23,15 +23,15 @@ struct TokenLossArgs {
   const void* logits;       // [N][V]
   void* dlogits;            // [N][V], or null: losses only
   const float* row_weight;  // [N] upstream gradient of each row's loss, or null: 1
-  float* row_loss;          // [N] (not kTokenLogp)
-  float* logp;              // [N] (not kDistill)
+  float* row_loss;          // [N], or null
+  float* logp;              // [N], or null
   float tau, inv_tau;       // temperature and its reciprocal
   float c2;                 // log2(e) / tau: exp(x / tau) = 2^(x c2)
   int ids64;                // actions / teacher ids are int64
-  // kTokenLogp, kPolicy
+  // kPolicy
   const void* actions;      // [N]
   const float* old_logp;
-  const float* adv;
+  const float* adv;         // or null: log-probabilities only
   const float* ref_logp;    // or null
   float clip_lo, clip_hi;   // bounds of the probability ratio
   float kl_coef;

@@ -181,7 +181,7 @@ moe_status moe_nvfp4_token_logp(const moe_logits* z, const void* actions, int32_
   a.actions = actions;
   a.ids64 = ids_int64;
   a.logp = logp;
-  return run(a, kTokenLogp, z->dtype, stream);
+  return run(a, kPolicy, z->dtype, stream);
 }
 
 moe_status moe_nvfp4_policy_loss(const moe_logits* z, const void* actions, int32_t ids_int64,

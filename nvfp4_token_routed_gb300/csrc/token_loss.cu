@@ -12,8 +12,9 @@
 //            dz_j = w tau (Q p_j - sum_{i: id_i = j} q_i)
 // So every gradient is a row constant times p_j, plus a few entries.
 //
-// One block per row, two readings of the row: the running maximum and sum, then
-// the gradient.
+// Short rows: one block a row, the row in registers.  Long rows: a persistent cluster
+// of blocks a row, the row in shared memory, loaded ahead by bulk copies.  Either way
+// a row is read once.
 #include "internal.h"
 #include "logits.cuh"
 #include "ptx.cuh"
@@ -22,33 +23,34 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-
 __device__ __forceinline__ float teacher_logit(const TokenLossArgs& a, int64_t i) {
   if (a.t_dtype == kF32) return static_cast<const float*>(a.t_logits)[i];
   const uint16_t* p = static_cast<const uint16_t*>(a.t_logits) + i;
   return a.t_dtype == kBf16 ? load_logit<kBf16>(p) : load_logit<kF16>(p);
 }
 
-// What a row adds to its softmax gradient: dz_j = soft p_j, plus `top` at the
-// chosen token or -slot_scale q_i at teacher slot i.
-struct RowGrad {
-  float soft, top, slot_scale;
-};
+// A row counts unless its weight is 0 or its action is no token.
+template <int MODE>
+__device__ __forceinline__ bool row_live(const TokenLossArgs& a, int row) {
+  bool live = !a.row_weight || a.row_weight[row] != 0.0f;
+  if (MODE == kPolicy) {
+    const int act = load_id(a.actions, a.ids64, row);
+    live = live && act >= 0 && act < a.V;
+  }
+  return live;
+}
 
-// Loss and gradient of the chosen token's log-probability (policy).
-__device__ __forceinline__ float policy_row(const TokenLossArgs& a, int row, float lp,
-                                            float* slope) {
-  const float A = a.adv[row];
-  const float ratio = expf(lp - a.old_logp[row]);
+// Loss and its slope in the chosen token's log-probability (policy).
+__device__ __forceinline__ float policy_row(const TokenLossArgs& a, float lp, float old, float A,
+                                            float ref, float* slope) {
+  const float ratio = expf(lp - old);
   const float rA = ratio * A;
   const float cA = fminf(fmaxf(ratio, a.clip_lo), a.clip_hi) * A;
   // the comparison is false for a NaN ratio, which then reaches the loss
   float loss = -(cA < rA ? cA : rA);
   float g = cA < rA ? 0.0f : -rA;
   if (a.ref_logp) {
-    const float x = a.ref_logp[row] - lp;
+    const float x = ref - lp;
     const float em1 = expm1f(x);
     loss += a.kl_coef * (em1 - x);
     g -= a.kl_coef * em1;
@@ -57,130 +59,756 @@ __device__ __forceinline__ float policy_row(const TokenLossArgs& a, int row, flo
   return loss;
 }
 
-template <int DT, int MODE>
-__global__ void __launch_bounds__(kThreads) token_loss_kernel(const TokenLossArgs a) {
+// How a row is divided: `head` logits up to the first 16-byte boundary and `tail`
+// after the last (the edges, at most 14), between them nb vectors of 16 bytes, `per`
+// of them to each of C blocks.
+struct Split {
+  int head, tail, nb, per;
+};
+constexpr int kMaxEdge = 14;
+template <int DT>
+__device__ __forceinline__ Split split_row(const void* row, int V, int C) {
+  constexpr int kSize = DT == kF32 ? 4 : 2;
+  Split s;
+  s.head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / kSize);
+  s.nb = (V - s.head) / Vec<DT>::kElems;
+  s.tail = V - s.head - s.nb * Vec<DT>::kElems;
+  s.per = (s.nb + C - 1) / C;
+  return s;
+}
+// Column of edge i.
+__device__ __forceinline__ int edge_column(const Split& s, int V, int i) {
+  return i < s.head ? i : V - s.tail + (i - s.head);
+}
+
+// A row's gradient: vector i of 16 bytes at the logits' boundaries, which are the
+// gradient's own where the two rows are aligned alike.
+template <int DT>
+struct GradRow {
   using L = typename LogitType<DT>::type;
+  L* body;  // the logit of vector 0
+  bool aligned;
+  __device__ __forceinline__ void store(int i, const Vec<DT>& g) const {
+    if (aligned) {
+      reinterpret_cast<uint4*>(body)[i] = g.v;
+      return;
+    }
+    L* p = body + (int64_t)i * Vec<DT>::kElems;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t x = g.word(w);
+      if constexpr (DT == kF32) {
+        p[w] = __uint_as_float(x);
+      } else {
+        p[2 * w] = (uint16_t)x;
+        p[2 * w + 1] = (uint16_t)(x >> 16);
+      }
+    }
+  }
+};
+template <int DT>
+__device__ __forceinline__ GradRow<DT> grad_row(const void* z, typename LogitType<DT>::type* dz,
+                                                int head) {
+  return {dz + head,
+          ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0};
+}
+
+// coef * 2^((z - m) c) of a vector.
+template <int DT>
+__device__ __forceinline__ Vec<DT> grad_vec(const Vec<DT>& d, f32x2 neg_m, f32x2 c2, f32x2 coef) {
+  Vec<DT> g;
+#pragma unroll
+  for (int j = 0; j < Vec<DT>::kPairs; ++j) {
+    const float2 x = unpack2(mul2(add2(d.pair(j), neg_m), c2));
+    g.set_pair(j, mul2(coef, pack2(ex2(x.x), ex2(x.y))));
+  }
+  return g;
+}
+
+// What a teacher's slots say without the student's normaliser, by one warp: q into
+// s_q (which holds the teacher's logits), Q = sum q, and kl, zr with
+//   sum q_i (log q_i - log p_i) = kl + Q ((m - zr) / tau + log s).
+struct TeacherSums {
+  float Q, kl, zr;
+};
+__device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int row, int lane,
+                                                    float* s_q, const float* s_z) {
+  float tm = -INFINITY, zr = -INFINITY;
+  for (int i = lane; i < a.k; i += 32) {
+    tm = fmaxf(tm, s_q[i]);
+    zr = fmaxf(zr, s_z[i]);
+  }
+  tm = finite_ref(warp_max(tm));
+  zr = finite_ref(warp_max(zr));
+  float ts = 0.0f;
+  for (int i = lane; i < a.k; i += 32) ts += expf((s_q[i] - tm) * a.inv_tau);
+  ts = warp_sum(ts);
+  // log q_i = (t_i - tm) / tau + shift
+  const float shift = a.t_lse ? tm * a.inv_tau - a.t_lse[row] : -logf(ts);
+  float Q = 0.0f, kl = 0.0f;
+  for (int i = lane; i < a.k; i += 32) {
+    const float lq = (s_q[i] - tm) * a.inv_tau + shift;
+    const float q = ts == 0.0f ? 0.0f : expf(lq);
+    s_q[i] = q;
+    Q += q;
+    if (q != 0.0f) kl += q * (lq - (s_z[i] - zr) * a.inv_tau);
+  }
+  return {warp_sum(Q), warp_sum(kl), zr};
+}
+
+// A row's results once its largest logit and sum v are known.
+struct RowResult {
+  float loss, logp;
+  float m;      // finite reference of the exponentials
+  float coef;   // dz_j = coef 2^((z_j - m) c) ...
+  float top;    // ... + top at the chosen token (policy)
+  float scale;  // ... - scale q_i at teacher slot i (distill)
+};
+template <int MODE>
+__device__ __forceinline__ RowResult finish_row(const TokenLossArgs& a, MaxSum v, float w,
+                                                const TeacherSums& t, float z_act, float old,
+                                                float adv, float ref) {
+  RowResult r = {0.0f, 0.0f, finite_ref(v.m), 0.0f, 0.0f, 0.0f};
+  if (v.s == 0.0f) return r;  // no finite logit
+  const float ln_s = logf(v.s);
+  float soft = 0.0f;
+  if (MODE == kDistill) {
+    if (t.Q == 0.0f) return r;  // no teacher
+    r.loss = a.tau * a.tau * (t.kl + t.Q * ((r.m - t.zr) * a.inv_tau + ln_s));
+    soft = w * a.tau * t.Q;
+    r.scale = w * a.tau;
+  } else {
+    r.logp = (z_act - r.m) * a.inv_tau - ln_s;
+    float slope = 0.0f;
+    if (a.adv) r.loss = policy_row(a, r.logp, old, adv, ref, &slope);
+    r.top = w * slope * a.inv_tau;
+    soft = -r.top;
+  }
+  r.coef = soft == 0.0f ? 0.0f : soft / v.s;
+  return r;
+}
+
+// ---------------------------------------------------------------- short rows
+//
+// Every thread keeps VPT vectors of the row in registers.
+
+template <int DT, int MODE, int NT, int VPT>
+__global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
+  using L = typename LogitType<DT>::type;
+  using V16 = Vec<DT>;
+  constexpr int kWarps = NT / 32;
+  constexpr int kSlots = MODE == kDistill ? kMaxTeacher : 1;
   __shared__ MaxSum s_ms[kWarps];
-  __shared__ int s_id[kMaxTeacher];
-  __shared__ float s_q[kMaxTeacher];
-  __shared__ float s_z[kMaxTeacher];
-  __shared__ float s_top, s_soft, s_scale;
+  __shared__ int s_id[kSlots];
+  __shared__ float s_q[kSlots];
+  __shared__ float s_z[kSlots];
+  __shared__ TeacherSums s_t;
+  __shared__ RowResult s_r;
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const L* z = static_cast<const L*>(a.logits) + row * a.ld;
   L* dz = static_cast<L*>(a.dlogits) + row * a.ld_grad;
-
-  const float w = a.row_weight ? a.row_weight[row] : 1.0f;
-  int act = -1;
-  bool live = w != 0.0f;
-  if (MODE != kDistill) {
-    act = load_id(a.actions, a.ids64, row);
-    live = live && act >= 0 && act < a.V;
-  }
-  if (!live) {  // left out: the row's logits are not looked at
+  const Split sp = split_row<DT>(z, a.V, 1);
+  const int edge = tid < sp.head + sp.tail ? edge_column(sp, a.V, tid) : -1;
+  const uint4* zv = reinterpret_cast<const uint4*>(z + sp.head);
+  const GradRow<DT> out = grad_row<DT>(z, dz, sp.head);
+  auto store_zeros = [&] {
+    V16 zero;
+    zero.fill(0);
+    for (int i = tid; i < sp.nb; i += NT) out.store(i, zero);
+    if (edge >= 0) store_logit<DT>(dz + edge, 0.0f);
+  };
+  if (!row_live<MODE>(a, row)) {  // left out: the row's logits are not looked at
     if (tid == 0) {
-      if (MODE != kTokenLogp) a.row_loss[row] = 0.0f;
-      if (MODE != kDistill) a.logp[row] = 0.0f;
+      if (a.row_loss) a.row_loss[row] = 0.0f;
+      if (a.logp) a.logp[row] = 0.0f;
     }
-    if (a.dlogits)
-      for (int j = tid; j < a.V; j += kThreads) store_logit<DT>(dz + j, 0.0f);
+    if (a.dlogits) store_zeros();
     return;
   }
 
-  // the logits at the teacher's slots, read before any gradient is written
+  V16 d[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int at = i * NT + tid;
+    if (at < sp.nb) d[i].v = zv[at];
+    else d[i].fill(V16::kNegInf);
+  }
+  const float x_edge = edge >= 0 ? load_logit<DT>(z + edge) : -INFINITY;
+
+  // the few logits that the loss picks out, read before any gradient is written
+  int act = -1;
+  float w = 1.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, z_act = 0.0f;
   if (MODE == kDistill) {
-    if (tid < a.k) {
-      const int64_t i = (int64_t)row * a.k + tid;
-      const int id = load_id(a.t_ids, a.ids64, i);
+    for (int i = tid; i < a.k; i += NT) {
+      const int64_t at = (int64_t)row * a.k + i;
+      const int id = load_id(a.t_ids, a.ids64, at);
       const bool ok = id >= 0 && id < a.V;
-      s_id[tid] = ok ? id : -1;
-      s_q[tid] = ok ? teacher_logit(a, i) : -INFINITY;
-      s_z[tid] = ok ? load_logit<DT>(z + id) : 0.0f;
+      s_id[i] = ok ? id : -1;
+      s_q[i] = ok ? teacher_logit(a, at) : -INFINITY;
+      s_z[i] = ok ? load_logit<DT>(z + id) : -INFINITY;
     }
-  } else if (tid == 0) {
-    s_z[0] = load_logit<DT>(z + act);
+  }
+  if (tid == 0) {
+    if (a.row_weight) w = a.row_weight[row];
+    if (MODE == kPolicy) {
+      act = load_id(a.actions, a.ids64, row);
+      z_act = load_logit<DT>(z + act);
+      if (a.adv) {
+        old = a.old_logp[row];
+        adv = a.adv[row];
+        ref = a.ref_logp ? a.ref_logp[row] : 0.0f;
+      }
+    }
   }
 
-  MaxSum v = {-INFINITY, 0.0f};
-  for (int j = tid; j < a.V; j += kThreads) v = merge(v, {load_logit<DT>(z + j), 1.0f}, a.c2);
-  v = warp_merge(v, a.c2);
-  if (lane == 0) s_ms[warp] = v;
+  // largest logit of the warp, then its sum of exponentials
+  uint32_t mw = d[0].v.x;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = i == 0 ? 1 : 0; j < 4; ++j) mw = V16::max_word(mw, d[i].word(j));
+  const float m_warp = warp_max(fmaxf(V16::max_of_word(mw), x_edge));
+  {
+    const float r = finite_ref(m_warp);
+    const f32x2 neg = pack2(-r, -r), c2 = pack2(a.c2, a.c2);
+    f32x2 acc[2] = {pack2(ex2((x_edge - r) * a.c2), 0.0f), 0};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < V16::kPairs; ++j) {
+        const float2 x = unpack2(mul2(add2(d[i].pair(j), neg), c2));
+        acc[j & 1] = add2(acc[j & 1], pack2(ex2(x.x), ex2(x.y)));
+      }
+    const float2 s = unpack2(add2(acc[0], acc[1]));
+    const float s_warp = warp_sum(s.x + s.y);
+    if (lane == 0) s_ms[warp] = {m_warp, s_warp};
+  }
   __syncthreads();
-  v = s_ms[0];
-  for (int i = 1; i < kWarps; ++i) v = merge(v, s_ms[i], a.c2);
-  const float m = finite_ref(v.m);
-
+  if (MODE == kDistill && warp == 1) {
+    const TeacherSums t = teacher_sums(a, row, lane, s_q, s_z);
+    if (lane == 0) s_t = t;
+  }
+  if (MODE == kDistill) __syncthreads();
   if (warp == 0) {
-    float loss = 0.0f, soft = 0.0f, top = 0.0f, scale = 0.0f, lp = 0.0f;
-    const float ln_s = logf(v.s);
-    if (MODE == kDistill) {
-      float tm = -INFINITY;
-      for (int i = lane; i < a.k; i += 32) tm = fmaxf(tm, s_q[i]);
-      tm = finite_ref(warp_max(tm));
-      float ts = 0.0f;
-      for (int i = lane; i < a.k; i += 32) ts += expf((s_q[i] - tm) * a.inv_tau);
-      ts = warp_sum(ts);
-      // log q_i = (t_i - tm) / tau + shift
-      const float shift = a.t_lse ? tm * a.inv_tau - a.t_lse[row] : -logf(ts);
-      float Q = 0.0f, kl = 0.0f;
-      for (int i = lane; i < a.k; i += 32) {
-        const float lq = (s_q[i] - tm) * a.inv_tau + shift;
-        const float q = ts == 0.0f ? 0.0f : expf(lq);
-        s_q[i] = q;
-        Q += q;
-        if (q != 0.0f) kl += q * (lq - (s_z[i] - m) * a.inv_tau + ln_s);
-      }
-      Q = warp_sum(Q);
-      kl = warp_sum(kl);
-      if (v.s != 0.0f && Q != 0.0f) {
-        loss = a.tau * a.tau * kl;
-        soft = w * a.tau * Q;
-        scale = w * a.tau;
-      }
-    } else if (v.s != 0.0f) {
-      lp = (s_z[0] - m) * a.inv_tau - ln_s;
-      float slope = 0.0f;
-      if (MODE == kPolicy) loss = policy_row(a, row, lp, &slope);
-      top = w * slope * a.inv_tau;
-      soft = -top;
-    }
+    MaxSum v = lane < kWarps ? s_ms[lane] : MaxSum{-INFINITY, 0.0f};
+    v = warp_merge(v, a.c2, kWarps);
     if (lane == 0) {
-      if (MODE != kTokenLogp) a.row_loss[row] = loss;
-      if (MODE != kDistill) a.logp[row] = lp;
-      s_soft = soft;
-      s_top = top;
-      s_scale = scale;
+      const RowResult r = finish_row<MODE>(a, v, w, MODE == kDistill ? s_t : TeacherSums{}, z_act,
+                                           old, adv, ref);
+      if (a.row_loss) a.row_loss[row] = r.loss;
+      if (a.logp) a.logp[row] = r.logp;
+      s_r = r;
     }
   }
   if (!a.dlogits) return;
   __syncthreads();
 
-  // a row without a finite logit or without a teacher has soft = 0: zeros
-  const float coef = s_soft == 0.0f ? 0.0f : s_soft / v.s;
-  for (int j = tid; j < a.V; j += kThreads) {
-    const float p = s_soft == 0.0f ? 0.0f : ex2((load_logit<DT>(z + j) - m) * a.c2);
-    store_logit<DT>(dz + j, coef * p);
+  const RowResult r = s_r;
+  if (r.coef == 0.0f) {  // clipped, no teacher, or no finite logit
+    store_zeros();
+    return;
   }
+  const f32x2 neg = pack2(-r.m, -r.m), c2 = pack2(a.c2, a.c2), cf = pack2(r.coef, r.coef);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int at = i * NT + tid;
+    if (at < sp.nb) out.store(at, grad_vec(d[i], neg, c2, cf));
+  }
+  if (edge >= 0) store_logit<DT>(dz + edge, r.coef * ex2((x_edge - r.m) * a.c2));
   __syncthreads();  // the few entries overwrite what the loop stored
   if (MODE == kDistill) {
-    if (tid < a.k && s_id[tid] >= 0 && s_scale != 0.0f) {
+    for (int i = tid; i < a.k; i += NT) {
+      const int id = s_id[i];
+      if (id < 0) continue;
       float q = 0.0f;  // slots that repeat a token add up, each writing the same sum
-      for (int i = 0; i < a.k; ++i) q += s_id[i] == s_id[tid] ? s_q[i] : 0.0f;
-      store_logit<DT>(dz + s_id[tid], coef * ex2((s_z[tid] - m) * a.c2) - s_scale * q);
+      for (int j = 0; j < a.k; ++j) q += s_id[j] == id ? s_q[j] : 0.0f;
+      store_logit<DT>(dz + id, r.coef * ex2((s_z[i] - r.m) * a.c2) - r.scale * q);
     }
-  } else if (tid == 0 && s_soft != 0.0f) {
-    store_logit<DT>(dz + act, coef * ex2((s_z[0] - m) * a.c2) + s_top);
+  } else if (tid == 0) {
+    store_logit<DT>(dz + act, r.coef * ex2((z_act - r.m) * a.c2) + r.top);
   }
+}
+
+// ---------------------------------------------------------------- long rows
+//
+// Persistent clusters of C blocks, one block per SM; a block has its C-th part of
+// each row.  Roles, which meet at mbarriers only:
+//   consumers (16 warps)  pass 1: running maximum and sum of the block's part, from
+//                         shared memory; pass 2: its gradient, from shared memory
+//   producer (1 warp)     bulk copies of the part's 16 KB chunks into a ring, as far
+//                         ahead as the ring has room
+//   gather (4 warps)      the few logits that the loss picks out, the row's edges and
+//                         the teacher's side, each warp every fourth row, up to four
+//                         rows ahead
+//   finish (1 warp)       joins the warps' sums, exchanges them within the cluster
+//                         (every block gets every other's pair), loss and gradient
+//                         constants; after pass 2 the edges and the few entries
+// Consumers take pass 1 of the next row before pass 2 of a row, so that nobody waits
+// for the exchange, while two rows' parts fit the ring (`skew`).  Rows that are left
+// out pass through no ring slot and no barrier.  All waits are bounded; a role whose
+// wait runs out leaves, and the rows not finished get NaN losses.
+
+constexpr int kConsumerWarps = 16;
+constexpr int kConsumers = kConsumerWarps * 32;
+constexpr int kGatherWarps = 4;
+constexpr int kLongThreads = kConsumers + (2 + kGatherWarps) * 32;
+constexpr int kChunkVecs = 1024;  // 16 KB
+constexpr int kChunks = 13;
+constexpr int kMaxCluster = 8;
+constexpr int kRingBytes = kChunks * kChunkVecs * 16;
+
+template <int MODE>
+struct Slot {  // what the gather warp prepares of a row
+  static constexpr int kSlots = MODE == kDistill ? kMaxTeacher : 4;
+  alignas(16) int id[kSlots];
+  alignas(16) float q[kSlots];
+  float z[kSlots];
+  float edge[kMaxEdge];
+  float in[5];  // policy: [1] weight, [2] old, [3] advantage, [4] reference
+  float w;      // distill: weight
+  TeacherSums t;
+};
+
+// q of every slot replaced by the sum over the slots of the same token, by one warp.
+__device__ __forceinline__ void repeated_slots(int k, int lane, const int* s_id, float* s_q) {
+  float sum[kMaxTeacher / 32];
+#pragma unroll
+  for (int u = 0; u < kMaxTeacher / 32; ++u) {
+    sum[u] = 0.0f;
+    if (32 * u >= k) break;
+    const int id = lane + 32 * u < k ? s_id[lane + 32 * u] : -1;
+    for (int j = 0; j < k; j += 4) {  // slots from k on are not of this row: masked by j
+      const int4 o = *reinterpret_cast<const int4*>(s_id + j);
+      const float4 q = *reinterpret_cast<const float4*>(s_q + j);
+      if (o.x == id) sum[u] += q.x;
+      if (o.y == id && j + 1 < k) sum[u] += q.y;
+      if (o.z == id && j + 2 < k) sum[u] += q.z;
+      if (o.w == id && j + 3 < k) sum[u] += q.w;
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < kMaxTeacher / 32; ++u)
+    if (lane + 32 * u < k) s_q[lane + 32 * u] = sum[u];
+  __syncwarp();
+}
+
+template <int MODE>
+struct LongShared {
+  Slot<MODE> slot[kGatherWarps];
+  MaxSum ms[2][kConsumerWarps];
+  alignas(16) MaxSum cl[2][kMaxCluster];
+  RowResult r[2];
+  alignas(8) uint64_t full[kChunks], empty[kChunks];
+  uint64_t sums[2], go[2], done[2], xch[2];
+  uint64_t ready[kGatherWarps], taken[kGatherWarps];
+};
+
+// The rows of one cluster in order, 32 at a time: which of them count.
+template <int MODE>
+struct RowWalk {
+  int first, step, N, lane;
+  uint32_t mask;
+  __device__ __forceinline__ bool live(const TokenLossArgs& a, int it) {
+    if ((it & 31) == 0) {
+      const int64_t r = first + (int64_t)(it + lane) * step;
+      mask = __ballot_sync(0xFFFFFFFFu, r < N && row_live<MODE>(a, (int)r));
+    }
+    return (mask >> (it & 31)) & 1;
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity));
+}
+
+template <int DT, int MODE>
+__global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLossArgs a,
+                                                                   const int skew) {
+  using L = typename LogitType<DT>::type;
+  using V16 = Vec<DT>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ LongShared<MODE> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = cluster_size(), rank = cluster_rank();
+  if (tid == 0) {
+    for (int i = 0; i < kChunks; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), kConsumerWarps);
+    }
+    for (int p = 0; p < 2; ++p) {
+      mbar_init(smem_u32(&sh.sums[p]), kConsumerWarps);
+      mbar_init(smem_u32(&sh.go[p]), 1);
+      mbar_init(smem_u32(&sh.done[p]), kConsumerWarps);
+      mbar_init(smem_u32(&sh.xch[p]), 1);
+    }
+    for (int g = 0; g < kGatherWarps; ++g) {
+      mbar_init(smem_u32(&sh.ready[g]), 1);
+      mbar_init(smem_u32(&sh.taken[g]), 1);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  cluster_arrive();  // before any block writes to another's barrier or memory
+  cluster_wait();
+  pdl_wait();
+  pdl_trigger();
+
+  const int first = blockIdx.x / C, step = gridDim.x / C;
+  RowWalk<MODE> walk = {first, step, a.N, lane, 0u};
+  const int rows = first < a.N ? (a.N - 1 - first) / step + 1 : 0;
+  const bool grad = a.dlogits != nullptr;
+  auto logits_of = [&](int row) { return static_cast<const L*>(a.logits) + row * a.ld; };
+  auto grad_of = [&](int row) { return static_cast<L*>(a.dlogits) + row * a.ld_grad; };
+  // this block's vectors of a row: [v0, v0 + nv)
+  struct Part {
+    Split sp;
+    int v0, nv, chunks;
+  };
+  auto part_of = [&](int row) {
+    Part p;
+    p.sp = split_row<DT>(logits_of(row), a.V, C);
+    p.v0 = rank * p.sp.per;
+    p.nv = max(0, min(p.sp.nb, p.v0 + p.sp.per) - p.v0);
+    p.chunks = (p.nv + kChunkVecs - 1) / kChunkVecs;
+    return p;
+  };
+
+  if (warp < kConsumerWarps) {
+    const f32x2 c2 = pack2(a.c2, a.c2);
+    int pos = 0;            // ring position (chunks passed) of the next row for pass 1
+    uint32_t lv = 0;        // live rows passed
+    bool ok = true;
+    int prev = -1, prev_pos = 0;
+    auto pass2 = [&](int row, int at, uint32_t l) {
+      if (!warp_wait(&sh.go[l & 1], (l >> 1) & 1)) return false;
+      if (!grad) return true;
+      const Part p = part_of(row);
+      const RowResult r = sh.r[l & 1];
+      const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
+      const f32x2 neg = pack2(-r.m, -r.m), cf = pack2(r.coef, r.coef);
+      for (int c = 0; c < p.chunks; ++c, ++at) {
+        const int slot = at % kChunks;
+        const uint4* src = reinterpret_cast<const uint4*>(ring) + slot * kChunkVecs;
+        const int n = min(kChunkVecs, p.nv - c * kChunkVecs);
+        const int base = p.v0 + c * kChunkVecs;
+#pragma unroll 2
+        for (int i = tid; i < n; i += kConsumers) {
+          V16 d, g;
+          d.v = src[i];
+          if (r.coef != 0.0f) g = grad_vec(d, neg, c2, cf);
+          else g.fill(0);  // clipped, no teacher, or no finite logit
+          out.store(base + i, g);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.done[l & 1]));
+      return true;
+    };
+    for (int it = 0; it < rows && ok; ++it) {
+      const int row = first + it * step;
+      const bool live = walk.live(a, it);
+      const Part p = part_of(row);
+      if (!live) {
+        if (grad) {
+          const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
+          V16 zero;
+          zero.fill(0);
+          for (int i = tid; i < p.nv; i += kConsumers) out.store(p.v0 + i, zero);
+        }
+        continue;
+      }
+      const int pos0 = pos;
+      MaxSum v = {-INFINITY, 0.0f};
+      for (int c = 0; c < p.chunks && ok; ++c, ++pos) {
+        const int slot = pos % kChunks;
+        ok = warp_wait(&sh.full[slot], (pos / kChunks) & 1);
+        if (!ok) break;
+        const uint4* src = reinterpret_cast<const uint4*>(ring) + slot * kChunkVecs;
+        const int n = min(kChunkVecs, p.nv - c * kChunkVecs);
+        V16 d[kChunkVecs / kConsumers];
+#pragma unroll
+        for (int u = 0; u < kChunkVecs / kConsumers; ++u) {
+          const int i = tid + u * kConsumers;
+          if (i < n) d[u].v = src[i];
+          else d[u].fill(V16::kNegInf);
+        }
+        uint32_t mw = d[0].v.x;
+#pragma unroll
+        for (int u = 0; u < kChunkVecs / kConsumers; ++u)
+#pragma unroll
+          for (int j = u == 0 ? 1 : 0; j < 4; ++j) mw = V16::max_word(mw, d[u].word(j));
+        const float m = fmaxf(v.m, V16::max_of_word(mw));
+        const float r = finite_ref(m);
+        const f32x2 neg = pack2(-r, -r);
+        f32x2 acc[2] = {pack2(v.s * ex2((v.m - r) * a.c2), 0.0f), 0};
+#pragma unroll
+        for (int u = 0; u < kChunkVecs / kConsumers; ++u)
+#pragma unroll
+          for (int j = 0; j < V16::kPairs; ++j) {
+            const float2 x = unpack2(mul2(add2(d[u].pair(j), neg), c2));
+            acc[j & 1] = add2(acc[j & 1], pack2(ex2(x.x), ex2(x.y)));
+          }
+        const float2 s = unpack2(add2(acc[0], acc[1]));
+        v = {m, s.x + s.y};
+        if (!grad) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
+        }
+      }
+      if (!ok) break;
+      v = warp_merge(v, a.c2, 32);
+      if (lane == 0) {
+        sh.ms[lv & 1][warp] = v;
+        mbar_arrive(smem_u32(&sh.sums[lv & 1]));
+      }
+      if (skew) {
+        if (prev >= 0) ok = pass2(prev, prev_pos, lv - 1);
+        prev = row;
+        prev_pos = pos0;
+      } else {
+        ok = pass2(row, pos0, lv);
+      }
+      ++lv;
+    }
+    if (ok && prev >= 0) pass2(prev, prev_pos, lv - 1);
+  } else if (warp == kConsumerWarps) {  // producer
+    int pos = 0;
+    bool ok = true;
+    for (int it = 0; it < rows && ok; ++it) {
+      const int row = first + it * step;
+      if (!walk.live(a, it)) continue;
+      const Part p = part_of(row);
+      const uint4* src = reinterpret_cast<const uint4*>(logits_of(row) + p.sp.head) + p.v0;
+      for (int c = 0; c < p.chunks; ++c, ++pos) {
+        const int slot = pos % kChunks;
+        ok = warp_wait(&sh.empty[slot], ((pos / kChunks) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t bytes = 16u * min(kChunkVecs, p.nv - c * kChunkVecs);
+          mbar_expect_tx(smem_u32(&sh.full[slot]), bytes);
+          bulk_load(smem_u32(ring) + slot * kChunkVecs * 16, src + c * kChunkVecs, bytes,
+                    smem_u32(&sh.full[slot]));
+        }
+        __syncwarp();
+      }
+    }
+    // no copy may be in flight when the block ends
+    for (int i = max(0, pos - kChunks); i < pos; ++i)
+      warp_wait(&sh.full[i % kChunks], (i / kChunks) & 1);
+  } else if (warp <= kConsumerWarps + kGatherWarps) {  // gather
+    const int g = warp - kConsumerWarps - 1;
+    Slot<MODE>& s = sh.slot[g];
+    uint32_t lv = 0;
+    for (int it = 0; it < rows; ++it) {
+      const int row = first + it * step;
+      if (!walk.live(a, it)) continue;
+      const uint32_t l = lv++;
+      if (l % kGatherWarps != g) continue;
+      const L* z = logits_of(row);
+      const Split sp = split_row<DT>(z, a.V, C);
+      if (!warp_wait(&sh.taken[g], ((l / kGatherWarps) & 1) ^ 1)) break;
+      const float x_edge = lane < sp.head + sp.tail
+                               ? load_logit<DT>(z + edge_column(sp, a.V, lane)) : 0.0f;
+      if (MODE == kDistill) {
+        for (int i = lane; i < a.k; i += 32) {
+          const int64_t at = (int64_t)row * a.k + i;
+          const int id = load_id(a.t_ids, a.ids64, at);
+          const bool in = id >= 0 && id < a.V;
+          s.id[i] = in ? id : -1;
+          s.q[i] = in ? teacher_logit(a, at) : -INFINITY;
+          s.z[i] = in ? load_logit<DT>(z + id) : -INFINITY;
+        }
+        __syncwarp();
+        const TeacherSums t = teacher_sums(a, row, lane, s.q, s.z);
+        if (lane == 0) {
+          s.t = t;
+          s.w = a.row_weight ? a.row_weight[row] : 1.0f;
+        }
+        __syncwarp();
+        if (grad) repeated_slots(a.k, lane, s.id, s.q);
+      } else if (lane < 5) {
+        const int act = lane == 0 ? load_id(a.actions, a.ids64, row) : 0;
+        const float* from = lane == 1   ? a.row_weight
+                            : lane == 2 ? a.old_logp
+                            : lane == 3 ? a.adv
+                                        : a.ref_logp;
+        if (lane > 0) s.in[lane] = from ? from[row] : 1.0f;
+        if (lane == 0) {
+          s.id[0] = act;
+          s.z[0] = load_logit<DT>(z + act);
+        }
+      }
+      if (lane < kMaxEdge) s.edge[lane] = x_edge;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[g]));
+    }
+  } else {  // finish
+    uint32_t lv = 0;
+    bool ok = true;
+    int prev = -1, it = 0;
+    auto entries = [&](int row, uint32_t l) {  // after pass 2
+      const int g = l % kGatherWarps;
+      const Slot<MODE>& s = sh.slot[g];
+      if (grad) {
+        if (!warp_wait(&sh.done[l & 1], (l >> 1) & 1)) return false;
+        const RowResult r = sh.r[l & 1];
+        const Part p = part_of(row);
+        L* dz = grad_of(row);
+        if (rank == 0 && lane < p.sp.head + p.sp.tail)
+          store_logit<DT>(dz + edge_column(p.sp, a.V, lane),
+                          r.coef == 0.0f ? 0.0f : r.coef * ex2((s.edge[lane] - r.m) * a.c2));
+        __syncwarp();
+        const int n = r.coef == 0.0f ? 0 : MODE == kDistill ? a.k : 1;
+        for (int i = lane; i < n; i += 32) {
+          const int id = s.id[i];
+          if (id < 0) continue;
+          const int e = id - p.sp.head;  // rank 0 has the edges, else whose vector it is
+          const int vec = e / V16::kElems - p.v0;
+          const bool mine = e < 0 || e >= p.sp.nb * V16::kElems ? rank == 0 : vec >= 0 && vec < p.nv;
+          const float more = MODE == kDistill ? -r.scale * s.q[i] : r.top;
+          if (mine) store_logit<DT>(dz + id, r.coef * ex2((s.z[i] - r.m) * a.c2) + more);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.taken[g]));
+      return true;
+    };
+    for (; it < rows && ok; ++it) {
+      const int row = first + it * step;
+      if (!walk.live(a, it)) {
+        if (rank == 0) {
+          if (lane == 0) {
+            if (a.row_loss) a.row_loss[row] = 0.0f;
+            if (a.logp) a.logp[row] = 0.0f;
+          }
+          const Split sp = split_row<DT>(logits_of(row), a.V, C);
+          if (grad && lane < sp.head + sp.tail)
+            store_logit<DT>(grad_of(row) + edge_column(sp, a.V, lane), 0.0f);
+        }
+        continue;
+      }
+      const int b = lv & 1, ph = (lv >> 1) & 1;
+      const int g = lv % kGatherWarps;
+      const Slot<MODE>& s = sh.slot[g];
+      ok = warp_wait(&sh.ready[g], (lv / kGatherWarps) & 1) && warp_wait(&sh.sums[b], ph);
+      if (!ok) break;
+      // lanes 0..15 the consumer warps' pairs, from 16 on rank 0's edges
+      const Split sp = split_row<DT>(logits_of(row), a.V, C);
+      MaxSum v = {-INFINITY, 0.0f};
+      if (lane < kConsumerWarps) v = sh.ms[b][lane];
+      else if (rank == 0 && lane - kConsumerWarps < sp.head + sp.tail)
+        v = {s.edge[lane - kConsumerWarps], 1.0f};
+      v = warp_merge(v, a.c2, 32);
+      if (C > 1) {
+        if (lane == 0) mbar_expect_tx(smem_u32(&sh.xch[b]), 8u * C);
+        __syncwarp();
+        if (lane < C)
+          st_async_f32x2(smem_u32(&sh.cl[b][rank]), smem_u32(&sh.xch[b]), lane, v.m, v.s);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.xch[b]), ph));
+        if (!ok) break;
+        v = lane < C ? sh.cl[b][lane] : MaxSum{-INFINITY, 0.0f};
+        v = warp_merge(v, a.c2, kMaxCluster);
+      }
+      if (lane == 0) {
+        const RowResult r =
+            MODE == kDistill
+                ? finish_row<MODE>(a, v, s.w, s.t, 0.0f, 0.0f, 0.0f, 0.0f)
+                : finish_row<MODE>(a, v, s.in[1], s.t, s.z[0], s.in[2], s.in[3], s.in[4]);
+        sh.r[b] = r;
+        mbar_arrive(smem_u32(&sh.go[b]));
+        if (rank == 0) {
+          if (a.row_loss) a.row_loss[row] = r.loss;
+          if (a.logp) a.logp[row] = r.logp;
+        }
+      }
+      __syncwarp();
+      if (skew) {
+        if (prev >= 0) ok = entries(prev, lv - 1);
+        prev = row;
+      } else {
+        ok = entries(row, lv);
+      }
+      ++lv;
+    }
+    if (ok && prev >= 0) ok = entries(prev, lv - 1);
+    if (!ok && rank == 0)  // a wait ran out: this row and the rest are not valid
+      for (int i = max(0, it - 1) + lane; i < rows; i += 32) {
+        if (a.row_loss) a.row_loss[first + i * step] = NAN;
+        if (a.logp) a.logp[first + i * step] = NAN;
+      }
+  }
+  __syncwarp();
+  cluster_arrive();  // no block leaves while another may still write to it
+  cluster_wait();
+}
+
+// ---------------------------------------------------------------- launches
+
+template <int DT, int MODE, int NT, int VPT>
+cudaError_t launch_short(const TokenLossArgs& a, cudaStream_t s) {
+  return launch_pdl(short_row_kernel<DT, MODE, NT, VPT>, dim3(a.N), dim3(NT), 0, s, a);
+}
+
+template <int DT, int MODE>
+cudaError_t launch_long(const TokenLossArgs& a, int C, int skew, cudaStream_t s) {
+  auto kernel = long_row_kernel<DT, MODE>;
+  static std::atomic<uint64_t> limit_set{0};
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kRingBytes, limit_set);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kLongThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // clusters of this size that run at once, asked once per device
+  static std::atomic<int> resident[64][kMaxCluster + 1];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int n = resident[dev & 63][C].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cfg.gridDim = dim3(C);
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+    if (n < 1) return cudaErrorLaunchOutOfResources;
+    resident[dev & 63][C].store(n, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3((unsigned)(a.N < n ? a.N : n) * C);
+  return cudaLaunchKernelEx(&cfg, kernel, a, skew);
+}
+
+constexpr int kPartChunks = 5;      // a block's part of a row, at most, while C <= 8 allows
+constexpr int kShortVecs = 2048;    // rows of 32 KB and less are short
+
+// The variant goes by the row's length alone, so that a row's bits do not depend on
+// the batch.
+template <int DT, int MODE>
+cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
+  const int nvec = a.V / Vec<DT>::kElems;  // at most so many vectors a row
+  if (nvec <= 128) return launch_short<DT, MODE, 128, 1>(a, s);
+  if (nvec <= 512) return launch_short<DT, MODE, 128, 4>(a, s);
+  if (nvec <= kShortVecs) return launch_short<DT, MODE, 512, 4>(a, s);
+  const int chunks = (nvec + kChunkVecs - 1) / kChunkVecs;
+  const int C = min(kMaxCluster, (chunks + kPartChunks - 1) / kPartChunks);
+  const int per = (nvec + C - 1) / C;
+  const int skew = 2 * ((per + kChunkVecs - 1) / kChunkVecs) <= kChunks;
+  return launch_long<DT, MODE>(a, C, skew, s);
 }
 
 template <int DT>
 cudaError_t launch_dtype(const TokenLossArgs& a, int mode, cudaStream_t s) {
-  const dim3 grid(a.N), block(kThreads);
-  if (mode == kTokenLogp) return launch_pdl(token_loss_kernel<DT, kTokenLogp>, grid, block, 0, s, a);
-  if (mode == kPolicy) return launch_pdl(token_loss_kernel<DT, kPolicy>, grid, block, 0, s, a);
-  return launch_pdl(token_loss_kernel<DT, kDistill>, grid, block, 0, s, a);
+  return mode == kDistill ? launch_mode<DT, kDistill>(a, s) : launch_mode<DT, kPolicy>(a, s);
 }
 
 }  // namespace
