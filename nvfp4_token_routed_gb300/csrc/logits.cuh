@@ -32,14 +32,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Two fp32 values in one 64-bit register: Blackwell adds and multiplies them in one
-// instruction.
+// Two fp32 values in one 64-bit register, multiplied and added by one instruction.
 using f32x2 = uint64_t;
 __device__ __forceinline__ f32x2 pack2(float lo, float hi) {
   f32x2 r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
 }
+__device__ __forceinline__ f32x2 pack2(float2 v) { return pack2(v.x, v.y); }
 __device__ __forceinline__ float2 unpack2(f32x2 v) {
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
@@ -53,6 +53,11 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   f32x2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
@@ -72,17 +77,15 @@ struct Vec {
     (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = w;
   }
   __device__ __forceinline__ void fill(uint32_t w) { v = make_uint4(w, w, w, w); }
-  __device__ __forceinline__ f32x2 pair(int i) const {
+  __device__ __forceinline__ float2 pair(int i) const {
     if constexpr (DT == kF32)
-      return pack2(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+      return make_float2(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
     const uint32_t w = word(i);
     if constexpr (DT == kBf16)
-      return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    return pack2(f.x, f.y);
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
-  __device__ __forceinline__ void set_pair(int i, f32x2 p) {
-    const float2 f = unpack2(p);
+  __device__ __forceinline__ void set_pair(int i, float2 f) {
     if constexpr (DT == kF32) {
       set_word(2 * i, __float_as_uint(f.x));
       set_word(2 * i + 1, __float_as_uint(f.y));
@@ -112,22 +115,87 @@ struct Vec {
   }
 };
 
-// A softmax's running pair: the largest logit m and s = sum 2^((z - m) c).
-// Scaling by the distance to m before exponentiating keeps every term in [0, 1]
-// for any finite logits; a set without a finite logit has m = -inf, s = 0; a
-// NaN or +inf logit makes s NaN.
+// A softmax's running pair: a reference logit m and s = sum 2^(z c - k), where k is m c
+// rounded: one fused multiply-add gives each exponent with a single rounding, and
+// rescaling from one reference to another by 2^(k - k') is exact in k.  The reference is
+// the largest logit of the first ones seen; larger ones move it only when their exponent
+// passes kMaxExponent (s stays far inside fp32), so that the exponentials need not wait
+// for the maximum.  Where m c is not within fp32 (all of a set near the type's lowest
+// value, say) the exponents are (z - m) c instead.  A set without a finite logit has
+// m = -inf, s = 0; a NaN or +inf logit makes s NaN.
+constexpr float kMaxExponent = 24.0f;
 struct MaxSum {
   float m, s;
 };
 __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ float ref_exponent(float m, float c) { return __fmul_rn(m, c); }
+__device__ __forceinline__ bool near_ref(float k) { return fabsf(k) < 1e38f; }
+// Exponent of logit z over the finite reference m.
+__device__ __forceinline__ float exponent(float z, float m, float c) {
+  const float k = ref_exponent(m, c);
+  return near_ref(k) ? fmaf(z, c, -k) : (z - m) * c;
+}
+// One logit as a pair.
+__device__ __forceinline__ MaxSum one_logit(float z, float c) {
+  return {z, z == -INFINITY ? 0.0f : ex2(exponent(z, z, c))};
+}
+// Exponent that takes sums over reference m to the finite reference `to`.
+__device__ __forceinline__ float rescale(float m, float to, float c) {
+  const float k = ref_exponent(to, c);
+  return near_ref(k) ? __fsub_rn(ref_exponent(m, c), k) : (m - to) * c;
+}
+__device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float c) {
+  const float m = fmaxf(a.m, b.m), r = finite_ref(m);
+  return {m, a.s * ex2(rescale(a.m, r, c)) + b.s * ex2(rescale(b.m, r, c))};
+}
 // Pairs of lanes 0..n-1 merged in every lane, n a power of two; the order of the
 // additions does not depend on the lane.
 __device__ __forceinline__ MaxSum warp_merge(MaxSum v, float c, int n) {
   float m = v.m;
   for (int off = n / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-  float s = v.s * ex2((v.m - finite_ref(m)) * c);
+  float s = v.s * ex2(rescale(v.m, finite_ref(m), c));
   for (int off = n / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
   return {m, s};
+}
+// The vectors d added to a pair.
+template <int DT, int U>
+__device__ __forceinline__ MaxSum add_vecs(MaxSum v, const Vec<DT> (&d)[U], float c) {
+  uint32_t w = d[0].v.x;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = u == 0 ? 1 : 0; j < 4; ++j) w = Vec<DT>::max_word(w, d[u].word(j));
+  const float top = Vec<DT>::max_of_word(w);
+  if (v.m == -INFINITY) v.m = top;
+  while (true) {
+    const float r = finite_ref(v.m), k = ref_exponent(r, c);
+    f32x2 acc[2] = {0, 0};
+    if (near_ref(k)) {
+      const f32x2 c2 = pack2(c, c), neg = pack2(-k, -k);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < Vec<DT>::kPairs; ++j) {
+          const float2 x = unpack2(fma2(pack2(d[u].pair(j)), c2, neg));
+          acc[j & 1] = add2(acc[j & 1], pack2(ex2(x.x), ex2(x.y)));
+        }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < Vec<DT>::kPairs; ++j) {
+          const float2 x = d[u].pair(j);
+          acc[0] = add2(acc[0], pack2(ex2((x.x - r) * c), ex2((x.y - r) * c)));
+        }
+    }
+    if (top > r && exponent(top, r, c) > kMaxExponent) {  // not with r = top: ends
+      v.s *= ex2(rescale(v.m, top, c));
+      v.m = top;
+      continue;
+    }
+    const float2 s = unpack2(add2(acc[0], acc[1]));
+    return {v.m, v.s + (s.x + s.y)};
+  }
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -88,9 +88,10 @@ struct GradRow {
   using L = typename LogitType<DT>::type;
   L* body;  // the logit of vector 0
   bool aligned;
+  __device__ __forceinline__ uint4* vecs() const { return reinterpret_cast<uint4*>(body); }
   __device__ __forceinline__ void store(int i, const Vec<DT>& g) const {
     if (aligned) {
-      reinterpret_cast<uint4*>(body)[i] = g.v;
+      vecs()[i] = g.v;
       return;
     }
     L* p = body + (int64_t)i * Vec<DT>::kElems;
@@ -113,21 +114,65 @@ __device__ __forceinline__ GradRow<DT> grad_row(const void* z, typename LogitTyp
           ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0};
 }
 
-// coef * 2^((z - m) c) of a vector.
+// The dense part of a row's gradient, coef 2^(z c - k) for every logit.  For 16-bit
+// gradients the size of coef is folded into the exponent, so that a pair of logits costs
+// one multiply-add, two exponentials and one conversion (which takes the sign); the
+// rounding of log2 |coef| - k is at most 2^-17 for |k| < kFoldRange, far below theirs.
+constexpr float kFoldRange = 256.0f;
+struct Soft {
+  float coef;  // 0: the gradient is 0
+  float m, k;  // reference
+  float fold;  // log2 |coef| - k
+};
+template <int DT, bool kNegative>
+__device__ __forceinline__ Vec<DT> soft_vec(const Vec<DT>& d, const Soft& r, float c) {
+  Vec<DT> g;
+  const float b = DT == kF32 ? -r.k : r.fold;
+  const f32x2 c2 = pack2(c, c), bias = pack2(b, b);
+#pragma unroll
+  for (int j = 0; j < Vec<DT>::kPairs; ++j) {
+    const float2 x = unpack2(fma2(pack2(d.pair(j)), c2, bias));
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    if constexpr (DT == kF32) g.set_pair(j, unpack2(mul2(pack2(r.coef, r.coef), pack2(e))));
+    else g.set_pair(j, kNegative ? make_float2(-e.x, -e.y) : e);
+  }
+  return g;
+}
 template <int DT>
-__device__ __forceinline__ Vec<DT> grad_vec(const Vec<DT>& d, f32x2 neg_m, f32x2 c2, f32x2 coef) {
+__device__ __forceinline__ Vec<DT> far_vec(const Vec<DT>& d, const Soft& r, float c) {
   Vec<DT> g;
 #pragma unroll
   for (int j = 0; j < Vec<DT>::kPairs; ++j) {
-    const float2 x = unpack2(mul2(add2(d.pair(j), neg_m), c2));
-    g.set_pair(j, mul2(coef, pack2(ex2(x.x), ex2(x.y))));
+    const float2 x = d.pair(j);
+    g.set_pair(j, make_float2(r.coef * ex2(exponent(x.x, r.m, c)),
+                              r.coef * ex2(exponent(x.y, r.m, c))));
   }
   return g;
+}
+// fn(vector function) for the row's kind: near and of either sign, far, or zero.
+template <int DT, typename F>
+__device__ __forceinline__ void with_soft(const Soft& r, float c, F fn) {
+  if (r.coef == 0.0f) {  // clipped, no teacher, or no finite logit
+    fn([&](const Vec<DT>&) {
+      Vec<DT> g;
+      g.fill(0);
+      return g;
+    });
+  } else if (!(fabsf(r.k) < (DT == kF32 ? 1e38f : kFoldRange))) {
+    fn([&](const Vec<DT>& d) { return far_vec<DT>(d, r, c); });
+  } else if (DT == kF32 || !(r.coef < 0.0f)) {
+    fn([&](const Vec<DT>& d) { return soft_vec<DT, false>(d, r, c); });
+  } else {
+    fn([&](const Vec<DT>& d) { return soft_vec<DT, true>(d, r, c); });
+  }
+}
+__device__ __forceinline__ float soft_at(float z, const Soft& r, float c) {
+  return r.coef == 0.0f ? 0.0f : r.coef * ex2(exponent(z, r.m, c));
 }
 
 // What a teacher's slots say without the student's normaliser, by one warp: q into
 // s_q (which holds the teacher's logits), Q = sum q, and kl, zr with
-//   sum q_i (log q_i - log p_i) = kl + Q ((m - zr) / tau + log s).
+//   sum q_i (log q_i - log p_i) = kl + Q (log s - (zr c - k) log 2).
 struct TeacherSums {
   float Q, kl, zr;
 };
@@ -158,33 +203,38 @@ __device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int 
 
 // A row's results once its largest logit and sum v are known.
 struct RowResult {
-  float loss, logp;
-  float m;      // finite reference of the exponentials
-  float coef;   // dz_j = coef 2^((z_j - m) c) ...
+  Soft soft;    // dz_j = soft_j ...
   float top;    // ... + top at the chosen token (policy)
   float scale;  // ... - scale q_i at teacher slot i (distill)
+  float loss, logp;
 };
 template <int MODE>
 __device__ __forceinline__ RowResult finish_row(const TokenLossArgs& a, MaxSum v, float w,
                                                 const TeacherSums& t, float z_act, float old,
                                                 float adv, float ref) {
-  RowResult r = {0.0f, 0.0f, finite_ref(v.m), 0.0f, 0.0f, 0.0f};
+  constexpr float kLn2 = 0.6931471805599453f;
+  const float m = finite_ref(v.m);
+  RowResult r = {{0.0f, m, ref_exponent(m, a.c2), 0.0f}, 0.0f, 0.0f, 0.0f, 0.0f};
   if (v.s == 0.0f) return r;  // no finite logit
   const float ln_s = logf(v.s);
   float soft = 0.0f;
   if (MODE == kDistill) {
     if (t.Q == 0.0f) return r;  // no teacher
-    r.loss = a.tau * a.tau * (t.kl + t.Q * ((r.m - t.zr) * a.inv_tau + ln_s));
+    r.loss = a.tau * a.tau * (t.kl + t.Q * (ln_s - exponent(t.zr, m, a.c2) * kLn2));
     soft = w * a.tau * t.Q;
     r.scale = w * a.tau;
   } else {
-    r.logp = (z_act - r.m) * a.inv_tau - ln_s;
+    const float e = exponent(z_act, m, a.c2);
+    r.logp = ex2(e) >= v.s ? 0.0f : e * kLn2 - ln_s;  // a token that is the whole sum: 0
     float slope = 0.0f;
     if (a.adv) r.loss = policy_row(a, r.logp, old, adv, ref, &slope);
     r.top = w * slope * a.inv_tau;
     soft = -r.top;
   }
-  r.coef = soft == 0.0f ? 0.0f : soft / v.s;
+  if (soft != 0.0f) {
+    r.soft.coef = soft / v.s;
+    r.soft.fold = log2f(fabsf(r.soft.coef)) - r.soft.k;
+  }
   return r;
 }
 
@@ -264,27 +314,10 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
     }
   }
 
-  // largest logit of the warp, then its sum of exponentials
-  uint32_t mw = d[0].v.x;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = i == 0 ? 1 : 0; j < 4; ++j) mw = V16::max_word(mw, d[i].word(j));
-  const float m_warp = warp_max(fmaxf(V16::max_of_word(mw), x_edge));
   {
-    const float r = finite_ref(m_warp);
-    const f32x2 neg = pack2(-r, -r), c2 = pack2(a.c2, a.c2);
-    f32x2 acc[2] = {pack2(ex2((x_edge - r) * a.c2), 0.0f), 0};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int j = 0; j < V16::kPairs; ++j) {
-        const float2 x = unpack2(mul2(add2(d[i].pair(j), neg), c2));
-        acc[j & 1] = add2(acc[j & 1], pack2(ex2(x.x), ex2(x.y)));
-      }
-    const float2 s = unpack2(add2(acc[0], acc[1]));
-    const float s_warp = warp_sum(s.x + s.y);
-    if (lane == 0) s_ms[warp] = {m_warp, s_warp};
+    const MaxSum v = add_vecs<DT, VPT>(one_logit(x_edge, a.c2), d, a.c2);
+    const MaxSum w = warp_merge(v, a.c2, 32);
+    if (lane == 0) s_ms[warp] = w;
   }
   __syncthreads();
   if (MODE == kDistill && warp == 1) {
@@ -307,17 +340,17 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
   __syncthreads();
 
   const RowResult r = s_r;
-  if (r.coef == 0.0f) {  // clipped, no teacher, or no finite logit
-    store_zeros();
-    return;
-  }
-  const f32x2 neg = pack2(-r.m, -r.m), c2 = pack2(a.c2, a.c2), cf = pack2(r.coef, r.coef);
+  with_soft<DT>(r.soft, a.c2, [&](auto grad_vec) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int at = i * NT + tid;
-    if (at < sp.nb) out.store(at, grad_vec(d[i], neg, c2, cf));
-  }
-  if (edge >= 0) store_logit<DT>(dz + edge, r.coef * ex2((x_edge - r.m) * a.c2));
+    for (int i = 0; i < VPT; ++i) d[i] = grad_vec(d[i]);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int at = i * NT + tid;
+      if (at < sp.nb) out.store(at, d[i]);
+    }
+  });
+  if (edge >= 0) store_logit<DT>(dz + edge, soft_at(x_edge, r.soft, a.c2));
+  if (r.soft.coef == 0.0f) return;
   __syncthreads();  // the few entries overwrite what the loop stored
   if (MODE == kDistill) {
     for (int i = tid; i < a.k; i += NT) {
@@ -325,10 +358,10 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
       if (id < 0) continue;
       float q = 0.0f;  // slots that repeat a token add up, each writing the same sum
       for (int j = 0; j < a.k; ++j) q += s_id[j] == id ? s_q[j] : 0.0f;
-      store_logit<DT>(dz + id, r.coef * ex2((s_z[i] - r.m) * a.c2) - r.scale * q);
+      store_logit<DT>(dz + id, soft_at(s_z[i], r.soft, a.c2) - r.scale * q);
     }
   } else if (tid == 0) {
-    store_logit<DT>(dz + act, r.coef * ex2((z_act - r.m) * a.c2) + r.top);
+    store_logit<DT>(dz + act, soft_at(z_act, r.soft, a.c2) + r.top);
   }
 }
 
@@ -336,27 +369,33 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
 //
 // Persistent clusters of C blocks, one block per SM; a block has its C-th part of
 // each row.  Roles, which meet at mbarriers only:
-//   consumers (16 warps)  pass 1: running maximum and sum of the block's part, from
-//                         shared memory; pass 2: its gradient, from shared memory
+//   consumers (2 or 3 groups of 8 warps, rows in turn)  pass 1: running reference and
+//                         sum of the block's part, from shared memory; pass 2: its
+//                         gradient, from shared memory
 //   producer (1 warp)     bulk copies of the part's 16 KB chunks into a ring, as far
 //                         ahead as the ring has room
 //   gather (4 warps)      the few logits that the loss picks out, the row's edges and
 //                         the teacher's side, each warp every fourth row, up to four
 //                         rows ahead
-//   finish (1 warp)       joins the warps' sums, exchanges them within the cluster
+//   finish (1 warp a group)  joins the warps' sums, exchanges them within the cluster
 //                         (every block gets every other's pair), loss and gradient
 //                         constants; after pass 2 the edges and the few entries
-// Consumers take pass 1 of the next row before pass 2 of a row, so that nobody waits
-// for the exchange, while two rows' parts fit the ring (`skew`).  Rows that are left
-// out pass through no ring slot and no barrier.  All waits are bounded; a role whose
-// wait runs out leaves, and the rows not finished get NaN losses.
+// One group's waits for the exchange are the other's time to compute.  Rows that are
+// left out pass through no ring slot and no barrier.  All waits are bounded; a role
+// whose wait runs out leaves, and the rows not finished get NaN losses.
 
-constexpr int kConsumerWarps = 16;
-constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kGatherWarps = 4;
-constexpr int kLongThreads = kConsumers + (2 + kGatherWarps) * 32;
+constexpr int kGroupWarps = 8;
+constexpr int kGroupThreads = kGroupWarps * 32;
+constexpr int kGatherWarps = 4;  // and slots: more than there are groups
+// Groups: with a gradient two, whose parts stay in the ring until pass 2; without, a
+// chunk is free again after pass 1, and a third group hides more of the other waits.
+constexpr int groups_of(bool grad) { return grad ? 2 : 3; }
+constexpr int long_threads(bool grad) {
+  return (groups_of(grad) * (kGroupWarps + 1) + 1 + kGatherWarps) * 32;
+}
 constexpr int kChunkVecs = 1024;  // 16 KB
 constexpr int kChunks = 13;
+constexpr int kPartsAhead = 8;    // parts that the ring may hold at once: a part has > 1 chunk
 constexpr int kMaxCluster = 8;
 constexpr int kRingBytes = kChunks * kChunkVecs * 16;
 
@@ -396,15 +435,19 @@ __device__ __forceinline__ void repeated_slots(int k, int lane, const int* s_id,
   __syncwarp();
 }
 
-template <int MODE>
+template <int MODE, int kGroups>
 struct LongShared {
+  // A block may send the sums of a group's next row before another has read the last
+  // ones, but not those of the row after that, as it has then had the other's next.
+  static constexpr int kExchanges = 2 * kGroups;
   Slot<MODE> slot[kGatherWarps];
-  MaxSum ms[2][kConsumerWarps];
-  alignas(16) MaxSum cl[2][kMaxCluster];
-  RowResult r[2];
-  alignas(8) uint64_t full[kChunks], empty[kChunks];
-  uint64_t sums[2], go[2], done[2], xch[2];
+  MaxSum ms[kGroups][kGroupWarps];
+  alignas(16) MaxSum cl[kExchanges][kMaxCluster];
+  Soft soft[kGroups];
+  alignas(8) uint64_t full[kPartsAhead], empty[kChunks];
+  uint64_t sums[kGroups], go[kGroups], done[kGroups], xch[kExchanges];
   uint64_t ready[kGatherWarps], taken[kGatherWarps];
+  volatile int failed;  // the producer's wait ran out
 };
 
 // The rows of one cluster in order, 32 at a time: which of them count.
@@ -421,34 +464,53 @@ struct RowWalk {
   }
 };
 
+// A place in the ring of chunks: its slot, and the parity of the slot's phase.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kChunks) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void skip(int chunks) {  // at most kChunks
+    slot += chunks;
+    if (slot >= kChunks) {
+      slot -= kChunks;
+      phase ^= 1;
+    }
+  }
+};
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity));
 }
 
-template <int DT, int MODE>
-__global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLossArgs a,
-                                                                   const int skew) {
+template <int DT, int MODE, bool kGrad>
+__global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const TokenLossArgs a) {
   using L = typename LogitType<DT>::type;
   using V16 = Vec<DT>;
+  constexpr int kGroups = groups_of(kGrad);
+  constexpr int kConsumerWarps = kGroups * kGroupWarps;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ LongShared<MODE> sh;
+  __shared__ LongShared<MODE, kGroups> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = cluster_size(), rank = cluster_rank();
   if (tid == 0) {
-    for (int i = 0; i < kChunks; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), kConsumerWarps);
-    }
-    for (int p = 0; p < 2; ++p) {
-      mbar_init(smem_u32(&sh.sums[p]), kConsumerWarps);
+    for (int i = 0; i < kPartsAhead; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
+    for (int i = 0; i < kChunks; ++i) mbar_init(smem_u32(&sh.empty[i]), kGroupWarps);
+    for (int p = 0; p < kGroups; ++p) {
+      mbar_init(smem_u32(&sh.sums[p]), kGroupWarps);
       mbar_init(smem_u32(&sh.go[p]), 1);
-      mbar_init(smem_u32(&sh.done[p]), kConsumerWarps);
-      mbar_init(smem_u32(&sh.xch[p]), 1);
+      mbar_init(smem_u32(&sh.done[p]), kGroupWarps);
     }
+    for (int p = 0; p < sh.kExchanges; ++p) mbar_init(smem_u32(&sh.xch[p]), 1);
     for (int g = 0; g < kGatherWarps; ++g) {
       mbar_init(smem_u32(&sh.ready[g]), 1);
       mbar_init(smem_u32(&sh.taken[g]), 1);
     }
+    sh.failed = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -460,7 +522,6 @@ __global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLo
   const int first = blockIdx.x / C, step = gridDim.x / C;
   RowWalk<MODE> walk = {first, step, a.N, lane, 0u};
   const int rows = first < a.N ? (a.N - 1 - first) / step + 1 : 0;
-  const bool grad = a.dlogits != nullptr;
   auto logits_of = [&](int row) { return static_cast<const L*>(a.logits) + row * a.ld; };
   auto grad_of = [&](int row) { return static_cast<L*>(a.dlogits) + row * a.ld_grad; };
   // this block's vectors of a row: [v0, v0 + nv)
@@ -468,7 +529,11 @@ __global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLo
     Split sp;
     int v0, nv, chunks;
   };
+  // rows a multiple of 16 bytes apart are divided alike
+  const bool alike = a.ld * (DT == kF32 ? 4 : 2) % 16 == 0;
+  Part common = {};
   auto part_of = [&](int row) {
+    if (alike && row != first) return common;
     Part p;
     p.sp = split_row<DT>(logits_of(row), a.V, C);
     p.v0 = rank * p.sp.per;
@@ -476,131 +541,146 @@ __global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLo
     p.chunks = (p.nv + kChunkVecs - 1) / kChunkVecs;
     return p;
   };
+  common = part_of(first);
 
   if (warp < kConsumerWarps) {
-    const f32x2 c2 = pack2(a.c2, a.c2);
-    int pos = 0;            // ring position (chunks passed) of the next row for pass 1
-    uint32_t lv = 0;        // live rows passed
-    bool ok = true;
-    int prev = -1, prev_pos = 0;
-    auto pass2 = [&](int row, int at, uint32_t l) {
-      if (!warp_wait(&sh.go[l & 1], (l >> 1) & 1)) return false;
-      if (!grad) return true;
-      const Part p = part_of(row);
-      const RowResult r = sh.r[l & 1];
-      const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
-      const f32x2 neg = pack2(-r.m, -r.m), cf = pack2(r.coef, r.coef);
-      for (int c = 0; c < p.chunks; ++c, ++at) {
-        const int slot = at % kChunks;
-        const uint4* src = reinterpret_cast<const uint4*>(ring) + slot * kChunkVecs;
-        const int n = min(kChunkVecs, p.nv - c * kChunkVecs);
-        const int base = p.v0 + c * kChunkVecs;
-#pragma unroll 2
-        for (int i = tid; i < n; i += kConsumers) {
-          V16 d, g;
-          d.v = src[i];
-          if (r.coef != 0.0f) g = grad_vec(d, neg, c2, cf);
-          else g.fill(0);  // clipped, no teacher, or no finite logit
-          out.store(base + i, g);
+    constexpr int kPer = kChunkVecs / kGroupThreads;  // vectors of a chunk a thread has
+    constexpr int kStep = kPer >= 4 ? 1 : 4 / kPer;   // chunks of a step
+    const int g = warp / kGroupWarps, gtid = tid - g * kGroupThreads;
+    RingPos pos;      // of the next row's part
+    uint32_t lv = 0;  // live rows passed
+    // fn(array of vectors, their chunk(s), first vector, vectors left) over a part, kStep
+    // chunks at a time while there are so many
+    auto steps = [&](int nv, RingPos at, auto fn) {
+      int left = nv;
+      if constexpr (kStep == 2) {
+        for (; left > kChunkVecs; left -= 2 * kChunkVecs) {
+          const int a0 = at.slot;
+          at.next();
+          V16 d[2 * kPer];
+          fn(d, a0, at.slot, nv - left, left);
+          at.next();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.done[l & 1]));
-      return true;
+      for (; left > 0; left -= kChunkVecs) {
+        V16 d[kPer];
+        fn(d, at.slot, at.slot, nv - left, left);
+        at.next();
+      }
     };
-    for (int it = 0; it < rows && ok; ++it) {
+    auto read = [&](auto& d, int a0, int a1) {
+      const uint4* r = reinterpret_cast<const uint4*>(ring) + gtid;
+      constexpr int U = sizeof(d) / sizeof(V16);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        d[u].v = r[(u < kPer ? a0 : a1) * kChunkVecs + (u % kPer) * kGroupThreads];
+    };
+    auto release = [&](int a0, int a1) {
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sh.empty[a0]));
+        if (a1 != a0) mbar_arrive(smem_u32(&sh.empty[a1]));
+      }
+    };
+    for (int it = 0; it < rows; ++it) {
       const int row = first + it * step;
       const bool live = walk.live(a, it);
       const Part p = part_of(row);
       if (!live) {
-        if (grad) {
+        if (kGrad && it % kGroups == g) {
           const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
           V16 zero;
           zero.fill(0);
-          for (int i = tid; i < p.nv; i += kConsumers) out.store(p.v0 + i, zero);
+          for (int i = gtid; i < p.nv; i += kGroupThreads) out.store(p.v0 + i, zero);
         }
         continue;
       }
-      const int pos0 = pos;
+      const uint32_t l = lv++;
+      const RingPos at = pos;
+      pos.skip(p.chunks);
+      if (l % kGroups != g) continue;
+      const uint32_t ph = (l / kGroups) & 1;
+
       MaxSum v = {-INFINITY, 0.0f};
-      for (int c = 0; c < p.chunks && ok; ++c, ++pos) {
-        const int slot = pos % kChunks;
-        ok = warp_wait(&sh.full[slot], (pos / kChunks) & 1);
-        if (!ok) break;
-        const uint4* src = reinterpret_cast<const uint4*>(ring) + slot * kChunkVecs;
-        const int n = min(kChunkVecs, p.nv - c * kChunkVecs);
-        V16 d[kChunkVecs / kConsumers];
+      if (!warp_wait(&sh.full[l % kPartsAhead], (l / kPartsAhead) & 1)) break;
+      steps(p.nv, at, [&](auto& d, int a0, int a1, int, int left) {
+        constexpr int U = sizeof(d) / sizeof(V16);
+        read(d, a0, a1);
+        if (!kGrad) release(a0, a1);
+        if (left < U * kGroupThreads) {
 #pragma unroll
-        for (int u = 0; u < kChunkVecs / kConsumers; ++u) {
-          const int i = tid + u * kConsumers;
-          if (i < n) d[u].v = src[i];
-          else d[u].fill(V16::kNegInf);
+          for (int u = 0; u < U; ++u)
+            if (gtid + u * kGroupThreads >= left) d[u].fill(V16::kNegInf);
         }
-        uint32_t mw = d[0].v.x;
-#pragma unroll
-        for (int u = 0; u < kChunkVecs / kConsumers; ++u)
-#pragma unroll
-          for (int j = u == 0 ? 1 : 0; j < 4; ++j) mw = V16::max_word(mw, d[u].word(j));
-        const float m = fmaxf(v.m, V16::max_of_word(mw));
-        const float r = finite_ref(m);
-        const f32x2 neg = pack2(-r, -r);
-        f32x2 acc[2] = {pack2(v.s * ex2((v.m - r) * a.c2), 0.0f), 0};
-#pragma unroll
-        for (int u = 0; u < kChunkVecs / kConsumers; ++u)
-#pragma unroll
-          for (int j = 0; j < V16::kPairs; ++j) {
-            const float2 x = unpack2(mul2(add2(d[u].pair(j), neg), c2));
-            acc[j & 1] = add2(acc[j & 1], pack2(ex2(x.x), ex2(x.y)));
-          }
-        const float2 s = unpack2(add2(acc[0], acc[1]));
-        v = {m, s.x + s.y};
-        if (!grad) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
-        }
-      }
-      if (!ok) break;
+        v = add_vecs<DT, U>(v, d, a.c2);
+      });
       v = warp_merge(v, a.c2, 32);
       if (lane == 0) {
-        sh.ms[lv & 1][warp] = v;
-        mbar_arrive(smem_u32(&sh.sums[lv & 1]));
+        sh.ms[g][warp - g * kGroupWarps] = v;
+        mbar_arrive(smem_u32(&sh.sums[g]));
       }
-      if (skew) {
-        if (prev >= 0) ok = pass2(prev, prev_pos, lv - 1);
-        prev = row;
-        prev_pos = pos0;
-      } else {
-        ok = pass2(row, pos0, lv);
-      }
-      ++lv;
+
+      if (!warp_wait(&sh.go[g], ph)) break;
+      if constexpr (!kGrad) continue;
+      const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
+      with_soft<DT>(sh.soft[g], a.c2, [&](auto grad_vec) {
+        steps(p.nv, at, [&](auto& d, int a0, int a1, int from, int left) {
+          constexpr int U = sizeof(d) / sizeof(V16);
+          read(d, a0, a1);  // beyond the part: what the slot held, not stored
+          release(a0, a1);
+          const int base = p.v0 + from + gtid;
+#pragma unroll
+          for (int u = 0; u < U; ++u) d[u] = grad_vec(d[u]);
+          if (out.aligned && left >= U * kGroupThreads) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) out.vecs()[base + u * kGroupThreads] = d[u].v;
+          } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (gtid + u * kGroupThreads < left) out.store(base + u * kGroupThreads, d[u]);
+          }
+        });
+      });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.done[g]));
     }
-    if (ok && prev >= 0) pass2(prev, prev_pos, lv - 1);
   } else if (warp == kConsumerWarps) {  // producer
-    int pos = 0;
+    RingPos pos;
+    uint32_t lv = 0;
     bool ok = true;
     for (int it = 0; it < rows && ok; ++it) {
       const int row = first + it * step;
       if (!walk.live(a, it)) continue;
       const Part p = part_of(row);
       const uint4* src = reinterpret_cast<const uint4*>(logits_of(row) + p.sp.head) + p.v0;
-      for (int c = 0; c < p.chunks; ++c, ++pos) {
-        const int slot = pos % kChunks;
-        ok = warp_wait(&sh.empty[slot], ((pos / kChunks) & 1) ^ 1);
+      uint64_t* full = &sh.full[lv % kPartsAhead];
+      for (int left = p.nv; left > 0; left -= kChunkVecs, pos.next()) {
+        ok = warp_wait(&sh.empty[pos.slot], pos.phase ^ 1);
         if (!ok) break;
         if (lane == 0) {
-          const uint32_t bytes = 16u * min(kChunkVecs, p.nv - c * kChunkVecs);
-          mbar_expect_tx(smem_u32(&sh.full[slot]), bytes);
-          bulk_load(smem_u32(ring) + slot * kChunkVecs * 16, src + c * kChunkVecs, bytes,
-                    smem_u32(&sh.full[slot]));
+          const uint32_t bytes = 16u * min(kChunkVecs, left);
+          // one arrival a part, with its last chunk: the bytes before it are counted too
+          if (left <= kChunkVecs) mbar_expect_tx(smem_u32(full), bytes);
+          else mbar_add_tx(smem_u32(full), bytes);
+          bulk_load(smem_u32(ring) + pos.slot * kChunkVecs * 16, src + (p.nv - left), bytes,
+                    smem_u32(full));
         }
         __syncwarp();
       }
+      if (ok && p.nv == 0 && lane == 0) mbar_arrive(smem_u32(full));
+      if (ok) ++lv;
+      else break;
     }
-    // no copy may be in flight when the block ends
-    for (int i = max(0, pos - kChunks); i < pos; ++i)
-      warp_wait(&sh.full[i % kChunks], (i / kChunks) & 1);
+    // no copy may be in flight when the block ends: a part that a wait cut short completes
+    // with the chunks it has, and its row is not valid
+    if (!ok && lane == 0) {
+      sh.failed = 1;
+      __threadfence_block();
+      mbar_arrive(smem_u32(&sh.full[lv % kPartsAhead]));
+    }
+    const uint32_t parts = ok ? lv : lv + 1;
+    for (uint32_t i = parts > kPartsAhead ? parts - kPartsAhead : 0; i < parts; ++i)
+      warp_wait(&sh.full[i % kPartsAhead], (i / kPartsAhead) & 1);
   } else if (warp <= kConsumerWarps + kGatherWarps) {  // gather
     const int g = warp - kConsumerWarps - 1;
     Slot<MODE>& s = sh.slot[g];
@@ -631,7 +711,7 @@ __global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLo
           s.w = a.row_weight ? a.row_weight[row] : 1.0f;
         }
         __syncwarp();
-        if (grad) repeated_slots(a.k, lane, s.id, s.q);
+        if (kGrad) repeated_slots(a.k, lane, s.id, s.q);
       } else if (lane < 5) {
         const int act = lane == 0 ? load_id(a.actions, a.ids64, row) : 0;
         const float* from = lane == 1   ? a.row_weight
@@ -649,78 +729,57 @@ __global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLo
       if (lane == 0) mbar_arrive(smem_u32(&sh.ready[g]));
     }
   } else {  // finish
+    const int b = warp - (kConsumerWarps + 1 + kGatherWarps);  // its group
     uint32_t lv = 0;
     bool ok = true;
-    int prev = -1, it = 0;
-    auto entries = [&](int row, uint32_t l) {  // after pass 2
-      const int g = l % kGatherWarps;
-      const Slot<MODE>& s = sh.slot[g];
-      if (grad) {
-        if (!warp_wait(&sh.done[l & 1], (l >> 1) & 1)) return false;
-        const RowResult r = sh.r[l & 1];
-        const Part p = part_of(row);
-        L* dz = grad_of(row);
-        if (rank == 0 && lane < p.sp.head + p.sp.tail)
-          store_logit<DT>(dz + edge_column(p.sp, a.V, lane),
-                          r.coef == 0.0f ? 0.0f : r.coef * ex2((s.edge[lane] - r.m) * a.c2));
-        __syncwarp();
-        const int n = r.coef == 0.0f ? 0 : MODE == kDistill ? a.k : 1;
-        for (int i = lane; i < n; i += 32) {
-          const int id = s.id[i];
-          if (id < 0) continue;
-          const int e = id - p.sp.head;  // rank 0 has the edges, else whose vector it is
-          const int vec = e / V16::kElems - p.v0;
-          const bool mine = e < 0 || e >= p.sp.nb * V16::kElems ? rank == 0 : vec >= 0 && vec < p.nv;
-          const float more = MODE == kDistill ? -r.scale * s.q[i] : r.top;
-          if (mine) store_logit<DT>(dz + id, r.coef * ex2((s.z[i] - r.m) * a.c2) + more);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.taken[g]));
-      return true;
-    };
+    int it = 0;
     for (; it < rows && ok; ++it) {
       const int row = first + it * step;
       if (!walk.live(a, it)) {
-        if (rank == 0) {
+        if (rank == 0 && it % kGroups == b) {
           if (lane == 0) {
             if (a.row_loss) a.row_loss[row] = 0.0f;
             if (a.logp) a.logp[row] = 0.0f;
           }
-          const Split sp = split_row<DT>(logits_of(row), a.V, C);
-          if (grad && lane < sp.head + sp.tail)
-            store_logit<DT>(grad_of(row) + edge_column(sp, a.V, lane), 0.0f);
+          if (kGrad) {
+            const Split sp = part_of(row).sp;
+            if (lane < sp.head + sp.tail)
+              store_logit<DT>(grad_of(row) + edge_column(sp, a.V, lane), 0.0f);
+          }
         }
         continue;
       }
-      const int b = lv & 1, ph = (lv >> 1) & 1;
-      const int g = lv % kGatherWarps;
+      const uint32_t l = lv++;
+      if (l % kGroups != b) continue;
+      const int g = l % kGatherWarps, x = l % sh.kExchanges;
+      const uint32_t ph = (l / kGroups) & 1;
       const Slot<MODE>& s = sh.slot[g];
-      ok = warp_wait(&sh.ready[g], (lv / kGatherWarps) & 1) && warp_wait(&sh.sums[b], ph);
+      const Part p = part_of(row);
+      ok = warp_wait(&sh.ready[g], (l / kGatherWarps) & 1) && warp_wait(&sh.sums[b], ph) &&
+           !sh.failed;
       if (!ok) break;
-      // lanes 0..15 the consumer warps' pairs, from 16 on rank 0's edges
-      const Split sp = split_row<DT>(logits_of(row), a.V, C);
-      MaxSum v = {-INFINITY, 0.0f};
-      if (lane < kConsumerWarps) v = sh.ms[b][lane];
-      else if (rank == 0 && lane - kConsumerWarps < sp.head + sp.tail)
-        v = {s.edge[lane - kConsumerWarps], 1.0f};
-      v = warp_merge(v, a.c2, 32);
+      // the consumer warps' pairs, and rank 0's edges
+      MaxSum v = lane < kGroupWarps ? sh.ms[b][lane] : MaxSum{-INFINITY, 0.0f};
+      if (rank == 0 && lane < p.sp.head + p.sp.tail)
+        v = merge(v, one_logit(s.edge[lane], a.c2), a.c2);
+      v = warp_merge(v, a.c2, 16);
       if (C > 1) {
-        if (lane == 0) mbar_expect_tx(smem_u32(&sh.xch[b]), 8u * C);
+        if (lane == 0) mbar_expect_tx(smem_u32(&sh.xch[x]), 8u * C);
         __syncwarp();
         if (lane < C)
-          st_async_f32x2(smem_u32(&sh.cl[b][rank]), smem_u32(&sh.xch[b]), lane, v.m, v.s);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.xch[b]), ph));
+          st_async_f32x2(smem_u32(&sh.cl[x][rank]), smem_u32(&sh.xch[x]), lane, v.m, v.s);
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait_cluster(smem_u32(&sh.xch[x]), (l / sh.kExchanges) & 1));
         if (!ok) break;
-        v = lane < C ? sh.cl[b][lane] : MaxSum{-INFINITY, 0.0f};
+        v = lane < C ? sh.cl[x][lane] : MaxSum{-INFINITY, 0.0f};
         v = warp_merge(v, a.c2, kMaxCluster);
       }
+      const RowResult r =  // lane 0's counts
+          MODE == kDistill
+              ? finish_row<MODE>(a, v, s.w, s.t, 0.0f, 0.0f, 0.0f, 0.0f)
+              : finish_row<MODE>(a, v, s.in[1], s.t, s.z[0], s.in[2], s.in[3], s.in[4]);
       if (lane == 0) {
-        const RowResult r =
-            MODE == kDistill
-                ? finish_row<MODE>(a, v, s.w, s.t, 0.0f, 0.0f, 0.0f, 0.0f)
-                : finish_row<MODE>(a, v, s.in[1], s.t, s.z[0], s.in[2], s.in[3], s.in[4]);
-        sh.r[b] = r;
+        if (kGrad) sh.soft[b] = r.soft;
         mbar_arrive(smem_u32(&sh.go[b]));
         if (rank == 0) {
           if (a.row_loss) a.row_loss[row] = r.loss;
@@ -728,17 +787,32 @@ __global__ void __launch_bounds__(kLongThreads, 1) long_row_kernel(const TokenLo
         }
       }
       __syncwarp();
-      if (skew) {
-        if (prev >= 0) ok = entries(prev, lv - 1);
-        prev = row;
-      } else {
-        ok = entries(row, lv);
+      if constexpr (kGrad) {  // after pass 2
+        const Soft soft = sh.soft[b];
+        const float scale = __shfl_sync(0xFFFFFFFFu, r.scale, 0);
+        const float top = __shfl_sync(0xFFFFFFFFu, r.top, 0);
+        ok = warp_wait(&sh.done[b], ph);
+        if (!ok) break;
+        L* dz = grad_of(row);
+        if (rank == 0 && lane < p.sp.head + p.sp.tail)
+          store_logit<DT>(dz + edge_column(p.sp, a.V, lane), soft_at(s.edge[lane], soft, a.c2));
+        __syncwarp();
+        const int n = soft.coef == 0.0f ? 0 : MODE == kDistill ? a.k : 1;
+        for (int i = lane; i < n; i += 32) {
+          const int id = s.id[i];
+          if (id < 0) continue;
+          const int e = id - p.sp.head;  // rank 0 has the edges, else whose vector it is
+          const int vec = e / V16::kElems - p.v0;
+          const bool mine = e < 0 || e >= p.sp.nb * V16::kElems ? rank == 0 : vec >= 0 && vec < p.nv;
+          const float more = MODE == kDistill ? -scale * s.q[i] : top;
+          if (mine) store_logit<DT>(dz + id, soft_at(s.z[i], soft, a.c2) + more);
+        }
+        __syncwarp();
       }
-      ++lv;
+      if (lane == 0) mbar_arrive(smem_u32(&sh.taken[g]));
     }
-    if (ok && prev >= 0) ok = entries(prev, lv - 1);
     if (!ok && rank == 0)  // a wait ran out: this row and the rest are not valid
-      for (int i = max(0, it - 1) + lane; i < rows; i += 32) {
+      for (int i = it + lane; i < rows; i += 32) {
         if (a.row_loss) a.row_loss[first + i * step] = NAN;
         if (a.logp) a.logp[first + i * step] = NAN;
       }
@@ -755,14 +829,14 @@ cudaError_t launch_short(const TokenLossArgs& a, cudaStream_t s) {
   return launch_pdl(short_row_kernel<DT, MODE, NT, VPT>, dim3(a.N), dim3(NT), 0, s, a);
 }
 
-template <int DT, int MODE>
-cudaError_t launch_long(const TokenLossArgs& a, int C, int skew, cudaStream_t s) {
-  auto kernel = long_row_kernel<DT, MODE>;
+template <int DT, int MODE, bool kGrad>
+cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s) {
+  auto kernel = long_row_kernel<DT, MODE, kGrad>;
   static std::atomic<uint64_t> limit_set{0};
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kRingBytes, limit_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kLongThreads);
+  cfg.blockDim = dim3(long_threads(kGrad));
   cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -785,10 +859,10 @@ cudaError_t launch_long(const TokenLossArgs& a, int C, int skew, cudaStream_t s)
     resident[dev & 63][C].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3((unsigned)(a.N < n ? a.N : n) * C);
-  return cudaLaunchKernelEx(&cfg, kernel, a, skew);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-constexpr int kPartChunks = 5;      // a block's part of a row, at most, while C <= 8 allows
+constexpr int kPartVecs = 5120;     // a block's part of a row, at most, while C <= 8 allows
 constexpr int kShortVecs = 2048;    // rows of 32 KB and less are short
 
 // The variant goes by the row's length alone, so that a row's bits do not depend on
@@ -799,11 +873,8 @@ cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
   if (nvec <= 128) return launch_short<DT, MODE, 128, 1>(a, s);
   if (nvec <= 512) return launch_short<DT, MODE, 128, 4>(a, s);
   if (nvec <= kShortVecs) return launch_short<DT, MODE, 512, 4>(a, s);
-  const int chunks = (nvec + kChunkVecs - 1) / kChunkVecs;
-  const int C = min(kMaxCluster, (chunks + kPartChunks - 1) / kPartChunks);
-  const int per = (nvec + C - 1) / C;
-  const int skew = 2 * ((per + kChunkVecs - 1) / kChunkVecs) <= kChunks;
-  return launch_long<DT, MODE>(a, C, skew, s);
+  const int C = min(kMaxCluster, (nvec + kPartVecs - 1) / kPartVecs);
+  return a.dlogits ? launch_long<DT, MODE, true>(a, C, s) : launch_long<DT, MODE, false>(a, C, s);
 }
 
 template <int DT>
