@@ -11,10 +11,14 @@
 // (the last term is the gradient of the scores w, a softmax over the chosen
 // logits).  The counts are constants of the gradient.
 //
-// Sums run in a fixed order, so equal inputs give equal bits.  Rows are cut into
-// chunks; chunk c of sequence s leaves its partial sums in slot c + s (walking
-// the rows, each step from one piece to the next raises c or s, so pieces have
-// different slots), and a second kernel adds a sequence's slots up in order.
+// One warp per row, the row in registers, the next row's loads in flight.  Sums run
+// in a fixed order, so equal inputs give equal bits: rows are cut into chunks, one a
+// block; chunk c of sequence s leaves its partial sums in slot c + s (walking the
+// rows, each step from one piece to the next raises c or s, so pieces have different
+// slots), and a second kernel adds a sequence's slots up in order, its last block the
+// sequences.  Small batches take one block and one launch.
+#include <type_traits>
+
 #include "internal.h"
 #include "logits.cuh"
 #include "ptx.cuh"
@@ -23,33 +27,47 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxPerLane = 32;  // E <= 1024
-constexpr int kChunkRows = 128;
+constexpr int kWarps = 8;        // of a block of many
+constexpr int kSmallWarps = 16;  // of the only block of a small batch
+constexpr int kSmallRows = 128;  // the largest small batch
+constexpr int kSmallSeqs = 4;
+constexpr int kTargetBlocks = 152 * 4;
 
-int num_chunks(int T) { return (T + kChunkRows - 1) / kChunkRows; }
+// Rows of a chunk: a block's warps share them; more rows per block than kWarps only
+// where the device is full.
+int chunk_rows(int T) {
+  const int r = (T + kTargetBlocks - 1) / kTargetBlocks;
+  return (r + kWarps - 1) / kWarps * kWarps;
+}
+// No fewer chunks than any smaller batch has.
+int max_chunks(int T) {
+  const int c = (T + kWarps - 1) / kWarps;
+  return c < kTargetBlocks ? c : kTargetBlocks;
+}
 
 // Workspace: the status word (as the forward's, for moe_nvfp4_read_status), the
-// second kernel's ticket, per sequence its share of the losses and the bad-id
-// flag, then per slot [E] probability sums, [E] counts, z sum, live rows, bad ids.
+// second kernel's ticket, per sequence its z sum and bad-id flag, per sequence and
+// 32 experts the sum of counts times probabilities, then per slot [E] probability
+// sums, [E] counts, z sum, live rows, bad ids.
 struct Ws {
   int32_t* status;
   int32_t* ticket;
-  float2* seq;      // [S] balance and z sums
-  int32_t* seq_bad; // [S]
-  float* slot;      // [slots][2 E + 3]
+  float2* seq;
+  float* dots;
+  float* slot;
 };
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-Ws carve(void* ws, int S) {
+int expert_blocks(int E) { return (E + 31) / 32; }
+size_t seq_bytes(int S) { return up256((size_t)S * sizeof(float2)); }
+size_t dots_bytes(int S, int E) { return up256((size_t)S * expert_blocks(E) * sizeof(float)); }
+Ws carve(void* ws, int E, int S) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   Ws w;
   w.status = reinterpret_cast<int32_t*>(p);
   w.ticket = w.status + kStatusWords;
   w.seq = reinterpret_cast<float2*>(p + 256);
-  w.seq_bad = reinterpret_cast<int32_t*>(p + 256 + up256((size_t)S * sizeof(float2)));
-  w.slot = reinterpret_cast<float*>(p + 256 + up256((size_t)S * sizeof(float2)) +
-                                    up256((size_t)S * sizeof(int32_t)));
+  w.dots = reinterpret_cast<float*>(p + 256 + seq_bytes(S));
+  w.slot = reinterpret_cast<float*>(p + 256 + seq_bytes(S) + dots_bytes(S, E));
   return w;
 }
 
@@ -66,54 +84,197 @@ __device__ __forceinline__ int sequence_of(const int32_t* off, int S, int row) {
   return lo;
 }
 
-// One router row in a warp's registers: lane + 32 i holds expert lane + 32 i.
-template <int DT>
-struct Row {
-  float p[kMaxPerLane];  // softmax, 0 beyond E
-  float m, r;            // the largest logit (0 if none is finite) and 1 / sum (0 then)
-  float lse;             // 0 for a row without a finite logit
-  __device__ __forceinline__ void load(const typename LogitType<DT>::type* x, int E, int lane) {
-    m = -INFINITY;
+// How a warp holds a row: NV vectors of 16 bytes a lane, vector i of lane l at column
+// (32 i + l) W.  Rows that do not start on 16-byte boundaries, or whose length is no
+// multiple of W, are read and written by the element, with the same columns in the same
+// lanes and so the same bits.
+template <int DT, int NV, bool kAligned>
+struct Raw {
+  using L = typename LogitType<DT>::type;
+  using V = Vec<DT>;
+  static constexpr int W = V::kElems;
+  static constexpr int kN = W * NV;
+  V v[NV];
+  static __device__ __forceinline__ int column(int n, int lane) {
+    return (n / W * 32 + lane) * W + n % W;
+  }
+  __device__ __forceinline__ void load(const L* row, int E, int lane) {
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-      if (32 * i >= E) break;
-      const int e = lane + 32 * i;
-      p[i] = e < E ? load_logit<DT>(x + e) : -INFINITY;
-      m = fmaxf(m, p[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (32 * i + lane) * W;
+      if (kAligned) {
+        if (c < E) v[i].v = *reinterpret_cast<const uint4*>(row + c);
+        else v[i].fill(V::kNegInf);
+      } else {
+        L x[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          if constexpr (DT == kF32) x[j] = c + j < E ? row[c + j] : -INFINITY;
+          else x[j] = c + j < E ? row[c + j] : (L)(V::kNegInf >> 16);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (DT == kF32) v[i].set_word(j, __float_as_uint(x[j]));
+          else v[i].set_word(j, (uint32_t)x[2 * j] | (uint32_t)x[2 * j + 1] << 16);
+        }
+      }
     }
-    m = finite_ref(warp_max(m));
-    float s = 0.0f;
+  }
+  __device__ __forceinline__ void get(float (&f)[kN]) const {
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-      if (32 * i >= E) break;
-      p[i] = ex2((p[i] - m) * kLog2e);
-      s += p[i];
+    for (int n = 0; n < kN; n += 2) {
+      const float2 p = v[n / W].pair(n % W / 2);
+      f[n] = p.x;
+      f[n + 1] = p.y;
     }
-    s = warp_sum(s);
-    lse = s == 0.0f ? 0.0f : m + logf(s);
-    r = s == 0.0f ? 0.0f : 1.0f / s;
+  }
+  static __device__ __forceinline__ void store(L* row, int E, int lane, const float (&f)[kN]) {
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-      if (32 * i >= E) break;
-      p[i] *= r;
+    for (int i = 0; i < NV; ++i) {
+      const int c = (32 * i + lane) * W;
+      if (kAligned) {
+        if (c >= E) break;
+        V g;
+#pragma unroll
+        for (int j = 0; j < V::kPairs; ++j)
+          g.set_pair(j, make_float2(f[i * W + 2 * j], f[i * W + 2 * j + 1]));
+        *reinterpret_cast<uint4*>(row + c) = g.v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (c + j < E) store_logit<DT>(row + c + j, f[i * W + j]);
+      }
     }
   }
 };
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) router_partial_kernel(const RouterLossArgs a, Ws w) {
-  using L = typename LogitType<DT>::type;
+// The row's softmax over its warp: p = 2^((x - m) log2 e) r; a row without a finite
+// logit has p = 0 and lse = 0.
+struct RowStats {
+  float m, r, lse;
+};
+template <int N>
+__device__ __forceinline__ RowStats softmax(float (&p)[N]) {
+  float m = p[0];
+#pragma unroll
+  for (int n = 1; n < N; ++n) m = fmaxf(m, p[n]);
+  m = finite_ref(warp_max(m));
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    p[n] = ex2((p[n] - m) * kLog2e);
+    s[n & 1] += p[n];
+  }
+  const float sum = warp_sum(s[0] + s[1]);
+  RowStats st;
+  st.m = m;
+  st.lse = sum == 0.0f ? 0.0f : m + logf(sum);
+  st.r = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int n = 0; n < N; ++n) p[n] *= st.r;
+  return st;
+}
+
+// One piece: the sums over the live rows of [row0, row1) by a block of NW warps.
+// Afterwards, for all threads: sum of the warps' s_p[w][e] is the probability sum,
+// s_hist the counts; z, n and bad are thread 0's.
+struct PieceScalars {
+  float z;
+  int n, bad;
+};
+template <int DT, int NV, bool kAligned, int NW>
+__device__ __forceinline__ PieceScalars piece_sums(const RouterLossArgs& a, int row0, int row1,
+                                                   float* s_p, int* s_hist) {
+  using R = Raw<DT, NV, kAligned>;
+  __shared__ float s_z[NW];
+  __shared__ int s_n[NW], s_bad[NW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int e = tid; e < a.E; e += NW * 32) s_hist[e] = 0;
+  __syncthreads();
+  float acc[R::kN];
+#pragma unroll
+  for (int i = 0; i < R::kN; ++i) acc[i] = 0.0f;
+  float z = 0.0f;
+  int n = 0, bad = 0;
+  const auto* base = static_cast<const typename R::L*>(a.logits);
+  auto live = [&](int t) { return t < row1 && (!a.mask || a.mask[t]); };
+  // an id below -1 or from E on is bad; 64-bit ids beyond 32 bits read as -2
+  auto id_of = [&](int t) {
+    if (lane >= a.K) return -1;
+    const int64_t at = (int64_t)t * a.K + lane;
+    if (!a.ids64) return static_cast<const int32_t*>(a.ids)[at];
+    const long long v = static_cast<const long long*>(a.ids)[at];
+    return v < -1 || v > INT32_MAX ? -2 : (int)v;
+  };
+  int t = row0 + warp;
+  R next;
+  int next_id = -1;
+  bool next_live = live(t);
+  if (next_live) {
+    next.load(base + t * a.ld, a.E, lane);
+    next_id = id_of(t);
+  }
+  for (; t < row1; t += NW) {
+    const R row = next;
+    const int id = next_id;
+    const bool use = next_live;
+    next_live = live(t + NW);
+    if (next_live) {
+      next.load(base + (t + NW) * a.ld, a.E, lane);
+      next_id = id_of(t + NW);
+    }
+    if (!use) continue;
+    float p[R::kN];
+    row.get(p);
+    const RowStats st = softmax(p);
+#pragma unroll
+    for (int i = 0; i < R::kN; ++i) acc[i] += p[i];
+    z += st.lse * st.lse;
+    ++n;
+    if (id >= 0 && id < a.E) atomicAdd(&s_hist[id], 1);
+    else if (id != -1) bad = 1;
+  }
+#pragma unroll
+  for (int i = 0; i < R::kN; ++i) {
+    const int e = R::column(i, lane);
+    if (e < a.E) s_p[warp * a.E + e] = acc[i];
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (lane == 0) {
+    s_z[warp] = z;
+    s_n[warp] = n;
+    s_bad[warp] = bad;
+  }
+  __syncthreads();
+  PieceScalars r = {0.0f, 0, 0};
+  if (tid == 0) {
+    for (int i = 0; i < NW; ++i) {
+      r.z += s_z[i];
+      r.n += s_n[i];
+      r.bad |= s_bad[i];
+    }
+  }
+  return r;
+}
+template <int NW>
+__device__ __forceinline__ float warps_sum(const float* s_p, int E, int e) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) sum += s_p[i * E + e];
+  return sum;
+}
+
+template <int DT, int NV, bool kAligned>
+__global__ void __launch_bounds__(kWarps * 32) router_partial_kernel(const RouterLossArgs a, Ws w,
+                                                                     int rows) {
   extern __shared__ float s_p[];  // [kWarps][E], then int[E]
   int* s_hist = reinterpret_cast<int*>(s_p + kWarps * a.E);
-  __shared__ float s_z[kWarps];
-  __shared__ int s_n[kWarps], s_bad[kWarps];
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  const int tid = threadIdx.x;
   if (blockIdx.x == 0 && tid == 0) *w.ticket = 0;
-  const int row_end = min(a.T, (int)(blockIdx.x + 1) * kChunkRows);
-  int row0 = blockIdx.x * kChunkRows;
-  for (int e = tid; e < a.E; e += kThreads) s_hist[e] = 0;
-  __syncthreads();
+  const int row_end = (int)min((int64_t)a.T, ((int64_t)blockIdx.x + 1) * rows);
+  int row0 = blockIdx.x * rows;
   while (row0 < row_end) {  // one piece: the rows of one sequence in this chunk
     const int s = sequence_of(a.offsets, a.S, row0);
     if (s < 0) {  // before the first sequence or past the last
@@ -121,237 +282,338 @@ __global__ void __launch_bounds__(kThreads) router_partial_kernel(const RouterLo
       continue;
     }
     const int row1 = a.offsets ? min(row_end, a.offsets[s + 1]) : row_end;
-    float acc[kMaxPerLane];
-#pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) acc[i] = 0.0f;
-    float z = 0.0f;
-    int n = 0, bad = 0;
-    for (int t = row0 + warp; t < row1; t += kWarps) {
-      if (a.mask && !a.mask[t]) continue;
-      Row<DT> r;
-      r.load(static_cast<const L*>(a.logits) + t * a.ld, a.E, lane);
-#pragma unroll
-      for (int i = 0; i < kMaxPerLane; ++i) {
-        if (32 * i >= a.E) break;
-        acc[i] += r.p[i];
-      }
-      z += r.lse * r.lse;
-      ++n;
-      if (lane < a.K) {
-        const int64_t at = (int64_t)t * a.K + lane;
-        const int id = load_id(a.ids, a.ids64, at);
-        if (id >= 0 && id < a.E) atomicAdd(&s_hist[id], 1);
-        const bool empty = a.ids64 ? static_cast<const long long*>(a.ids)[at] == -1 : id == -1;
-        bad |= !(id >= 0 && id < a.E) && !empty;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E) s_p[warp * a.E + e] = acc[i];
-    }
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) {
-      s_z[warp] = z;
-      s_n[warp] = n;
-      s_bad[warp] = bad;
-    }
-    __syncthreads();
+    const PieceScalars r = piece_sums<DT, NV, kAligned, kWarps>(a, row0, row1, s_p, s_hist);
     float* slot = w.slot + (size_t)(blockIdx.x + s) * (2 * a.E + 3);
-    for (int e = tid; e < a.E; e += kThreads) {
-      float sum = 0.0f;
-      for (int i = 0; i < kWarps; ++i) sum += s_p[i * a.E + e];
-      slot[e] = sum;
+    for (int e = tid; e < a.E; e += kWarps * 32) {
+      slot[e] = warps_sum<kWarps>(s_p, a.E, e);
       slot[a.E + e] = __int_as_float(s_hist[e]);
-      s_hist[e] = 0;
     }
     if (tid == 0) {
-      float zs = 0.0f;
-      int ns = 0, bs = 0;
-      for (int i = 0; i < kWarps; ++i) {
-        zs += s_z[i];
-        ns += s_n[i];
-        bs |= s_bad[i];
-      }
-      slot[2 * a.E] = zs;
-      slot[2 * a.E + 1] = __int_as_float(ns);
-      slot[2 * a.E + 2] = __int_as_float(bs);
+      slot[2 * a.E] = r.z;
+      slot[2 * a.E + 1] = __int_as_float(r.n);
+      slot[2 * a.E + 2] = __int_as_float(r.bad);
     }
     __syncthreads();
     row0 = max(row1, row0 + 1);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) router_combine_kernel(const RouterLossArgs a, Ws w,
-                                                                  int chunks) {
-  __shared__ float s_a[kThreads], s_b[kThreads];
-  __shared__ int s_i[kThreads];
+// The two losses from the sums, and what goes with them.
+__device__ __forceinline__ void write_losses(const RouterLossArgs& a, const Ws& w, float bal,
+                                             float z, int n, int bad) {
+  const float per = n > 0 ? 1.0f / (float)n : 0.0f;
+  a.losses[0] = n > 0 ? a.balance_coef * bal * per : 0.0f;
+  a.losses[1] = n > 0 ? a.z_coef * z * per : 0.0f;
+  a.tokens[a.S] = n;
+  *w.status = bad ? kFlagBadExpertId : 0;
+}
+__device__ __forceinline__ float even_share(const RouterLossArgs& a, int n_s) {
+  return n_s > 0 ? (float)a.E / ((float)a.K * (float)n_s) : 0.0f;
+}
+
+// Block (s, j): sequence s, experts 32 j to 32 j + 31 along x, its slots along y.
+__global__ void __launch_bounds__(1024) router_combine_kernel(const RouterLossArgs a, Ws w,
+                                                              int rows) {
+  __shared__ float s_a[1024], s_b[1024];
+  __shared__ int s_i[1024];
   __shared__ int s_last;
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.x, tid = threadIdx.x;
-  const int r0 = a.offsets ? a.offsets[s] : 0, r1 = a.offsets ? a.offsets[s + 1] : a.T;
-  int c0 = max(0, r0) / kChunkRows, c1 = (min(r1, a.T) + kChunkRows - 1) / kChunkRows;
-  if (r1 <= r0) c1 = c0;
-  float z = 0.0f;
-  int n = 0, bad = 0;
-  for (int c = c0; c < c1; ++c) {
-    const float* slot = w.slot + (size_t)(c + s) * (2 * a.E + 3);
-    z += slot[2 * a.E];
-    n += __float_as_int(slot[2 * a.E + 1]);
-    bad |= __float_as_int(slot[2 * a.E + 2]);
-  }
-  float dot = 0.0f;
-  for (int e = tid; e < a.E; e += kThreads) {
-    float p = 0.0f;
-    int cnt = 0;
-    for (int c = c0; c < c1; ++c) {
-      const float* slot = w.slot + (size_t)(c + s) * (2 * a.E + 3);
+  const int s = blockIdx.x, lane = threadIdx.x, y = threadIdx.y, Y = blockDim.y;
+  const int tid = y * 32 + lane, threads = Y * 32;
+  const int e = blockIdx.y * 32 + lane;
+  const int r0 = a.offsets ? max(0, a.offsets[s]) : 0;
+  const int r1 = a.offsets ? min(a.T, a.offsets[s + 1]) : a.T;
+  const int c0 = r0 / rows, c1 = r1 > r0 ? (r1 + rows - 1) / rows : c0;
+  const size_t stride = 2 * (size_t)a.E + 3;
+  float p = 0.0f, z = 0.0f;
+  int cnt = 0, n = 0, bad = 0;
+  const bool meta = blockIdx.y == 0 && lane == 0;
+#pragma unroll 4
+  for (int c = c0 + y; c < c1; c += Y) {
+    const float* slot = w.slot + (size_t)(c + s) * stride;
+    if (e < a.E) {
       p += slot[e];
       cnt += __float_as_int(slot[a.E + e]);
     }
-    a.counts[(size_t)s * a.E + e] = cnt;
-    dot += (float)cnt * p;
+    if (meta) {
+      z += slot[2 * a.E];
+      n += __float_as_int(slot[2 * a.E + 1]);
+      bad |= __float_as_int(slot[2 * a.E + 2]);
+    }
   }
-  s_a[tid] = dot;
+  s_a[tid] = p;
+  s_i[tid] = cnt;
   __syncthreads();
-  if (tid == 0) {
-    float sum = 0.0f;
-    for (int i = 0; i < kThreads; ++i) sum += s_a[i];
-    const float f = n > 0 ? (float)a.E / ((float)a.K * (float)n) : 0.0f;
-    w.seq[s] = make_float2(n > 0 ? f * sum : 0.0f, z);
-    w.seq_bad[s] = bad;
-    a.tokens[s] = n;
-    s_last = atom_add_acq_rel_gpu(w.ticket, 1) == (int)gridDim.x - 1;
+  if (y == 0) {
+    for (int i = 1; i < Y; ++i) {
+      p += s_a[i * 32 + lane];
+      cnt += s_i[i * 32 + lane];
+    }
+    if (e < a.E) a.counts[(size_t)s * a.E + e] = cnt;
+    const float dot = warp_sum(e < a.E ? (float)cnt * p : 0.0f);
+    if (lane == 0) w.dots[(size_t)s * gridDim.y + blockIdx.y] = dot;
   }
+  __syncthreads();
+  if (blockIdx.y == 0) {
+    if (lane == 0) {
+      s_a[y] = z;
+      s_i[y] = n;
+      s_i[32 + y] = bad;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < Y; ++i) {
+        z += s_a[i];
+        n += s_i[i];
+        bad |= s_i[32 + i];
+      }
+      w.seq[s] = make_float2(z, __int_as_float(bad));
+      a.tokens[s] = n;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0)
+    s_last = atom_add_acq_rel_gpu(w.ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
   __syncthreads();
   if (!s_last) return;
   // the last block adds the sequences up
-  float bal = 0.0f, zs = 0.0f;
-  int total = 0;
-  bad = 0;
-  for (int i = tid; i < a.S; i += kThreads) {
+  float bal = 0.0f;
+  z = 0.0f;
+  n = bad = 0;
+  for (int i = tid; i < a.S; i += threads) {
+    float dot = 0.0f;
+    for (int j = 0; j < (int)gridDim.y; ++j) dot += __ldcg(&w.dots[(size_t)i * gridDim.y + j]);
+    const int n_s = __ldcg(&a.tokens[i]);
     const float2 v = __ldcg(&w.seq[i]);
-    bal += v.x;
-    zs += v.y;
-    total += __ldcg(&a.tokens[i]);
-    bad |= __ldcg(&w.seq_bad[i]);
+    bal += n_s > 0 ? even_share(a, n_s) * dot : 0.0f;
+    z += v.x;
+    n += n_s;
+    bad |= __float_as_int(v.y);
   }
+  const int any_bad = __syncthreads_or(bad);
   s_a[tid] = bal;
-  s_b[tid] = zs;
-  s_i[tid] = total;
-  bad = __syncthreads_or(bad);
-  if (tid == 0) {
-    bal = zs = 0.0f;
-    total = 0;
-    for (int i = 0; i < kThreads; ++i) {
-      bal += s_a[i];
-      zs += s_b[i];
-      total += s_i[i];
+  s_b[tid] = z;
+  s_i[tid] = n;
+  __syncthreads();
+  for (int half = threads / 2; half > 0; half >>= 1) {
+    if (tid < half) {
+      s_a[tid] += s_a[tid + half];
+      s_b[tid] += s_b[tid + half];
+      s_i[tid] += s_i[tid + half];
     }
-    const float per = total > 0 ? 1.0f / (float)total : 0.0f;
-    a.losses[0] = total > 0 ? a.balance_coef * bal * per : 0.0f;
-    a.losses[1] = total > 0 ? a.z_coef * zs * per : 0.0f;
-    a.tokens[a.S] = total;
-    *w.status = bad ? kFlagBadExpertId : 0;
+    __syncthreads();
   }
+  if (tid == 0) write_losses(a, w, s_a[0], s_b[0], s_i[0], any_bad);
 }
 
-// One warp per row.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) router_grad_kernel(const RouterLossArgs a) {
+// A small batch: one block, the sequences one after another.
+template <int DT, int NV, bool kAligned>
+__global__ void __launch_bounds__(kSmallWarps * 32) router_small_kernel(const RouterLossArgs a,
+                                                                        Ws w) {
+  extern __shared__ float s_p[];  // [kSmallWarps][E], then int[E]
+  int* s_hist = reinterpret_cast<int*>(s_p + kSmallWarps * a.E);
+  __shared__ float s_dot[kSmallWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float bal = 0.0f, z = 0.0f;
+  int n = 0, bad = 0;
+  for (int s = 0; s < a.S; ++s) {
+    const int r0 = a.offsets ? max(0, a.offsets[s]) : 0;
+    const int r1 = a.offsets ? min(a.T, a.offsets[s + 1]) : a.T;
+    const PieceScalars r = piece_sums<DT, NV, kAligned, kSmallWarps>(a, r0, r1, s_p, s_hist);
+    float dot = 0.0f;
+    for (int e = tid; e < a.E; e += kSmallWarps * 32) {
+      const int cnt = s_hist[e];
+      a.counts[(size_t)s * a.E + e] = cnt;
+      dot += (float)cnt * warps_sum<kSmallWarps>(s_p, a.E, e);
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) s_dot[warp] = dot;
+    __syncthreads();
+    if (tid == 0) {
+      dot = 0.0f;
+      for (int i = 0; i < kSmallWarps; ++i) dot += s_dot[i];
+      if (r.n > 0) bal += even_share(a, r.n) * dot;
+      a.tokens[s] = r.n;
+      z += r.z;
+      n += r.n;
+      bad |= r.bad;
+    }
+  }
+  if (tid == 0) write_losses(a, w, bal, z, n, bad);
+}
+
+// One warp per `rows` consecutive rows; f_se stays in registers while the sequence does.
+template <int DT, int NV, bool kAligned>
+__global__ void __launch_bounds__(kWarps * 32) router_grad_kernel(const RouterLossArgs a,
+                                                                  int rows) {
+  using R = Raw<DT, NV, kAligned>;
   using L = typename LogitType<DT>::type;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const L* x = static_cast<const L*>(a.logits) + t * a.ld;
-  L* dx = static_cast<L*>(a.dlogits) + t * a.ld_grad;
-  const int s = sequence_of(a.offsets, a.S, t);
-  if (s < 0 || (a.mask && !a.mask[t])) {
-    for (int e = lane; e < a.E; e += 32) store_logit<DT>(dx + e, 0.0f);
-    return;
-  }
-  // the scores' gradient at this lane's slot; slots that repeat an expert add up
-  int id = -1;
-  float v = 0.0f, xid = 0.0f;
-  if (a.topk_w) {
-    float wk = 0.0f, dwk = 0.0f;
-    if (lane < a.K) {
-      id = load_id(a.ids, a.ids64, (int64_t)t * a.K + lane);
-      if (id >= a.E) id = -1;
-      if (id >= 0) {
-        wk = a.topk_w[(int64_t)t * a.K + lane];
-        dwk = a.d_topk_w[(int64_t)t * a.K + lane];
-        xid = load_logit<DT>(x + id);
-      }
-    }
-    const float mine = wk * (dwk - warp_sum(wk * dwk));
-    for (int k = 0; k < a.K; ++k) {
-      const float o = __shfl_sync(0xFFFFFFFFu, mine, k);
-      v += __shfl_sync(0xFFFFFFFFu, id, k) == id ? o : 0.0f;
-    }
-  }
-  Row<DT> r;
-  r.load(x, a.E, lane);
-  const int n_s = a.tokens[s], n = a.tokens[a.S];
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
+  const int end = (int)min((int64_t)a.T, first + rows);
+  const L* x = static_cast<const L*>(a.logits);
+  L* dx = static_cast<L*>(a.dlogits);
+  auto live = [&](int64_t t) { return t < end && (!a.mask || a.mask[t]); };
+  const int n = a.tokens[a.S];
   const float per = n > 0 ? 1.0f / (float)n : 0.0f;
-  const float f1 = n_s > 0 ? (float)a.E / ((float)a.K * (float)n_s) : 0.0f;
   const float gb = (a.loss_grad ? a.loss_grad[0] : 1.0f) * a.balance_coef * per;
   const float gz = (a.loss_grad ? a.loss_grad[1] : 1.0f) * 2.0f * a.z_coef * per;
-  const int32_t* cnt = a.counts + (size_t)s * a.E;
-  float dot = 0.0f;
+  int s = -1, s_end = 0;  // sequence of the rows before s_end
+  float f[R::kN];
 #pragma unroll
-  for (int i = 0; i < kMaxPerLane; ++i) {
-    if (32 * i >= a.E) break;
-    const int e = lane + 32 * i;
-    if (e < a.E) dot += (float)cnt[e] * f1 * r.p[i];
-  }
-  dot = warp_sum(dot);
-  const float add = gz * r.lse;
+  for (int i = 0; i < R::kN; ++i) f[i] = 0.0f;
+  R next;
+  bool next_live = live(first);
+  if (next_live) next.load(x + first * a.ld, a.E, lane);
+  for (int t = (int)min(first, (int64_t)a.T); t < end; ++t) {
+    const R row = next;
+    bool use = next_live;
+    next_live = live(t + 1);
+    if (next_live) next.load(x + (int64_t)(t + 1) * a.ld, a.E, lane);
+    if (t >= s_end || s < 0) {
+      s = sequence_of(a.offsets, a.S, t);
+      if (s >= 0) {
+        s_end = a.offsets ? a.offsets[s + 1] : a.T;
+        const float f1 = even_share(a, a.tokens[s]);
 #pragma unroll
-  for (int i = 0; i < kMaxPerLane; ++i) {
-    if (32 * i >= a.E) break;
-    const int e = lane + 32 * i;
-    if (e < a.E) store_logit<DT>(dx + e, r.p[i] * (gb * ((float)cnt[e] * f1 - dot) + add));
-  }
-  if (a.topk_w) {
-    __syncwarp();  // the chosen experts' entries overwrite what the loop stored
-    if (id >= 0) {
-      const float p = ex2((xid - r.m) * kLog2e) * r.r;
-      store_logit<DT>(dx + id, p * (gb * ((float)cnt[id] * f1 - dot) + add) + v);
+        for (int i = 0; i < R::kN; ++i) {
+          const int e = R::column(i, lane);
+          f[i] = e < a.E ? (float)a.counts[(size_t)s * a.E + e] * f1 : 0.0f;
+        }
+      }
+    }
+    use = use && s >= 0;
+    float p[R::kN];
+    if (!use) {
+#pragma unroll
+      for (int i = 0; i < R::kN; ++i) p[i] = 0.0f;
+      R::store(dx + t * a.ld_grad, a.E, lane, p);
+      continue;
+    }
+    // the scores' gradient at this lane's slot; slots that repeat an expert add up
+    int id = -1;
+    float v = 0.0f, x_id = 0.0f, f_id = 0.0f;
+    if (a.topk_w) {
+      float wk = 0.0f, dwk = 0.0f;
+      if (lane < a.K) {
+        const int64_t at = (int64_t)t * a.K + lane;
+        id = load_id(a.ids, a.ids64, at);
+        if (id < 0 || id >= a.E) id = -1;
+        wk = id >= 0 ? a.topk_w[at] : 0.0f;
+        dwk = id >= 0 ? a.d_topk_w[at] : 0.0f;
+        x_id = id >= 0 ? load_logit<DT>(x + t * a.ld + id) : 0.0f;
+        f_id = id >= 0 ? (float)a.counts[(size_t)s * a.E + id] : 0.0f;
+      }
+      const float mine = wk * (dwk - warp_sum(wk * dwk));
+      for (int k = 0; k < a.K; ++k) {
+        const float o = __shfl_sync(0xFFFFFFFFu, mine, k);
+        v += __shfl_sync(0xFFFFFFFFu, id, k) == id ? o : 0.0f;
+      }
+    }
+    row.get(p);
+    const RowStats st = softmax(p);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R::kN; ++i) dot += f[i] * p[i];
+    dot = warp_sum(dot);
+    const float add = gz * st.lse - gb * dot;
+#pragma unroll
+    for (int i = 0; i < R::kN; ++i) p[i] *= gb * f[i] + add;
+    R::store(dx + t * a.ld_grad, a.E, lane, p);
+    if (a.topk_w) {
+      __syncwarp();  // the chosen experts' entries overwrite what the warp stored
+      if (id >= 0) {
+        const float p_id = ex2((x_id - st.m) * kLog2e) * st.r;
+        store_logit<DT>(dx + t * a.ld_grad + id,
+                        p_id * (gb * f_id * even_share(a, a.tokens[s]) + add) + v);
+      }
     }
   }
 }
 
+// fn(vectors a lane, rows aligned) for a batch.
+template <int DT, typename F>
+cudaError_t with_layout(const RouterLossArgs& a, F fn) {
+  constexpr int kW = Vec<DT>::kElems, kSize = DT == kF32 ? 4 : 2;
+  auto aligned = [&](const void* p, int64_t ld) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * kSize % 16 == 0);
+  };
+  const bool al = a.E % kW == 0 && aligned(a.logits, a.ld) && aligned(a.dlogits, a.ld_grad);
+  auto with = [&](auto nv) {
+    return al ? fn(nv, std::true_type{}) : fn(nv, std::false_type{});
+  };
+  const int nv = (a.E + 32 * kW - 1) / (32 * kW);
+  if (nv == 1) return with(std::integral_constant<int, 1>{});
+  if (nv == 2) return with(std::integral_constant<int, 2>{});
+  if constexpr (DT == kF32) {
+    if (nv == 3) return with(std::integral_constant<int, 3>{});
+    if (nv > 4) return with(std::integral_constant<int, 8>{});
+  }
+  return with(std::integral_constant<int, 4>{});
+}
+
 template <int DT>
-cudaError_t launch_partial(const RouterLossArgs& a, const Ws& w, cudaStream_t s) {
-  const int smem = (kWarps + 1) * a.E * (int)sizeof(float);  // at most 36 KB
-  return launch_pdl(router_partial_kernel<DT>, dim3(num_chunks(a.T)), dim3(kThreads), smem, s, a, w);
+cudaError_t launch_loss(const RouterLossArgs& a, cudaStream_t s) {
+  const Ws w = carve(a.ws, a.E, a.S);
+  return with_layout<DT>(a, [&](auto nv, auto al) {
+    constexpr int kNV = decltype(nv)::value;
+    constexpr bool kAl = decltype(al)::value;
+    if (a.T <= kSmallRows && a.S <= kSmallSeqs) {
+      auto kernel = router_small_kernel<DT, kNV, kAl>;
+      static std::atomic<uint64_t> limit_set{0};
+      const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel),
+                                              (kSmallWarps + 1) * 1024 * 4, limit_set);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kernel, dim3(1), dim3(kSmallWarps * 32), (kSmallWarps + 1) * a.E * 4, s, a,
+                        w);
+    }
+    const int rows = chunk_rows(a.T), chunks = (a.T + rows - 1) / rows;
+    const cudaError_t e =
+        launch_pdl(router_partial_kernel<DT, kNV, kAl>, dim3(chunks), dim3(kWarps * 32),
+                   (kWarps + 1) * a.E * 4, s, a, w, rows);
+    if (e != cudaSuccess) return e;
+    int Y = 1;  // about a thread per two slots of a sequence
+    while (Y < 32 && 2 * Y * a.S < chunks + a.S) Y *= 2;
+    return launch_pdl(router_combine_kernel, dim3(a.S, expert_blocks(a.E)), dim3(32, Y), 0, s, a, w,
+                      rows);
+  });
+}
+
+template <int DT>
+cudaError_t launch_grad(const RouterLossArgs& a, cudaStream_t s) {
+  return with_layout<DT>(a, [&](auto nv, auto al) {
+    // several rows a warp once there are rows for twice the warps of kTargetBlocks
+    const int rows = (a.T + kTargetBlocks * kWarps * 2 - 1) / (kTargetBlocks * kWarps * 2);
+    const int64_t per_block = (int64_t)rows * kWarps;
+    return launch_pdl(router_grad_kernel<DT, decltype(nv)::value, decltype(al)::value>,
+                      dim3((unsigned)((a.T + per_block - 1) / per_block)), dim3(kWarps * 32), 0, s,
+                      a, rows);
+  });
 }
 
 }  // namespace
 
 size_t router_loss_ws_bytes(int T, int E, int S) {
-  return 256 + up256((size_t)S * sizeof(float2)) + up256((size_t)S * sizeof(int32_t)) +
-         ((size_t)num_chunks(T) + S) * (2 * (size_t)E + 3) * sizeof(float);
+  return 256 + seq_bytes(S) + dots_bytes(S, E) +
+         ((size_t)max_chunks(T) + S) * (2 * (size_t)E + 3) * sizeof(float);
 }
 
 cudaError_t launch_router_loss(const RouterLossArgs& a, int dtype, cudaStream_t s) {
-  const Ws w = carve(a.ws, a.S);
-  const cudaError_t e = dtype == kF32    ? launch_partial<kF32>(a, w, s)
-                        : dtype == kBf16 ? launch_partial<kBf16>(a, w, s)
-                                         : launch_partial<kF16>(a, w, s);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(router_combine_kernel, dim3(a.S), dim3(kThreads), 0, s, a, w, num_chunks(a.T));
+  if (dtype == kF32) return launch_loss<kF32>(a, s);
+  if (dtype == kBf16) return launch_loss<kBf16>(a, s);
+  return launch_loss<kF16>(a, s);
 }
 
 cudaError_t launch_router_loss_grad(const RouterLossArgs& a, int dtype, cudaStream_t s) {
-  const dim3 grid((a.T + kWarps - 1) / kWarps), block(kThreads);
-  if (dtype == kF32) return launch_pdl(router_grad_kernel<kF32>, grid, block, 0, s, a);
-  if (dtype == kBf16) return launch_pdl(router_grad_kernel<kBf16>, grid, block, 0, s, a);
-  return launch_pdl(router_grad_kernel<kF16>, grid, block, 0, s, a);
+  if (dtype == kF32) return launch_grad<kF32>(a, s);
+  if (dtype == kBf16) return launch_grad<kBf16>(a, s);
+  return launch_grad<kF16>(a, s);
 }
 
 }  // namespace moe
