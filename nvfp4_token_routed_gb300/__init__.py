@@ -561,7 +561,9 @@ def _dlogits(t, logits, stream):
 
 
 def _raw(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def token_logp(logits, actions, temperature=1.0, logp=None, stream=None):

@@ -157,6 +157,18 @@ __device__ __forceinline__ MaxSum warp_merge(MaxSum v, float c, int n) {
   for (int off = n / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
   return {m, s};
 }
+// Sum of 2^((z - m) c) over a vector, for references outside fp32 (rare: not inlined).
+template <int DT>
+__device__ __noinline__ float far_sum(uint4 v, float m, float c) {
+  const Vec<DT> d = {v};
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < Vec<DT>::kPairs; ++j) {
+    const float2 x = d.pair(j);
+    s += ex2((x.x - m) * c) + ex2((x.y - m) * c);
+  }
+  return s;
+}
 // The vectors d added to a pair.
 template <int DT, int U>
 __device__ __forceinline__ MaxSum add_vecs(MaxSum v, const Vec<DT> (&d)[U], float c) {
@@ -182,11 +194,7 @@ __device__ __forceinline__ MaxSum add_vecs(MaxSum v, const Vec<DT> (&d)[U], floa
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < Vec<DT>::kPairs; ++j) {
-          const float2 x = d[u].pair(j);
-          acc[0] = add2(acc[0], pack2(ex2((x.x - r) * c), ex2((x.y - r) * c)));
-        }
+        acc[0] = add2(acc[0], pack2(far_sum<DT>(d[u].v, r, c), 0.0f));
     }
     if (top > r && exponent(top, r, c) > kMaxExponent) {  // not with r = top: ends
       v.s *= ex2(rescale(v.m, top, c));

@@ -63,6 +63,7 @@ struct RouterLossArgs {
   const float* topk_w;        // [T][K] routing scores and
   const float* d_topk_w;      // [T][K] their upstream gradients, or null
   void* dlogits;              // [T][E]
+  bool aligned;               // rows are whole 16-byte vectors
 };
 
 size_t router_loss_ws_bytes(int T, int E, int S);

@@ -11,8 +11,9 @@
 // (the last term is the gradient of the scores w, a softmax over the chosen
 // logits).  The counts are constants of the gradient.
 //
-// One warp per row, the row in registers, the next row's loads in flight.  Sums run
-// in a fixed order, so equal inputs give equal bits: rows are cut into chunks, one a
+// A row lies in the registers of 8, 16 or 32 lanes, 32 values a lane at most, with the
+// next row's loads in flight: the fewer lanes, the fewer instructions a row (a warp's
+// shuffles, logarithms and score slots serve 4 or 2 rows at once).  Sums run in a fixed order, so equal inputs give equal bits: rows are cut into chunks, one a
 // block; chunk c of sequence s leaves its partial sums in slot c + s (walking the
 // rows, each step from one piece to the next raises c or s, so pieces have different
 // slots), and a second kernel adds a sequence's slots up in order, its last block the
@@ -84,61 +85,69 @@ __device__ __forceinline__ int sequence_of(const int32_t* off, int S, int row) {
   return lo;
 }
 
-// How a warp holds a row: NV vectors of 16 bytes a lane, vector i of lane l at column
-// (32 i + l) W.  Rows that do not start on 16-byte boundaries, or whose length is no
+// How NL lanes hold a row: NV vectors of 16 bytes a lane, vector i of lane l at column
+// (NL i + l) W.  Rows that do not start on 16-byte boundaries, or whose length is no
 // multiple of W, are read and written by the element, with the same columns in the same
 // lanes and so the same bits.
-template <int DT, int NV, bool kAligned>
+template <int DT, int NL, int NV>
 struct Raw {
   using L = typename LogitType<DT>::type;
   using V = Vec<DT>;
   static constexpr int W = V::kElems;
   static constexpr int kN = W * NV;
   V v[NV];
-  static __device__ __forceinline__ int column(int n, int lane) {
-    return (n / W * 32 + lane) * W + n % W;
+  static __device__ __forceinline__ int column(int n, int l) {
+    return (n / W * NL + l) * W + n % W;
   }
-  __device__ __forceinline__ void load(const L* row, int E, int lane) {
+  __device__ __forceinline__ void load(const L* row, int E, int l, bool aligned) {
+    if (aligned) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (32 * i + lane) * W;
-      if (kAligned) {
+      for (int i = 0; i < NV; ++i) {
+        const int c = (NL * i + l) * W;
         if (c < E) v[i].v = *reinterpret_cast<const uint4*>(row + c);
         else v[i].fill(V::kNegInf);
-      } else {
-        L x[W];
+      }
+      return;
+    }
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          if constexpr (DT == kF32) x[j] = c + j < E ? row[c + j] : -INFINITY;
-          else x[j] = c + j < E ? row[c + j] : (L)(V::kNegInf >> 16);
-        }
+    for (int i = 0; i < NV; ++i) {
+      const int c = (NL * i + l) * W;
+      L x[W];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (DT == kF32) v[i].set_word(j, __float_as_uint(x[j]));
-          else v[i].set_word(j, (uint32_t)x[2 * j] | (uint32_t)x[2 * j + 1] << 16);
-        }
+      for (int j = 0; j < W; ++j) {
+        if constexpr (DT == kF32) x[j] = c + j < E ? row[c + j] : -INFINITY;
+        else x[j] = c + j < E ? row[c + j] : (L)(V::kNegInf >> 16);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == kF32) v[i].set_word(j, __float_as_uint(x[j]));
+        else v[i].set_word(j, (uint32_t)x[2 * j] | (uint32_t)x[2 * j + 1] << 16);
       }
     }
+  }
+  __device__ __forceinline__ void fill() {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i].fill(V::kNegInf);
   }
   __device__ __forceinline__ void get(float (&f)[kN]) const {
 #pragma unroll
     for (int n = 0; n < kN; n += 2) {
-      const float2 p = v[n / W].pair(n % W / 2);
+      const float2 p = unpack2(pack2(v[n / W].pair(n % W / 2)));
       f[n] = p.x;
       f[n + 1] = p.y;
     }
   }
-  static __device__ __forceinline__ void store(L* row, int E, int lane, const float (&f)[kN]) {
+  static __device__ __forceinline__ void store(L* row, int E, int l, bool aligned,
+                                               const float (&f)[kN]) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (32 * i + lane) * W;
-      if (kAligned) {
-        if (c >= E) break;
+      const int c = (NL * i + l) * W;
+      if (aligned) {
         V g;
 #pragma unroll
         for (int j = 0; j < V::kPairs; ++j)
           g.set_pair(j, make_float2(f[i * W + 2 * j], f[i * W + 2 * j + 1]));
-        *reinterpret_cast<uint4*>(row + c) = g.v;
+        if (c < E) *reinterpret_cast<uint4*>(row + c) = g.v;
       } else {
 #pragma unroll
         for (int j = 0; j < W; ++j)
@@ -148,30 +157,42 @@ struct Raw {
   }
 };
 
-// The row's softmax over its warp: p = 2^((x - m) log2 e) r; a row without a finite
-// logit has p = 0 and lse = 0.
+// Sum and maximum over the NL lanes of a row.
+template <int NL>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int off = NL / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
+}
+template <int NL>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int off = NL / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+  return v;
+}
+
+// The row's softmax over its lanes: e = 2^((x - m) log2 e), p = e r; a row without a
+// finite logit has p = 0 and lse = 0.
 struct RowStats {
   float m, r, lse;
 };
-template <int N>
-__device__ __forceinline__ RowStats softmax(float (&p)[N]) {
+template <int NL, int N>
+__device__ __forceinline__ RowStats exponentials(float (&p)[N]) {
   float m = p[0];
 #pragma unroll
   for (int n = 1; n < N; ++n) m = fmaxf(m, p[n]);
-  m = finite_ref(warp_max(m));
+  m = finite_ref(row_max<NL>(m));
   float s[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     p[n] = ex2((p[n] - m) * kLog2e);
     s[n & 1] += p[n];
   }
-  const float sum = warp_sum(s[0] + s[1]);
+  const float sum = row_sum<NL>(s[0] + s[1]);
   RowStats st;
   st.m = m;
   st.lse = sum == 0.0f ? 0.0f : m + logf(sum);
   st.r = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int n = 0; n < N; ++n) p[n] *= st.r;
   return st;
 }
 
@@ -182,13 +203,14 @@ struct PieceScalars {
   float z;
   int n, bad;
 };
-template <int DT, int NV, bool kAligned, int NW>
+template <int DT, int NL, int NV, int NW>
 __device__ __forceinline__ PieceScalars piece_sums(const RouterLossArgs& a, int row0, int row1,
                                                    float* s_p, int* s_hist) {
-  using R = Raw<DT, NV, kAligned>;
+  using R = Raw<DT, NL, NV>;
+  constexpr int kRows = 32 / NL * NW;  // rows at a time
   __shared__ float s_z[NW];
   __shared__ int s_n[NW], s_bad[NW];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % NL;
   for (int e = tid; e < a.E; e += NW * 32) s_hist[e] = 0;
   __syncthreads();
   float acc[R::kN];
@@ -197,47 +219,63 @@ __device__ __forceinline__ PieceScalars piece_sums(const RouterLossArgs& a, int 
   float z = 0.0f;
   int n = 0, bad = 0;
   const auto* base = static_cast<const typename R::L*>(a.logits);
-  auto live = [&](int t) { return t < row1 && (!a.mask || a.mask[t]); };
-  // an id below -1 or from E on is bad; 64-bit ids beyond 32 bits read as -2
-  auto id_of = [&](int t) {
-    if (lane >= a.K) return -1;
-    const int64_t at = (int64_t)t * a.K + lane;
-    if (!a.ids64) return static_cast<const int32_t*>(a.ids)[at];
-    const long long v = static_cast<const long long*>(a.ids)[at];
-    return v < -1 || v > INT32_MAX ? -2 : (int)v;
+  // the lane's slot of row t; an id below -1 or from E on is bad, 64-bit ids beyond 32
+  // bits read as -2
+  auto fetch = [&](int t, R& row, int& id) {
+    const bool live = t < row1 && (!a.mask || a.mask[t]);
+    id = -1;
+    if (!live) return false;
+    row.load(base + t * a.ld, a.E, l, a.aligned);
+    if (l < a.K) {
+      const int64_t at = (int64_t)t * a.K + l;
+      if (!a.ids64) {
+        id = static_cast<const int32_t*>(a.ids)[at];
+      } else {
+        const long long v = static_cast<const long long*>(a.ids)[at];
+        id = v < -1 || v > INT32_MAX ? -2 : (int)v;
+      }
+    }
+    return true;
   };
-  int t = row0 + warp;
+  const int trips = (row1 - row0 + kRows - 1) / kRows;
+  int t = row0 + tid / NL;
   R next;
-  int next_id = -1;
-  bool next_live = live(t);
-  if (next_live) {
-    next.load(base + t * a.ld, a.E, lane);
-    next_id = id_of(t);
-  }
-  for (; t < row1; t += NW) {
+  next.fill();
+  int next_id;
+  bool next_live = fetch(t, next, next_id);
+  for (int i = 0; i < trips; ++i, t += kRows) {
     const R row = next;
     const int id = next_id;
-    const bool use = next_live;
-    next_live = live(t + NW);
-    if (next_live) {
-      next.load(base + (t + NW) * a.ld, a.E, lane);
-      next_id = id_of(t + NW);
-    }
-    if (!use) continue;
+    const bool live = next_live;
+    next_live = fetch(t + kRows, next, next_id);
+    if (!__any_sync(0xFFFFFFFFu, live)) continue;
     float p[R::kN];
     row.get(p);
-    const RowStats st = softmax(p);
+    const RowStats st = exponentials<NL>(p);
+    const float r = live ? st.r : 0.0f;
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < R::kN; ++i) acc[i] += p[i];
-    z += st.lse * st.lse;
-    ++n;
+      for (int i = 0; i < R::kN; ++i) acc[i] += p[i] * r;
+      z += st.lse * st.lse;
+      ++n;
+    }
     if (id >= 0 && id < a.E) atomicAdd(&s_hist[id], 1);
     else if (id != -1) bad = 1;
   }
+  // the warp's rows: lanes NL apart hold the same columns
 #pragma unroll
-  for (int i = 0; i < R::kN; ++i) {
-    const int e = R::column(i, lane);
-    if (e < a.E) s_p[warp * a.E + e] = acc[i];
+  for (int off = NL; off < 32; off <<= 1) {
+#pragma unroll
+    for (int i = 0; i < R::kN; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], off);
+    z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
+    n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+  }
+  if (lane < NL) {
+#pragma unroll
+    for (int i = 0; i < R::kN; ++i) {
+      const int e = R::column(i, l);
+      if (e < a.E) s_p[warp * a.E + e] = acc[i];
+    }
   }
   bad = __any_sync(0xFFFFFFFFu, bad);
   if (lane == 0) {
@@ -264,7 +302,7 @@ __device__ __forceinline__ float warps_sum(const float* s_p, int E, int e) {
   return sum;
 }
 
-template <int DT, int NV, bool kAligned>
+template <int DT, int NL, int NV>
 __global__ void __launch_bounds__(kWarps * 32) router_partial_kernel(const RouterLossArgs a, Ws w,
                                                                      int rows) {
   extern __shared__ float s_p[];  // [kWarps][E], then int[E]
@@ -282,7 +320,7 @@ __global__ void __launch_bounds__(kWarps * 32) router_partial_kernel(const Route
       continue;
     }
     const int row1 = a.offsets ? min(row_end, a.offsets[s + 1]) : row_end;
-    const PieceScalars r = piece_sums<DT, NV, kAligned, kWarps>(a, row0, row1, s_p, s_hist);
+    const PieceScalars r = piece_sums<DT, NL, NV, kWarps>(a, row0, row1, s_p, s_hist);
     float* slot = w.slot + (size_t)(blockIdx.x + s) * (2 * a.E + 3);
     for (int e = tid; e < a.E; e += kWarps * 32) {
       slot[e] = warps_sum<kWarps>(s_p, a.E, e);
@@ -409,7 +447,7 @@ __global__ void __launch_bounds__(1024) router_combine_kernel(const RouterLossAr
 }
 
 // A small batch: one block, the sequences one after another.
-template <int DT, int NV, bool kAligned>
+template <int DT, int NV>
 __global__ void __launch_bounds__(kSmallWarps * 32) router_small_kernel(const RouterLossArgs a,
                                                                         Ws w) {
   extern __shared__ float s_p[];  // [kSmallWarps][E], then int[E]
@@ -423,7 +461,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) router_small_kernel(const Ro
   for (int s = 0; s < a.S; ++s) {
     const int r0 = a.offsets ? max(0, a.offsets[s]) : 0;
     const int r1 = a.offsets ? min(a.T, a.offsets[s + 1]) : a.T;
-    const PieceScalars r = piece_sums<DT, NV, kAligned, kSmallWarps>(a, r0, r1, s_p, s_hist);
+    const PieceScalars r = piece_sums<DT, 32, NV, kSmallWarps>(a, r0, r1, s_p, s_hist);
     float dot = 0.0f;
     for (int e = tid; e < a.E; e += kSmallWarps * 32) {
       const int cnt = s_hist[e];
@@ -446,136 +484,173 @@ __global__ void __launch_bounds__(kSmallWarps * 32) router_small_kernel(const Ro
   if (tid == 0) write_losses(a, w, bal, z, n, bad);
 }
 
-// One warp per `rows` consecutive rows; f_se stays in registers while the sequence does.
-template <int DT, int NV, bool kAligned>
+// NL lanes for `rows` rows, 32 / NL apart; f_se stays in registers while the sequence does.
+template <int DT, int NL, int NV>
 __global__ void __launch_bounds__(kWarps * 32) router_grad_kernel(const RouterLossArgs a,
                                                                   int rows) {
-  using R = Raw<DT, NV, kAligned>;
+  using R = Raw<DT, NL, NV>;
   using L = typename LogitType<DT>::type;
+  constexpr int kSub = 32 / NL;  // rows of a warp at a time
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
-  const int end = (int)min((int64_t)a.T, first + rows);
+  const int lane = threadIdx.x & 31, l = lane % NL;
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows * kSub;
   const L* x = static_cast<const L*>(a.logits);
   L* dx = static_cast<L*>(a.dlogits);
-  auto live = [&](int64_t t) { return t < end && (!a.mask || a.mask[t]); };
   const int n = a.tokens[a.S];
   const float per = n > 0 ? 1.0f / (float)n : 0.0f;
   const float gb = (a.loss_grad ? a.loss_grad[0] : 1.0f) * a.balance_coef * per;
   const float gz = (a.loss_grad ? a.loss_grad[1] : 1.0f) * 2.0f * a.z_coef * per;
   int s = -1, s_end = 0;  // sequence of the rows before s_end
-  float f[R::kN];
+  float f1 = 0.0f, f[R::kN];
 #pragma unroll
   for (int i = 0; i < R::kN; ++i) f[i] = 0.0f;
+  // a row and this lane's slot of its scores
+  struct Slot {
+    int id;
+    float w, dw;
+  };
+  auto fetch = [&](int64_t t, R& row, Slot& k) {
+    k = {-1, 0.0f, 0.0f};
+    if (t >= a.T || (a.mask && !a.mask[t])) return false;
+    row.load(x + t * a.ld, a.E, l, a.aligned);
+    if (a.topk_w && l < a.K) {
+      const int64_t at = t * a.K + l;
+      const int id = load_id(a.ids, a.ids64, at);
+      if (id >= 0 && id < a.E) k = {id, a.topk_w[at], a.d_topk_w[at]};
+    }
+    return true;
+  };
   R next;
-  bool next_live = live(first);
-  if (next_live) next.load(x + first * a.ld, a.E, lane);
-  for (int t = (int)min(first, (int64_t)a.T); t < end; ++t) {
+  next.fill();
+  Slot next_slot;
+  int64_t t = first + lane / NL;
+  bool next_live = fetch(t, next, next_slot);
+  for (int step = 0; step < rows; ++step, t += kSub) {
     const R row = next;
-    bool use = next_live;
-    next_live = live(t + 1);
-    if (next_live) next.load(x + (int64_t)(t + 1) * a.ld, a.E, lane);
-    if (t >= s_end || s < 0) {
-      s = sequence_of(a.offsets, a.S, t);
+    const Slot slot = next_slot;
+    bool live = next_live;
+    next_live = step + 1 < rows && fetch(t + kSub, next, next_slot);
+    if (live && (t >= s_end || s < 0)) {
+      s = sequence_of(a.offsets, a.S, (int)t);
       if (s >= 0) {
         s_end = a.offsets ? a.offsets[s + 1] : a.T;
-        const float f1 = even_share(a, a.tokens[s]);
+        f1 = even_share(a, a.tokens[s]);
 #pragma unroll
         for (int i = 0; i < R::kN; ++i) {
-          const int e = R::column(i, lane);
+          const int e = R::column(i, l);
           f[i] = e < a.E ? (float)a.counts[(size_t)s * a.E + e] * f1 : 0.0f;
         }
       }
     }
-    use = use && s >= 0;
-    float p[R::kN];
-    if (!use) {
-#pragma unroll
-      for (int i = 0; i < R::kN; ++i) p[i] = 0.0f;
-      R::store(dx + t * a.ld_grad, a.E, lane, p);
-      continue;
-    }
-    // the scores' gradient at this lane's slot; slots that repeat an expert add up
-    int id = -1;
+    live = live && s >= 0;
+    // the chosen experts' entries
+    int id = live ? slot.id : -1;
     float v = 0.0f, x_id = 0.0f, f_id = 0.0f;
     if (a.topk_w) {
-      float wk = 0.0f, dwk = 0.0f;
-      if (lane < a.K) {
-        const int64_t at = (int64_t)t * a.K + lane;
-        id = load_id(a.ids, a.ids64, at);
-        if (id < 0 || id >= a.E) id = -1;
-        wk = id >= 0 ? a.topk_w[at] : 0.0f;
-        dwk = id >= 0 ? a.d_topk_w[at] : 0.0f;
-        x_id = id >= 0 ? load_logit<DT>(x + t * a.ld + id) : 0.0f;
-        f_id = id >= 0 ? (float)a.counts[(size_t)s * a.E + id] : 0.0f;
+      if (id >= 0) {
+        x_id = load_logit<DT>(x + t * a.ld + id);
+        f_id = (float)a.counts[(size_t)s * a.E + id] * f1;
       }
-      const float mine = wk * (dwk - warp_sum(wk * dwk));
-      for (int k = 0; k < a.K; ++k) {
-        const float o = __shfl_sync(0xFFFFFFFFu, mine, k);
-        v += __shfl_sync(0xFFFFFFFFu, id, k) == id ? o : 0.0f;
+      const float mean = row_sum<NL>(id >= 0 ? slot.w * slot.dw : 0.0f);
+      const float mine = id >= 0 ? slot.w * (slot.dw - mean) : 0.0f;
+      v = mine;
+      // slots that repeat an expert add up, in the order of the slots
+      const uint32_t key = id >= 0 ? (uint32_t)(lane / NL) << 16 | id : 0x80000000u | lane;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, key);
+      if (__any_sync(0xFFFFFFFFu, (same & (same - 1)) != 0)) {
+        v = 0.0f;
+        for (int k = 0; k < 32; ++k) {
+          const float o = __shfl_sync(0xFFFFFFFFu, mine, k);
+          v += (same >> k) & 1 ? o : 0.0f;
+        }
       }
     }
+    float p[R::kN];
     row.get(p);
-    const RowStats st = softmax(p);
+    const RowStats st = exponentials<NL>(p);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < R::kN; ++i) dot += f[i] * p[i];
-    dot = warp_sum(dot);
-    const float add = gz * st.lse - gb * dot;
+    dot = row_sum<NL>(dot) * st.r;
+    const float add = gz * st.lse - gb * dot, r = live ? st.r : 0.0f;
+    const float c1 = gb * r, c0 = add * r;
 #pragma unroll
-    for (int i = 0; i < R::kN; ++i) p[i] *= gb * f[i] + add;
-    R::store(dx + t * a.ld_grad, a.E, lane, p);
+    for (int i = 0; i < R::kN; ++i) p[i] = live ? p[i] * fmaf(c1, f[i], c0) : 0.0f;
+    __syncwarp();  // in place, x_id was read before the lanes overwrite the row
+    if (t < a.T) R::store(dx + t * a.ld_grad, a.E, l, a.aligned, p);
     if (a.topk_w) {
-      __syncwarp();  // the chosen experts' entries overwrite what the warp stored
-      if (id >= 0) {
-        const float p_id = ex2((x_id - st.m) * kLog2e) * st.r;
+      __syncwarp();  // the entries overwrite what the lanes stored
+      if (id >= 0)
         store_logit<DT>(dx + t * a.ld_grad + id,
-                        p_id * (gb * f_id * even_share(a, a.tokens[s]) + add) + v);
-      }
+                        ex2((x_id - st.m) * kLog2e) * fmaf(c1, f_id, c0) + v);
     }
   }
 }
 
-// fn(vectors a lane, rows aligned) for a batch.
+// fn(lanes a row, vectors a lane): 32 lanes where rows are few (latency counts) or K
+// needs them, else the fewest that hold the row at 32 values a lane.
+#ifndef RL_MANY
+#define RL_MANY 4096
+#endif
+template <int V>
+using Int = std::integral_constant<int, V>;
 template <int DT, typename F>
 cudaError_t with_layout(const RouterLossArgs& a, F fn) {
-  constexpr int kW = Vec<DT>::kElems, kSize = DT == kF32 ? 4 : 2;
-  auto aligned = [&](const void* p, int64_t ld) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * kSize % 16 == 0);
-  };
-  const bool al = a.E % kW == 0 && aligned(a.logits, a.ld) && aligned(a.dlogits, a.ld_grad);
-  auto with = [&](auto nv) {
-    return al ? fn(nv, std::true_type{}) : fn(nv, std::false_type{});
-  };
-  const int nv = (a.E + 32 * kW - 1) / (32 * kW);
-  if (nv == 1) return with(std::integral_constant<int, 1>{});
-  if (nv == 2) return with(std::integral_constant<int, 2>{});
-  if constexpr (DT == kF32) {
-    if (nv == 3) return with(std::integral_constant<int, 3>{});
-    if (nv > 4) return with(std::integral_constant<int, 8>{});
+  constexpr int W = Vec<DT>::kElems;
+  const int nv = (a.E + W - 1) / W;  // vectors a row
+  if (a.T >= RL_MANY && a.K <= 8) {
+    if (nv <= 8) return fn(Int<8>{}, Int<1>{});
+    if (nv <= 16) return fn(Int<8>{}, Int<2>{});
+    if (nv <= 32) return fn(Int<8>{}, Int<4>{});
+    if constexpr (DT == kF32)
+      if (nv <= 64) return fn(Int<8>{}, Int<8>{});
   }
-  return with(std::integral_constant<int, 4>{});
+  if (a.T >= RL_MANY && a.K <= 16) {
+    if constexpr (DT == kF32) {
+      if (nv > 64 && nv <= 96) return fn(Int<16>{}, Int<6>{});
+      if (nv > 64 && nv <= 128) return fn(Int<16>{}, Int<8>{});
+    } else {
+      if (nv > 32 && nv <= 48) return fn(Int<16>{}, Int<3>{});
+      if (nv > 32 && nv <= 64) return fn(Int<16>{}, Int<4>{});
+    }
+  }
+  if (nv <= 32) return fn(Int<32>{}, Int<1>{});
+  if (nv <= 64) return fn(Int<32>{}, Int<2>{});
+  if constexpr (DT == kF32) {
+    if (nv <= 96) return fn(Int<32>{}, Int<3>{});
+    if (nv > 128) return fn(Int<32>{}, Int<8>{});
+  }
+  return fn(Int<32>{}, Int<4>{});
+}
+template <int DT>
+bool rows_aligned(const RouterLossArgs& a) {
+  auto ok = [](const void* p, int64_t ld) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (DT == kF32 ? 4 : 2) % 16 == 0);
+  };
+  return a.E % Vec<DT>::kElems == 0 && ok(a.logits, a.ld) && ok(a.dlogits, a.ld_grad);
 }
 
 template <int DT>
-cudaError_t launch_loss(const RouterLossArgs& a, cudaStream_t s) {
+cudaError_t launch_loss(RouterLossArgs a, cudaStream_t s) {
   const Ws w = carve(a.ws, a.E, a.S);
-  return with_layout<DT>(a, [&](auto nv, auto al) {
-    constexpr int kNV = decltype(nv)::value;
-    constexpr bool kAl = decltype(al)::value;
-    if (a.T <= kSmallRows && a.S <= kSmallSeqs) {
-      auto kernel = router_small_kernel<DT, kNV, kAl>;
-      static std::atomic<uint64_t> limit_set{0};
-      const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel),
-                                              (kSmallWarps + 1) * 1024 * 4, limit_set);
-      if (e != cudaSuccess) return e;
-      return launch_pdl(kernel, dim3(1), dim3(kSmallWarps * 32), (kSmallWarps + 1) * a.E * 4, s, a,
-                        w);
+  a.aligned = rows_aligned<DT>(a);
+  return with_layout<DT>(a, [&](auto nl, auto nv) {
+    constexpr int kNL = decltype(nl)::value, kNV = decltype(nv)::value;
+    if constexpr (kNL == 32) {
+      if (a.T <= kSmallRows && a.S <= kSmallSeqs) {
+        auto kernel = router_small_kernel<DT, kNV>;
+        static std::atomic<uint64_t> limit_set{0};
+        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel),
+                                                (kSmallWarps + 1) * 1024 * 4, limit_set);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(1), dim3(kSmallWarps * 32), (kSmallWarps + 1) * a.E * 4, s,
+                          a, w);
+      }
     }
     const int rows = chunk_rows(a.T), chunks = (a.T + rows - 1) / rows;
     const cudaError_t e =
-        launch_pdl(router_partial_kernel<DT, kNV, kAl>, dim3(chunks), dim3(kWarps * 32),
+        launch_pdl(router_partial_kernel<DT, kNL, kNV>, dim3(chunks), dim3(kWarps * 32),
                    (kWarps + 1) * a.E * 4, s, a, w, rows);
     if (e != cudaSuccess) return e;
     int Y = 1;  // about a thread per two slots of a sequence
@@ -586,14 +661,16 @@ cudaError_t launch_loss(const RouterLossArgs& a, cudaStream_t s) {
 }
 
 template <int DT>
-cudaError_t launch_grad(const RouterLossArgs& a, cudaStream_t s) {
-  return with_layout<DT>(a, [&](auto nv, auto al) {
-    // several rows a warp once there are rows for twice the warps of kTargetBlocks
-    const int rows = (a.T + kTargetBlocks * kWarps * 2 - 1) / (kTargetBlocks * kWarps * 2);
-    const int64_t per_block = (int64_t)rows * kWarps;
-    return launch_pdl(router_grad_kernel<DT, decltype(nv)::value, decltype(al)::value>,
-                      dim3((unsigned)((a.T + per_block - 1) / per_block)), dim3(kWarps * 32), 0, s,
-                      a, rows);
+cudaError_t launch_grad(RouterLossArgs a, cudaStream_t s) {
+  a.aligned = rows_aligned<DT>(a);
+  return with_layout<DT>(a, [&](auto nl, auto nv) {
+    constexpr int kNL = decltype(nl)::value;
+    // several rows a lane once there are rows for twice the warps of kTargetBlocks
+    const int64_t at_once = (int64_t)kWarps * (32 / kNL);
+    const int rows = (int)((a.T + at_once * kTargetBlocks * 2 - 1) / (at_once * kTargetBlocks * 2));
+    return launch_pdl(router_grad_kernel<DT, kNL, decltype(nv)::value>,
+                      dim3((unsigned)((a.T + at_once * rows - 1) / (at_once * rows))),
+                      dim3(kWarps * 32), 0, s, a, rows);
   });
 }
 

@@ -15,6 +15,8 @@
 // Short rows: one block a row, the row in registers.  Long rows: a persistent cluster
 // of blocks a row, the row in shared memory, loaded ahead by bulk copies.  Either way
 // a row is read once.
+#include <type_traits>
+
 #include "internal.h"
 #include "logits.cuh"
 #include "ptx.cuh"
@@ -139,31 +141,33 @@ __device__ __forceinline__ Vec<DT> soft_vec(const Vec<DT>& d, const Soft& r, flo
   return g;
 }
 template <int DT>
-__device__ __forceinline__ Vec<DT> far_vec(const Vec<DT>& d, const Soft& r, float c) {
+__device__ __noinline__ uint4 far_vec(uint4 v, float coef, float m, float c) {
+  const Vec<DT> d = {v};
   Vec<DT> g;
 #pragma unroll
   for (int j = 0; j < Vec<DT>::kPairs; ++j) {
     const float2 x = d.pair(j);
-    g.set_pair(j, make_float2(r.coef * ex2(exponent(x.x, r.m, c)),
-                              r.coef * ex2(exponent(x.y, r.m, c))));
+    g.set_pair(j, make_float2(coef * ex2(exponent(x.x, m, c)), coef * ex2(exponent(x.y, m, c))));
   }
-  return g;
+  return g.v;
 }
-// fn(vector function) for the row's kind: near and of either sign, far, or zero.
+// fn(vector function, std::true_type) for a row whose gradient is dense and near, of
+// either sign; fn(vector function, std::false_type) for one that is 0 (clipped, no
+// teacher, or no finite logit) or far.
 template <int DT, typename F>
 __device__ __forceinline__ void with_soft(const Soft& r, float c, F fn) {
-  if (r.coef == 0.0f) {  // clipped, no teacher, or no finite logit
-    fn([&](const Vec<DT>&) {
+  const bool near = fabsf(r.k) < (DT == kF32 ? 1e38f : kFoldRange);
+  if (r.coef == 0.0f || !near) {
+    fn([&](const Vec<DT>& d) {
       Vec<DT> g;
-      g.fill(0);
+      if (r.coef == 0.0f) g.fill(0);
+      else g.v = far_vec<DT>(d.v, r.coef, r.m, c);
       return g;
-    });
-  } else if (!(fabsf(r.k) < (DT == kF32 ? 1e38f : kFoldRange))) {
-    fn([&](const Vec<DT>& d) { return far_vec<DT>(d, r, c); });
+    }, std::false_type{});
   } else if (DT == kF32 || !(r.coef < 0.0f)) {
-    fn([&](const Vec<DT>& d) { return soft_vec<DT, false>(d, r, c); });
+    fn([&](const Vec<DT>& d) { return soft_vec<DT, false>(d, r, c); }, std::true_type{});
   } else {
-    fn([&](const Vec<DT>& d) { return soft_vec<DT, true>(d, r, c); });
+    fn([&](const Vec<DT>& d) { return soft_vec<DT, true>(d, r, c); }, std::true_type{});
   }
 }
 __device__ __forceinline__ float soft_at(float z, const Soft& r, float c) {
@@ -199,6 +203,66 @@ __device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int 
     if (q != 0.0f) kl += q * (lq - (s_z[i] - zr) * a.inv_tau);
   }
   return {warp_sum(Q), warp_sum(kl), zr};
+}
+
+// A row's teacher slots into shared memory, by NT threads: ids (-1: empty), the teacher's
+// logits and the student's at those tokens.  All ids are loaded before the first logit.
+// s_id may be null.
+template <int DT, int NT>
+__device__ __forceinline__ void gather_slots(const TokenLossArgs& a, int row,
+                                             const typename LogitType<DT>::type* z, int tid,
+                                             int* s_id, float* s_t, float* s_z) {
+  constexpr int U = kMaxTeacher / NT > 0 ? kMaxTeacher / NT : 1;
+  int id[U];
+  float t[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = tid + NT * u;
+    const int64_t at = (int64_t)row * a.k + i;
+    id[u] = i < a.k ? load_id(a.t_ids, a.ids64, at) : -1;
+    t[u] = i < a.k ? teacher_logit(a, at) : -INFINITY;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = tid + NT * u;
+    const bool in = id[u] >= 0 && id[u] < a.V;
+    const float zi = in ? load_logit<DT>(z + id[u]) : -INFINITY;
+    if (i < a.k) {
+      if (s_id) s_id[i] = in ? id[u] : -1;
+      s_t[i] = in ? t[u] : -INFINITY;
+      s_z[i] = zi;
+    }
+  }
+}
+
+// The slots whose token may be an earlier slot's too, by one warp: bit i % 32 of
+// s_again[i / 32].  A hash of the tokens seen decides; it may name a slot too many.
+constexpr int kSeenWords = 64;  // 2048 bits
+__device__ __forceinline__ void name_repeats(int k, int lane, const int* s_id, uint32_t* s_seen,
+                                             uint32_t* s_again) {
+  for (int i = lane; i < kSeenWords; i += 32) s_seen[i] = 0;
+  __syncwarp();
+  for (int i = lane; i - lane < k; i += 32) {
+    const int id = i < k ? s_id[i] : -1;
+    const uint32_t h = ((uint32_t)id * 2654435761u) >> 21, bit = 1u << (h & 31);
+    const bool again = id >= 0 && (atomicOr(&s_seen[h >> 5], bit) & bit);
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, again);
+    if (lane == 0) s_again[i / 32] = all;
+  }
+  __syncwarp();
+}
+// fn(slot, sum of q over the slots of its token) for each of them, by one warp.
+template <typename F>
+__device__ __forceinline__ void for_repeats(int k, int lane, const int* s_id, const float* s_q,
+                                            const uint32_t* s_again, F fn) {
+  for (int u = 0; 32 * u < k; ++u) {
+    for (uint32_t m = s_again[u]; m; m &= m - 1) {
+      const int slot = 32 * u + __ffs(m) - 1, id = s_id[slot];
+      float part = 0.0f;
+      for (int i = lane; i < k; i += 32) part += s_id[i] == id ? s_q[i] : 0.0f;
+      fn(slot, warp_sum(part));
+    }
+  }
 }
 
 // A row's results once its largest logit and sum v are known.
@@ -240,24 +304,37 @@ __device__ __forceinline__ RowResult finish_row(const TokenLossArgs& a, MaxSum v
 
 // ---------------------------------------------------------------- short rows
 //
-// Every thread keeps VPT vectors of the row in registers.
+// NT threads a row, each with VPT vectors of it in registers; a warp's worth of threads
+// or one block.
+
+constexpr int short_rows_per_block(int NT) { return NT == 32 ? 8 : 1; }
 
 template <int DT, int MODE, int NT, int VPT>
-__global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
+__global__ void __launch_bounds__(NT * short_rows_per_block(NT))
+    short_row_kernel(const TokenLossArgs a) {
   using L = typename LogitType<DT>::type;
   using V16 = Vec<DT>;
-  constexpr int kWarps = NT / 32;
+  constexpr int kWarps = NT / 32, kRows = short_rows_per_block(NT);
   constexpr int kSlots = MODE == kDistill ? kMaxTeacher : 1;
-  __shared__ MaxSum s_ms[kWarps];
-  __shared__ int s_id[kSlots];
-  __shared__ float s_q[kSlots];
-  __shared__ float s_z[kSlots];
-  __shared__ TeacherSums s_t;
-  __shared__ RowResult s_r;
+  struct Shared {
+    MaxSum ms[kWarps];
+    int id[kSlots];
+    float q[kSlots], z[kSlots];
+    uint32_t seen[kSeenWords], again[kMaxTeacher / 32];
+    TeacherSums t;
+    RowResult r;
+  };
+  __shared__ Shared shared[kRows];
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int sub = threadIdx.x / NT, tid = threadIdx.x % NT, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x * kRows + sub;
+  if (row >= a.N) return;
+  Shared& sh = shared[sub];
+  auto sync = [] {  // the row's threads
+    if (NT == 32) __syncwarp();
+    else __syncthreads();
+  };
   const L* z = static_cast<const L*>(a.logits) + row * a.ld;
   L* dz = static_cast<L*>(a.dlogits) + row * a.ld_grad;
   const Split sp = split_row<DT>(z, a.V, 1);
@@ -291,16 +368,7 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
   // the few logits that the loss picks out, read before any gradient is written
   int act = -1;
   float w = 1.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, z_act = 0.0f;
-  if (MODE == kDistill) {
-    for (int i = tid; i < a.k; i += NT) {
-      const int64_t at = (int64_t)row * a.k + i;
-      const int id = load_id(a.t_ids, a.ids64, at);
-      const bool ok = id >= 0 && id < a.V;
-      s_id[i] = ok ? id : -1;
-      s_q[i] = ok ? teacher_logit(a, at) : -INFINITY;
-      s_z[i] = ok ? load_logit<DT>(z + id) : -INFINITY;
-    }
-  }
+  if (MODE == kDistill) gather_slots<DT, NT>(a, row, z, tid, sh.id, sh.q, sh.z);
   if (tid == 0) {
     if (a.row_weight) w = a.row_weight[row];
     if (MODE == kPolicy) {
@@ -313,34 +381,37 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
       }
     }
   }
-
-  {
-    const MaxSum v = add_vecs<DT, VPT>(one_logit(x_edge, a.c2), d, a.c2);
-    const MaxSum w = warp_merge(v, a.c2, 32);
-    if (lane == 0) s_ms[warp] = w;
+  MaxSum v = add_vecs<DT, VPT>(one_logit(x_edge, a.c2), d, a.c2);
+  v = warp_merge(v, a.c2, 32);
+  if (kWarps > 1 && lane == 0) sh.ms[warp] = v;
+  sync();
+  if (MODE == kDistill) {
+    if (warp == kWarps - 1) {
+      const TeacherSums t = teacher_sums(a, row, lane, sh.q, sh.z);
+      if (lane == 0) sh.t = t;
+      __syncwarp();
+      if (a.dlogits) name_repeats(a.k, lane, sh.id, sh.seen, sh.again);
+    }
+    sync();
   }
-  __syncthreads();
-  if (MODE == kDistill && warp == 1) {
-    const TeacherSums t = teacher_sums(a, row, lane, s_q, s_z);
-    if (lane == 0) s_t = t;
-  }
-  if (MODE == kDistill) __syncthreads();
   if (warp == 0) {
-    MaxSum v = lane < kWarps ? s_ms[lane] : MaxSum{-INFINITY, 0.0f};
-    v = warp_merge(v, a.c2, kWarps);
+    if (kWarps > 1) {
+      v = lane < kWarps ? sh.ms[lane] : MaxSum{-INFINITY, 0.0f};
+      v = warp_merge(v, a.c2, kWarps);
+    }
     if (lane == 0) {
-      const RowResult r = finish_row<MODE>(a, v, w, MODE == kDistill ? s_t : TeacherSums{}, z_act,
+      const RowResult r = finish_row<MODE>(a, v, w, MODE == kDistill ? sh.t : TeacherSums{}, z_act,
                                            old, adv, ref);
       if (a.row_loss) a.row_loss[row] = r.loss;
       if (a.logp) a.logp[row] = r.logp;
-      s_r = r;
+      sh.r = r;
     }
   }
   if (!a.dlogits) return;
-  __syncthreads();
+  sync();
 
-  const RowResult r = s_r;
-  with_soft<DT>(r.soft, a.c2, [&](auto grad_vec) {
+  const RowResult r = sh.r;
+  with_soft<DT>(r.soft, a.c2, [&](auto grad_vec, auto) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) d[i] = grad_vec(d[i]);
 #pragma unroll
@@ -351,15 +422,19 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
   });
   if (edge >= 0) store_logit<DT>(dz + edge, soft_at(x_edge, r.soft, a.c2));
   if (r.soft.coef == 0.0f) return;
-  __syncthreads();  // the few entries overwrite what the loop stored
+  sync();  // the few entries overwrite what the threads stored
   if (MODE == kDistill) {
     for (int i = tid; i < a.k; i += NT) {
-      const int id = s_id[i];
-      if (id < 0) continue;
-      float q = 0.0f;  // slots that repeat a token add up, each writing the same sum
-      for (int j = 0; j < a.k; ++j) q += s_id[j] == id ? s_q[j] : 0.0f;
-      store_logit<DT>(dz + id, soft_at(s_z[i], r.soft, a.c2) - r.scale * q);
+      const int id = sh.id[i];
+      if (id >= 0)
+        store_logit<DT>(dz + id, soft_at(sh.z[i], r.soft, a.c2) - r.scale * sh.q[i]);
     }
+    sync();
+    if (warp == 0)
+      for_repeats(a.k, lane, sh.id, sh.q, sh.again, [&](int i, float q) {
+        if (lane == 0)
+          store_logit<DT>(dz + sh.id[i], soft_at(sh.z[i], r.soft, a.c2) - r.scale * q);
+      });
   } else if (tid == 0) {
     store_logit<DT>(dz + act, soft_at(z_act, r.soft, a.c2) + r.top);
   }
@@ -374,80 +449,64 @@ __global__ void __launch_bounds__(NT) short_row_kernel(const TokenLossArgs a) {
 //                         gradient, from shared memory
 //   producer (1 warp)     bulk copies of the part's 16 KB chunks into a ring, as far
 //                         ahead as the ring has room
-//   gather (4 warps)      the few logits that the loss picks out, the row's edges and
-//                         the teacher's side, each warp every fourth row, up to four
-//                         rows ahead
+//   gather (3 or 4 warps, rows in turn)  ahead of the consumers the few logits that the
+//                         loss picks out, the row's edges and the teacher's side; after
+//                         pass 2 the gradient's edges and few entries
 //   finish (1 warp a group)  joins the warps' sums, exchanges them within the cluster
 //                         (every block gets every other's pair), loss and gradient
-//                         constants; after pass 2 the edges and the few entries
+//                         constants
+// A group's rows always meet the same finish warp, and a slot's rows the same gather
+// warp, group and finish warp, so that each waits on a barrier phase by phase.
 // One group's waits for the exchange are the other's time to compute.  Rows that are
 // left out pass through no ring slot and no barrier.  All waits are bounded; a role
 // whose wait runs out leaves, and the rows not finished get NaN losses.
 
 constexpr int kGroupWarps = 8;
 constexpr int kGroupThreads = kGroupWarps * 32;
-constexpr int kGatherWarps = 4;  // and slots: more than there are groups
 // Groups: with a gradient two, whose parts stay in the ring until pass 2; without, a
 // chunk is free again after pass 1, and a third group hides more of the other waits.
+// Slots of rows gathered ahead: multiples of the groups and of the gather warps.
 constexpr int groups_of(bool grad) { return grad ? 2 : 3; }
+constexpr int gather_warps(bool grad) { return grad ? 4 : 3; }
+constexpr int slots_of(bool grad) { return grad ? 4 : 6; }
 constexpr int long_threads(bool grad) {
-  return (groups_of(grad) * (kGroupWarps + 1) + 1 + kGatherWarps) * 32;
+  return (groups_of(grad) * (kGroupWarps + 1) + 1 + gather_warps(grad)) * 32;
 }
 constexpr int kChunkVecs = 1024;  // 16 KB
 constexpr int kChunks = 13;
-constexpr int kPartsAhead = 8;    // parts that the ring may hold at once: a part has > 1 chunk
+constexpr int kPartsAhead = 16;   // more parts than the ring may hold
 constexpr int kMaxCluster = 8;
 constexpr int kRingBytes = kChunks * kChunkVecs * 16;
 
-template <int MODE>
-struct Slot {  // what the gather warp prepares of a row
-  static constexpr int kSlots = MODE == kDistill ? kMaxTeacher : 4;
-  alignas(16) int id[kSlots];
-  alignas(16) float q[kSlots];
-  float z[kSlots];
+template <int MODE, bool kGrad>
+struct Slot {  // a row: what the gather warp prepares, and what comes of it
+  static constexpr int kIds = MODE == kDistill && kGrad ? kMaxTeacher : 1;
+  static constexpr int kFew = MODE == kDistill ? kMaxTeacher : 1;
+  int id[kIds];
+  float q[kFew], z[kFew];
+  uint32_t seen[MODE == kDistill && kGrad ? kSeenWords : 1], again[kMaxTeacher / 32];
   float edge[kMaxEdge];
   float in[5];  // policy: [1] weight, [2] old, [3] advantage, [4] reference
   float w;      // distill: weight
   TeacherSums t;
+  Soft soft;    // the finish warp's
+  float top, scale;
 };
 
-// q of every slot replaced by the sum over the slots of the same token, by one warp.
-__device__ __forceinline__ void repeated_slots(int k, int lane, const int* s_id, float* s_q) {
-  float sum[kMaxTeacher / 32];
-#pragma unroll
-  for (int u = 0; u < kMaxTeacher / 32; ++u) {
-    sum[u] = 0.0f;
-    if (32 * u >= k) break;
-    const int id = lane + 32 * u < k ? s_id[lane + 32 * u] : -1;
-    for (int j = 0; j < k; j += 4) {  // slots from k on are not of this row: masked by j
-      const int4 o = *reinterpret_cast<const int4*>(s_id + j);
-      const float4 q = *reinterpret_cast<const float4*>(s_q + j);
-      if (o.x == id) sum[u] += q.x;
-      if (o.y == id && j + 1 < k) sum[u] += q.y;
-      if (o.z == id && j + 2 < k) sum[u] += q.z;
-      if (o.w == id && j + 3 < k) sum[u] += q.w;
-    }
-  }
-  __syncwarp();
-#pragma unroll
-  for (int u = 0; u < kMaxTeacher / 32; ++u)
-    if (lane + 32 * u < k) s_q[lane + 32 * u] = sum[u];
-  __syncwarp();
-}
-
-template <int MODE, int kGroups>
+template <int MODE, bool kGrad>
 struct LongShared {
+  static constexpr int kGroups = groups_of(kGrad), kSlots = slots_of(kGrad);
   // A block may send the sums of a group's next row before another has read the last
   // ones, but not those of the row after that, as it has then had the other's next.
   static constexpr int kExchanges = 2 * kGroups;
-  Slot<MODE> slot[kGatherWarps];
+  Slot<MODE, kGrad> slot[kSlots];
   MaxSum ms[kGroups][kGroupWarps];
   alignas(16) MaxSum cl[kExchanges][kMaxCluster];
-  Soft soft[kGroups];
   alignas(8) uint64_t full[kPartsAhead], empty[kChunks];
-  uint64_t sums[kGroups], go[kGroups], done[kGroups], xch[kExchanges];
-  uint64_t ready[kGatherWarps], taken[kGatherWarps];
-  volatile int failed;  // the producer's wait ran out
+  uint64_t sums[kGroups], go[kGroups], xch[kExchanges];
+  uint64_t ready[kSlots];  // gathered
+  uint64_t over[kSlots];   // read for the last time: pass 2 done, or without one the loss
+  volatile int failed;     // the producer's wait ran out
 };
 
 // The rows of one cluster in order, 32 at a time: which of them count.
@@ -491,10 +550,12 @@ template <int DT, int MODE, bool kGrad>
 __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const TokenLossArgs a) {
   using L = typename LogitType<DT>::type;
   using V16 = Vec<DT>;
-  constexpr int kGroups = groups_of(kGrad);
+  constexpr int kGroups = groups_of(kGrad), kSlots = slots_of(kGrad);
+  constexpr int kGatherWarps = gather_warps(kGrad);
   constexpr int kConsumerWarps = kGroups * kGroupWarps;
+  static_assert(kSlots % kGroups == 0 && kSlots % kGatherWarps == 0, "one user a slot");
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ LongShared<MODE, kGroups> sh;
+  __shared__ LongShared<MODE, kGrad> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = cluster_size(), rank = cluster_rank();
   if (tid == 0) {
@@ -503,12 +564,11 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
     for (int p = 0; p < kGroups; ++p) {
       mbar_init(smem_u32(&sh.sums[p]), kGroupWarps);
       mbar_init(smem_u32(&sh.go[p]), 1);
-      mbar_init(smem_u32(&sh.done[p]), kGroupWarps);
     }
     for (int p = 0; p < sh.kExchanges; ++p) mbar_init(smem_u32(&sh.xch[p]), 1);
-    for (int g = 0; g < kGatherWarps; ++g) {
-      mbar_init(smem_u32(&sh.ready[g]), 1);
-      mbar_init(smem_u32(&sh.taken[g]), 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&sh.ready[i]), 1);
+      mbar_init(smem_u32(&sh.over[i]), kGrad ? kGroupWarps : 1);
     }
     sh.failed = 0;
     fence_barrier_init();
@@ -545,42 +605,47 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
 
   if (warp < kConsumerWarps) {
     constexpr int kPer = kChunkVecs / kGroupThreads;  // vectors of a chunk a thread has
-    constexpr int kStep = kPer >= 4 ? 1 : 4 / kPer;   // chunks of a step
     const int g = warp / kGroupWarps, gtid = tid - g * kGroupThreads;
     RingPos pos;      // of the next row's part
     uint32_t lv = 0;  // live rows passed
-    // fn(array of vectors, their chunk(s), first vector, vectors left) over a part, kStep
-    // chunks at a time while there are so many
-    auto steps = [&](int nv, RingPos at, auto fn) {
+    // fn(array of a thread's vectors, their chunk, first vector, vectors left, whether it
+    // is the chunk's last call) over a part: a chunk at a time, the last one with as few
+    // vectors a thread as it needs; where `whole` is false always with one
+    auto steps = [&](int nv, RingPos at, auto whole, auto fn) {
       int left = nv;
-      if constexpr (kStep == 2) {
-        for (; left > kChunkVecs; left -= 2 * kChunkVecs) {
-          const int a0 = at.slot;
-          at.next();
-          V16 d[2 * kPer];
-          fn(d, a0, at.slot, nv - left, left);
-          at.next();
+      if constexpr (decltype(whole)::value) {
+        for (; left > kChunkVecs / 2; left -= kChunkVecs, at.next()) {
+          V16 d[kPer];
+          fn(d, at.slot, nv - left, left, true);
+        }
+        if (left > kChunkVecs / 4) {
+          V16 d[kPer / 2];
+          fn(d, at.slot, nv - left, left, true);
+        } else if (left > 0) {
+          V16 d[kPer / 4];
+          fn(d, at.slot, nv - left, left, true);
+        }
+      } else {
+        for (int q = 0; left > 0; left -= kGroupThreads) {
+          V16 d[1];
+          const bool last = q == kPer - 1 || left <= kGroupThreads;
+          fn(d, at.slot, nv - left, left, last);
+          if (++q == kPer) {
+            q = 0;
+            at.next();
+          }
         }
       }
-      for (; left > 0; left -= kChunkVecs) {
-        V16 d[kPer];
-        fn(d, at.slot, at.slot, nv - left, left);
-        at.next();
-      }
     };
-    auto read = [&](auto& d, int a0, int a1) {
-      const uint4* r = reinterpret_cast<const uint4*>(ring) + gtid;
-      constexpr int U = sizeof(d) / sizeof(V16);
+    auto read = [&](auto& d, int slot, int from) {
+      const uint4* r =
+          reinterpret_cast<const uint4*>(ring) + slot * kChunkVecs + from % kChunkVecs + gtid;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        d[u].v = r[(u < kPer ? a0 : a1) * kChunkVecs + (u % kPer) * kGroupThreads];
+      for (int u = 0; u < (int)(sizeof(d) / sizeof(V16)); ++u) d[u].v = r[u * kGroupThreads];
     };
-    auto release = [&](int a0, int a1) {
+    auto release = [&](int slot) {
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sh.empty[a0]));
-        if (a1 != a0) mbar_arrive(smem_u32(&sh.empty[a1]));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
     };
     for (int it = 0; it < rows; ++it) {
       const int row = first + it * step;
@@ -603,10 +668,10 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
 
       MaxSum v = {-INFINITY, 0.0f};
       if (!warp_wait(&sh.full[l % kPartsAhead], (l / kPartsAhead) & 1)) break;
-      steps(p.nv, at, [&](auto& d, int a0, int a1, int, int left) {
+      steps(p.nv, at, std::true_type{}, [&](auto& d, int slot, int from, int left, bool) {
         constexpr int U = sizeof(d) / sizeof(V16);
-        read(d, a0, a1);
-        if (!kGrad) release(a0, a1);
+        read(d, slot, from);
+        if (!kGrad) release(slot);
         if (left < U * kGroupThreads) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -623,11 +688,11 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       if (!warp_wait(&sh.go[g], ph)) break;
       if constexpr (!kGrad) continue;
       const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
-      with_soft<DT>(sh.soft[g], a.c2, [&](auto grad_vec) {
-        steps(p.nv, at, [&](auto& d, int a0, int a1, int from, int left) {
+      with_soft<DT>(sh.slot[l % kSlots].soft, a.c2, [&](auto grad_vec, auto whole) {
+        steps(p.nv, at, whole, [&](auto& d, int slot, int from, int left, bool last) {
           constexpr int U = sizeof(d) / sizeof(V16);
-          read(d, a0, a1);  // beyond the part: what the slot held, not stored
-          release(a0, a1);
+          read(d, slot, from);  // beyond the part: what the slot held, not stored
+          if (last) release(slot);
           const int base = p.v0 + from + gtid;
 #pragma unroll
           for (int u = 0; u < U; ++u) d[u] = grad_vec(d[u]);
@@ -642,7 +707,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         });
       });
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.done[g]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.over[l % kSlots]));
     }
   } else if (warp == kConsumerWarps) {  // producer
     RingPos pos;
@@ -683,35 +748,28 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       warp_wait(&sh.full[i % kPartsAhead], (i / kPartsAhead) & 1);
   } else if (warp <= kConsumerWarps + kGatherWarps) {  // gather
     const int g = warp - kConsumerWarps - 1;
-    Slot<MODE>& s = sh.slot[g];
     uint32_t lv = 0;
     for (int it = 0; it < rows; ++it) {
       const int row = first + it * step;
       if (!walk.live(a, it)) continue;
       const uint32_t l = lv++;
       if (l % kGatherWarps != g) continue;
+      const int i = l % kSlots;
+      const uint32_t ph = (l / kSlots) & 1;
+      Slot<MODE, kGrad>& s = sh.slot[i];
       const L* z = logits_of(row);
-      const Split sp = split_row<DT>(z, a.V, C);
-      if (!warp_wait(&sh.taken[g], ((l / kGatherWarps) & 1) ^ 1)) break;
-      const float x_edge = lane < sp.head + sp.tail
-                               ? load_logit<DT>(z + edge_column(sp, a.V, lane)) : 0.0f;
+      const Part p = part_of(row);
+      if (!kGrad && !warp_wait(&sh.over[i], ph ^ 1)) break;
+      const float x_edge = lane < p.sp.head + p.sp.tail
+                               ? load_logit<DT>(z + edge_column(p.sp, a.V, lane)) : 0.0f;
       if (MODE == kDistill) {
-        for (int i = lane; i < a.k; i += 32) {
-          const int64_t at = (int64_t)row * a.k + i;
-          const int id = load_id(a.t_ids, a.ids64, at);
-          const bool in = id >= 0 && id < a.V;
-          s.id[i] = in ? id : -1;
-          s.q[i] = in ? teacher_logit(a, at) : -INFINITY;
-          s.z[i] = in ? load_logit<DT>(z + id) : -INFINITY;
-        }
+        gather_slots<DT, 32>(a, row, z, lane, kGrad ? s.id : nullptr, s.q, s.z);
         __syncwarp();
         const TeacherSums t = teacher_sums(a, row, lane, s.q, s.z);
         if (lane == 0) {
           s.t = t;
           s.w = a.row_weight ? a.row_weight[row] : 1.0f;
         }
-        __syncwarp();
-        if (kGrad) repeated_slots(a.k, lane, s.id, s.q);
       } else if (lane < 5) {
         const int act = lane == 0 ? load_id(a.actions, a.ids64, row) : 0;
         const float* from = lane == 1   ? a.row_weight
@@ -726,7 +784,35 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       }
       if (lane < kMaxEdge) s.edge[lane] = x_edge;
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[g]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[i]));
+      if constexpr (kGrad) {
+        if (MODE == kDistill) name_repeats(a.k, lane, s.id, s.seen, s.again);
+        if (!warp_wait(&sh.over[i], ph)) break;  // pass 2 is done
+        const Soft soft = s.soft;
+        L* dz = grad_of(row);
+        if (rank == 0 && lane < p.sp.head + p.sp.tail)
+          store_logit<DT>(dz + edge_column(p.sp, a.V, lane), soft_at(x_edge, soft, a.c2));
+        if (soft.coef == 0.0f) continue;
+        auto store_entry = [&](int j, float more) {
+          const int id = s.id[j];
+          if (id < 0) return;
+          const int e = id - p.sp.head;  // rank 0 has the edges, else whose vector it is
+          const int vec = e / V16::kElems - p.v0;
+          const bool mine = e < 0 || e >= p.sp.nb * V16::kElems ? rank == 0 : vec >= 0 && vec < p.nv;
+          if (mine) store_logit<DT>(dz + id, soft_at(s.z[j], soft, a.c2) + more);
+        };
+        __syncwarp();
+        if (MODE == kDistill) {
+          for (int j = lane; j < a.k; j += 32) store_entry(j, -s.scale * s.q[j]);
+          __syncwarp();
+          for_repeats(a.k, lane, s.id, s.q, s.again, [&](int j, float q) {
+            if (lane == 0) store_entry(j, -s.scale * q);
+          });
+        } else if (lane == 0) {
+          store_entry(0, s.top);
+        }
+        __syncwarp();
+      }
     }
   } else {  // finish
     const int b = warp - (kConsumerWarps + 1 + kGatherWarps);  // its group
@@ -751,12 +837,11 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       }
       const uint32_t l = lv++;
       if (l % kGroups != b) continue;
-      const int g = l % kGatherWarps, x = l % sh.kExchanges;
-      const uint32_t ph = (l / kGroups) & 1;
-      const Slot<MODE>& s = sh.slot[g];
+      const int i = l % kSlots, x = l % sh.kExchanges;
+      Slot<MODE, kGrad>& s = sh.slot[i];
       const Part p = part_of(row);
-      ok = warp_wait(&sh.ready[g], (l / kGatherWarps) & 1) && warp_wait(&sh.sums[b], ph) &&
-           !sh.failed;
+      ok = warp_wait(&sh.ready[i], (l / kSlots) & 1) &&
+           warp_wait(&sh.sums[b], (l / kGroups) & 1) && !sh.failed;
       if (!ok) break;
       // the consumer warps' pairs, and rank 0's edges
       MaxSum v = lane < kGroupWarps ? sh.ms[b][lane] : MaxSum{-INFINITY, 0.0f};
@@ -774,42 +859,24 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         v = lane < C ? sh.cl[x][lane] : MaxSum{-INFINITY, 0.0f};
         v = warp_merge(v, a.c2, kMaxCluster);
       }
-      const RowResult r =  // lane 0's counts
-          MODE == kDistill
-              ? finish_row<MODE>(a, v, s.w, s.t, 0.0f, 0.0f, 0.0f, 0.0f)
-              : finish_row<MODE>(a, v, s.in[1], s.t, s.z[0], s.in[2], s.in[3], s.in[4]);
       if (lane == 0) {
-        if (kGrad) sh.soft[b] = r.soft;
+        const RowResult r =
+            MODE == kDistill
+                ? finish_row<MODE>(a, v, s.w, s.t, 0.0f, 0.0f, 0.0f, 0.0f)
+                : finish_row<MODE>(a, v, s.in[1], s.t, s.z[0], s.in[2], s.in[3], s.in[4]);
+        if (kGrad) {
+          s.soft = r.soft;
+          s.top = r.top;
+          s.scale = r.scale;
+        }
         mbar_arrive(smem_u32(&sh.go[b]));
+        if (!kGrad) mbar_arrive(smem_u32(&sh.over[i]));
         if (rank == 0) {
           if (a.row_loss) a.row_loss[row] = r.loss;
           if (a.logp) a.logp[row] = r.logp;
         }
       }
       __syncwarp();
-      if constexpr (kGrad) {  // after pass 2
-        const Soft soft = sh.soft[b];
-        const float scale = __shfl_sync(0xFFFFFFFFu, r.scale, 0);
-        const float top = __shfl_sync(0xFFFFFFFFu, r.top, 0);
-        ok = warp_wait(&sh.done[b], ph);
-        if (!ok) break;
-        L* dz = grad_of(row);
-        if (rank == 0 && lane < p.sp.head + p.sp.tail)
-          store_logit<DT>(dz + edge_column(p.sp, a.V, lane), soft_at(s.edge[lane], soft, a.c2));
-        __syncwarp();
-        const int n = soft.coef == 0.0f ? 0 : MODE == kDistill ? a.k : 1;
-        for (int i = lane; i < n; i += 32) {
-          const int id = s.id[i];
-          if (id < 0) continue;
-          const int e = id - p.sp.head;  // rank 0 has the edges, else whose vector it is
-          const int vec = e / V16::kElems - p.v0;
-          const bool mine = e < 0 || e >= p.sp.nb * V16::kElems ? rank == 0 : vec >= 0 && vec < p.nv;
-          const float more = MODE == kDistill ? -scale * s.q[i] : top;
-          if (mine) store_logit<DT>(dz + id, soft_at(s.z[i], soft, a.c2) + more);
-        }
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(smem_u32(&sh.taken[g]));
     }
     if (!ok && rank == 0)  // a wait ran out: this row and the rest are not valid
       for (int i = it + lane; i < rows; i += 32) {
@@ -826,7 +893,9 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
 
 template <int DT, int MODE, int NT, int VPT>
 cudaError_t launch_short(const TokenLossArgs& a, cudaStream_t s) {
-  return launch_pdl(short_row_kernel<DT, MODE, NT, VPT>, dim3(a.N), dim3(NT), 0, s, a);
+  constexpr int kRows = short_rows_per_block(NT);
+  return launch_pdl(short_row_kernel<DT, MODE, NT, VPT>, dim3((a.N + kRows - 1) / kRows),
+                    dim3(NT * kRows), 0, s, a);
 }
 
 template <int DT, int MODE, bool kGrad>
@@ -862,18 +931,23 @@ cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-constexpr int kPartVecs = 5120;     // a block's part of a row, at most, while C <= 8 allows
-constexpr int kShortVecs = 2048;    // rows of 32 KB and less are short
+#ifndef TL_SHORT
+#define TL_SHORT 1024
+#endif
+constexpr int kPartVecs = 5120;  // a block's part of a long row
 
 // The variant goes by the row's length alone, so that a row's bits do not depend on
 // the batch.
 template <int DT, int MODE>
 cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
   const int nvec = a.V / Vec<DT>::kElems;  // at most so many vectors a row
-  if (nvec <= 128) return launch_short<DT, MODE, 128, 1>(a, s);
+  if (nvec <= 128) return launch_short<DT, MODE, 32, 4>(a, s);
   if (nvec <= 512) return launch_short<DT, MODE, 128, 4>(a, s);
-  if (nvec <= kShortVecs) return launch_short<DT, MODE, 512, 4>(a, s);
-  const int C = min(kMaxCluster, (nvec + kPartVecs - 1) / kPartVecs);
+  if (nvec <= TL_SHORT) return launch_short<DT, MODE, 256, 4>(a, s);
+  int C = (nvec + kPartVecs - 1) / kPartVecs;
+  // clusters of 6 fill 138 SMs, of 7 and 8 only 105 and 120: the longest parts of which
+  // two fit the ring come first
+  if (C > 6) C = nvec <= 6 * kChunkVecs * 6 ? 6 : kMaxCluster;
   return a.dlogits ? launch_long<DT, MODE, true>(a, C, s) : launch_long<DT, MODE, false>(a, C, s);
 }
 

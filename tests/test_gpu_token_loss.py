@@ -120,6 +120,42 @@ def test_logp_and_loss_only_calls_agree_with_the_gradient_call():
         assert torch.equal(M.token_logp(zc, ac.to(torch.int32)), out[1])
 
 
+@pytest.mark.parametrize("V", [700, 10000, 20000, 60000])
+@pytest.mark.parametrize("k", [1, 33, 64, 256])
+def test_many_rows(V, k):
+    """Many rows a block, some left out at random: the calls with and without a gradient
+    give the same losses, rows that start on 16 bytes the same when cut out of the batch,
+    and every gradient row sums to 0."""
+    N = 6000 if V < 30000 else 2500
+    z = _logits(64, V, "bf16", V + k).to(DEV)
+    pick = torch.randint(64, (N,), generator=torch.Generator().manual_seed(k)).to(DEV)
+    ids, t, _ = _teacher(z.cpu(), k, 5)
+    z, ids, t = z[pick], ids.to(DEV)[pick], t.to(DEV)[pick]
+    w = (torch.rand(N, generator=torch.Generator().manual_seed(k + 1)) < 0.7).float().to(DEV)
+    loss = M.distill_loss(z, ids, t)
+    for _ in range(5):
+        assert torch.equal(M.distill_loss(z, ids, t), loss)
+    got, d = M.distill_loss_grad(z, ids, t, w)
+    assert torch.equal(got, loss * w)
+    assert not d[w == 0].any()
+    # bf16 rounding of V entries, each at most 2^-8 of its size, of a row whose positive
+    # entries sum to at most 1
+    assert torch.all(d.double().sum(1).abs() <= 2.0 ** -7)
+    if V % 8:
+        return  # rows that do not start on 16 bytes are summed in an order of their own
+    rows = torch.tensor([0, 1, 151, 152, 999, N - 1], device=DEV)
+    assert torch.equal(M.distill_loss(z[rows], ids[rows], t[rows]), loss[rows])
+    same = M.distill_loss_grad(z[rows], ids[rows], t[rows], w[rows])
+    assert torch.equal(same[1], d[rows])
+    a = ids[:, 0].clone()
+    a[::7] = -1
+    lp = M.token_logp(z, a)
+    zero = torch.zeros(N, device=DEV)
+    out = M.policy_loss_grad(z, a, zero - 1.0, zero + 1.0, w)
+    assert torch.equal(out[1], lp * w) and torch.equal(M.token_logp(z[rows], a[rows]), lp[rows])
+    assert not out[2][(w == 0) | (a < 0)].any()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("V", [37, 1000, 50001])
 def test_masked_vocabulary_entries(V, dtype):
