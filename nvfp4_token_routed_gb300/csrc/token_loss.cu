@@ -205,35 +205,40 @@ __device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int 
   return {warp_sum(Q), warp_sum(kl), zr};
 }
 
-// A row's teacher slots into shared memory, by NT threads: ids (-1: empty), the teacher's
-// logits and the student's at those tokens.  All ids are loaded before the first logit.
-// s_id may be null.
+// A row's teacher slots, spread over NT threads: ids (-1: empty), the teacher's logits
+// and the student's at those tokens.  All ids are loaded before the first logit.
 template <int DT, int NT>
-__device__ __forceinline__ void gather_slots(const TokenLossArgs& a, int row,
-                                             const typename LogitType<DT>::type* z, int tid,
-                                             int* s_id, float* s_t, float* s_z) {
-  constexpr int U = kMaxTeacher / NT > 0 ? kMaxTeacher / NT : 1;
+struct TeacherSlots {
+  static constexpr int U = kMaxTeacher / NT;
   int id[U];
-  float t[U];
+  float t[U], z[U];
+  __device__ __forceinline__ void load(const TokenLossArgs& a, int row,
+                                       const typename LogitType<DT>::type* z_row, int tid) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int i = tid + NT * u;
-    const int64_t at = (int64_t)row * a.k + i;
-    id[u] = i < a.k ? load_id(a.t_ids, a.ids64, at) : -1;
-    t[u] = i < a.k ? teacher_logit(a, at) : -INFINITY;
-  }
+    for (int u = 0; u < U; ++u) {
+      const int i = tid + NT * u;
+      const int64_t at = (int64_t)row * a.k + i;
+      id[u] = i < a.k ? load_id(a.t_ids, a.ids64, at) : -1;
+      t[u] = i < a.k ? teacher_logit(a, at) : 0.0f;
+    }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int i = tid + NT * u;
-    const bool in = id[u] >= 0 && id[u] < a.V;
-    const float zi = in ? load_logit<DT>(z + id[u]) : -INFINITY;
-    if (i < a.k) {
-      if (s_id) s_id[i] = in ? id[u] : -1;
-      s_t[i] = in ? t[u] : -INFINITY;
-      s_z[i] = zi;
+    for (int u = 0; u < U; ++u) {
+      if (id[u] >= a.V) id[u] = -1;
+      z[u] = id[u] >= 0 ? load_logit<DT>(z_row + id[u]) : -INFINITY;
     }
   }
-}
+  // s_id may be null.
+  __device__ __forceinline__ void write(int k, int tid, int* s_id, float* s_t, float* s_z) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = tid + NT * u;
+      if (i >= k) break;
+      if (s_id) s_id[i] = max(id[u], -1);
+      s_t[i] = id[u] >= 0 ? t[u] : -INFINITY;
+      s_z[i] = z[u];
+    }
+  }
+};
 
 // The slots whose token may be an earlier slot's too, by one warp: bit i % 32 of
 // s_again[i / 32].  A hash of the tokens seen decides; it may name a slot too many.
@@ -368,7 +373,11 @@ __global__ void __launch_bounds__(NT * short_rows_per_block(NT))
   // the few logits that the loss picks out, read before any gradient is written
   int act = -1;
   float w = 1.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, z_act = 0.0f;
-  if (MODE == kDistill) gather_slots<DT, NT>(a, row, z, tid, sh.id, sh.q, sh.z);
+  if constexpr (MODE == kDistill) {
+    TeacherSlots<DT, NT> few;
+    few.load(a, row, z, tid);
+    few.write(a.k, tid, sh.id, sh.q, sh.z);
+  }
   if (tid == 0) {
     if (a.row_weight) w = a.row_weight[row];
     if (MODE == kPolicy) {
@@ -486,8 +495,7 @@ struct Slot {  // a row: what the gather warp prepares, and what comes of it
   float q[kFew], z[kFew];
   uint32_t seen[MODE == kDistill && kGrad ? kSeenWords : 1], again[kMaxTeacher / 32];
   float edge[kMaxEdge];
-  float in[5];  // policy: [1] weight, [2] old, [3] advantage, [4] reference
-  float w;      // distill: weight
+  float in[4];  // weight; policy: old log-probability, advantage, reference
   TeacherSums t;
   Soft soft;    // the finish warp's
   float top, scale;
@@ -643,9 +651,16 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
 #pragma unroll
       for (int u = 0; u < (int)(sizeof(d) / sizeof(V16)); ++u) d[u].v = r[u * kGroupThreads];
     };
-    auto release = [&](int slot) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
+    // Gives a chunk back once the vectors read from it have arrived in registers: the
+    // barrier's address takes a word of each (and itself again, so nothing is added).  An
+    // arrival alone does not wait for loads in flight, and the next copy into the chunk is
+    // not ordered behind them: with the load pipe busy it overtook them.
+    auto release = [&](const auto& d, int slot) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int u = 0; u < (int)(sizeof(d) / sizeof(V16)); ++u) w ^= d[u].v.x;
+      const uint32_t same = __shfl_sync(0xFFFFFFFFu, w, 0);
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]) + (same ^ w));
     };
     for (int it = 0; it < rows; ++it) {
       const int row = first + it * step;
@@ -671,7 +686,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       steps(p.nv, at, std::true_type{}, [&](auto& d, int slot, int from, int left, bool) {
         constexpr int U = sizeof(d) / sizeof(V16);
         read(d, slot, from);
-        if (!kGrad) release(slot);
+        if (!kGrad) release(d, slot);
         if (left < U * kGroupThreads) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -692,7 +707,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         steps(p.nv, at, whole, [&](auto& d, int slot, int from, int left, bool last) {
           constexpr int U = sizeof(d) / sizeof(V16);
           read(d, slot, from);  // beyond the part: what the slot held, not stored
-          if (last) release(slot);
+          if (last) release(d, slot);
           const int base = p.v0 + from + gtid;
 #pragma unroll
           for (int u = 0; u < U; ++u) d[u] = grad_vec(d[u]);
@@ -748,50 +763,76 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       warp_wait(&sh.full[i % kPartsAhead], (i / kPartsAhead) & 1);
   } else if (warp <= kConsumerWarps + kGatherWarps) {  // gather
     const int g = warp - kConsumerWarps - 1;
+    int it = 0;
     uint32_t lv = 0;
-    for (int it = 0; it < rows; ++it) {
-      const int row = first + it * step;
-      if (!walk.live(a, it)) continue;
-      const uint32_t l = lv++;
-      if (l % kGatherWarps != g) continue;
+    auto next_row = [&] {  // this warp's, or -1
+      while (it < rows) {
+        const int row = first + it * step;
+        if (walk.live(a, it++) && lv++ % kGatherWarps == g) return row;
+      }
+      return -1;
+    };
+    // a row's loads, in flight while the row before it is waited for
+    TeacherSlots<DT, 32> few;
+    int act = 0;
+    float x_edge = 0.0f, x_act = 0.0f, in = 0.0f;
+    auto fetch = [&](int row) {
+      const L* z = logits_of(row);
+      const Split sp = part_of(row).sp;
+      x_edge = lane < sp.head + sp.tail ? load_logit<DT>(z + edge_column(sp, a.V, lane)) : 0.0f;
+      if (MODE == kDistill) {
+        few.load(a, row, z, lane);
+        in = a.row_weight ? a.row_weight[row] : 1.0f;
+      } else {
+        const float* from = lane == 0   ? a.row_weight
+                            : lane == 1 ? a.old_logp
+                            : lane == 2 ? a.adv
+                            : lane == 3 ? a.ref_logp
+                                        : nullptr;
+        in = from ? from[row] : 1.0f;
+        if (lane == 0) {
+          act = load_id(a.actions, a.ids64, row);
+          x_act = load_logit<DT>(z + act);
+        }
+      }
+    };
+    int row = next_row();
+    if (row >= 0) fetch(row);
+    for (uint32_t l = lv - 1; row >= 0; l = lv - 1) {
       const int i = l % kSlots;
       const uint32_t ph = (l / kSlots) & 1;
       Slot<MODE, kGrad>& s = sh.slot[i];
-      const L* z = logits_of(row);
-      const Part p = part_of(row);
       if (!kGrad && !warp_wait(&sh.over[i], ph ^ 1)) break;
-      const float x_edge = lane < p.sp.head + p.sp.tail
-                               ? load_logit<DT>(z + edge_column(p.sp, a.V, lane)) : 0.0f;
-      if (MODE == kDistill) {
-        gather_slots<DT, 32>(a, row, z, lane, kGrad ? s.id : nullptr, s.q, s.z);
+      if constexpr (MODE == kDistill) {
+        few.write(a.k, lane, kGrad ? s.id : nullptr, s.q, s.z);
         __syncwarp();
         const TeacherSums t = teacher_sums(a, row, lane, s.q, s.z);
         if (lane == 0) {
           s.t = t;
-          s.w = a.row_weight ? a.row_weight[row] : 1.0f;
+          s.in[0] = in;
         }
-      } else if (lane < 5) {
-        const int act = lane == 0 ? load_id(a.actions, a.ids64, row) : 0;
-        const float* from = lane == 1   ? a.row_weight
-                            : lane == 2 ? a.old_logp
-                            : lane == 3 ? a.adv
-                                        : a.ref_logp;
-        if (lane > 0) s.in[lane] = from ? from[row] : 1.0f;
+      } else {
+        if (lane < 4) s.in[lane] = in;
         if (lane == 0) {
           s.id[0] = act;
-          s.z[0] = load_logit<DT>(z + act);
+          s.z[0] = x_act;
         }
       }
       if (lane < kMaxEdge) s.edge[lane] = x_edge;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.ready[i]));
+      const int done = row;
+      row = next_row();
+      if (row >= 0) fetch(row);
       if constexpr (kGrad) {
         if (MODE == kDistill) name_repeats(a.k, lane, s.id, s.seen, s.again);
         if (!warp_wait(&sh.over[i], ph)) break;  // pass 2 is done
         const Soft soft = s.soft;
-        L* dz = grad_of(row);
+        const Part p = part_of(done);
+        L* dz = grad_of(done);
         if (rank == 0 && lane < p.sp.head + p.sp.tail)
-          store_logit<DT>(dz + edge_column(p.sp, a.V, lane), soft_at(x_edge, soft, a.c2));
+          store_logit<DT>(dz + edge_column(p.sp, a.V, lane), soft_at(s.edge[lane], soft, a.c2));
+        __syncwarp();
         if (soft.coef == 0.0f) continue;
         auto store_entry = [&](int j, float more) {
           const int id = s.id[j];
@@ -801,7 +842,6 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
           const bool mine = e < 0 || e >= p.sp.nb * V16::kElems ? rank == 0 : vec >= 0 && vec < p.nv;
           if (mine) store_logit<DT>(dz + id, soft_at(s.z[j], soft, a.c2) + more);
         };
-        __syncwarp();
         if (MODE == kDistill) {
           for (int j = lane; j < a.k; j += 32) store_entry(j, -s.scale * s.q[j]);
           __syncwarp();
@@ -862,8 +902,8 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       if (lane == 0) {
         const RowResult r =
             MODE == kDistill
-                ? finish_row<MODE>(a, v, s.w, s.t, 0.0f, 0.0f, 0.0f, 0.0f)
-                : finish_row<MODE>(a, v, s.in[1], s.t, s.z[0], s.in[2], s.in[3], s.in[4]);
+                ? finish_row<MODE>(a, v, s.in[0], s.t, 0.0f, 0.0f, 0.0f, 0.0f)
+                : finish_row<MODE>(a, v, s.in[0], s.t, s.z[0], s.in[1], s.in[2], s.in[3]);
         if (kGrad) {
           s.soft = r.soft;
           s.top = r.top;

@@ -124,15 +124,17 @@ def test_logp_and_loss_only_calls_agree_with_the_gradient_call():
 @pytest.mark.parametrize("k", [1, 33, 64, 256])
 def test_many_rows(V, k):
     """Many rows a block, some left out at random: the calls with and without a gradient
-    give the same losses, rows that start on 16 bytes the same when cut out of the batch,
+    give the same, right losses, rows that start on 16 bytes the same when cut out of the batch,
     and every gradient row sums to 0."""
     N = 6000 if V < 30000 else 2500
     z = _logits(64, V, "bf16", V + k).to(DEV)
     pick = torch.randint(64, (N,), generator=torch.Generator().manual_seed(k)).to(DEV)
     ids, t, _ = _teacher(z.cpu(), k, 5)
+    want = R.distill(z.cpu(), ids, t, None, None, 1.0)[0].to(DEV)[pick]
     z, ids, t = z[pick], ids.to(DEV)[pick], t.to(DEV)[pick]
     w = (torch.rand(N, generator=torch.Generator().manual_seed(k + 1)) < 0.7).float().to(DEV)
     loss = M.distill_loss(z, ids, t)
+    assert torch.all((loss.double() - want).abs() <= 1e-5 + 2.0 ** -20 * 30)
     for _ in range(5):
         assert torch.equal(M.distill_loss(z, ids, t), loss)
     got, d = M.distill_loss_grad(z, ids, t, w)
