@@ -655,10 +655,13 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
     // barrier's address takes a word of each (and itself again, so nothing is added).  An
     // arrival alone does not wait for loads in flight, and the next copy into the chunk is
     // not ordered behind them: with the load pipe busy it overtook them.
-    auto release = [&](const auto& d, int slot) {
+    auto word_of = [](const auto& d) {
       uint32_t w = 0;
 #pragma unroll
       for (int u = 0; u < (int)(sizeof(d) / sizeof(V16)); ++u) w ^= d[u].v.x;
+      return w;
+    };
+    auto release = [&](int slot, uint32_t w) {
       const uint32_t same = __shfl_sync(0xFFFFFFFFu, w, 0);
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]) + (same ^ w));
     };
@@ -686,13 +689,14 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       steps(p.nv, at, std::true_type{}, [&](auto& d, int slot, int from, int left, bool) {
         constexpr int U = sizeof(d) / sizeof(V16);
         read(d, slot, from);
-        if (!kGrad) release(d, slot);
+        const uint32_t w = word_of(d);
         if (left < U * kGroupThreads) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
             if (gtid + u * kGroupThreads >= left) d[u].fill(V16::kNegInf);
         }
         v = add_vecs<DT, U>(v, d, a.c2);
+        if (!kGrad) release(slot, w);
       });
       v = warp_merge(v, a.c2, 32);
       if (lane == 0) {
@@ -707,7 +711,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         steps(p.nv, at, whole, [&](auto& d, int slot, int from, int left, bool last) {
           constexpr int U = sizeof(d) / sizeof(V16);
           read(d, slot, from);  // beyond the part: what the slot held, not stored
-          if (last) release(d, slot);
+          const uint32_t w = word_of(d);
           const int base = p.v0 + from + gtid;
 #pragma unroll
           for (int u = 0; u < U; ++u) d[u] = grad_vec(d[u]);
@@ -719,6 +723,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
             for (int u = 0; u < U; ++u)
               if (gtid + u * kGroupThreads < left) out.store(base + u * kGroupThreads, d[u]);
           }
+          if (last) release(slot, w);
         });
       });
       __syncwarp();
