@@ -242,14 +242,14 @@ struct TeacherSlots {
 
 // The slots whose token may be an earlier slot's too, by one warp: bit i % 32 of
 // s_again[i / 32].  A hash of the tokens seen decides; it may name a slot too many.
-constexpr int kSeenWords = 64;  // 2048 bits
+constexpr int kSeenWords = 256;  // 8192 bits: a false name every fourth row at 64 slots
 __device__ __forceinline__ void name_repeats(int k, int lane, const int* s_id, uint32_t* s_seen,
                                              uint32_t* s_again) {
   for (int i = lane; i < kSeenWords; i += 32) s_seen[i] = 0;
   __syncwarp();
   for (int i = lane; i - lane < k; i += 32) {
     const int id = i < k ? s_id[i] : -1;
-    const uint32_t h = ((uint32_t)id * 2654435761u) >> 21, bit = 1u << (h & 31);
+    const uint32_t h = ((uint32_t)id * 2654435761u) >> 19, bit = 1u << (h & 31);
     const bool again = id >= 0 && (atomicOr(&s_seen[h >> 5], bit) & bit);
     const uint32_t all = __ballot_sync(0xFFFFFFFFu, again);
     if (lane == 0) s_again[i / 32] = all;
