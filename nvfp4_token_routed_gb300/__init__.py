@@ -694,17 +694,19 @@ def router_loss(logits, topk_ids, balance_coef, z_coef=0.0, seq_offsets=None, to
     token_mask bool [T], False: left out."""
     b = _router_batch(logits, topk_ids, balance_coef, z_coef, seq_offsets, token_mask)
     T, E = logits.shape
+    S = b.S
     losses = _out(losses, "losses", (2,), torch.float32, logits, stream)
-    counts = _out(counts, "counts", (b.S, E), torch.int32, logits, stream)
-    tokens = _out(tokens, "tokens", (b.S + 1,), torch.int32, logits, stream)
+    counts = _out(counts, "counts", (S, E), torch.int32, logits, stream)
+    tokens = _out(tokens, "tokens", (S + 1,), torch.int32, logits, stream)
+    L = lib()
     if ws is None:
-        n = moe_nvfp4_router_loss_workspace_bytes(T, E, b.S)
+        n = L.moe_nvfp4_router_loss_workspace_bytes(T, E, S)
         ws = _out(None, "ws", (n,), torch.uint8, logits, stream)
     else:
+        n = ws.numel()
         _arg(ws, "ws", ws.shape, (torch.uint8,), logits)
-    _check(lib().moe_nvfp4_router_loss(b, losses.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
-                                       ws.data_ptr(), ws.numel(), _raw(stream)),
-           "moe_nvfp4_router_loss")
+    _check(L.moe_nvfp4_router_loss(b, losses.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
+                                   ws.data_ptr(), n, _raw(stream)), "moe_nvfp4_router_loss")
     return losses, counts, tokens
 
 

@@ -64,6 +64,7 @@ struct RouterLossArgs {
   const float* d_topk_w;      // [T][K] their upstream gradients, or null
   void* dlogits;              // [T][E]
   bool aligned;               // rows are whole 16-byte vectors
+  bool counts_aligned;        // as are the counts'
 };
 
 size_t router_loss_ws_bytes(int T, int E, int S);

@@ -212,19 +212,28 @@ struct TeacherSlots {
   static constexpr int U = kMaxTeacher / NT;
   int id[U];
   float t[U], z[U];
-  __device__ __forceinline__ void load(const TokenLossArgs& a, int row,
-                                       const typename LogitType<DT>::type* z_row, int tid) {
+  __device__ __forceinline__ void load_ids(const TokenLossArgs& a, int row, int tid) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      id[u] = -1;
+      t[u] = 0.0f;
+      if (NT * u >= a.k) continue;
       const int i = tid + NT * u;
       const int64_t at = (int64_t)row * a.k + i;
-      id[u] = i < a.k ? load_id(a.t_ids, a.ids64, at) : -1;
-      t[u] = i < a.k ? teacher_logit(a, at) : 0.0f;
+      if (i < a.k) {
+        id[u] = load_id(a.t_ids, a.ids64, at);
+        t[u] = teacher_logit(a, at);
+      }
     }
+  }
+  __device__ __forceinline__ void load_logits(const TokenLossArgs& a,
+                                              const typename LogitType<DT>::type* z_row) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      z[u] = -INFINITY;
+      if (NT * u >= a.k) continue;
       if (id[u] >= a.V) id[u] = -1;
-      z[u] = id[u] >= 0 ? load_logit<DT>(z_row + id[u]) : -INFINITY;
+      if (id[u] >= 0) z[u] = load_logit<DT>(z_row + id[u]);
     }
   }
   // s_id may be null.
@@ -375,7 +384,8 @@ __global__ void __launch_bounds__(NT * short_rows_per_block(NT))
   float w = 1.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, z_act = 0.0f;
   if constexpr (MODE == kDistill) {
     TeacherSlots<DT, NT> few;
-    few.load(a, row, z, tid);
+    few.load_ids(a, row, tid);
+    few.load_logits(a, z);
     few.write(a.k, tid, sh.id, sh.q, sh.z);
   }
   if (tid == 0) {
@@ -781,13 +791,15 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
     TeacherSlots<DT, 32> few;
     int act = 0;
     float x_edge = 0.0f, x_act = 0.0f, in = 0.0f;
-    auto fetch = [&](int row) {
+    auto fetch = [&](int row, auto meanwhile) {
       const L* z = logits_of(row);
       const Split sp = part_of(row).sp;
       x_edge = lane < sp.head + sp.tail ? load_logit<DT>(z + edge_column(sp, a.V, lane)) : 0.0f;
       if (MODE == kDistill) {
-        few.load(a, row, z, lane);
+        few.load_ids(a, row, lane);
         in = a.row_weight ? a.row_weight[row] : 1.0f;
+        meanwhile();
+        few.load_logits(a, z);
       } else {
         const float* from = lane == 0   ? a.row_weight
                             : lane == 1 ? a.old_logp
@@ -802,7 +814,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       }
     };
     int row = next_row();
-    if (row >= 0) fetch(row);
+    if (row >= 0) fetch(row, [] {});
     for (uint32_t l = lv - 1; row >= 0; l = lv - 1) {
       const int i = l % kSlots;
       const uint32_t ph = (l / kSlots) & 1;
@@ -828,9 +840,12 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       if (lane == 0) mbar_arrive(smem_u32(&sh.ready[i]));
       const int done = row;
       row = next_row();
-      if (row >= 0) fetch(row);
+      auto name = [&] {
+        if (MODE == kDistill && kGrad) name_repeats(a.k, lane, s.id, s.seen, s.again);
+      };
+      if (row >= 0) fetch(row, name);
+      else name();
       if constexpr (kGrad) {
-        if (MODE == kDistill) name_repeats(a.k, lane, s.id, s.seen, s.again);
         if (!warp_wait(&sh.over[i], ph)) break;  // pass 2 is done
         const Soft soft = s.soft;
         const Part p = part_of(done);
@@ -976,9 +991,7 @@ cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-#ifndef TL_SHORT
-#define TL_SHORT 1024
-#endif
+
 constexpr int kPartVecs = 5120;  // a block's part of a long row
 
 // The variant goes by the row's length alone, so that a row's bits do not depend on
@@ -988,7 +1001,7 @@ cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
   const int nvec = a.V / Vec<DT>::kElems;  // at most so many vectors a row
   if (nvec <= 128) return launch_short<DT, MODE, 32, 4>(a, s);
   if (nvec <= 512) return launch_short<DT, MODE, 128, 4>(a, s);
-  if (nvec <= TL_SHORT) return launch_short<DT, MODE, 256, 4>(a, s);
+  if (nvec <= 1024) return launch_short<DT, MODE, 256, 4>(a, s);
   int C = (nvec + kPartVecs - 1) / kPartVecs;
   // clusters of 6 fill 138 SMs, of 7 and 8 only 105 and 120: the longest parts of which
   // two fit the ring come first
