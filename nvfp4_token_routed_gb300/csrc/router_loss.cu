@@ -303,7 +303,7 @@ __device__ __forceinline__ float warps_sum(const float* s_p, int E, int e) {
 }
 
 template <int DT, int NL, int NV>
-__global__ void __launch_bounds__(kWarps * 32) router_partial_kernel(const RouterLossArgs a, Ws w,
+__global__ void __launch_bounds__(kWarps * 32, 2) router_partial_kernel(const RouterLossArgs a, Ws w,
                                                                      int rows) {
   extern __shared__ float s_p[];  // [kWarps][E], then int[E]
   int* s_hist = reinterpret_cast<int*>(s_p + kWarps * a.E);
@@ -349,7 +349,8 @@ __device__ __forceinline__ float even_share(const RouterLossArgs& a, int n_s) {
   return n_s > 0 ? (float)a.E / ((float)a.K * (float)n_s) : 0.0f;
 }
 
-// Block (s, j): sequence s, experts 32 j to 32 j + 31 along x, its slots along y.
+// Block (s, j): sequence s, groups j, j + gridDim.y, ... of 32 experts along x, the
+// sequence's slots along y.
 __global__ void __launch_bounds__(1024) router_combine_kernel(const RouterLossArgs a, Ws w,
                                                               int rows) {
   __shared__ float s_a[1024], s_b[1024];
@@ -359,43 +360,48 @@ __global__ void __launch_bounds__(1024) router_combine_kernel(const RouterLossAr
   pdl_trigger();
   const int s = blockIdx.x, lane = threadIdx.x, y = threadIdx.y, Y = blockDim.y;
   const int tid = y * 32 + lane, threads = Y * 32;
-  const int e = blockIdx.y * 32 + lane;
   const int r0 = a.offsets ? max(0, a.offsets[s]) : 0;
   const int r1 = a.offsets ? min(a.T, a.offsets[s + 1]) : a.T;
   const int c0 = r0 / rows, c1 = r1 > r0 ? (r1 + rows - 1) / rows : c0;
   const size_t stride = 2 * (size_t)a.E + 3;
-  float p = 0.0f, z = 0.0f;
-  int cnt = 0, n = 0, bad = 0;
-  const bool meta = blockIdx.y == 0 && lane == 0;
+  float z = 0.0f, dots = 0.0f;
+  int n = 0, bad = 0;
+  for (int e = blockIdx.y * 32 + lane; e - lane < a.E; e += gridDim.y * 32) {
+    float p = 0.0f;
+    int cnt = 0;
+    const bool meta = blockIdx.y == 0 && e == 0;
 #pragma unroll 8
-  for (int c = c0 + y; c < c1; c += Y) {
-    const float* slot = w.slot + (size_t)(c + s) * stride;
-    if (e < a.E) {
-      p += slot[e];
-      cnt += __float_as_int(slot[a.E + e]);
+    for (int c = c0 + y; c < c1; c += Y) {
+      const float* slot = w.slot + (size_t)(c + s) * stride;
+      if (e < a.E) {
+        p += slot[e];
+        cnt += __float_as_int(slot[a.E + e]);
+      }
+      if (meta) {
+        z += slot[2 * a.E];
+        n += __float_as_int(slot[2 * a.E + 1]);
+        bad |= __float_as_int(slot[2 * a.E + 2]);
+      }
     }
-    if (meta) {
-      z += slot[2 * a.E];
-      n += __float_as_int(slot[2 * a.E + 1]);
-      bad |= __float_as_int(slot[2 * a.E + 2]);
-    }
-  }
-  s_a[tid] = p;
-  s_i[tid] = cnt;
-  __syncthreads();
-  for (int half = Y / 2; half > 0; half >>= 1) {
-    if (y < half) {
-      s_a[tid] += s_a[tid + half * 32];
-      s_i[tid] += s_i[tid + half * 32];
-    }
+    __syncthreads();  // the sums below of the group before
+    s_a[tid] = p;
+    s_i[tid] = cnt;
     __syncthreads();
+    for (int half = Y / 2; half > 0; half >>= 1) {
+      if (y < half) {
+        s_a[tid] += s_a[tid + half * 32];
+        s_i[tid] += s_i[tid + half * 32];
+      }
+      __syncthreads();
+    }
+    if (y == 0 && e < a.E) {
+      a.counts[(size_t)s * a.E + e] = s_i[lane];
+      dots += (float)s_i[lane] * s_a[lane];
+    }
   }
   if (y == 0) {
-    p = s_a[lane];
-    cnt = s_i[lane];
-    if (e < a.E) a.counts[(size_t)s * a.E + e] = cnt;
-    const float dot = warp_sum(e < a.E ? (float)cnt * p : 0.0f);
-    if (lane == 0) w.dots[(size_t)s * gridDim.y + blockIdx.y] = dot;
+    dots = warp_sum(dots);
+    if (lane == 0) w.dots[(size_t)s * gridDim.y + blockIdx.y] = dots;
   }
   __syncthreads();
   if (blockIdx.y == 0) {
@@ -425,15 +431,19 @@ __global__ void __launch_bounds__(1024) router_combine_kernel(const RouterLossAr
   float bal = 0.0f;
   z = 0.0f;
   n = bad = 0;
-  for (int i = tid; i < a.S; i += threads) {
-    float dot = 0.0f;
-    for (int j = 0; j < (int)gridDim.y; ++j) dot += __ldcg(&w.dots[(size_t)i * gridDim.y + j]);
-    const int n_s = __ldcg(&a.tokens[i]);
-    const float2 v = __ldcg(&w.seq[i]);
+  const int eb = gridDim.y;
+#pragma unroll 4
+  for (int i = tid; i < a.S * eb; i += threads) {
+    const int n_s = __ldcg(&a.tokens[i / eb]);
+    const float dot = __ldcg(&w.dots[i]);
     bal += n_s > 0 ? even_share(a, n_s) * dot : 0.0f;
+  }
+#pragma unroll 4
+  for (int i = tid; i < a.S; i += threads) {
+    const float2 v = __ldcg(&w.seq[i]);
     z += v.x;
-    n += n_s;
     bad |= __float_as_int(v.y);
+    n += __ldcg(&a.tokens[i]);
   }
   const int any_bad = __syncthreads_or(bad);
   s_a[tid] = bal;
@@ -491,7 +501,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) router_small_kernel(const Ro
 
 // NL lanes for `rows` rows, 32 / NL apart; f_se stays in registers while the sequence does.
 template <int DT, int NL, int NV>
-__global__ void __launch_bounds__(kWarps * 32) router_grad_kernel(const RouterLossArgs a,
+__global__ void __launch_bounds__(kWarps * 32, 2) router_grad_kernel(const RouterLossArgs a,
                                                                   int rows) {
   using R = Raw<DT, NL, NV>;
   using L = typename LogitType<DT>::type;
@@ -619,11 +629,10 @@ cudaError_t with_layout(const RouterLossArgs& a, F fn) {
     if (nv <= 8) return fn(Int<8>{}, Int<1>{});
     if (nv <= 16) return fn(Int<8>{}, Int<2>{});
     if (nv <= 32) return fn(Int<8>{}, Int<4>{});
-    if constexpr (DT == kF32)
-      if (nv <= 64) return fn(Int<8>{}, Int<8>{});
   }
   if (many && a.K <= 16) {
     if constexpr (DT == kF32) {
+      if (nv > 32 && nv <= 64) return fn(Int<16>{}, Int<4>{});
       if (nv > 64 && nv <= 96) return fn(Int<16>{}, Int<6>{});
       if (nv > 64 && nv <= 128) return fn(Int<16>{}, Int<8>{});
     } else {
@@ -671,10 +680,12 @@ cudaError_t launch_loss(RouterLossArgs a, cudaStream_t s) {
         launch_pdl(router_partial_kernel<DT, kNL, kNV>, dim3(chunks), dim3(kWarps * 32),
                    (kWarps + 1) * a.E * 4, s, a, w, rows);
     if (e != cudaSuccess) return e;
-    int Y = 1;  // about a thread per two slots of a sequence
+    int Y = 8;  // about a thread per two slots of a sequence; 256 threads for the last block
     while (Y < 32 && 2 * Y * a.S < chunks + a.S) Y *= 2;
-    return launch_pdl(router_combine_kernel, dim3(a.S, expert_blocks(a.E)), dim3(32, Y), 0, s, a, w,
-                      rows);
+    // a block per sequence and 32 experts while that is not more than fill the device
+    int groups = kMaxBlocks / a.S;
+    groups = groups < 1 ? 1 : groups < expert_blocks(a.E) ? groups : expert_blocks(a.E);
+    return launch_pdl(router_combine_kernel, dim3(a.S, groups), dim3(32, Y), 0, s, a, w, rows);
   });
 }
 
