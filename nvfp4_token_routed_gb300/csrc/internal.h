@@ -83,10 +83,6 @@ struct GemmArgs {
   unsigned long long* span;  // profiling: [0] min CTA start, [1] max CTA end (%globaltimer), or null
 };
 
-// moe_status of the current device (MOE_OK: compute capability 10.3), checked once
-// per device; its SM count in sms_out unless null.
-int device_status(int* sms_out);
-
 // Launch with programmatic stream serialization: the kernel may start while the
 // previous kernel of the stream finishes; it calls pdl_wait() before reading
 // anything that kernel wrote.

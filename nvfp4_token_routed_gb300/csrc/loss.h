@@ -8,6 +8,10 @@
 
 namespace moe {
 
+// moe_status of the current device (MOE_OK: compute capability 10.3), checked once per
+// device; its SM count in sms_out unless null.
+int device_status(int* sms_out);
+
 // Logits types, as moe_dtype in include/moe_nvfp4.h.
 enum LossDtype { kF32 = 0, kBf16 = 1, kF16 = 2 };
 

@@ -14,6 +14,7 @@
 
 #include "../../include/moe_nvfp4.h"
 #include "internal.h"
+#include "loss.h"
 
 using namespace moe;
 

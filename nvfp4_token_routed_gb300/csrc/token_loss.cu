@@ -17,9 +17,9 @@
 // a row is read once.
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "internal.h"
 #include "logits.cuh"
-#include "ptx.cuh"
 
 namespace moe {
 
