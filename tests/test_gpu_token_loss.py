@@ -307,6 +307,20 @@ def test_rows_do_not_depend_on_the_batch(V):
     assert all(torch.equal(x[sel], y) for x, y in zip(full, part))
 
 
+def test_largest_rows_many_to_a_cluster():
+    """fp32 rows of 2^18 logits: a block's part is more than half its ring."""
+    V, N = 262144, 70
+    z = _logits(8, V, "f32", 2).to(DEV)
+    pick = torch.randint(8, (N,), generator=torch.Generator().manual_seed(3)).to(DEV)
+    a, old, adv, ref, w = _policy_inputs(z.cpu(), 4, 1.0)
+    one = _run_policy(z.cpu(), a, old, adv, ref, w, 1.0)
+    _check_policy(one, z.cpu(), a, old, adv, ref, w, 1.0)
+    p = pick.cpu()
+    many = _run_policy(z[pick].cpu(), a[p], old[p], adv[p], ref[p], w[p], 1.0)
+    assert all(torch.equal(x, y[pick]) for x, y in zip(many, one))
+    assert torch.equal(M.token_logp(z[pick], a.to(DEV)[pick]), many[1])
+
+
 def test_offsets_beyond_32_bits():
     V, N = 262144, 8600  # 2.25e9 logits: elements and bytes pass 2^31
     z = torch.empty(N, V, dtype=torch.bfloat16, device=DEV)
