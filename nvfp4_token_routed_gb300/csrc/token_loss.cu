@@ -126,17 +126,22 @@ struct Soft {
   float m, k;  // reference
   float fold;  // log2 |coef| - k
 };
-template <int DT, bool kNegative>
+template <int DT>
 __device__ __forceinline__ Vec<DT> soft_vec(const Vec<DT>& d, const Soft& r, float c) {
   Vec<DT> g;
   const float b = DT == kF32 ? -r.k : r.fold;
   const f32x2 c2 = pack2(c, c), bias = pack2(b, b);
+  const uint32_t sign = r.coef < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
   for (int j = 0; j < Vec<DT>::kPairs; ++j) {
     const float2 x = unpack2(fma2(pack2(d.pair(j)), c2, bias));
     const float2 e = make_float2(ex2(x.x), ex2(x.y));
-    if constexpr (DT == kF32) g.set_pair(j, unpack2(mul2(pack2(r.coef, r.coef), pack2(e))));
-    else g.set_pair(j, kNegative ? make_float2(-e.x, -e.y) : e);
+    if constexpr (DT == kF32) {
+      g.set_pair(j, unpack2(mul2(pack2(r.coef, r.coef), pack2(e))));
+    } else {
+      g.set_pair(j, e);
+      g.set_word(j, g.word(j) ^ sign);
+    }
   }
   return g;
 }
@@ -164,10 +169,8 @@ __device__ __forceinline__ void with_soft(const Soft& r, float c, F fn) {
       else g.v = far_vec<DT>(d.v, r.coef, r.m, c);
       return g;
     }, std::false_type{});
-  } else if (DT == kF32 || !(r.coef < 0.0f)) {
-    fn([&](const Vec<DT>& d) { return soft_vec<DT, false>(d, r, c); }, std::true_type{});
   } else {
-    fn([&](const Vec<DT>& d) { return soft_vec<DT, true>(d, r, c); }, std::true_type{});
+    fn([&](const Vec<DT>& d) { return soft_vec<DT>(d, r, c); }, std::true_type{});
   }
 }
 __device__ __forceinline__ float soft_at(float z, const Soft& r, float c) {
@@ -725,6 +728,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
           const int base = p.v0 + from + gtid;
 #pragma unroll
           for (int u = 0; u < U; ++u) d[u] = grad_vec(d[u]);
+          if (last) release(slot, w);
           if (out.aligned && left >= U * kGroupThreads) {
 #pragma unroll
             for (int u = 0; u < U; ++u) out.vecs()[base + u * kGroupThreads] = d[u].v;
@@ -733,7 +737,6 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
             for (int u = 0; u < U; ++u)
               if (gtid + u * kGroupThreads < left) out.store(base + u * kGroupThreads, d[u]);
           }
-          if (last) release(slot, w);
         });
       });
       __syncwarp();
