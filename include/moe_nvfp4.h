@@ -372,7 +372,9 @@ moe_status moe_nvfp4_profile_spans(void* device_spans);
  *     probability and gradient 0.  NaN and +inf reach their row's loss and
  *     gradient, and no other row.
  *   - A row of a row-wise loss depends on that row alone; where every row starts
- *     on a 16-byte boundary its bits do not depend on the other rows or on N. */
+ *     on a 16-byte boundary its bits do not depend on the other rows or on N.
+ *   - Waits inside the kernels are bounded (2 s).  Should one run out, the rows it
+ *     leaves unfinished get NaN losses and log-probabilities. */
 typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
 
 /* A matrix of logits. */
