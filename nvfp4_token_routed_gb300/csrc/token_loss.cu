@@ -217,7 +217,7 @@ __device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int 
 // and the student's at those tokens.  All ids are loaded before the first logit.
 template <int DT, int NT>
 struct TeacherSlots {
-  static constexpr int U = kMaxTeacher / NT;
+  static constexpr int U = (kMaxTeacher + NT - 1) / NT;
   int id[U];
   float t[U], z[U];
   __device__ __forceinline__ void load_ids(const TokenLossArgs& a, int row, int tid) {
@@ -327,15 +327,20 @@ __device__ __forceinline__ RowResult finish_row(const TokenLossArgs& a, MaxSum v
 // ---------------------------------------------------------------- short rows
 //
 // NT threads a row, each with VPT vectors of it in registers: one warp (rows of 2 KB and
-// less, no block-wide wait), or a block of 128 or 256.  Many small blocks an SM overlap
+// less, no block-wide wait), or a block of 64 to 256.  Many small blocks an SM overlap
 // one's loads with another's reductions; a row's latency is what bounds them (16384 bf16
-// rows of 4096, policy gradient: 61 us, 0.65 of the copy rate; of 1000: 21 us, 0.47).
-// Persistent blocks with the next row in registers took 117 of them and 76 us.
+// rows of 4096, policy gradient: 60 us, 0.66 of the copy rate; of 1000: 21 us, 0.47; fp32
+// rows of 4096: 78 us, 1.0).  Persistent blocks with the next row in registers took 117 of
+// them and 76 us for the first of these.
 
 constexpr int short_rows_per_block(int NT) { return NT == 32 ? 8 : 1; }
+// Threads an SM is to hold, 64 registers each: without the bound the compiler takes up to
+// 110 (distillation of 16384 x 4096: 116 us, with it 74, with room for 1280 threads 84).
+constexpr int kShortResident = 1024;
 
 template <int DT, int MODE, int NT, int VPT>
-__global__ void __launch_bounds__(NT * short_rows_per_block(NT))
+__global__ void __launch_bounds__(NT * short_rows_per_block(NT),
+                                  kShortResident / (NT * short_rows_per_block(NT)))
     short_row_kernel(const TokenLossArgs a) {
   using L = typename LogitType<DT>::type;
   using V16 = Vec<DT>;
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(NT * short_rows_per_block(NT))
     MaxSum ms[kWarps];
     int id[kSlots];
     float q[kSlots], z[kSlots];
-    uint32_t seen[kSeenWords], again[kMaxTeacher / 32];
+    uint32_t seen[MODE == kDistill ? kSeenWords : 1], again[kMaxTeacher / 32];
     TeacherSums t;
     RowResult r;
   };
@@ -1015,10 +1020,13 @@ constexpr int kPartVecs = 5120;
 template <int DT, int MODE>
 cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
   const int nvec = a.V / Vec<DT>::kElems;  // at most so many vectors a row
+  // 16384 bf16 rows of 8192, policy gradient: 120 us here, 163 in the ring; rows of 16384
+  // 225 here, 192 there.  fp32 vectors have half the work: fewer threads with more of them
+  // (rows of 4096: 78 us by 128 threads, 96 by 256; bf16 rows of 8192 144 and 120).
   if (nvec <= 128) return launch_short<DT, MODE, 32, 4>(a, s);
-  if (nvec <= 512) return launch_short<DT, MODE, 128, 4>(a, s);
-  // 16384 bf16 rows of 8192: 110 us here, 163 in the ring; of 16384: 225 here, 192 there
-  if (nvec <= 1024) return launch_short<DT, MODE, 256, 4>(a, s);
+  constexpr bool kWide = DT == kF32;
+  if (nvec <= 512) return launch_short<DT, MODE, kWide ? 64 : 128, kWide ? 8 : 4>(a, s);
+  if (nvec <= 1024) return launch_short<DT, MODE, kWide ? 128 : 256, kWide ? 8 : 4>(a, s);
   int C = (nvec + kPartVecs - 1) / kPartVecs;
   // clusters of 6 fill 138 SMs, of 7 and 8 only 105 and 120 (4096 x 262144 bf16: 742 us
   // with 6, 890 with 8): parts of which two just fit the ring come first
