@@ -1014,6 +1014,12 @@ cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s) {
 // A block's part of a long row: two of 80 KB and less leave room to load ahead (8192 x
 // 131072 bf16, by parts of 32, 48, 64 and 85 KB: 3164, 1118, 874 and 904 us at the time).
 constexpr int kPartVecs = 5120;
+// Two of 96 KB still fit with a chunk ahead.  That is better than one block more where
+// clusters of C fill more SMs than those of C + 1 (1 to 5: 152, 152, 138, 144, 140): bf16
+// gradients of 6000 x 43000 by one block 161 us, by two 185; losses of 6000 x 98000 by two
+// 162, by three 195; 4000 x 196000 by four 217, by five 234; but 6000 x 128000 gradients by
+// three 498, by four 444.
+constexpr int kLargePartVecs = 6 * kChunkVecs;
 
 // The variant goes by the row's length alone, so that a row's bits do not depend on
 // the batch.
@@ -1028,9 +1034,10 @@ cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
   if (nvec <= 512) return launch_short<DT, MODE, kWide ? 64 : 128, kWide ? 8 : 4>(a, s);
   if (nvec <= 1024) return launch_short<DT, MODE, kWide ? 128 : 256, kWide ? 8 : 4>(a, s);
   int C = (nvec + kPartVecs - 1) / kPartVecs;
+  if ((C == 2 || C == 3 || C == 5) && nvec <= (C - 1) * kLargePartVecs) --C;
   // clusters of 6 fill 138 SMs, of 7 and 8 only 105 and 120 (4096 x 262144 bf16: 742 us
   // with 6, 890 with 8): parts of which two just fit the ring come first
-  if (C > 6) C = nvec <= 6 * kChunkVecs * 6 ? 6 : kMaxCluster;
+  if (C > 6) C = nvec <= 6 * kLargePartVecs ? 6 : kMaxCluster;
   return a.dlogits ? launch_long<DT, MODE, true>(a, C, s) : launch_long<DT, MODE, false>(a, C, s);
 }
 

@@ -158,6 +158,12 @@ def test_many_rows(V, k):
     assert not out[2][(w == 0) | (a < 0)].any()
 
 
+@pytest.mark.parametrize("V", [49152, 49153, 98304, 98311, 196608, 196616])
+def test_many_rows_of_full_parts(V):
+    """Rows whose parts are the longest that one, two and four blocks take, and a little more."""
+    test_many_rows(V, 33)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("V", [37, 1000, 50001])
 def test_masked_vocabulary_entries(V, dtype):
