@@ -117,19 +117,22 @@ struct Vec {
 
 // A softmax's running pair: a reference logit m and s = sum 2^(z c - k), where k is m c
 // rounded: one fused multiply-add gives each exponent with a single rounding, and
-// rescaling from one reference to another by 2^(k - k') is exact in k.  The reference is
+// rescaling from one reference to another by 2^(k - k') takes k as it is.  The reference is
 // the largest logit of the first ones seen; larger ones move it only when their exponent
 // passes kMaxExponent (s stays far inside fp32), so that the exponentials need not wait
-// for the maximum.  Where m c is not within fp32 (all of a set near the type's lowest
-// value, say) the exponents are (z - m) c instead.  A set without a finite logit has
-// m = -inf, s = 0; a NaN or +inf logit makes s NaN.
+// for the maximum.  What rounding takes from k stays in the exponents of the reference
+// itself: half a unit in the last place, 1/8 at most for |k| < kNearRef, but 64 at 2^31 and
+// more than fp32's range soon after, where finite masks (-1e10, -1e30, the type's lowest
+// value) may be the only logits of a set.  From kNearRef on the exponents are (z - m) c.
+// A set without a finite logit has m = -inf, s = 0; a NaN or +inf logit makes s NaN.
+constexpr float kNearRef = 4194304.0f;  // 2^22
 constexpr float kMaxExponent = 24.0f;
 struct MaxSum {
   float m, s;
 };
 __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.0f : m; }
 __device__ __forceinline__ float ref_exponent(float m, float c) { return __fmul_rn(m, c); }
-__device__ __forceinline__ bool near_ref(float k) { return fabsf(k) < 1e38f; }
+__device__ __forceinline__ bool near_ref(float k) { return fabsf(k) < kNearRef; }
 // Exponent of logit z over the finite reference m.
 __device__ __forceinline__ float exponent(float z, float m, float c) {
   const float k = ref_exponent(m, c);
@@ -139,10 +142,12 @@ __device__ __forceinline__ float exponent(float z, float m, float c) {
 __device__ __forceinline__ MaxSum one_logit(float z, float c) {
   return {z, z == -INFINITY ? 0.0f : ex2(exponent(z, z, c))};
 }
-// Exponent that takes sums over reference m to the finite reference `to`.
+// Exponent that takes sums over reference m to the finite reference `to`, each m c rounded
+// where it is near and as it is where not.
 __device__ __forceinline__ float rescale(float m, float to, float c) {
-  const float k = ref_exponent(to, c);
-  return near_ref(k) ? __fsub_rn(ref_exponent(m, c), k) : (m - to) * c;
+  const float from = ref_exponent(m, c), k = ref_exponent(to, c);
+  if (near_ref(k)) return near_ref(from) ? __fsub_rn(from, k) : fmaf(m, c, -k);
+  return near_ref(from) ? fmaf(-to, c, from) : (m - to) * c;
 }
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float c) {
   const float m = fmaxf(a.m, b.m), r = finite_ref(m);
@@ -157,7 +162,7 @@ __device__ __forceinline__ MaxSum warp_merge(MaxSum v, float c, int n) {
   for (int off = n / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
   return {m, s};
 }
-// Sum of 2^((z - m) c) over a vector, for references outside fp32 (rare: not inlined).
+// Sum of 2^((z - m) c) over a vector, for references that are not near (rare: not inlined).
 template <int DT>
 __device__ __noinline__ float far_sum(uint4 v, float m, float c) {
   const Vec<DT> d = {v};

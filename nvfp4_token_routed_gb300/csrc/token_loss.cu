@@ -166,7 +166,7 @@ __device__ __noinline__ uint4 far_vec(uint4 v, float coef, float m, float c) {
 // teacher, or no finite logit) or far.
 template <int DT, typename F>
 __device__ __forceinline__ void with_soft(const Soft& r, float c, F fn) {
-  const bool near = fabsf(r.k) < (DT == kF32 ? 1e38f : kFoldRange);
+  const bool near = DT == kF32 ? near_ref(r.k) : fabsf(r.k) < kFoldRange;
   if (r.coef == 0.0f || !near) {
     fn([&](const Vec<DT>& d) {
       Vec<DT> g;

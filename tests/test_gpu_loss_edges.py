@@ -1,0 +1,86 @@
+"""Vocabulary losses where their arithmetic leaves the ordinary range, against plain
+64-bit definitions.  Bounds as in test_gpu_token_loss.py: REL of the terms of a gradient,
+1e-5 and 2^-20 of the magnitudes for a log-probability, tau^2 times that for a divergence.
+"""
+import math
+
+import pytest
+import torch
+
+import nvfp4_token_routed_gb300 as M
+import loss_refs as R
+from test_gpu_token_loss import DEV, REL, TYPES, _check_policy, _cuda, _run_policy
+
+pytestmark = pytest.mark.gpu
+SHAPES = [37, 1000, 4096, 50001]
+
+
+def _rows(V, dtype, fill, seed):
+    """Rows with masked columns of one finite value; also the columns that may be chosen."""
+    g = torch.Generator().manual_seed(seed)
+    z = (2.0 * torch.randn(7, V, generator=g)).to(TYPES[dtype])
+    keep = torch.ones(7, V, dtype=torch.bool)
+    keep[0, [0, V - 1]] = False          # the first and last column
+    keep[1, :3 * V // 4] = False         # what the first vectors hold
+    keep[2] = False
+    keep[2, V // 2] = True               # all but one
+    keep[3] = False                      # all: uniform
+    keep[4, ::2] = False
+    keep[5, 1:V // 2] = False
+    z[~keep] = fill
+    z[6, V // 2:] = 0.5 * fill           # masked a second time, by half as much
+    keep[6, V // 2:] = False
+    pick = keep.clone()
+    pick[3] = True
+    ids = torch.multinomial(pick.float(), 4, replacement=True, generator=g)
+    return z, ids
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("dtype,fill,tau", [
+    ("f32", -1e9, 1.0), ("f32", -1e10, 1.0), ("f32", -1e20, 0.7), ("f32", -1e30, 1.0),
+    ("f32", "lowest", 5.0), ("f32", "lowest", 8.0), ("bf16", -1e9, 1.0), ("bf16", -1e10, 1.0),
+    ("bf16", -1e20, 2.0), ("bf16", -1e30, 1.0), ("bf16", "lowest", 5.0),
+    ("bf16", "lowest", 6.0), ("bf16", "lowest", 8.0), ("f16", "lowest", 0.5)])
+def test_masks_of_any_finite_value(V, dtype, fill, tau):
+    if fill == "lowest":
+        fill = torch.finfo(TYPES[dtype]).min
+    z, ids = _rows(V, dtype, fill, V)
+    g = torch.Generator().manual_seed(V + 1)
+    N = z.shape[0]
+    store = torch.zeros(N, V + 2, dtype=z.dtype, device=DEV)
+    for zc in (z.to(DEV), store[:, 1:1 + V].copy_(z)):  # rows on and off 16-byte boundaries
+        t, w = torch.randn(N, 4, generator=g), torch.rand(N, generator=g) + 0.1
+        ic, tc, wc = _cuda(ids, t, w)
+        loss, d = M.distill_loss_grad(zc, ic, tc, wc, temperature=tau)
+        want, dw, mag = R.distill(z, ids, t, None, w, tau)
+        tol = tau * tau * (1e-5 + 2.0 ** -20 * 30)
+        assert torch.all((loss.cpu().double() - want).abs() <= tol), (loss.cpu(), want)
+        R.check_grad(d, dw, mag, REL)
+        assert torch.equal(M.distill_loss(zc, ic, tc, temperature=tau), loss)
+        a = ids[:, 0].contiguous()
+        x = z.double() / tau
+        lp = torch.log_softmax(x, 1).gather(1, a[:, None])[:, 0]
+        old, adv = (lp + 0.5).float(), torch.randn(N, generator=g)
+        out = _run_policy(z, a, old, adv, None, w, tau)
+        _check_policy(out, z, a, old, adv, None, w, tau)
+        got = M.token_logp(zc, a.to(DEV), temperature=tau).cpu().double()
+        assert torch.all((got - lp).abs() <= 1e-5 + 2.0 ** -20 * (1.0 + lp.abs()))
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("at", [1.0, 2.0 ** 21, 2.0 ** 22, 2.0 ** 23, 2.0 ** 26])
+def test_logits_about_a_large_value(V, at):
+    """Rows whose logits straddle the size at which exponents are taken another way: +-at in
+    units of log2 e, less than 60 apart."""
+    g = torch.Generator().manual_seed(V)
+    step = max(0.25, at * 2.0 ** -23)
+    n = int(30 / step)
+    for sign in (1.0, -1.0):
+        z = (sign * at / 1.4426950408889634
+             + step * torch.randint(-n, n + 1, (4, V), generator=g).float())
+        a = torch.randint(V, (4,), generator=g)
+        x = z.double()
+        lp = torch.log_softmax(x, 1).gather(1, a[:, None])[:, 0]
+        old, adv, w = (lp + 0.5).float(), torch.randn(4, generator=g), torch.ones(4)
+        _check_policy(_run_policy(z, a, old, adv, None, w, 1.0), z, a, old, adv, None, w, 1.0)
