@@ -11,6 +11,7 @@
 namespace moe {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const typename LogitType<DT>::type* p) {
@@ -137,6 +138,13 @@ __device__ __forceinline__ bool near_ref(float k) { return fabsf(k) < kNearRef; 
 __device__ __forceinline__ float exponent(float z, float m, float c) {
   const float k = ref_exponent(m, c);
   return near_ref(k) ? fmaf(z, c, -k) : (z - m) * c;
+}
+// Natural logarithm of logit z's weight over the finite reference m.  A token of the type's
+// lowest value keeps a finite one of about that size: its exponent, 1.44 times as large,
+// may pass fp32 where the logarithm does not.
+__device__ __forceinline__ float log_weight(float z, float m, float c, float inv_tau) {
+  const float e = exponent(z, m, c);
+  return isinf(e) ? (z - m) * inv_tau : e * kLn2;
 }
 // One logit as a pair.
 __device__ __forceinline__ MaxSum one_logit(float z, float c) {

@@ -184,7 +184,9 @@ __device__ __forceinline__ float soft_at(float z, const Soft& r, float c) {
 
 // What a teacher's slots say without the student's normaliser, by one warp: q into
 // s_q (which holds the teacher's logits), Q = sum q, and kl, zr with
-//   sum q_i (log q_i - log p_i) = kl + Q (log s - (zr c - k) log 2).
+//   sum q_i (log q_i - log p_i) = kl + Q (log s - log weight of zr),
+// zr the largest of the student's logits at the slots; -inf: none is finite, and kl is
+// without it.
 struct TeacherSums {
   float Q, kl, zr;
 };
@@ -196,7 +198,8 @@ __device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int 
     zr = fmaxf(zr, s_z[i]);
   }
   tm = finite_ref(warp_max(tm));
-  zr = finite_ref(warp_max(zr));
+  zr = warp_max(zr);
+  const float base = finite_ref(zr);
   float ts = 0.0f;
   for (int i = lane; i < a.k; i += 32) ts += expf((s_q[i] - tm) * a.inv_tau);
   ts = warp_sum(ts);
@@ -208,7 +211,7 @@ __device__ __forceinline__ TeacherSums teacher_sums(const TokenLossArgs& a, int 
     const float q = ts == 0.0f ? 0.0f : expf(lq);
     s_q[i] = q;
     Q += q;
-    if (q != 0.0f) kl += q * (lq - (s_z[i] - zr) * a.inv_tau);
+    if (q != 0.0f) kl += q * (lq - (s_z[i] - base) * a.inv_tau);
   }
   return {warp_sum(Q), warp_sum(kl), zr};
 }
@@ -298,7 +301,6 @@ template <int MODE>
 __device__ __forceinline__ RowResult finish_row(const TokenLossArgs& a, MaxSum v, float w,
                                                 const TeacherSums& t, float z_act, float old,
                                                 float adv, float ref) {
-  constexpr float kLn2 = 0.6931471805599453f;
   const float m = finite_ref(v.m);
   RowResult r = {{0.0f, m, ref_exponent(m, a.c2), 0.0f}, 0.0f, 0.0f, 0.0f, 0.0f};
   if (v.s == 0.0f) return r;  // no finite logit
@@ -306,12 +308,15 @@ __device__ __forceinline__ RowResult finish_row(const TokenLossArgs& a, MaxSum v
   float soft = 0.0f;
   if (MODE == kDistill) {
     if (t.Q == 0.0f) return r;  // no teacher
-    r.loss = a.tau * a.tau * (t.kl + t.Q * (ln_s - exponent(t.zr, m, a.c2) * kLn2));
+    const float lw = t.zr == -INFINITY ? 0.0f : log_weight(t.zr, m, a.c2, a.inv_tau);
+    r.loss = a.tau * a.tau * (t.kl + t.Q * (ln_s - lw));
     soft = w * a.tau * t.Q;
     r.scale = w * a.tau;
   } else {
-    const float e = exponent(z_act, m, a.c2);
-    r.logp = ex2(e) >= v.s ? 0.0f : e * kLn2 - ln_s;  // a token that is the whole sum: 0
+    // a token that is the whole sum: 0
+    r.logp = ex2(exponent(z_act, m, a.c2)) >= v.s
+                 ? 0.0f
+                 : log_weight(z_act, m, a.c2, a.inv_tau) - ln_s;
     float slope = 0.0f;
     if (a.adv) r.loss = policy_row(a, r.logp, old, adv, ref, &slope);
     r.top = w * slope * a.inv_tau;

@@ -84,3 +84,30 @@ def test_logits_about_a_large_value(V, at):
         lp = torch.log_softmax(x, 1).gather(1, a[:, None])[:, 0]
         old, adv, w = (lp + 0.5).float(), torch.randn(4, generator=g), torch.ones(4)
         _check_policy(_run_policy(z, a, old, adv, None, w, 1.0), z, a, old, adv, None, w, 1.0)
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("tau", [1.0, 3.0])
+def test_tokens_of_the_lowest_value(V, dtype, tau):
+    """A chosen token, or all of a teacher's, at the type's lowest logit: a finite
+    log-probability of about that size, no gradient from the row's other tokens lost."""
+    g = torch.Generator().manual_seed(V)
+    lowest = torch.finfo(TYPES[dtype]).min
+    z = torch.randn(3, V, generator=g).to(TYPES[dtype])
+    z[:, [0, V // 2, V - 1]] = lowest
+    z[2] = -math.inf               # nothing but a token of the lowest value: probability 1
+    z[2, V // 2] = lowest
+    a = torch.tensor([0, V - 1, V // 2])
+    x = z.double() / tau
+    lp = torch.log_softmax(x, 1).gather(1, a[:, None])[:, 0]
+    got = M.token_logp(z.to(DEV), a.to(DEV), temperature=tau).cpu().double()
+    assert torch.allclose(got, lp, rtol=1e-5, atol=2e-5), (got, lp)
+    ids = torch.tensor([[0, V // 2], [V - 1, V - 1], [V // 2, V // 2]])
+    t = torch.randn(3, 2, generator=g)
+    # half the mass, so that the loss stays within fp32 (tau^2 Q (3.4e38 / tau))
+    lse = torch.logsumexp(t / tau, 1) + math.log(8.0)
+    loss, d = M.distill_loss_grad(*_cuda(z, ids, t), teacher_lse=lse.to(DEV), temperature=tau)
+    want, dw, mag = R.distill(z, ids, t, lse, None, tau)
+    assert torch.allclose(loss.cpu().double(), want, rtol=1e-5, atol=tau * tau * 4e-5), (loss, want)
+    R.check_grad(d, dw, mag, REL)
