@@ -51,7 +51,8 @@ __device__ __forceinline__ bool row_live(const TokenLossArgs& a, int row) {
 __device__ __forceinline__ float policy_row(const TokenLossArgs& a, float lp, float old, float A,
                                             float ref, float* slope) {
   const float ratio = expf(lp - old);
-  const float rA = ratio * A;
+  // a ratio beyond fp32 times no advantage is nothing; a NaN ratio stays one
+  const float rA = A == 0.0f && ratio > a.clip_hi ? 0.0f : ratio * A;
   const float cA = fminf(fmaxf(ratio, a.clip_lo), a.clip_hi) * A;
   // the comparison is false for a NaN ratio, which then reaches the loss
   float loss = -(cA < rA ? cA : rA);

@@ -111,3 +111,27 @@ def test_tokens_of_the_lowest_value(V, dtype, tau):
     want, dw, mag = R.distill(z, ids, t, lse, None, tau)
     assert torch.allclose(loss.cpu().double(), want, rtol=1e-5, atol=tau * tau * 4e-5), (loss, want)
     R.check_grad(d, dw, mag, REL)
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_zero_advantage_with_a_ratio_beyond_fp32(V, dtype):
+    """A row without an advantage costs nothing, however far its policy has moved; a NaN
+    in its logits still reaches it."""
+    z = torch.randn(5, V, generator=torch.Generator().manual_seed(V)).to(TYPES[dtype])
+    a = torch.zeros(5, dtype=torch.int64)
+    lp = z.double()[:, 0] - torch.logsumexp(z.double(), 1)
+    old, adv = (lp - 100.0).float(), torch.tensor([0.0, -0.0, 1.0, 0.0, 0.0])
+    ref = (lp + 0.3).float()
+    z[4, V - 1] = math.nan
+    zc, ac, oc, vc, rc = _cuda(z, a, old, adv, ref)
+    for r, beta in ((None, 0.0), (rc, 0.1)):
+        loss, _, d = M.policy_loss_grad(zc, ac, oc, vc, ref_logp=r, clip_low=0.2, clip_high=0.28,
+                                        kl_coef=beta)
+        want, _, dw, mag = R.policy(z[:4], a[:4], old[:4], adv[:4], None if r is None else ref[:4],
+                                    None, 0.2, 0.28, beta, 1.0)
+        assert torch.all((loss[:4].cpu().double() - want).abs() <= 2e-5), loss
+        R.check_grad(d[:4], dw, mag, 2 * REL)
+        assert torch.isnan(loss[4]) and torch.isnan(d[4].float()).any()
+        only = M.policy_loss(zc, ac, oc, vc, ref_logp=r, clip_low=0.2, clip_high=0.28, kl_coef=beta)
+        assert torch.equal(only[0][:4], loss[:4])
