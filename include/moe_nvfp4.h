@@ -397,7 +397,7 @@ moe_status moe_nvfp4_token_logp(const moe_logits* z, const void* actions, int32_
 typedef struct {
   float clip_low;    /* the ratio is clipped to [1 - clip_low, 1 + clip_high], */
   float clip_high;   /* 0 <= clip_low <= 1, clip_high >= 0                      */
-  float kl_coef;     /* b; not 0 needs ref_logp */
+  float kl_coef;     /* b; not 0 needs ref_logp, 0 does not look at it */
   float temperature; /* of the softmax, > 0 */
 } moe_policy_opts;
 

@@ -95,7 +95,7 @@ moe_status policy_impl(const moe_logits* z, const void* actions, int32_t ids_int
   a.ids64 = ids_int64;
   a.old_logp = old_logp;
   a.adv = adv;
-  a.ref_logp = ref_logp;
+  a.ref_logp = o->kl_coef != 0.0f ? ref_logp : nullptr;  // a term switched off is not 0 * inf
   a.clip_lo = 1.0f - o->clip_low;
   a.clip_hi = 1.0f + o->clip_high;
   a.kl_coef = o->kl_coef;

@@ -135,3 +135,23 @@ def test_zero_advantage_with_a_ratio_beyond_fp32(V, dtype):
         assert torch.isnan(loss[4]) and torch.isnan(d[4].float()).any()
         only = M.policy_loss(zc, ac, oc, vc, ref_logp=r, clip_low=0.2, clip_high=0.28, kl_coef=beta)
         assert torch.equal(only[0][:4], loss[:4])
+
+
+@pytest.mark.parametrize("V", SHAPES)
+def test_a_kl_term_switched_off_adds_nothing(V):
+    """kl_coef 0 with a reference at hand: as without one, whatever the reference holds."""
+    z = torch.randn(5, V, generator=torch.Generator().manual_seed(V))
+    a = torch.zeros(5, dtype=torch.int64)
+    z[0, 0] = -math.inf                   # a chosen token that is masked
+    lp = z.double()[:, 0] - torch.logsumexp(z.double(), 1)
+    old = torch.where(torch.isfinite(lp), lp, -3.0).float()
+    ref = (lp + torch.tensor([0.0, 100.0, -1e30, math.inf, math.nan])).float()
+    ref[0] = -3.0
+    zc, ac, oc, rc = _cuda(z, a, old, ref)
+    adv = torch.ones(5, device=DEV)
+    plain = M.policy_loss_grad(zc, ac, oc, adv)
+    off = M.policy_loss_grad(zc, ac, oc, adv, ref_logp=rc, kl_coef=0.0)
+    assert torch.isfinite(plain[0]).all() and torch.isfinite(plain[2]).all()
+    assert all(torch.equal(x, y) for x, y in zip(plain, off)), (plain, off)
+    assert all(torch.equal(x, y) for x, y in zip(
+        M.policy_loss(zc, ac, oc, adv, ref_logp=rc), M.policy_loss(zc, ac, oc, adv)))
