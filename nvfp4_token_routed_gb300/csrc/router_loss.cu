@@ -341,7 +341,8 @@ __device__ __forceinline__ void write_losses(const RouterLossArgs& a, const Ws& 
                                              float z, int n, int bad) {
   const float per = n > 0 ? 1.0f / (float)n : 0.0f;
   a.losses[0] = n > 0 ? a.balance_coef * bal * per : 0.0f;
-  a.losses[1] = n > 0 ? a.z_coef * z * per : 0.0f;
+  // a row of the lowest logits has a square beyond fp32: not 0 * inf where the term is off
+  a.losses[1] = n > 0 && !(a.z_coef == 0.0f && isinf(z)) ? a.z_coef * z * per : 0.0f;
   a.tokens[a.S] = n;
   *w.status = bad ? kFlagBadExpertId : 0;
 }
