@@ -150,12 +150,18 @@ __device__ __forceinline__ float log_weight(float z, float m, float c, float inv
 __device__ __forceinline__ MaxSum one_logit(float z, float c) {
   return {z, z == -INFINITY ? 0.0f : ex2(exponent(z, z, c))};
 }
-// Exponent that takes sums over reference m to the finite reference `to`, each m c rounded
-// where it is near and as it is where not.
-__device__ __forceinline__ float rescale(float m, float to, float c) {
+// Exponent that takes sums over reference m to the finite reference `to`, not below m, each
+// m c rounded where it is near and as it is where not.
+static __device__ __noinline__ float far_rescale(float m, float to, float c) {
   const float from = ref_exponent(m, c), k = ref_exponent(to, c);
   if (near_ref(k)) return near_ref(from) ? __fsub_rn(from, k) : fmaf(m, c, -k);
   return near_ref(from) ? fmaf(-to, c, from) : (m - to) * c;
+}
+__device__ __forceinline__ float rescale(float m, float to, float c) {
+  const float k = ref_exponent(to, c);
+  // here a reference that is not near lies so far below that nothing is left of its sums
+  if (fabsf(k) < kNearRef - 512.0f) return __fsub_rn(ref_exponent(m, c), k);
+  return far_rescale(m, to, c);
 }
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float c) {
   const float m = fmaxf(a.m, b.m), r = finite_ref(m);
