@@ -374,7 +374,8 @@ moe_status moe_nvfp4_profile_spans(void* device_spans);
  *   - A row of a row-wise loss depends on that row alone; where every row starts
  *     on a 16-byte boundary its bits do not depend on the other rows or on N.
  *   - Waits inside the kernels are bounded (2 s).  Should one run out, the rows it
- *     leaves unfinished get NaN losses and log-probabilities. */
+ *     leaves unfinished, loss or gradient, get NaN losses and log-probabilities, and
+ *     so may finished ones after them. */
 typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
 
 /* A matrix of logits. */
@@ -422,6 +423,19 @@ moe_status moe_nvfp4_policy_loss_grad(const moe_logits* z, const void* actions,
                                       const float* ref_logp, const float* row_weight,
                                       const moe_policy_opts* opts, float* row_loss, float* logp,
                                       void* dlogits, int64_t ld_grad, moe_stream_t stream);
+
+/* Test hook of those bounded waits: moe_nvfp4_policy_loss_grad (clipping 0.2, no KL
+ * term, temperature 1) of bf16 rows longer than 16 KB by four groups of blocks that
+ * take every fourth row.  In the first group, from `row` on, the given role of the
+ * block of rank `rank` leaves: 0 the consumers between the row's sum and its
+ * gradient, 1 the producer, 2 a row's gather warp before the gradient's few entries,
+ * 3 the finish warps.  Waits run out (about 2 s), rows row, row + 4, ... (row a
+ * multiple of 4) get NaN, every other row its results, and the context stays usable. */
+moe_status moe_nvfp4_selftest_loss_timeout(const moe_logits* z, const void* actions,
+                                           int32_t ids_int64, const float* old_logp,
+                                           const float* adv, int32_t role, int32_t rank,
+                                           int32_t row, float* row_loss, float* logp,
+                                           void* dlogits, int64_t ld_grad, moe_stream_t stream);
 
 /* A teacher's top logits: K slots per row. */
 typedef struct {

@@ -129,6 +129,8 @@ def lib():
         L.moe_nvfp4_policy_loss.argtypes = [zp, vp, i32, vp, vp, vp, po, vp, vp, vp]
         L.moe_nvfp4_policy_loss_grad.argtypes = [zp, vp, i32, vp, vp, vp, vp, po, vp, vp, vp, i64,
                                                  vp]
+        L.moe_nvfp4_selftest_loss_timeout.argtypes = [zp, vp, i32, vp, vp, i32, i32, i32, vp, vp,
+                                                      vp, i64, vp]
         L.moe_nvfp4_distill_loss.argtypes = [zp, tp, f32, vp, vp]
         L.moe_nvfp4_distill_loss_grad.argtypes = [zp, tp, vp, f32, vp, vp, i64, vp]
         L.moe_nvfp4_router_loss_workspace_bytes.restype = sz
@@ -136,6 +138,7 @@ def lib():
         L.moe_nvfp4_router_loss.argtypes = [rb, vp, vp, vp, vp, sz, vp]
         L.moe_nvfp4_router_loss_grad.argtypes = [rb, vp, vp, vp, vp, vp, vp, i64, vp]
         for f in ["moe_nvfp4_token_logp", "moe_nvfp4_policy_loss", "moe_nvfp4_policy_loss_grad",
+                  "moe_nvfp4_selftest_loss_timeout",
                   "moe_nvfp4_distill_loss", "moe_nvfp4_distill_loss_grad",
                   "moe_nvfp4_router_loss", "moe_nvfp4_router_loss_grad",
                   "moe_nvfp4_selftest_wait_timeout",
@@ -616,6 +619,18 @@ def policy_loss_grad(logits, actions, old_logp, advantages, row_weight=None, ref
                                             row_loss.data_ptr(), logp.data_ptr(),
                                             dlogits.data_ptr(), ld, _raw(stream)),
            "moe_nvfp4_policy_loss_grad")
+    return row_loss, logp, dlogits
+
+
+def moe_nvfp4_selftest_loss_timeout(logits, actions, old_logp, advantages, role, rank, row):
+    """policy_loss_grad by a kernel in which one role leaves (include/moe_nvfp4.h):
+    (row_loss, logp, dlogits)."""
+    args = _policy_args(logits, actions, old_logp, advantages, None)[:5]
+    row_loss, logp = torch.empty_like(old_logp), torch.empty_like(old_logp)
+    dlogits, ld = _dlogits(None, logits, None)
+    _check(lib().moe_nvfp4_selftest_loss_timeout(*args, role, rank, row, row_loss.data_ptr(),
+                                                 logp.data_ptr(), dlogits.data_ptr(), ld,
+                                                 _raw(None)), "moe_nvfp4_selftest_loss_timeout")
     return row_loss, logp, dlogits
 
 

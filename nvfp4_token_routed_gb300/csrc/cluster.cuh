@@ -1,6 +1,6 @@
 // cluster.cuh -- inline-PTX wrappers for thread-block clusters: ranks, the cluster
-// barrier, mbarriers that other blocks of the cluster complete, and stores into their
-// shared memory.
+// barrier, mbarriers that other blocks of the cluster complete, and stores and minima into
+// their shared memory.
 #pragma once
 #include "ptx.cuh"
 
@@ -57,6 +57,13 @@ __device__ __forceinline__ void st_async_f32x2(uint32_t dst, uint32_t bar, uint3
           rdst),
       "f"(a), "f"(b), "r"(rbar)
       : "memory");
+}
+// Lower the int at this CTA's shared address `dst` in the CTA of rank `cta` to v.
+__device__ __forceinline__ void red_min_cluster(uint32_t dst, uint32_t cta, int v) {
+  uint32_t rdst;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rdst) : "r"(dst), "r"(cta));
+  asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(rdst), "r"(v)
+               : "memory");
 }
 
 }  // namespace moe

@@ -47,7 +47,19 @@ struct TokenLossArgs {
   const float* t_lse;       // [N] log-sum-exp of the teacher's whole row over tau, or null
 };
 
+// Roles of the long rows' kernel that its self-test makes leave.
+enum LongRole { kConsumers = 0, kProducer = 1, kGather = 2, kFinish = 3 };
+struct LeaveArgs {
+  int role, rank, row;  // from this row of cluster 0 on, in the block of this rank
+};
+
 cudaError_t launch_token_loss(const TokenLossArgs& a, int mode, int dtype, cudaStream_t s);
+// Blocks a row of V logits is divided among; 0: a short row.
+int token_loss_cluster(int V, int dtype);
+// The policy gradient of long bf16 rows by kLeaveClusters clusters, a role of which leaves.
+constexpr int kLeaveClusters = 4;
+cudaError_t launch_token_loss_leave(const TokenLossArgs& a, const LeaveArgs& leave,
+                                    cudaStream_t s);
 
 struct RouterLossArgs {
   int T, E, K, S;

@@ -76,7 +76,7 @@ moe_status policy_impl(const moe_logits* z, const void* actions, int32_t ids_int
                        const float* old_logp, const float* adv, const float* ref_logp,
                        const moe_policy_opts* o, const float* row_weight, float* row_loss,
                        float* logp, void* dlogits, int64_t ld_grad, bool grad,
-                       moe_stream_t stream) {
+                       moe_stream_t stream, const LeaveArgs* leave = nullptr) {
   moe_status st = check_logits(z, kMaxVocab);
   if (st != MOE_OK) return st;
   if (!o || !bool_ok(ids_int64) || !(o->clip_low >= 0.0f && o->clip_low <= 1.0f) ||
@@ -101,6 +101,13 @@ moe_status policy_impl(const moe_logits* z, const void* actions, int32_t ids_int
   a.kl_coef = o->kl_coef;
   a.row_loss = row_loss;
   a.logp = logp;
+  if (leave) {
+    const int C = token_loss_cluster(z->cols, kBf16);
+    if (z->dtype != MOE_DTYPE_BF16 || C == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (leave->rank >= C) return MOE_ERR_INVALID_ARG;
+    if ((st = (moe_status)device_status(nullptr)) != MOE_OK) return st;
+    return cuda_status(launch_token_loss_leave(a, *leave, reinterpret_cast<cudaStream_t>(stream)));
+  }
   return run(a, kPolicy, z->dtype, stream);
 }
 
@@ -212,6 +219,18 @@ moe_status moe_nvfp4_distill_loss_grad(const moe_logits* z, const moe_teacher* t
                                        moe_stream_t stream) {
   return distill_impl(z, teacher, row_weight, temperature, row_loss, dlogits, ld_grad, true,
                       stream);
+}
+
+moe_status moe_nvfp4_selftest_loss_timeout(const moe_logits* z, const void* actions,
+                                           int32_t ids_int64, const float* old_logp,
+                                           const float* adv, int32_t role, int32_t rank,
+                                           int32_t row, float* row_loss, float* logp,
+                                           void* dlogits, int64_t ld_grad, moe_stream_t stream) {
+  const moe_policy_opts o = {0.2f, 0.2f, 0.0f, 1.0f};
+  const LeaveArgs leave = {role, rank, row};
+  if (role < kConsumers || role > kFinish || rank < 0 || row < 0) return MOE_ERR_INVALID_ARG;
+  return policy_impl(z, actions, ids_int64, old_logp, adv, nullptr, &o, nullptr, row_loss, logp,
+                     dlogits, ld_grad, true, stream, &leave);
 }
 
 size_t moe_nvfp4_router_loss_workspace_bytes(int32_t T, int32_t E, int32_t S) {

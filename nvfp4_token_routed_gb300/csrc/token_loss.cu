@@ -20,6 +20,7 @@
 // 12000 x 32000 f16 logits in 113 us (1.0).  The bound beside memory is instruction issue:
 // at two exponentials a bf16 logit and 4 bytes, a reading and a writing leave about 22
 // lane instructions a logit, and the kernel takes 12.
+#include <climits>
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -504,7 +505,9 @@ __global__ void __launch_bounds__(NT * short_rows_per_block(NT),
 // third group left 16 KB and took 877 us, but helps where there is no gradient (12000 x
 // 32000: 138 us with two, 109 with three).  Rows that are
 // left out pass through no ring slot and no barrier.  All waits are bounded; a role
-// whose wait runs out leaves, and the rows not finished get NaN losses.
+// whose wait runs out leaves, and soon the others do.  Each tells rank 0 the row it gave up;
+// from the first of these on, a row may lack its gradient in any block, whatever its loss:
+// at the end the cluster's rows from there on get NaN losses and log-probabilities.
 
 constexpr int kGroupWarps = 8;
 constexpr int kGroupThreads = kGroupWarps * 32;
@@ -550,7 +553,8 @@ struct LongShared {
   uint64_t sums[kGroups], go[kGroups], xch[kExchanges];
   uint64_t ready[kSlots];  // gathered
   uint64_t over[kSlots];   // read for the last time: pass 2 done, or without one the loss
-  volatile int failed;     // the producer's wait ran out
+  volatile int unloaded;    // the first row that the producer gave up
+  volatile int unfinished;  // rank 0's: the first row of the cluster that a role gave up
 };
 
 // The rows of one cluster in order, 32 at a time: which of them count.
@@ -590,8 +594,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity));
 }
 
-template <int DT, int MODE, bool kGrad>
-__global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const TokenLossArgs a) {
+// kTest: a role of cluster 0 leaves as if a wait had run out.
+template <int DT, int MODE, bool kGrad, bool kTest>
+__global__ void __launch_bounds__(long_threads(kGrad), 1)
+    long_row_kernel(const TokenLossArgs a, const LeaveArgs leave) {
   using L = typename LogitType<DT>::type;
   using V16 = Vec<DT>;
   constexpr int kGroups = groups_of(kGrad), kSlots = slots_of(kGrad);
@@ -614,7 +620,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       mbar_init(smem_u32(&sh.ready[i]), 1);
       mbar_init(smem_u32(&sh.over[i]), kGrad ? kGroupWarps : 1);
     }
-    sh.failed = 0;
+    sh.unloaded = sh.unfinished = INT_MAX;
     fence_barrier_init();
   }
   __syncthreads();
@@ -646,6 +652,11 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
     return p;
   };
   common = part_of(first);
+  int done = INT_MAX;  // rows that this warp's role has finished, where a wait runs out
+  auto leaves = [&](int role, int it) {
+    return kTest && first == 0 && rank == leave.rank && role == leave.role &&
+           it * step >= leave.row;
+  };
 
   if (warp < kConsumerWarps) {
     constexpr int kPer = kChunkVecs / kGroupThreads;  // vectors of a chunk a thread has
@@ -701,7 +712,8 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       const uint32_t same = __shfl_sync(0xFFFFFFFFu, w, 0);
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]) + (same ^ w));
     };
-    for (int it = 0; it < rows; ++it) {
+    int it = 0;
+    for (; it < rows; ++it) {
       const int row = first + it * step;
       const bool live = walk.live(a, it);
       const Part p = part_of(row);
@@ -740,7 +752,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         mbar_arrive(smem_u32(&sh.sums[g]));
       }
 
-      if (!warp_wait(&sh.go[g], ph)) break;
+      if (leaves(kConsumers, it) || !warp_wait(&sh.go[g], ph)) break;
       if constexpr (!kGrad) continue;
       const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
       with_soft<DT>(sh.slot[l % kSlots].soft, a.c2, [&](auto grad_vec, auto whole) {
@@ -765,18 +777,20 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.over[l % kSlots]));
     }
+    done = it;
   } else if (warp == kConsumerWarps) {  // producer
     RingPos pos;
     uint32_t lv = 0;
     bool ok = true;
-    for (int it = 0; it < rows && ok; ++it) {
+    int it = 0;
+    for (; it < rows; ++it) {
       const int row = first + it * step;
       if (!walk.live(a, it)) continue;
       const Part p = part_of(row);
       const uint4* src = reinterpret_cast<const uint4*>(logits_of(row) + p.sp.head) + p.v0;
       uint64_t* full = &sh.full[lv % kPartsAhead];
       for (int left = p.nv; left > 0; left -= kChunkVecs, pos.next()) {
-        ok = warp_wait(&sh.empty[pos.slot], pos.phase ^ 1);
+        ok = !leaves(kProducer, it) && warp_wait(&sh.empty[pos.slot], pos.phase ^ 1);
         if (!ok) break;
         if (lane == 0) {
           const uint32_t bytes = 16u * min(kChunkVecs, left);
@@ -788,14 +802,15 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         }
         __syncwarp();
       }
-      if (ok && p.nv == 0 && lane == 0) mbar_arrive(smem_u32(full));
-      if (ok) ++lv;
-      else break;
+      if (!ok) break;
+      if (p.nv == 0 && lane == 0) mbar_arrive(smem_u32(full));
+      ++lv;
     }
     // no copy may be in flight when the block ends: a part that a wait cut short completes
     // with the chunks it has, and its row is not valid
+    done = it;
     if (!ok && lane == 0) {
-      sh.failed = 1;
+      sh.unloaded = it;
       __threadfence_block();
       mbar_arrive(smem_u32(&sh.full[lv % kPartsAhead]));
     }
@@ -845,7 +860,10 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       const int i = l % kSlots;
       const uint32_t ph = (l / kSlots) & 1;
       Slot<MODE, kGrad>& s = sh.slot[i];
-      if (!kGrad && !warp_wait(&sh.over[i], ph ^ 1)) break;
+      if (!kGrad && !warp_wait(&sh.over[i], ph ^ 1)) {
+        done = (row - first) / step;
+        break;
+      }
       if constexpr (MODE == kDistill) {
         few.write(a.k, lane, kGrad ? s.id : nullptr, s.q, s.z);
         __syncwarp();
@@ -864,7 +882,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       if (lane < kMaxEdge) s.edge[lane] = x_edge;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.ready[i]));
-      const int done = row;
+      const int last = row;
       row = next_row();
       auto name = [&] {
         if (MODE == kDistill && kGrad) name_repeats(a.k, lane, s.id, s.seen, s.again);
@@ -872,10 +890,13 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       if (row >= 0) fetch(row, name);
       else name();
       if constexpr (kGrad) {
-        if (!warp_wait(&sh.over[i], ph)) break;  // pass 2 is done
+        if (leaves(kGather, (last - first) / step) || !warp_wait(&sh.over[i], ph)) {
+          done = (last - first) / step;
+          break;
+        }
         const Soft soft = s.soft;
-        const Part p = part_of(done);
-        L* dz = grad_of(done);
+        const Part p = part_of(last);  // whose pass 2 is done
+        L* dz = grad_of(last);
         if (rank == 0 && lane < p.sp.head + p.sp.tail)
           store_logit<DT>(dz + edge_column(p.sp, a.V, lane), soft_at(s.edge[lane], soft, a.c2));
         __syncwarp();
@@ -903,9 +924,8 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
   } else {  // finish
     const int b = warp - (kConsumerWarps + 1 + kGatherWarps);  // its group
     uint32_t lv = 0;
-    bool ok = true;
     int it = 0;
-    for (; it < rows && ok; ++it) {
+    for (; it < rows; ++it) {
       const int row = first + it * step;
       if (!walk.live(a, it)) {
         if (rank == 0 && it % kGroups == b) {
@@ -926,9 +946,9 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       const int i = l % kSlots, x = l % sh.kExchanges;
       Slot<MODE, kGrad>& s = sh.slot[i];
       const Part p = part_of(row);
-      ok = warp_wait(&sh.ready[i], (l / kSlots) & 1) &&
-           warp_wait(&sh.sums[b], (l / kGroups) & 1) && !sh.failed;
-      if (!ok) break;
+      if (leaves(kFinish, it) || !warp_wait(&sh.ready[i], (l / kSlots) & 1) ||
+          !warp_wait(&sh.sums[b], (l / kGroups) & 1) || it >= sh.unloaded)
+        break;
       // the consumer warps' pairs, and rank 0's edges
       MaxSum v = lane < kGroupWarps ? sh.ms[b][lane] : MaxSum{-INFINITY, 0.0f};
       if (rank == 0 && lane < p.sp.head + p.sp.tail)
@@ -939,9 +959,9 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
         __syncwarp();
         if (lane < C)
           st_async_f32x2(smem_u32(&sh.cl[x][rank]), smem_u32(&sh.xch[x]), lane, v.m, v.s);
-        ok = __all_sync(0xFFFFFFFFu,
-                        mbar_wait_cluster(smem_u32(&sh.xch[x]), (l / sh.kExchanges) & 1));
-        if (!ok) break;
+        if (!__all_sync(0xFFFFFFFFu,
+                        mbar_wait_cluster(smem_u32(&sh.xch[x]), (l / sh.kExchanges) & 1)))
+          break;
         v = lane < C ? sh.cl[x][lane] : MaxSum{-INFINITY, 0.0f};
         v = warp_merge(v, a.c2, kMaxCluster);
       }
@@ -964,15 +984,17 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1) long_row_kernel(const 
       }
       __syncwarp();
     }
-    if (!ok && rank == 0)  // a wait ran out: this row and the rest are not valid
-      for (int i = it + lane; i < rows; i += 32) {
-        if (a.row_loss) a.row_loss[first + i * step] = NAN;
-        if (a.logp) a.logp[first + i * step] = NAN;
-      }
+    done = it;
   }
+  if (done < rows && lane == 0) red_min_cluster(smem_u32((const void*)&sh.unfinished), 0, done);
   __syncwarp();
   cluster_arrive();  // no block leaves while another may still write to it
   cluster_wait();
+  if (rank == 0 && sh.unfinished < rows)
+    for (int it = sh.unfinished + tid; it < rows; it += long_threads(kGrad)) {
+      if (a.row_loss) a.row_loss[first + it * step] = NAN;
+      if (a.logp) a.logp[first + it * step] = NAN;
+    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -984,9 +1006,9 @@ cudaError_t launch_short(const TokenLossArgs& a, cudaStream_t s) {
                     dim3(NT * kRows), 0, s, a);
 }
 
-template <int DT, int MODE, bool kGrad>
-cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s) {
-  auto kernel = long_row_kernel<DT, MODE, kGrad>;
+template <int DT, int MODE, bool kGrad, bool kTest = false>
+cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s, LeaveArgs leave = {}) {
+  auto kernel = long_row_kernel<DT, MODE, kGrad, kTest>;
   static std::atomic<uint64_t> limit_set{0};
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kRingBytes, limit_set);
   if (e != cudaSuccess) return e;
@@ -1013,8 +1035,9 @@ cudaError_t launch_long(const TokenLossArgs& a, int C, cudaStream_t s) {
     if (n < 1) return cudaErrorLaunchOutOfResources;
     resident[dev & 63][C].store(n, std::memory_order_relaxed);
   }
+  if (kTest && n > kLeaveClusters) n = kLeaveClusters;
   cfg.gridDim = dim3((unsigned)(a.N < n ? a.N : n) * C);
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a, leave);
 }
 
 // A block's part of a long row: two of 80 KB and less leave room to load ahead (8192 x
@@ -1027,6 +1050,17 @@ constexpr int kPartVecs = 5120;
 // three 498, by four 444.
 constexpr int kLargePartVecs = 6 * kChunkVecs;
 
+// Blocks of a long row of nvec vectors.
+int cluster_of(int nvec) {
+  int C = (nvec + kPartVecs - 1) / kPartVecs;
+  if ((C == 2 || C == 3 || C == 5) && nvec <= (C - 1) * kLargePartVecs) --C;
+  // clusters of 6 fill 138 SMs, of 7 and 8 only 105 and 120 (4096 x 262144 bf16: 742 us
+  // with 6, 890 with 8): parts of which two just fit the ring come first
+  if (C > 6) C = nvec <= 6 * kLargePartVecs ? 6 : kMaxCluster;
+  return C;
+}
+constexpr int kShortVecs = 1024;
+
 // The variant goes by the row's length alone, so that a row's bits do not depend on
 // the batch.
 template <int DT, int MODE>
@@ -1038,12 +1072,8 @@ cudaError_t launch_mode(const TokenLossArgs& a, cudaStream_t s) {
   if (nvec <= 128) return launch_short<DT, MODE, 32, 4>(a, s);
   constexpr bool kWide = DT == kF32;
   if (nvec <= 512) return launch_short<DT, MODE, kWide ? 64 : 128, kWide ? 8 : 4>(a, s);
-  if (nvec <= 1024) return launch_short<DT, MODE, kWide ? 128 : 256, kWide ? 8 : 4>(a, s);
-  int C = (nvec + kPartVecs - 1) / kPartVecs;
-  if ((C == 2 || C == 3 || C == 5) && nvec <= (C - 1) * kLargePartVecs) --C;
-  // clusters of 6 fill 138 SMs, of 7 and 8 only 105 and 120 (4096 x 262144 bf16: 742 us
-  // with 6, 890 with 8): parts of which two just fit the ring come first
-  if (C > 6) C = nvec <= 6 * kLargePartVecs ? 6 : kMaxCluster;
+  if (nvec <= kShortVecs) return launch_short<DT, MODE, kWide ? 128 : 256, kWide ? 8 : 4>(a, s);
+  const int C = cluster_of(nvec);
   return a.dlogits ? launch_long<DT, MODE, true>(a, C, s) : launch_long<DT, MODE, false>(a, C, s);
 }
 
@@ -1058,6 +1088,16 @@ cudaError_t launch_token_loss(const TokenLossArgs& a, int mode, int dtype, cudaS
   if (dtype == kF32) return launch_dtype<kF32>(a, mode, s);
   if (dtype == kBf16) return launch_dtype<kBf16>(a, mode, s);
   return launch_dtype<kF16>(a, mode, s);
+}
+
+int token_loss_cluster(int V, int dtype) {
+  const int nvec = V / (dtype == kF32 ? Vec<kF32>::kElems : Vec<kBf16>::kElems);
+  return nvec <= kShortVecs ? 0 : cluster_of(nvec);
+}
+
+cudaError_t launch_token_loss_leave(const TokenLossArgs& a, const LeaveArgs& leave,
+                                    cudaStream_t s) {
+  return launch_long<kBf16, kPolicy, true, true>(a, token_loss_cluster(a.V, kBf16), s, leave);
 }
 
 }  // namespace moe
