@@ -9,7 +9,8 @@ import torch
 
 import nvfp4_token_routed_gb300 as M
 import loss_refs as R
-from test_gpu_token_loss import DEV, REL, TYPES, _check_policy, _cuda, _run_policy
+from test_gpu_token_loss import (DEV, REL, TYPES, _check_policy, _cuda, _policy_inputs,
+                                 _run_policy)
 
 pytestmark = pytest.mark.gpu
 SHAPES = [37, 1000, 4096, 50001]
@@ -155,3 +156,36 @@ def test_a_kl_term_switched_off_adds_nothing(V):
     assert all(torch.equal(x, y) for x, y in zip(plain, off)), (plain, off)
     assert all(torch.equal(x, y) for x, y in zip(
         M.policy_loss(zc, ac, oc, adv, ref_logp=rc), M.policy_loss(zc, ac, oc, adv)))
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("weight", [1.0, 2.0 ** -9])
+def test_gradients_about_the_limit_of_the_folded_factor(V, dtype, weight):
+    """16-bit gradients whose reference exponent is about 256 in size, on either side of it:
+    temperature 0.1, logits about 17.75."""
+    g = torch.Generator().manual_seed(V)
+    z = 2.0 * torch.randn(6, V, generator=g)
+    for i, top in enumerate((17.5, 17.75, 18.0)):
+        z[i, torch.randint(V, (9,), generator=g)] = top
+        z[i + 3] = -top + 0.125 * torch.randint(-3, 4, (V,), generator=g).float()
+    z = z.to(TYPES[dtype])
+    a = z.float().argmax(1)
+    x = z.double() / 0.1
+    lp = torch.log_softmax(x, 1).gather(1, a[:, None])[:, 0]
+    old, adv = (lp + 0.5).float(), torch.randn(6, generator=g)
+    w = torch.full((6,), weight)
+    _check_policy(_run_policy(z, a, old, adv, None, w, 0.1), z, a, old, adv, None, w, 0.1)
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_policy_loss_without_a_gradient(V, dtype):
+    z = (2.0 * torch.randn(9, V, generator=torch.Generator().manual_seed(V))).to(TYPES[dtype])
+    a, old, adv, ref, w = _policy_inputs(z, V, 0.8)
+    loss, logp, _ = _run_policy(z, a, old, adv, ref, None, 0.8)
+    _check_policy(_run_policy(z, a, old, adv, ref, w, 0.8), z, a, old, adv, ref, w, 0.8)
+    zc, ac, oc, vc, rc = _cuda(z, a, old, adv, ref)
+    only = M.policy_loss(zc, ac, oc, vc, ref_logp=rc, clip_low=0.2, clip_high=0.28, kl_coef=0.1,
+                         temperature=0.8)
+    assert torch.equal(only[0], loss) and torch.equal(only[1], logp)
