@@ -122,11 +122,13 @@ struct Vec {
 // the largest logit of the first ones seen; larger ones move it only when their exponent
 // passes kMaxExponent (s stays far inside fp32), so that the exponentials need not wait
 // for the maximum.  What rounding takes from k stays in the exponents of the reference
-// itself: half a unit in the last place, 1/8 at most for |k| < kNearRef, but 64 at 2^31 and
-// more than fp32's range soon after, where finite masks (-1e10, -1e30, the type's lowest
-// value) may be the only logits of a set.  From kNearRef on the exponents are (z - m) c.
-// A set without a finite logit has m = -inf, s = 0; a NaN or +inf logit makes s NaN.
-constexpr float kNearRef = 4194304.0f;  // 2^22
+// itself: half a unit in the last place, so 64 at most for |k| < kNearRef, which the sums'
+// range holds, but more than fp32's soon after, where finite masks (-1e10, -1e30, the type's
+// lowest value) may be the only logits of a set.  From kNearRef on the exponents are
+// (z - m) c.  Distinct logits on either side of it are 128 or more apart in their exponents,
+// so sums of the two kinds never weigh in one another.  A set without a finite logit has
+// m = -inf, s = 0; a NaN or +inf logit makes s NaN.
+constexpr float kNearRef = 2147483648.0f;  // 2^31
 constexpr float kMaxExponent = 24.0f;
 struct MaxSum {
   float m, s;
@@ -150,18 +152,10 @@ __device__ __forceinline__ float log_weight(float z, float m, float c, float inv
 __device__ __forceinline__ MaxSum one_logit(float z, float c) {
   return {z, z == -INFINITY ? 0.0f : ex2(exponent(z, z, c))};
 }
-// Exponent that takes sums over reference m to the finite reference `to`, not below m, each
-// m c rounded where it is near and as it is where not.
-static __device__ __noinline__ float far_rescale(float m, float to, float c) {
-  const float from = ref_exponent(m, c), k = ref_exponent(to, c);
-  if (near_ref(k)) return near_ref(from) ? __fsub_rn(from, k) : fmaf(m, c, -k);
-  return near_ref(from) ? fmaf(-to, c, from) : (m - to) * c;
-}
+// Exponent that takes sums over reference m to the finite reference `to`.
 __device__ __forceinline__ float rescale(float m, float to, float c) {
   const float k = ref_exponent(to, c);
-  // here a reference that is not near lies so far below that nothing is left of its sums
-  if (fabsf(k) < kNearRef - 512.0f) return __fsub_rn(ref_exponent(m, c), k);
-  return far_rescale(m, to, c);
+  return near_ref(k) ? __fsub_rn(ref_exponent(m, c), k) : (m - to) * c;
 }
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float c) {
   const float m = fmaxf(a.m, b.m), r = finite_ref(m);

@@ -189,3 +189,30 @@ def test_policy_loss_without_a_gradient(V, dtype):
     only = M.policy_loss(zc, ac, oc, vc, ref_logp=rc, clip_low=0.2, clip_high=0.28, kl_coef=0.1,
                          temperature=0.8)
     assert torch.equal(only[0], loss) and torch.equal(only[1], logp)
+
+
+@pytest.mark.parametrize("V", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_of_neighbouring_values_about_a_billion(V, dtype):
+    """Rows of a few neighbouring values, +-2^28 .. 2^34 in units of log2 e: the largest share
+    the row, as every other is 64 and more lower."""
+    g = torch.Generator().manual_seed(V)
+    bits = 23 if dtype == "f32" else 7
+    for e in (28, 30, 31, 32, 34):
+        for sign in (1.0, -1.0):
+            mid = sign * 2.0 ** e / 1.4426950408889634
+            ulp = 2.0 ** (math.floor(math.log2(abs(mid))) - bits)
+            z = (round(mid / ulp) + torch.randint(-3, 4, (4, V), generator=g)).double() * ulp
+            assert torch.equal(z.to(TYPES[dtype]).double(), z)
+            z = z.to(TYPES[dtype])
+            a = torch.cat([z[:2].float().argmax(1), torch.randint(V, (2,), generator=g)])
+            lp = torch.log_softmax(z.double(), 1).gather(1, a[:, None])[:, 0]
+            old = M.token_logp(z.to(DEV), a.to(DEV)).cpu()
+            assert torch.all((old.double() - lp).abs() <= 1e-5 + 2.0 ** -20 * (1.0 + lp.abs()))
+            # the ratio is 1: a gradient of probabilities alone, those of 2^-64 and less apart
+            w = torch.full((4,), 0.5)
+            d = _run_policy(z, a, old, torch.ones(4), None, w, 1.0)[2].cpu().double()
+            p = torch.softmax(z.double(), 1)
+            want = 0.5 * p
+            want[torch.arange(4), a] -= 0.5
+            assert torch.all((d - want).abs() <= R.ROUND[z.dtype][0] * want.abs() + REL + 2e-19)
