@@ -652,10 +652,9 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
     return p;
   };
   common = part_of(first);
-  int done = INT_MAX;  // rows that this warp's role has finished, where a wait runs out
-  auto leaves = [&](int role, int it) {
-    return kTest && first == 0 && rank == leave.rank && role == leave.role &&
-           it * step >= leave.row;
+  int lost = INT_MAX;  // the first row that this warp's role gave up; none: one beyond the last
+  auto leaves = [&](int role, int row) {
+    return kTest && first == 0 && rank == leave.rank && role == leave.role && row >= leave.row;
   };
 
   if (warp < kConsumerWarps) {
@@ -752,7 +751,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
         mbar_arrive(smem_u32(&sh.sums[g]));
       }
 
-      if (leaves(kConsumers, it) || !warp_wait(&sh.go[g], ph)) break;
+      if (leaves(kConsumers, row) || !warp_wait(&sh.go[g], ph)) break;
       if constexpr (!kGrad) continue;
       const GradRow<DT> out = grad_row<DT>(logits_of(row), grad_of(row), p.sp.head);
       with_soft<DT>(sh.slot[l % kSlots].soft, a.c2, [&](auto grad_vec, auto whole) {
@@ -777,7 +776,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.over[l % kSlots]));
     }
-    done = it;
+    lost = first + it * step;
   } else if (warp == kConsumerWarps) {  // producer
     RingPos pos;
     uint32_t lv = 0;
@@ -790,7 +789,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
       const uint4* src = reinterpret_cast<const uint4*>(logits_of(row) + p.sp.head) + p.v0;
       uint64_t* full = &sh.full[lv % kPartsAhead];
       for (int left = p.nv; left > 0; left -= kChunkVecs, pos.next()) {
-        ok = !leaves(kProducer, it) && warp_wait(&sh.empty[pos.slot], pos.phase ^ 1);
+        ok = !leaves(kProducer, row) && warp_wait(&sh.empty[pos.slot], pos.phase ^ 1);
         if (!ok) break;
         if (lane == 0) {
           const uint32_t bytes = 16u * min(kChunkVecs, left);
@@ -808,7 +807,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
     }
     // no copy may be in flight when the block ends: a part that a wait cut short completes
     // with the chunks it has, and its row is not valid
-    done = it;
+    lost = first + it * step;
     if (!ok && lane == 0) {
       sh.unloaded = it;
       __threadfence_block();
@@ -861,7 +860,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
       const uint32_t ph = (l / kSlots) & 1;
       Slot<MODE, kGrad>& s = sh.slot[i];
       if (!kGrad && !warp_wait(&sh.over[i], ph ^ 1)) {
-        done = (row - first) / step;
+        lost = row;
         break;
       }
       if constexpr (MODE == kDistill) {
@@ -890,8 +889,8 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
       if (row >= 0) fetch(row, name);
       else name();
       if constexpr (kGrad) {
-        if (leaves(kGather, (last - first) / step) || !warp_wait(&sh.over[i], ph)) {
-          done = (last - first) / step;
+        if (leaves(kGather, last) || !warp_wait(&sh.over[i], ph)) {
+          lost = last;
           break;
         }
         const Soft soft = s.soft;
@@ -946,7 +945,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
       const int i = l % kSlots, x = l % sh.kExchanges;
       Slot<MODE, kGrad>& s = sh.slot[i];
       const Part p = part_of(row);
-      if (leaves(kFinish, it) || !warp_wait(&sh.ready[i], (l / kSlots) & 1) ||
+      if (leaves(kFinish, row) || !warp_wait(&sh.ready[i], (l / kSlots) & 1) ||
           !warp_wait(&sh.sums[b], (l / kGroups) & 1) || it >= sh.unloaded)
         break;
       // the consumer warps' pairs, and rank 0's edges
@@ -984,16 +983,16 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
       }
       __syncwarp();
     }
-    done = it;
+    lost = first + it * step;
   }
-  if (done < rows && lane == 0) red_min_cluster(smem_u32((const void*)&sh.unfinished), 0, done);
+  if (lost < a.N && lane == 0) red_min_cluster(smem_u32((const void*)&sh.unfinished), 0, lost);
   __syncwarp();
   cluster_arrive();  // no block leaves while another may still write to it
   cluster_wait();
-  if (rank == 0 && sh.unfinished < rows)
-    for (int it = sh.unfinished + tid; it < rows; it += long_threads(kGrad)) {
-      if (a.row_loss) a.row_loss[first + it * step] = NAN;
-      if (a.logp) a.logp[first + it * step] = NAN;
+  if (rank == 0 && sh.unfinished < a.N)
+    for (int row = sh.unfinished + tid * step; row < a.N; row += long_threads(kGrad) * step) {
+      if (a.row_loss) a.row_loss[row] = NAN;
+      if (a.logp) a.logp[row] = NAN;
     }
 }
 
