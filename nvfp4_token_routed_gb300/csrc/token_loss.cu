@@ -594,6 +594,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity));
 }
 
+// NaN for the cluster's rows from `row` on.
+__device__ __noinline__ void mark_unfinished(float* row_loss, float* logp, int row, int N) {
+  const int step = gridDim.x / cluster_size();
+  for (row += threadIdx.x * step; row < N; row += blockDim.x * step) {
+    if (row_loss) row_loss[row] = NAN;
+    if (logp) logp[row] = NAN;
+  }
+}
+
 // kTest: a role of cluster 0 leaves as if a wait had run out.
 template <int DT, int MODE, bool kGrad, bool kTest>
 __global__ void __launch_bounds__(long_threads(kGrad), 1)
@@ -989,11 +998,7 @@ __global__ void __launch_bounds__(long_threads(kGrad), 1)
   __syncwarp();
   cluster_arrive();  // no block leaves while another may still write to it
   cluster_wait();
-  if (rank == 0 && sh.unfinished < a.N)
-    for (int row = sh.unfinished + tid * step; row < a.N; row += long_threads(kGrad) * step) {
-      if (a.row_loss) a.row_loss[row] = NAN;
-      if (a.logp) a.logp[row] = NAN;
-    }
+  if (sh.unfinished != INT_MAX) mark_unfinished(a.row_loss, a.logp, sh.unfinished, a.N);
 }
 
 // ---------------------------------------------------------------- launches
