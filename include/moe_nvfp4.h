@@ -367,10 +367,15 @@ moe_status moe_nvfp4_profile_spans(void* device_spans);
  *     A gradient has its logits' type and its own row stride, is rounded once
  *     from fp32, and may be the logits' buffer itself (same pointer and stride);
  *     any other overlap is not allowed.
- *   - Logits may be -inf or the type's lowest value (masked entries: probability
- *     0, gradient 0).  A row without a finite logit is left out: loss, log-
- *     probability and gradient 0.  NaN and +inf reach their row's loss and
- *     gradient, and no other row.
+ *   - Masked logits may be -inf or any finite value, the type's lowest among them.
+ *     Where other logits of the row lie far above, their probability is 0, and
+ *     their gradient but for what a row's chosen token or a teacher's slot adds; a
+ *     row that holds one finite value everywhere is uniform.  A row without a
+ *     finite logit is left out: loss, log-probability and gradient 0.  NaN and
+ *     +inf reach their row's loss and gradient, and no other row.
+ *   - Sums, log-probabilities and losses are fp32: probabilities below 2^-126 are 0,
+ *     and so is a teacher's, which then adds nothing; log-probabilities beyond
+ *     fp32 (a token of the lowest value at a temperature below 1) are -inf.
  *   - A row of a row-wise loss depends on that row alone; where every row starts
  *     on a 16-byte boundary its bits do not depend on the other rows or on N.
  *   - Waits inside the kernels are bounded (2 s).  Should one run out, the rows it

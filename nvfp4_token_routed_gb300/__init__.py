@@ -506,6 +506,9 @@ def ws_view(ws, layout, name, dtype, shape):
 # in include/moe_nvfp4.h).  Logits may be views of row-strided storage; every other
 # tensor is contiguous.  Outputs passed in are written and returned, else allocated
 # on the stream of the call.  With `stream`, the inputs must be ready on that stream.
+# Nothing is recorded for autograd: losses come back detached, also from logits that
+# require a gradient; the gradients are what the *_grad calls return (pass them on with
+# logits.backward(dlogits)).
 
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _IDS64 = {torch.int32: 0, torch.int64: 1}
@@ -591,7 +594,7 @@ def _policy_args(logits, actions, old_logp, advantages, ref_logp):
 
 def policy_loss(logits, actions, old_logp, advantages, ref_logp=None, clip_low=0.2, clip_high=0.2,
                 kl_coef=0.0, temperature=1.0, row_loss=None, logp=None, stream=None):
-    """Clipped policy loss with a KL term: (row_loss [N], logp [N]) fp32."""
+    """Clipped policy loss with a KL term: (row_loss [N], logp [N]) fp32, detached."""
     args = _policy_args(logits, actions, old_logp, advantages, ref_logp)
     n = logits.shape[:1]
     row_loss = _out(row_loss, "row_loss", n, torch.float32, logits, stream)
@@ -607,7 +610,9 @@ def policy_loss_grad(logits, actions, old_logp, advantages, row_weight=None, ref
                      clip_low=0.2, clip_high=0.2, kl_coef=0.0, temperature=1.0, row_loss=None,
                      logp=None, dlogits=None, stream=None):
     """policy_loss and the gradient of sum(row_weight * row_loss) (weights None: 1):
-    (row_loss, logp, dlogits).  dlogits may be the logits tensor itself."""
+    (row_loss, logp, dlogits).  dlogits may be the logits tensor itself.  Rows of logits and
+    gradient that lie alike to 16 bytes are fastest: for a slice of a padded head give a
+    dlogits with its row stride."""
     args = _policy_args(logits, actions, old_logp, advantages, ref_logp)
     n = logits.shape[:1]
     w = _arg(row_weight, "row_weight", n, _F32, logits)
@@ -645,8 +650,8 @@ def _teacher(logits, ids, t_logits, lse):
 
 def distill_loss(logits, teacher_ids, teacher_logits, teacher_lse=None, temperature=1.0,
                  row_loss=None, stream=None):
-    """KL divergence [N] fp32 of softmax(logits / temperature) from a teacher's top
-    logits: teacher_ids int32 / int64 [N, K] (outside [0, V): empty slot) and
+    """KL divergence [N] fp32 (detached) of softmax(logits / temperature) from a teacher's
+    top logits: teacher_ids int32 / int64 [N, K] (outside [0, V): empty slot) and
     teacher_logits [N, K]; teacher_lse [N]: the teacher's whole row's, at the same
     temperature (else the slots are renormalised)."""
     z = _matrix(logits, "logits")
@@ -705,8 +710,8 @@ def router_loss(logits, topk_ids, balance_coef, z_coef=0.0, seq_offsets=None, to
                 ws=None, losses=None, counts=None, tokens=None, stream=None):
     """Balance and z loss of router logits [T, E] and the load of the chosen experts
     topk_ids [T, K]: (losses [2] fp32, counts [S, E] int32, tokens [S + 1] int32: rows
-    that count per sequence, then in all).  seq_offsets int32 [S + 1] on the device;
-    token_mask bool [T], False: left out."""
+    that count per sequence, then in all), detached.  seq_offsets int32 [S + 1] on the
+    device; token_mask bool [T], False: left out."""
     b = _router_batch(logits, topk_ids, balance_coef, z_coef, seq_offsets, token_mask)
     T, E = logits.shape
     S = b.S
