@@ -517,6 +517,137 @@ moe_status moe_nvfp4_router_loss_grad(const moe_router_batch* b, const int32_t* 
                                       const float* topk_w, const float* d_topk_w, void* dlogits,
                                       int64_t ld_grad, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- routed rows
+ *
+ * The pieces of a differentiable pass through routed experts: routes sorted by expert,
+ * token rows to the experts and back, the experts' activation with its input kept in 8
+ * bits, and products of microscaled FP4 rows and weights.  Conventions beyond those
+ * above:
+ *   - rows are fp32, bf16 or f16, of any row stride (ld >= the row length); a pointer
+ *     needs its element's alignment only.  Rows whose base, stride and length are
+ *     multiples of 16 bytes are fastest.
+ *   - The route rows of a batch are numbered 0 .. T*K-1, experts in ascending order;
+ *     empty slots have no row, so a batch with empty slots leaves the last rows unused.
+ *     Unused rows are neither read nor written.  Where a call takes n_rows, a DEVICE
+ *     int32 (offsets + E of moe_nvfp4_sort_routes), rows from *n_rows on are left alone;
+ *     NULL: every row counts.
+ *   - Sums are fp32 in a fixed order, results rounded once: equal inputs give equal bits,
+ *     and a row's results do not depend on the other rows.
+ *   - Outputs do not overlap inputs unless a call says so. */
+typedef moe_logits moe_rows; /* data, ld, rows, cols, dtype */
+
+/* Bytes of the workspace of moe_nvfp4_sort_routes; 0 for invalid arguments.  Host only. */
+size_t moe_nvfp4_sort_routes_workspace_bytes(int32_t T, int32_t K, int32_t E);
+
+/* Stable counting sort of the routes by expert.  topk_ids int32 or int64 [T][K], -1 = empty
+ * slot; another id outside [0, E) is treated as empty and reported by
+ * moe_nvfp4_read_status(ws).  A token may name an expert more than once.
+ *   offsets [E+1]  expert e has the rows [offsets[e], offsets[e+1])
+ *   perm [T*K]     route t*K+k of each row; -1 from offsets[E] on
+ *   inv [T][K]     row of each route, -1 for an empty slot
+ * 1 <= E <= 1024, 1 <= K <= min(32, E), T*K <= 2^26.  ws: 256-byte aligned, one per stream;
+ * its contents before the call do not matter.  T == 0 writes offsets (zeros) only. */
+moe_status moe_nvfp4_sort_routes(int32_t T, int32_t K, int32_t E, const void* topk_ids,
+                                 int32_t ids_int64, int32_t* offsets, int32_t* perm, int32_t* inv,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Token rows to their routes' rows: rows[inv[t][k]] = x[t], x [T][H] (1 <= H <= 65536),
+ * rows [T*K][H] of x's type, row stride ld_rows.  An inv outside [0, T*K) is an empty slot.
+ * The gradient of dispatch is moe_nvfp4_combine without weights. */
+moe_status moe_nvfp4_dispatch(const moe_rows* x, int32_t K, const int32_t* inv, void* rows,
+                              int64_t ld_rows, moe_stream_t stream);
+
+/* Route rows back to their tokens: out[t] = sum_{k ascending} topk_w[t][k] *
+ * rows[inv[t][k]] over the slots that have a row; no row gives zeros.  rows [T*K][H],
+ * topk_w fp32 [T][K] or NULL (1), out [T][H] of the rows' type. */
+moe_status moe_nvfp4_combine(const moe_rows* rows, int32_t T, int32_t K, const int32_t* inv,
+                             const float* topk_w, void* out, int64_t ld_out, moe_stream_t stream);
+
+/* Gradient of combine: drows[inv[t][k]] = topk_w[t][k] * dout[t], and where d_topk_w is not
+ * NULL d_topk_w[t][k] = sum_h rows[inv[t][k]][h] * dout[t][h] (fp32; 0 for an empty slot).
+ * rows->data is looked at only for d_topk_w; drows [T*K][H] may be that buffer itself (same
+ * pointer and stride). */
+moe_status moe_nvfp4_combine_grad(const moe_rows* rows, int32_t T, int32_t K, const int32_t* inv,
+                                  const float* topk_w, const void* dout, int64_t ld_dout,
+                                  void* drows, int64_t ld_drows, float* d_topk_w,
+                                  moe_stream_t stream);
+
+/* Rows kept in 8 bits: E4M3 times a power of two 2^e per 32 consecutive values, e the
+ * smallest with which no value passes 448, -127 <= e <= 127, stored as e + 127.  A value is
+ * rounded to nearest even: off by at most 2^-4 of itself or half of 2^(e-9).  A block with an
+ * infinity or a NaN (byte 255) reads as NaN.
+ *   codes  [R][W32], W32 = cols rounded up to 32, zeros behind the row; 8-byte aligned
+ *   scales [R][W32 / 32]
+ * cols <= 2^20. */
+moe_status moe_nvfp4_checkpoint(const moe_rows* x, uint8_t* codes, uint8_t* scales,
+                                const int32_t* n_rows, moe_stream_t stream);
+/* The kept values as rows of out's type (out->data is written), rounded once. */
+moe_status moe_nvfp4_restore(const uint8_t* codes, const uint8_t* scales, const moe_rows* out,
+                             const int32_t* n_rows, moe_stream_t stream);
+
+/* The experts' activation of FC1 rows h: [R][2I] = [gate | up] for MOE_ACT_SWIGLU, [R][I]
+ * for MOE_ACT_RELU2 (I <= 2^19); y [R][I] of h's type.
+ *   swiglu: y = silu(gate) * up; swiglu_limit L > 0: gate = min(gate, L),
+ *           up = min(max(up, -L), L) first;   relu2: y = max(h, 0)^2
+ * Where codes is not NULL, h is kept in 8 bits beside it, each half blocked for itself:
+ * codes [R][halves][I32], scales [R][halves][I32 / 32]. */
+moe_status moe_nvfp4_expert_act(const moe_rows* h, int32_t act, float swiglu_limit, void* y,
+                                int64_t ld_y, uint8_t* codes, uint8_t* scales,
+                                const int32_t* n_rows, moe_stream_t stream);
+/* Its gradient at the kept values: dy [R][I] -> dh [R][2I] or [R][I] of dy's type.  A
+ * clamped value passes a gradient where it lies within the limit, the limit included. */
+moe_status moe_nvfp4_expert_act_grad(const uint8_t* codes, const uint8_t* scales, int32_t act,
+                                     float swiglu_limit, const moe_rows* dy, void* dh,
+                                     int64_t ld_dh, const int32_t* n_rows, moe_stream_t stream);
+
+/* A matrix in microscaled FP4: E2M1 times a power of two 2^e per 32 consecutive values of a
+ * row, e the smallest with which no value passes 6, -127 <= e <= 127; rounding, e's byte and
+ * non-finite blocks as above.  Dp = cols rounded up to 256, Rp = rows rounded up to 2.
+ *   codes  [rows][Dp / 2], value 2j in the low nibble of byte j, zeros behind the row
+ *   scales [Dp / 256][Rp][8]: the 8 scales of a row's 256 values, rows one after another
+ * Both 16-byte aligned.  1 <= cols <= 65536, rows <= 2^26. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int32_t rows;
+  int32_t cols;
+} moe_mx;
+
+/* Bytes of codes and scales.  Host only. */
+moe_status moe_nvfp4_mx_sizes(int32_t rows, int32_t cols, size_t bytes_out[2]);
+
+moe_status moe_nvfp4_mx_quantize(const moe_rows* x, const moe_mx* out, const int32_t* n_rows,
+                                 moe_stream_t stream);
+/* The columns of a stack of matrices x [batch][D][C] (contiguous) as rows: out has batch * C
+ * rows of D values (a weight stack for the product with its transpose). */
+moe_status moe_nvfp4_mx_quantize_transposed(int32_t batch, int32_t D, int32_t C, const void* x,
+                                            int32_t dtype, const moe_mx* out,
+                                            moe_stream_t stream);
+/* The values that `x` stands for, rounded once to out's type (out->data is written). */
+moe_status moe_nvfp4_mx_restore(const moe_mx* x, const moe_rows* out, const int32_t* n_rows,
+                                moe_stream_t stream);
+/* moe_nvfp4_dispatch of a microscaled matrix: out has x->rows * K rows. */
+moe_status moe_nvfp4_mx_dispatch(const moe_mx* x, int32_t K, const int32_t* inv,
+                                 const moe_mx* out, moe_stream_t stream);
+
+/* Product with the weights of each row's expert:
+ *   out[r][n] = sum_d x[r][d] * w[e * N + n][d], e the expert with offsets[e] <= r <
+ *   offsets[e+1]; w->rows = E * N, w->cols = x->cols.
+ * offsets: device [E+1] ascending, 1 <= E <= 1024; or NULL with E == 1: every row.  Rows
+ * outside all groups are left as they were.  1 <= N <= 65536.  out: row stride ld_out >= N,
+ * `dtype`; accumulated in fp32 on the tensor cores, rounded once.  A row's bits do not
+ * depend on the other rows.  Waits inside the kernel are bounded (2 s); should one run out,
+ * what is left unfinished gets NaN. */
+moe_status moe_nvfp4_mx_product(const moe_mx* x, const moe_mx* w, int32_t E,
+                                const int32_t* offsets, int32_t dtype, void* out, int64_t ld_out,
+                                moe_stream_t stream);
+
+/* Test hook of those bounded waits: the same by a kernel in which the loads of rows leave
+ * before work item `item` of the block that takes it. */
+moe_status moe_nvfp4_selftest_product_timeout(const moe_mx* x, const moe_mx* w, int32_t E,
+                                              const int32_t* offsets, int32_t item, int32_t dtype,
+                                              void* out, int64_t ld_out, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -72,6 +72,11 @@ class moe_router_batch(C.Structure):
                 ("ids_int64", C.c_int32), ("balance_coef", C.c_float), ("z_coef", C.c_float)]
 
 
+class moe_mx(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int32),
+                ("cols", C.c_int32)]
+
+
 class moe_ws_layout(C.Structure):
     _fields_ = [(n, C.c_int64 if n == "rows_cap" else C.c_size_t) for n in _LAYOUT_FIELDS]
 
@@ -137,7 +142,31 @@ def lib():
         L.moe_nvfp4_router_loss_workspace_bytes.argtypes = [i32, i32, i32]
         L.moe_nvfp4_router_loss.argtypes = [rb, vp, vp, vp, vp, sz, vp]
         L.moe_nvfp4_router_loss_grad.argtypes = [rb, vp, vp, vp, vp, vp, vp, i64, vp]
-        for f in ["moe_nvfp4_token_logp", "moe_nvfp4_policy_loss", "moe_nvfp4_policy_loss_grad",
+        mp = C.POINTER(moe_mx)
+        L.moe_nvfp4_sort_routes_workspace_bytes.restype = sz
+        L.moe_nvfp4_sort_routes_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_nvfp4_sort_routes.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_nvfp4_dispatch.argtypes = [zp, i32, vp, vp, i64, vp]
+        L.moe_nvfp4_combine.argtypes = [zp, i32, i32, vp, vp, vp, i64, vp]
+        L.moe_nvfp4_combine_grad.argtypes = [zp, i32, i32, vp, vp, vp, i64, vp, i64, vp, vp]
+        L.moe_nvfp4_checkpoint.argtypes = [zp, vp, vp, vp, vp]
+        L.moe_nvfp4_restore.argtypes = [vp, vp, zp, vp, vp]
+        L.moe_nvfp4_expert_act.argtypes = [zp, i32, f32, vp, i64, vp, vp, vp, vp]
+        L.moe_nvfp4_expert_act_grad.argtypes = [vp, vp, i32, f32, zp, vp, i64, vp, vp]
+        L.moe_nvfp4_mx_sizes.argtypes = [i32, i32, C.POINTER(sz)]
+        L.moe_nvfp4_mx_quantize.argtypes = [zp, mp, vp, vp]
+        L.moe_nvfp4_mx_quantize_transposed.argtypes = [i32, i32, i32, vp, i32, mp, vp]
+        L.moe_nvfp4_mx_restore.argtypes = [mp, zp, vp, vp]
+        L.moe_nvfp4_mx_dispatch.argtypes = [mp, i32, vp, mp, vp]
+        L.moe_nvfp4_mx_product.argtypes = [mp, mp, i32, vp, i32, vp, i64, vp]
+        L.moe_nvfp4_selftest_product_timeout.argtypes = [mp, mp, i32, vp, i32, i32, vp, i64, vp]
+        for f in ["moe_nvfp4_sort_routes", "moe_nvfp4_dispatch", "moe_nvfp4_combine",
+                  "moe_nvfp4_combine_grad", "moe_nvfp4_checkpoint", "moe_nvfp4_restore",
+                  "moe_nvfp4_expert_act", "moe_nvfp4_expert_act_grad", "moe_nvfp4_mx_sizes",
+                  "moe_nvfp4_mx_quantize", "moe_nvfp4_mx_quantize_transposed",
+                  "moe_nvfp4_mx_restore", "moe_nvfp4_mx_dispatch", "moe_nvfp4_mx_product",
+                  "moe_nvfp4_selftest_product_timeout",
+                  "moe_nvfp4_token_logp", "moe_nvfp4_policy_loss", "moe_nvfp4_policy_loss_grad",
                   "moe_nvfp4_selftest_loss_timeout",
                   "moe_nvfp4_distill_loss", "moe_nvfp4_distill_loss_grad",
                   "moe_nvfp4_router_loss", "moe_nvfp4_router_loss_grad",
@@ -748,3 +777,12 @@ def router_loss_grad(logits, topk_ids, counts, tokens, balance_coef, z_coef=0.0,
         _arg(d_topk_w, "d_topk_w", topk_ids.shape, _F32, logits),
         dlogits.data_ptr(), ld, _raw(stream)), "moe_nvfp4_router_loss_grad")
     return dlogits
+
+
+# ------------------------------------------------------------------ routed rows
+
+from .experts import (  # noqa: E402
+    Checkpoint, MxExperts, MxTensor, RoutePlan, checkpoint, combine, combine_grad, dispatch,
+    dispatch_grad, expert_act, expert_act_grad, moe_nvfp4_selftest_product_timeout,
+    moe_nvfp4_sort_routes_workspace_bytes, mx_product, mx_quantize, mx_quantize_transposed,
+    mx_restore, restore, sort_routes, sort_routes_workspace)

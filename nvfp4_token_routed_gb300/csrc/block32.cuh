@@ -1,0 +1,204 @@
+// block32.cuh -- blocks of 32 values that share a power of two: exponents, and the
+// reading and writing of runs of 8 values of any alignment.
+//
+// A block holds x_i = 2^e q_i with q_i of an 8- or 4-bit float type whose largest value
+// is qmax.  e is the smallest exponent with max |x_i| <= qmax 2^e, so that no value is
+// cut off and each is off by at most half a step of its type (or of its smallest step).
+// With max |x_i| = m 2^k, 1 <= m < 2, and qmax = f 2^j: e = k - j + (m > f), which needs
+// the bits of the largest magnitude and no division.  e is kept in [-127, 127] as the
+// byte e + 127; byte 255 marks a block with an infinity or a NaN, which reads as NaN.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "loss.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+struct E4m3 {  // qmax = 448 = 1.75 * 2^8
+  static constexpr int kMaxExp = 8;
+  static constexpr uint32_t kMaxMantissa = 0x600000u;
+};
+struct E2m1 {  // qmax = 6 = 1.5 * 2^2
+  static constexpr int kMaxExp = 2;
+  static constexpr uint32_t kMaxMantissa = 0x400000u;
+};
+
+// Scale byte of a block from the bits of its largest magnitude.
+template <typename F>
+__device__ __forceinline__ uint32_t block_scale_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return 255u;
+  const int b = (int)(amax_bits >> 23) - F::kMaxExp + ((amax_bits & 0x7FFFFFu) > F::kMaxMantissa);
+  return (uint32_t)max(b, 0);  // fp32 subnormals come out below 0 as well
+}
+// 2^-e, for byte 255 0: its codes are zeros.
+__device__ __forceinline__ float block_inverse(uint32_t byte) {
+  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+// 2^e, NaN for byte 255.
+__device__ __forceinline__ float block_scale(uint32_t byte) {
+  return byte == 0u ? __uint_as_float(0x00400000u)
+                    : byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
+}
+
+// 8 values of a row in fp32.
+struct Run8 {
+  float v[8];
+  // Bits of the largest magnitude; infinities and NaN above every finite value.
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+  }
+};
+
+template <int DT>
+struct Elem {
+  using type = uint16_t;
+};
+template <>
+struct Elem<kF32> {
+  using type = uint32_t;
+};
+template <int DT>
+__device__ __forceinline__ float elem_to_float(uint32_t b) {
+  if constexpr (DT == kF32) return __uint_as_float(b);
+  if constexpr (DT == kBf16) return __uint_as_float(b << 16);
+  if constexpr (DT == kF16) return __half2float(__ushort_as_half((unsigned short)b));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t float_to_elem(float v) {
+  if constexpr (DT == kF32) return __float_as_uint(v);
+  if constexpr (DT == kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  if constexpr (DT == kF16) return __half_as_ushort(__float2half_rn(v));
+}
+
+// 32-bit words of 8 elements.
+template <int DT>
+constexpr int kRunWords = DT == kF32 ? 8 : 4;
+
+// Reads elements [0, n) of a run of 8 (n <= 0: none, the rest zeros) by accesses of VB
+// bytes; with VB over the element's size n is 0 or 8 or a multiple of VB's elements.
+template <int DT, int VB>
+__device__ __forceinline__ void run_load_raw(const void* p, int n, uint32_t (&w)[kRunWords<DT>]) {
+  constexpr int kSize = DT == kF32 ? 4 : 2;
+  constexpr int kPer = VB / kSize;  // elements an access
+  const char* c = static_cast<const char*>(p);
+#pragma unroll
+  for (int i = 0; i < kRunWords<DT>; ++i) w[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < 8 / kPer; ++i) {
+    if (i * kPer >= n) continue;
+    if constexpr (VB == 16) {
+      const uint4 t = *reinterpret_cast<const uint4*>(c + 16 * i);
+      w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+    } else if constexpr (VB == 8) {
+      const uint2 t = *reinterpret_cast<const uint2*>(c + 8 * i);
+      w[2 * i] = t.x, w[2 * i + 1] = t.y;
+    } else if constexpr (VB == 4) {
+      w[i] = *reinterpret_cast<const uint32_t*>(c + 4 * i);
+    } else {
+      w[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(c + 2 * i) << (16 * (i & 1));
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void run_unpack(const uint32_t (&w)[kRunWords<DT>], Run8& r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (DT == kF32)
+      r.v[i] = __uint_as_float(w[i]);
+    else
+      r.v[i] = elem_to_float<DT>((w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+  }
+}
+template <int DT, int VB>
+__device__ __forceinline__ void run_store(void* p, int n, const Run8& r) {
+  constexpr int kSize = DT == kF32 ? 4 : 2;
+  constexpr int kPer = VB / kSize;
+  uint32_t w[kRunWords<DT>];
+#pragma unroll
+  for (int i = 0; i < kRunWords<DT>; ++i)
+    w[i] = DT == kF32 ? float_to_elem<DT>(r.v[i])
+                      : float_to_elem<DT>(r.v[(2 * i) & 7]) |
+                            (float_to_elem<DT>(r.v[(2 * i + 1) & 7]) << 16);
+  char* c = static_cast<char*>(p);
+#pragma unroll
+  for (int i = 0; i < 8 / kPer; ++i) {
+    if (i * kPer >= n) continue;
+    if constexpr (VB == 16)
+      *reinterpret_cast<uint4*>(c + 16 * i) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    else if constexpr (VB == 8)
+      *reinterpret_cast<uint2*>(c + 8 * i) = make_uint2(w[2 * i], w[2 * i + 1]);
+    else if constexpr (VB == 4)
+      *reinterpret_cast<uint32_t*>(c + 4 * i) = w[i];
+    else
+      *reinterpret_cast<uint16_t*>(c + 2 * i) = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// E4M3 codes of 8 values times `inv` (|v inv| <= 448), value i in byte i.
+__device__ __forceinline__ uint2 e4m3x8(const Run8& r, float inv) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t o;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(o)
+        : "f"(r.v[2 * i + 1] * inv), "f"(r.v[2 * i] * inv));
+    h[i] = o;
+  }
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+__device__ __forceinline__ void e4m3x8_to_float(const uint2& c, float scale, Run8& r) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+    r.v[2 * i] = f.x * scale;
+    r.v[2 * i + 1] = f.y * scale;
+  }
+}
+// E2M1 codes of 8 values times `inv`, value i in nibble i.
+__device__ __forceinline__ uint32_t e2m1x8(const Run8& r, float inv) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o |= cvt_e2m1x2(r.v[2 * i] * inv, r.v[2 * i + 1] * inv) << (8 * i);
+  return o;
+}
+__device__ __forceinline__ void e2m1x8_to_float(uint32_t c, float scale, Run8& r) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 t0, t1, t2, t3;\n mov.b32 {t0, t1, t2, t3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, t0;\n cvt.rn.f16x2.e2m1x2 %1, t1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, t2;\n cvt.rn.f16x2.e2m1x2 %3, t3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+    r.v[2 * i] = f.x * scale;
+    r.v[2 * i + 1] = f.y * scale;
+  }
+}
+
+// Largest over the 4 lanes that hold a block of 32 values.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+}
+
+// Widest access (bytes, at most 16) by which rows of `row_bytes` at base, stride
+// ld_bytes, can be read and written.
+inline int access_bytes(const void* base, int64_t ld_bytes, int64_t row_bytes) {
+  const uint64_t m = reinterpret_cast<uintptr_t>(base) | (uint64_t)ld_bytes | (uint64_t)row_bytes;
+  return m % 16 == 0 ? 16 : m % 8 == 0 ? 8 : m % 4 == 0 ? 4 : 2;
+}
+
+}  // namespace moe

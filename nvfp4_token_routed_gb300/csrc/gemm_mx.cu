@@ -1,0 +1,502 @@
+// gemm_mx.cu -- product of microscaled FP4 rows with their expert's weights:
+//   y[r][n] = sum_d x[r][d] w[e(r)][n][d],  both E2M1 with a power of two per 32 values,
+// on tcgen05 tensor cores (kind::mxf4, K = 64 an instruction, fp32 accumulators in TMEM).
+// Rows lie sorted by expert (or form one group); groups start at any row.
+//
+// Weights are the M = 128 operand and rows the N operand, so that the few rows of a
+// decode step do not leave a 128-row instruction idle.  Bounds: a launch reads each
+// used weight once (17/32 byte a value) and is bound by HBM up to some 500 rows an
+// expert, beyond by what the tensor cores are fed with.
+//
+//   * Persistent CTAs, one an SM.  Work item = (tile of up to 192 rows of one expert,
+//     128-row weight tile); a group's rows are cut into equal tiles of whole 16s.  Items
+//     are numbered expert by expert and weight-tile-major, so that the row tiles of one
+//     weight tile run next to each other and it comes from HBM once.  Every CTA adds the
+//     groups up for itself and takes items blockIdx.x, + gridDim.x, ...: no counter, no
+//     workspace, nothing to reset between launches.
+//   * Warp 0 loads weight tiles (TMA, 128-byte swizzle) and their scales, warp 10 row
+//     tiles (boxes of 128 / 64 / 32 / 16 rows) and theirs; a stage is 256 values deep.
+//     A stage's scales are one contiguous piece of a panel (mx_quant.cu), which starts on
+//     an even row: 8 bytes a row, 16 a bulk copy's boundary.
+//   * Warps 6-9 move a stage's scales to TMEM: row r at lane r % 32, column r / 32, in
+//     all four lane quadrants; one 32-bit column holds 128 values' four scales, and the
+//     instruction takes two of them by its scale id.
+//   * Warp 1 issues the MMAs, warps 2-5 drain the accumulators (two, or four where no
+//     tile passes 64 rows): a lane holds one output feature, lanes exchange pairs so that
+//     every store is 4 bytes of one row.
+//   * Waits are bounded.  A CTA in which one runs out drains its copies and MMAs, frees
+//     TMEM, and writes NaN to the items that it leaves.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include <cstdint>
+
+#include "block32.cuh"
+#include "experts.h"
+#include "gemm_common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowBytes = kMxPanel / 2;        // code bytes of a row and stage
+constexpr int kABytes = 128 * kRowBytes;
+constexpr int kSfaBytes = 1152;                // 130 rows of 8 bytes, padded
+constexpr int kTileN = 192;                    // rows of the largest tile
+constexpr int kStages = 12;                    // at most
+constexpr int kAccs = 4;
+constexpr int kTmemCols = 512;
+constexpr int kSmem = 227 * 1024;
+constexpr int kThreads = 352;                  // 11 warps
+// mbarriers
+constexpr int kFull = 0;
+constexpr int kEmpty = kStages;
+constexpr int kSfReady = 2 * kStages;
+constexpr int kAccFull = 3 * kStages;
+constexpr int kAccEmpty = kAccFull + kAccs;
+constexpr int kDrain = kAccEmpty + kAccs;
+constexpr int kBars = kDrain + 1;
+constexpr int kFlagsOff = 8 * kBars;           // tmem slot, abort flag, stop flag, tile height
+constexpr int kWarpSumOff = kFlagsOff + 32;    // two ints a warp
+constexpr int kGroupsOff = 512;                // first item [E + 1], first row [E + 1]
+static_assert(kWarpSumOff + 8 * (kThreads / 32) <= kGroupsOff, "barrier area");
+
+struct MxMaps {
+  CUtensorMap w;
+  CUtensorMap x[4];  // 16, 32, 64, 128 rows
+};
+
+__device__ __forceinline__ uint2 lds64(uint32_t saddr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr));
+  return v;
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 x E2M1, UE8M0 scales, K-major operands.
+__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t M, uint32_t N) {
+  return (1u << 7) | (1u << 10) | (((N >> 3) & 0x3F) << 17) | (1u << 23) |
+         (((M >> 4) & 0x1F) << 24);
+}
+// By a converged warp; the elected lane issues.
+__device__ __forceinline__ void mma_mxf4_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+      " [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+__device__ __forceinline__ bool wait_or_leave(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// A CTA's walk over its items.
+struct Item {
+  int e, mt;
+  int row0, rows;  // first row of the tile, rows
+};
+struct Walk {
+  const int* first_item;  // [E + 1]
+  const int* first_row;   // [E + 1], the last one past the last group
+  int m_tiles, e;
+  // Row tiles of a group are equal and whole 16s.
+  __device__ __forceinline__ Item at(int item) {
+    while (item >= first_item[e + 1]) ++e;
+    const int tiles = (first_item[e + 1] - first_item[e]) / m_tiles;
+    const int local = item - first_item[e], group = first_row[e + 1] - first_row[e];
+    const int h = ((group + tiles - 1) / tiles + 15) & ~15;
+    const int tt = local % tiles;
+    return Item{e, local / tiles, first_row[e] + tt * h, min(h, group - tt * h)};
+  }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_mx_kernel(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const Ring R{smem};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kFlagsOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* epi_stop = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* s_max16 = reinterpret_cast<int*>(tmem_slot + 3);
+  int* s_sum = reinterpret_cast<int*>(smem + kWarpSumOff);
+  int* first_item = reinterpret_cast<int*>(smem + kGroupsOff);
+  int* first_row = first_item + a.E + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m_tiles = (a.N + 127) / 128;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(R.bar(kFull + s), 2);  // both producers
+      mbar_init(R.bar(kEmpty + s), 1);
+      mbar_init(R.bar(kSfReady + s), 4);
+    }
+    for (int b = 0; b < kAccs; ++b) {
+      mbar_init(R.bar(kAccFull + b), 1);
+      mbar_init(R.bar(kAccEmpty + b), 128);
+    }
+    mbar_init(R.bar(kDrain), 1);
+    *abort_flag = 0;
+    *epi_stop = 0;
+    *s_max16 = 16;
+    fence_barrier_init();
+    prefetch_tmap(&maps.w);
+    for (int i = 0; i < 4; ++i) prefetch_tmap(&maps.x[i]);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- groups: first row and first item of each expert (thread i: kPer experts)
+  {
+    const int per = (a.E + kThreads - 1) / kThreads;
+    const int e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
+    auto bound = [&](int e) {  // rows outside [0, R] are no rows
+      return a.offsets ? max(0, min(a.R, a.offsets[e])) : e ? a.R : 0;
+    };
+    int items = 0, most = 16;
+    for (int e = e0; e < e1; ++e) {
+      const int rows = max(0, bound(e + 1) - bound(e));
+      const int tiles = (rows + kTileN - 1) / kTileN;
+      items += tiles * m_tiles;
+      if (tiles) most = max(most, ((rows + tiles - 1) / tiles + 15) & ~15);
+    }
+    int x = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    atomicMax(s_max16, most);
+    __syncthreads();
+    int before = x - items;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    for (int e = e0; e < e1; ++e) {
+      const int b0 = bound(e), rows = max(0, bound(e + 1) - b0);
+      first_item[e] = before;
+      first_row[e] = b0;
+      before += (rows + kTileN - 1) / kTileN * m_tiles;
+      if (e == a.E - 1) {
+        first_item[a.E] = before;
+        first_row[a.E] = b0 + rows;
+      }
+    }
+    __syncthreads();
+  }
+  const int n_items = first_item[a.E];
+
+  // ---- geometry from the largest tile
+  const int max16 = *s_max16;
+  const int acc_stride = (max16 + 31) & ~31;
+  const int sfb_bytes = (8 * (acc_stride + 2) + 127) & ~127;  // a warp reads whole 32s, from an odd row on
+  const int off_b = kABytes, off_sfa = off_b + max16 * kRowBytes, off_sfb = off_sfa + kSfaBytes;
+  const int stage_bytes = (off_sfb + sfb_bytes + 1023) & ~1023;
+  const int nbuf = max16 <= 64 ? 4 : 2;
+  const int nrb = max16 <= 128 ? 4 : 8;       // 32-row columns of a row tile's scales
+  const int slot_cols = 8 + 2 * nrb;
+  const int sf_base = nbuf * acc_stride;
+  const int head = (kGroupsOff + 8 * (a.E + 1) + 1023) & ~1023;
+  uint8_t* stages = smem + head;
+  int n_stages = min(kStages, (kSmem - 1024 - head) / stage_bytes);
+  n_stages = min(n_stages, (kTmemCols - sf_base) / slot_cols);
+
+  Walk walk{first_item, first_row, m_tiles, 0};
+  if (warp == 0) {
+    // ------------------------------------------------------------ weight producer
+    if (lane == 0) {
+      int last_par[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) last_par[s] = -1;
+      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
+      const int64_t w_rows = ((int64_t)a.E * a.N + 1) & ~int64_t(1);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+        const Item it = walk.at(item);
+        // a weight tile of one row tile is not read again
+        const uint64_t pol =
+            first_item[it.e + 1] - first_item[it.e] == m_tiles ? once : keep;
+        const int64_t row = (int64_t)it.e * a.N + it.mt * 128, r0 = row & ~int64_t(1);
+        const uint32_t sf = 8u * (uint32_t)min((int64_t)(row != r0 ? 130 : 128), w_rows - r0);
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+          if (!wait_or_leave(R.bar(kEmpty + stage), phase ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sb = stages + stage * stage_bytes;
+          const uint32_t full = R.bar(kFull + stage);
+          mbar_expect_tx(full, kABytes + sf);
+          tma_load_2d_hint(smem_u32(sb), &maps.w, full, kb * kRowBytes, (int)row, pol);
+          bulk_load(smem_u32(sb + off_sfa), a.sw + kb * a.sw_panel + 8 * r0, sf, full);
+          last_par[stage] = (int)phase;
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok || *abort_flag) drain_stages(R, kFull, last_par, kStages);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ row producer
+    if (lane == 0) {
+      int last_par[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) last_par[s] = -1;
+      const uint64_t pol = policy_evict_last();
+      const int rows_p = (a.R + 1) & ~1;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+        if (item == a.leave_item) break;
+        const Item it = walk.at(item);
+        const int n16 = (it.rows + 15) & ~15, r0 = it.row0 & ~1;
+        const uint32_t sf = 8u * (uint32_t)min(n16 + (it.row0 != r0 ? 2 : 0), rows_p - r0);
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+          if (!wait_or_leave(R.bar(kEmpty + stage), phase ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sb = stages + stage * stage_bytes;
+          const uint32_t full = R.bar(kFull + stage);
+          mbar_expect_tx(full, n16 * kRowBytes + sf);
+          for (int r = 0; r < n16;) {
+            const int rem = n16 - r;
+            const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
+            tma_load_2d_hint(smem_u32(sb + off_b + r * kRowBytes), &maps.x[lg], full,
+                             kb * kRowBytes, it.row0 + r, pol);
+            r += 16 << lg;
+          }
+          bulk_load(smem_u32(sb + off_sfb), a.sx + kb * a.sx_panel + 8 * (int64_t)r0, sf, full);
+          last_par[stage] = (int)phase;
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok || *abort_flag) drain_stages(R, kFull, last_par, kStages);
+    }
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------ scales to TMEM
+    const uint32_t lane_q = (uint32_t)((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+      const Item it = walk.at(item);
+      const int odd_w = (int)(((int64_t)it.e * a.N) & 1), odd_x = it.row0 & 1;
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        if (!wait_or_leave(R.bar(kFull + stage), phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
+        const uint32_t col = tmem + lane_q + sf_base + stage * slot_cols;
+        const uint32_t sa = sb + off_sfa + 8 * (odd_w + lane), sx = sb + off_sfb + 8 * (odd_x + lane);
+        {
+          const uint2 p0 = lds64(sa), p1 = lds64(sa + 256), p2 = lds64(sa + 512),
+                      p3 = lds64(sa + 768);
+          tmem_st4(col, make_uint4(p0.x, p1.x, p2.x, p3.x));
+          tmem_st4(col + 4, make_uint4(p0.y, p1.y, p2.y, p3.y));
+        }
+        for (int b = 0; b < nrb; b += 4) {
+          if (32 * b >= it.rows) break;
+          // rows past the tile's are read from what lies there: only their own, unstored
+          // columns would see them
+          uint2 p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            p[j] = 32 * (b + j) < it.rows ? lds64(sx + 256 * (b + j)) : make_uint2(0u, 0u);
+          tmem_st4(col + 8 + b, make_uint4(p[0].x, p[1].x, p[2].x, p[3].x));
+          tmem_st4(col + 8 + nrb + b, make_uint4(p[0].y, p[1].y, p[2].y, p[3].y));
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(R.bar(kSfReady + stage));
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    int stage = 0, local = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+      const Item it = walk.at(item);
+      const uint32_t idesc = idesc_mxf4(128, (it.rows + 15) & ~15);
+      const int buf = local % nbuf;
+      ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(kAccEmpty + buf),
+                                                 ((uint32_t)(local / nbuf) & 1u) ^ 1u, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * acc_stride;
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        wait_or_leave(R.bar(kSfReady + stage), phase, abort_flag) &&
+                            wait_or_leave(R.bar(kFull + stage), phase, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
+        const uint32_t col = tmem + sf_base + stage * slot_cols;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t id = 2u * (ks & 1);  // which two of a column's four scales
+          mma_mxf4_warp(acc, smem_desc(sb + ks * 32, 16, 1024, 2),
+                        smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
+                        idesc | (id << 4) | (id << 29), col + 4 * (ks >> 1),
+                        col + 8 + nrb * (ks >> 1), (kb | ks) != 0 ? 1u : 0u);
+        }
+        issued = true;
+        tc_commit_warp(R.bar(kEmpty + stage));
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      tc_commit_warp(R.bar(kAccFull + buf));
+      ++local;
+    }
+    if ((!ok || *abort_flag) && issued) {
+      tc_commit_warp(R.bar(kDrain));
+      mbar_wait(R.bar(kDrain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    using T = typename Elem<DT>::type;
+    const int q = warp & 3;
+    const int et = threadIdx.x - 64;
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    T* out = static_cast<T*>(a.out);
+    int local = 0;
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+      const Item it = walk.at(item);
+      const int n = it.mt * 128 + q * 32 + lane;  // this lane's feature
+      const int n16 = (it.rows + 15) & ~15;
+      const int buf = local % nbuf;
+      if (!wait_or_leave(R.bar(kAccFull + buf), (uint32_t)(local / nbuf) & 1u, abort_flag))
+        *epi_stop = 1;
+      named_bar_sync(1, 128);
+      const bool stop = *epi_stop != 0;
+      named_bar_sync(1, 128);
+      if (stop) {
+        // what this CTA leaves: NaN, by one thread a feature
+        for (; item < n_items; item += gridDim.x) {
+          const Item left = walk.at(item);
+          const int f = left.mt * 128 + et;
+          for (int j = 0; f < a.N && j < left.rows; ++j)
+            out[(left.row0 + j) * a.ld + f] = (T)float_to_elem<DT>(__int_as_float(0x7FC00000));
+        }
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + lane_addr + buf * acc_stride;
+      for (int c0 = 0; c0 < n16; c0 += 32) {
+        const int ncol = min(32, n16 - c0);
+        float v[32];
+        tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
+        if (ncol > 16) tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+        tmem_wait_ld();
+        if (c0 + 32 >= n16) {
+          tc_fence_before();
+          mbar_arrive(R.bar(kAccEmpty + buf));
+        }
+        const int m = min(32, it.rows - c0);
+        T* o = out + (int64_t)(it.row0 + c0) * a.ld;
+        if (DT != kF32 && a.wide) {
+          // lanes 2i and 2i + 1 hold features f, f + 1: the even lane stores both of row j,
+          // the odd lane both of row j + 1
+          const bool odd = lane & 1;
+          const int f = n & ~1;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            if (j >= m) break;
+            const uint32_t b0 = float_to_elem<DT>(v[j]), b1 = float_to_elem<DT>(v[j + 1]);
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? b0 : b1, 1);
+            const uint32_t w = odd ? got | (b1 << 16) : b0 | (got << 16);
+            if (j + (int)odd < m && f < a.N)
+              *reinterpret_cast<uint32_t*>(o + (j + odd) * a.ld + f) = w;
+          }
+        } else if (n < a.N) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < m) o[j * a.ld + n] = (T)float_to_elem<DT>(v[j]);
+        }
+      }
+      ++local;
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int DT>
+cudaError_t launch_typed(const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gemm_mx_kernel<DT>), kSmem,
+                                    configured);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(gemm_mx_kernel<DT>, dim3(grid), dim3(kThreads), (size_t)kSmem, s, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mx(const MxGemmArgs& a, const uint8_t* x_codes, const uint8_t* w_codes,
+                           int sms, cudaStream_t s) {
+  MxMaps maps;
+  const uint64_t row_bytes = (uint64_t)a.kblocks * kRowBytes;
+  if (!byte_map(&maps.w, w_codes, row_bytes, (uint64_t)a.E * a.N, 128)) return cudaErrorInvalidValue;
+  for (int i = 0; i < 4; ++i)
+    if (!byte_map(&maps.x[i], x_codes, row_bytes, a.R, 16u << i)) return cudaErrorInvalidValue;
+  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kTileN + a.E);
+  const int grid = (int)std::min<int64_t>(sms, tiles * ((a.N + 127) / 128));
+  return a.dtype == kF32    ? launch_typed<kF32>(maps, a, grid, s)
+         : a.dtype == kBf16 ? launch_typed<kBf16>(maps, a, grid, s)
+                            : launch_typed<kF16>(maps, a, grid, s);
+}
+
+}  // namespace moe

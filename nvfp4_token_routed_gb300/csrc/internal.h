@@ -119,6 +119,11 @@ inline cudaError_t ensure_smem_limit(const void* fn, int bytes, std::atomic<uint
   return e;
 }
 
+// Tensor map of a byte matrix [rows][row_bytes] in boxes of box_rows x 128 bytes, 128-byte
+// swizzle (moe_api.cu).
+bool byte_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+              uint32_t box_rows);
+
 // static_enc: null for the per-token recipe, else the device encode scale a1 of
 // the per-tensor recipe (scale is then not written).
 void launch_quantize_tokens(int T, int H, int Hp, const void* x, uint8_t* codes, uint8_t* sf,

@@ -255,6 +255,10 @@ T* at(void* ws, size_t off) {
 namespace moe {
 int route_kernel_launches(int64_t TK);  // routing + gather launches; next to those kernels
 int device_status(int* sms_out) { return check_device(sms_out); }
+bool byte_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+              uint32_t box_rows) {
+  return make_tmap_bytes(m, base, row_bytes, rows, box_rows);
+}
 }  // namespace moe
 
 extern "C" {

@@ -1,0 +1,157 @@
+// mx_quant.cu -- microscaled FP4: rows to E2M1 codes with one power of two per 32 values
+// (block32.cuh), and back.
+//
+// Codes lie as the rows do, two to a byte, a row padded with zeros to a multiple of 256
+// values (one stage of the product).  Scales lie in panels: the 8 bytes of a row's 256
+// values, rows one after the other, panel after panel, the number of rows rounded up to
+// even.  So the scales that a stage of the product needs for any run of consecutive rows
+// are one contiguous piece, which one bulk copy brings, and a run of rows may start at any
+// row: experts' groups need no padding.
+//
+// A warp takes 256 values of a row, 8 a lane; bound by HBM.
+#include "block32.cuh"
+#include "experts.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// A warp's 256 values (lane l holds 8l ... 8l+7): 4 bytes of codes a lane, 8 of scales.
+__device__ __forceinline__ void write_panel(const MxQuantArgs& a, int64_t r, int panel,
+                                            const Run8& v) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t byte = block_scale_byte<E2m1>(quad_max(v.amax_bits()));
+  reinterpret_cast<uint32_t*>(a.codes + r * (a.Dp / 2) + panel * (kMxPanel / 2))[lane] =
+      byte == 255u ? 0u : e2m1x8(v, block_inverse(byte));
+  // lane 4b holds block b's byte; lanes 0 and 16 gather four each
+  uint32_t lo = byte | (__shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8);
+  lo |= __shfl_down_sync(0xFFFFFFFFu, lo, 8) << 16;
+  const uint32_t hi = __shfl_sync(0xFFFFFFFFu, lo, 16);
+  const int64_t rows_p = (a.R + 1) & ~1;
+  if (lane == 0)
+    *reinterpret_cast<uint2*>(a.scales + (panel * rows_p + r) * 8) = make_uint2(lo, hi);
+}
+
+template <int DT, int VB>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const MxQuantArgs a, int panels) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t r = i / panels;
+  const int panel = (int)(i - r * panels);
+  const int rows = a.n_rows ? min(a.R, *a.n_rows) : a.R;
+  if (r >= rows) return;  // the whole warp
+  const int c = panel * kMxPanel + (threadIdx.x & 31) * 8;
+  uint32_t w[kRunWords<DT>];
+  run_load_raw<DT, VB>(static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ld_x + c, a.D - c,
+                       w);
+  Run8 v;
+  run_unpack<DT>(w, v);
+  write_panel(a, r, panel, v);
+}
+
+template <int DT, int VB>
+__global__ void __launch_bounds__(kThreads) restore_kernel(const MxQuantArgs a, int panels) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t r = i / panels;
+  const int panel = (int)(i - r * panels);
+  const int rows = a.n_rows ? min(a.R, *a.n_rows) : a.R;
+  if (r >= rows) return;
+  const int lane = threadIdx.x & 31, c = panel * kMxPanel + lane * 8;
+  if (c >= a.D) return;
+  const int64_t rows_p = (a.R + 1) & ~1;
+  const uint32_t code =
+      reinterpret_cast<const uint32_t*>(a.codes + r * (a.Dp / 2) + panel * (kMxPanel / 2))[lane];
+  Run8 v;
+  e2m1x8_to_float(code, block_scale(a.scales[(panel * rows_p + r) * 8 + (lane >> 2)]), v);
+  run_store<DT, VB>(static_cast<typename Elem<DT>::type*>(a.out) + r * a.ld_out + c, a.D - c, v);
+}
+
+// Columns of a stack of matrices as rows: 256 values of 32 columns a block, through
+// shared memory (a column's stride of 261 words keeps a warp's reads of 8 consecutive
+// values at most 8 to a bank, and its writes free of conflicts).
+constexpr int kColsT = 32, kStrideT = kMxPanel + 5;
+template <int DT>
+__global__ void __launch_bounds__(kThreads) quantize_t_kernel(const MxQuantArgs a, int C) {
+  __shared__ float tile[kColsT * kStrideT];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * kColsT, panel = blockIdx.y;
+  const int64_t b = blockIdx.z;
+  const auto* x = static_cast<const typename Elem<DT>::type*>(a.x) + b * a.D * C;
+  for (int j = warp; j < kMxPanel; j += kThreads / 32) {
+    const int d = panel * kMxPanel + j;
+    tile[lane * kStrideT + j] =
+        d < a.D && c0 + lane < C ? elem_to_float<DT>(x[(int64_t)d * C + c0 + lane]) : 0.0f;
+  }
+  __syncthreads();
+  for (int j = warp; j < kColsT && c0 + j < C; j += kThreads / 32) {
+    Run8 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.v[i] = tile[j * kStrideT + lane * 8 + i];
+    write_panel(a, b * C + c0 + j, panel, v);
+  }
+}
+
+int size_of(int dtype) { return dtype == kF32 ? 4 : 2; }
+
+template <typename K>
+cudaError_t go(K kernel, const MxQuantArgs& a, cudaStream_t s) {
+  const int panels = a.Dp / kMxPanel;
+  const int64_t warps = (int64_t)a.R * panels;
+  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, panels);
+}
+
+template <int DT>
+cudaError_t quantize_typed(const MxQuantArgs& a, cudaStream_t s) {
+  switch (access_bytes(a.x, a.ld_x * size_of(DT), (int64_t)a.D * size_of(DT))) {
+    case 16: return go(quantize_kernel<DT, 16>, a, s);
+    case 8: return go(quantize_kernel<DT, 8>, a, s);
+    case 4: return go(quantize_kernel<DT, 4>, a, s);
+    default: break;
+  }
+  if constexpr (DT != kF32) return go(quantize_kernel<DT, 2>, a, s);
+  return cudaErrorInvalidValue;
+}
+template <int DT>
+cudaError_t restore_typed(const MxQuantArgs& a, cudaStream_t s) {
+  switch (access_bytes(a.out, a.ld_out * size_of(DT), (int64_t)a.D * size_of(DT))) {
+    case 16: return go(restore_kernel<DT, 16>, a, s);
+    case 8: return go(restore_kernel<DT, 8>, a, s);
+    case 4: return go(restore_kernel<DT, 4>, a, s);
+    default: break;
+  }
+  if constexpr (DT != kF32) return go(restore_kernel<DT, 2>, a, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, cudaStream_t s) {
+  return dtype == kF32    ? quantize_typed<kF32>(a, s)
+         : dtype == kBf16 ? quantize_typed<kBf16>(a, s)
+                          : quantize_typed<kF16>(a, s);
+}
+cudaError_t launch_mx_restore(const MxQuantArgs& a, int dtype, cudaStream_t s) {
+  return dtype == kF32    ? restore_typed<kF32>(a, s)
+         : dtype == kBf16 ? restore_typed<kBf16>(a, s)
+                          : restore_typed<kF16>(a, s);
+}
+cudaError_t launch_mx_quantize_t(const MxQuantArgs& a, int C, int dtype, cudaStream_t s) {
+  const dim3 grid((C + kColsT - 1) / kColsT, a.Dp / kMxPanel, a.R / C);
+  return dtype == kF32
+             ? launch_pdl(quantize_t_kernel<kF32>, grid, dim3(kThreads), 0, s, a, C)
+         : dtype == kBf16
+             ? launch_pdl(quantize_t_kernel<kBf16>, grid, dim3(kThreads), 0, s, a, C)
+             : launch_pdl(quantize_t_kernel<kF16>, grid, dim3(kThreads), 0, s, a, C);
+}
+
+}  // namespace moe

@@ -1,0 +1,388 @@
+"""A differentiable pass through routed experts: routes sorted by expert, token rows to the
+experts and back, activations kept in 8 bits, products in microscaled FP4, and MxExperts,
+which runs them together.
+
+Formulas, layouts and limits are in include/moe_nvfp4.h ("routed rows").  Rows may be views
+of row-strided storage; every other tensor is contiguous.  Outputs passed in are written and
+returned, else allocated on the stream of the call.  With `stream`, the inputs must be ready
+on that stream.  Nothing is recorded for autograd: the gradients are what the *_grad calls
+return.
+"""
+from collections import namedtuple
+
+import torch
+
+from . import (_DTYPE, _F32, _I32, _ID, _IDS64, ACT, MoeError, _arg, _check, _matrix, _out, _raw,
+               lib, moe_mx, padded)
+
+_U8 = (torch.uint8,)
+
+
+def _like(t, name, shape, dtype, like, stream):
+    """An output matrix: `t` (rows may be strided) or a new one; and its moe_rows."""
+    if t is None:
+        t = _out(None, name, shape, dtype, like, stream)
+    elif t.shape != torch.Size(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of "
+                         f"{t.dtype}")
+    m = _matrix(t, name)
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name}: expected a tensor on {like.device}, got {t.device}")
+    return t, m
+
+
+def _n_rows(t, like):
+    return _arg(t, "n_rows", (1,), _I32, like) if t is not None else None
+
+
+# ------------------------------------------------------------------ routes
+
+class RoutePlan(namedtuple("RoutePlan", "offsets perm inv")):
+    """Routes sorted by expert: offsets [E + 1], perm [T * K] (route of each row, -1 behind
+    the last), inv [T, K] (row of each route, -1: empty slot), all int32."""
+    __slots__ = ()
+
+    @property
+    def n_rows(self):
+        """Rows in use, a device int32 [1]: for the calls that take n_rows."""
+        return self.offsets[-1:]
+
+
+def moe_nvfp4_sort_routes_workspace_bytes(T, K, E):
+    return int(lib().moe_nvfp4_sort_routes_workspace_bytes(T, K, E))
+
+
+def sort_routes_workspace(T_max, K, E, device="cuda"):
+    """A workspace for sort_routes with up to T_max tokens."""
+    n = moe_nvfp4_sort_routes_workspace_bytes(T_max, K, E)
+    if n == 0:
+        raise MoeError(2, "moe_nvfp4_sort_routes_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sort_routes(topk_ids, E, plan=None, ws=None, stream=None):
+    """Stable counting sort of the routes topk_ids [T, K] (int32 or int64, -1: empty slot) by
+    expert: a RoutePlan.  Ids outside [-1, E) are empty slots too; moe_nvfp4_read_status(ws)
+    reports them."""
+    if topk_ids.dim() != 2 or not topk_ids.is_cuda:
+        raise ValueError("topk_ids: a 2-D tensor of the current CUDA device (no CPU path exists)")
+    ids = _arg(topk_ids, "topk_ids", topk_ids.shape, _ID, topk_ids)
+    if topk_ids.get_device() != torch.cuda.current_device():
+        raise ValueError("topk_ids: a tensor of the current CUDA device")
+    T, K = topk_ids.shape
+    if plan is None:
+        plan = RoutePlan(_out(None, "offsets", (E + 1,), torch.int32, topk_ids, stream),
+                         _out(None, "perm", (T * K,), torch.int32, topk_ids, stream),
+                         _out(None, "inv", (T, K), torch.int32, topk_ids, stream))
+    L = lib()
+    if ws is None:
+        n = L.moe_nvfp4_sort_routes_workspace_bytes(T, K, E)
+        ws = _out(None, "ws", (n,), torch.uint8, topk_ids, stream)
+    else:
+        n = ws.numel()
+    _check(L.moe_nvfp4_sort_routes(
+        T, K, E, ids, _IDS64[topk_ids.dtype],
+        _arg(plan.offsets, "offsets", (E + 1,), _I32, topk_ids),
+        _arg(plan.perm, "perm", (T * K,), _I32, topk_ids),
+        _arg(plan.inv, "inv", topk_ids.shape, _I32, topk_ids),
+        _arg(ws, "ws", ws.shape, _U8, topk_ids), n, _raw(stream)), "moe_nvfp4_sort_routes")
+    return plan
+
+
+def dispatch(x, plan, rows=None, stream=None):
+    """Token rows x [T, H] to their routes' rows [T * K, H]; x may be an MxTensor.  Rows behind
+    the last route are left as they were (a new tensor's: undefined)."""
+    T, K = plan.inv.shape
+    if x.shape[0] != T:
+        raise ValueError(f"x: expected {T} rows, got {x.shape[0]}")
+    if isinstance(x, MxTensor):
+        out = rows if rows is not None else MxTensor.empty((T * K, x.shape[1]), x.codes, stream)
+        inv = _arg(plan.inv, "inv", (T, K), _I32, x.codes)
+        _check(lib().moe_nvfp4_mx_dispatch(x._c(), K, inv, out._c(), _raw(stream)),
+               "moe_nvfp4_mx_dispatch")
+        return out
+    m = _matrix(x, "x")
+    rows, mo = _like(rows, "rows", (T * K, x.shape[1]), x.dtype, x, stream)
+    _check(lib().moe_nvfp4_dispatch(m, K, _arg(plan.inv, "inv", (T, K), _I32, x), mo.data, mo.ld,
+                                    _raw(stream)), "moe_nvfp4_dispatch")
+    return rows
+
+
+def combine(rows, plan, topk_w=None, out=None, stream=None):
+    """Route rows [T * K, H] back to their tokens [T, H], times topk_w fp32 [T, K] (None: 1)."""
+    m = _matrix(rows, "rows")
+    T, K = plan.inv.shape
+    out, mo = _like(out, "out", (T, rows.shape[1]), rows.dtype, rows, stream)
+    _check(lib().moe_nvfp4_combine(m, T, K, _arg(plan.inv, "inv", (T, K), _I32, rows),
+                                   _arg(topk_w, "topk_w", (T, K), _F32, rows), mo.data, mo.ld,
+                                   _raw(stream)), "moe_nvfp4_combine")
+    return out
+
+
+def dispatch_grad(drows, plan, dx=None, stream=None):
+    """Gradient [T, H] of dispatch: the sum of each token's route rows."""
+    return combine(drows, plan, None, dx, stream)
+
+
+def combine_grad(rows, plan, topk_w, dout, drows=None, d_topk_w=None, stream=None):
+    """Gradients of combine: (drows [T * K, H], d_topk_w [T, K] fp32).  drows may be the rows
+    tensor itself; its rows behind the last route are left as they were."""
+    m = _matrix(rows, "rows")
+    T, K = plan.inv.shape
+    if dout.shape != (T, rows.shape[1]) or dout.dtype != rows.dtype:
+        raise ValueError("dout: one row per token, of the rows' length and type")
+    md = _matrix(dout, "dout")
+    drows, mo = _like(drows, "drows", rows.shape, rows.dtype, rows, stream)
+    dw = _out(d_topk_w, "d_topk_w", (T, K), torch.float32, rows, stream)
+    _check(lib().moe_nvfp4_combine_grad(m, T, K, _arg(plan.inv, "inv", (T, K), _I32, rows),
+                                        _arg(topk_w, "topk_w", (T, K), _F32, rows), md.data, md.ld,
+                                        mo.data, mo.ld, dw.data_ptr(), _raw(stream)),
+           "moe_nvfp4_combine_grad")
+    return drows, dw
+
+
+# ------------------------------------------------------------------ 8 bits
+
+class Checkpoint(namedtuple("Checkpoint", "codes scales cols dtype act swiglu_limit")):
+    """Rows kept in 8 bits: codes [R, halves, W32] and scales [R, halves, W32 / 32] uint8, of
+    `cols` values a half.  act: None for checkpoint's, else the activation whose input it is."""
+    __slots__ = ()
+
+    @staticmethod
+    def empty(R, cols, dtype, like, act=None, swiglu_limit=0.0, stream=None):
+        halves, w = 2 if act == "swiglu" else 1, (cols + 31) // 32 * 32
+        return Checkpoint(_out(None, "codes", (R, halves, w), torch.uint8, like, stream),
+                          _out(None, "scales", (R, halves, w // 32), torch.uint8, like, stream),
+                          cols, dtype, act, swiglu_limit)
+
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+    def _ptrs(self, R, cols, halves, like):
+        w = (cols + 31) // 32 * 32
+        return (_arg(self.codes, "codes", (R, halves, w), _U8, like),
+                _arg(self.scales, "scales", (R, halves, w // 32), _U8, like))
+
+
+def checkpoint(x, kept=None, n_rows=None, stream=None):
+    """Rows x [R, D] in 8 bits (E4M3, a power of two per 32 values): a Checkpoint."""
+    m = _matrix(x, "x")
+    R, D = x.shape
+    kept = kept if kept is not None else Checkpoint.empty(R, D, x.dtype, x, stream=stream)
+    codes, scales = kept._ptrs(R, D, 1, x)
+    _check(lib().moe_nvfp4_checkpoint(m, codes, scales, _n_rows(n_rows, x), _raw(stream)),
+           "moe_nvfp4_checkpoint")
+    return kept
+
+
+def restore(kept, dtype=None, out=None, n_rows=None, stream=None):
+    """The rows that checkpoint kept, of `dtype` (None: the type they had)."""
+    if kept.act is not None:
+        raise ValueError("kept: an activation's input is read by expert_act_grad")
+    R = kept.codes.shape[0]
+    out, mo = _like(out, "out", (R, kept.cols), dtype or kept.dtype, kept.codes, stream)
+    codes, scales = kept._ptrs(R, kept.cols, 1, out)
+    _check(lib().moe_nvfp4_restore(codes, scales, mo, _n_rows(n_rows, out), _raw(stream)),
+           "moe_nvfp4_restore")
+    return out
+
+
+def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_rows=None,
+               stream=None):
+    """The experts' activation of FC1 rows h: [R, 2I] = [gate | up] ("swiglu") or [R, I]
+    ("relu2") -> y [R, I].  With checkpoint (or `kept`, a Checkpoint to fill) h is kept in 8
+    bits for expert_act_grad: (y, kept), else y."""
+    m = _matrix(h, "h")
+    halves = 2 if act == "swiglu" else 1
+    R, I = h.shape[0], h.shape[1] // halves
+    y, my = _like(y, "y", (R, I), h.dtype, h, stream)
+    codes = scales = None
+    if kept is None and checkpoint:
+        kept = Checkpoint.empty(R, I, h.dtype, h, act, float(swiglu_limit), stream)
+    if kept is not None:
+        if kept.act != act or kept.swiglu_limit != float(swiglu_limit):
+            raise ValueError("kept: made for another activation")
+        codes, scales = kept._ptrs(R, I, halves, h)
+    _check(lib().moe_nvfp4_expert_act(m, ACT[act], swiglu_limit, my.data, my.ld, codes, scales,
+                                      _n_rows(n_rows, h), _raw(stream)), "moe_nvfp4_expert_act")
+    return y if kept is None else (y, kept)
+
+
+def expert_act_grad(kept, dy, dh=None, n_rows=None, stream=None):
+    """Gradient of expert_act at the values that `kept` holds: dy [R, I] -> dh [R, 2I] (swiglu)
+    or [R, I], of dy's type."""
+    if kept.act is None:
+        raise ValueError("kept: expected what expert_act kept")
+    m = _matrix(dy, "dy")
+    R, I = dy.shape
+    if I != kept.cols:
+        raise ValueError(f"dy: expected rows of {kept.cols}, got {I}")
+    halves = 2 if kept.act == "swiglu" else 1
+    codes, scales = kept._ptrs(R, I, halves, dy)
+    dh, mo = _like(dh, "dh", (R, halves * I), dy.dtype, dy, stream)
+    _check(lib().moe_nvfp4_expert_act_grad(codes, scales, ACT[kept.act], kept.swiglu_limit, m,
+                                           mo.data, mo.ld, _n_rows(n_rows, dy), _raw(stream)),
+           "moe_nvfp4_expert_act_grad")
+    return dh
+
+
+# ------------------------------------------------------------------ microscaled FP4
+
+class MxTensor(namedtuple("MxTensor", "codes scales shape")):
+    """A matrix [R, D], or a stack [E, N, D], in microscaled FP4: codes uint8 [rows, Dp / 2] and
+    scales uint8 [Dp / 256, Rp, 8] (Dp: D rounded up to 256, rows: R or E * N, Rp: rows rounded
+    up to even; layouts in include/moe_nvfp4.h)."""
+    __slots__ = ()
+
+    @staticmethod
+    def empty(shape, like, stream=None):
+        rows, dp = _mx_rows(shape), padded(shape[-1])
+        return MxTensor(_out(None, "codes", (rows, dp // 2), torch.uint8, like, stream),
+                        _out(None, "scales", (dp // 256, (rows + 1) // 2 * 2, 8), torch.uint8,
+                             like, stream), tuple(shape))
+
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+    def _c(self):
+        rows, dp = _mx_rows(self.shape), padded(self.shape[-1])
+        if not self.codes.is_cuda or self.codes.get_device() != torch.cuda.current_device():
+            raise ValueError("codes: a tensor of the current CUDA device (no CPU path exists)")
+        return moe_mx(_arg(self.codes, "codes", (rows, dp // 2), _U8, self.codes),
+                      _arg(self.scales, "scales", (dp // 256, (rows + 1) // 2 * 2, 8), _U8,
+                           self.codes), rows, self.shape[-1])
+
+
+def _mx_rows(shape):
+    if len(shape) not in (2, 3):
+        raise ValueError("shape: [rows, D] or [E, N, D]")
+    return shape[0] * shape[1] if len(shape) == 3 else shape[0]
+
+
+def mx_quantize(x, out=None, n_rows=None, stream=None):
+    """x [R, D] (rows may be strided) or [E, N, D] (contiguous) in microscaled FP4 (E2M1, a power
+    of two per 32 values of a row): an MxTensor."""
+    shape = tuple(x.shape)
+    if x.dim() == 3:
+        if not x.is_contiguous():
+            raise ValueError("x: a stack must be contiguous")
+        x = x.view(-1, shape[2])
+    m = _matrix(x, "x")
+    out = out if out is not None else MxTensor.empty(shape, x, stream)
+    if out.shape != shape:
+        raise ValueError(f"out: expected {shape}, got {out.shape}")
+    _check(lib().moe_nvfp4_mx_quantize(m, out._c(), _n_rows(n_rows, x), _raw(stream)),
+           "moe_nvfp4_mx_quantize")
+    return out
+
+
+def mx_quantize_transposed(x, out=None, stream=None):
+    """A stack x [E, D, C] (or a matrix [D, C]), transposed: an MxTensor of [E, C, D], scaled along
+    D."""
+    if x.dim() not in (2, 3) or x.dtype not in _DTYPE or not x.is_contiguous():
+        raise ValueError("x: a contiguous float32, bfloat16 or float16 stack [E, D, C] or matrix")
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError("x: a tensor of the current CUDA device (no CPU path exists)")
+    D, C = x.shape[-2:]
+    shape = (x.shape[0], C, D) if x.dim() == 3 else (C, D)
+    out = out if out is not None else MxTensor.empty(shape, x, stream)
+    if out.shape != shape:
+        raise ValueError(f"out: expected {shape}, got {out.shape}")
+    _check(lib().moe_nvfp4_mx_quantize_transposed(x.shape[0] if x.dim() == 3 else 1, D, C,
+                                                  x.data_ptr(), _DTYPE[x.dtype], out._c(),
+                                                  _raw(stream)),
+           "moe_nvfp4_mx_quantize_transposed")
+    return out
+
+
+def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
+    """The values of an MxTensor, as a tensor of its shape."""
+    c = x._c()
+    out, mo = _like(out, "out", (c.rows, c.cols), dtype, x.codes, stream)
+    _check(lib().moe_nvfp4_mx_restore(c, mo, _n_rows(n_rows, out), _raw(stream)),
+           "moe_nvfp4_mx_restore")
+    return out.view(x.shape) if out.is_contiguous() else out
+
+
+def _product_args(x, w, offsets, dtype, out, stream):
+    if len(x.shape) != 2:
+        raise ValueError("x: an MxTensor of rows [R, D]")
+    E, N = (w.shape[0], w.shape[1]) if len(w.shape) == 3 else (1, w.shape[0])
+    if E > 1 and offsets is None:
+        raise ValueError("offsets: needed for a stack of weights")
+    cx, cw = x._c(), w._c()
+    off = None if offsets is None else _arg(offsets, "offsets", (E + 1,), _I32, x.codes)
+    if w.codes.get_device() != x.codes.get_device():
+        raise ValueError("w: expected a tensor on the rows' device")
+    out, mo = _like(out, "out", (x.shape[0], N), out.dtype if out is not None else dtype, x.codes,
+                    stream)
+    return out, mo, (cx, cw, E, off)
+
+
+def mx_product(x, w, offsets=None, dtype=torch.bfloat16, out=None, stream=None):
+    """x [R, D] times the weights of each row's expert: w [E, N, D] with offsets int32 [E + 1]
+    (RoutePlan.offsets), or one matrix [N, D].  -> [R, N] of `dtype`; rows outside the groups
+    are left as they were."""
+    out, mo, args = _product_args(x, w, offsets, dtype, out, stream)
+    _check(lib().moe_nvfp4_mx_product(*args, mo.dtype, mo.data, mo.ld, _raw(stream)),
+           "moe_nvfp4_mx_product")
+    return out
+
+
+def moe_nvfp4_selftest_product_timeout(x, w, offsets, item, dtype=torch.bfloat16):
+    """mx_product by a kernel whose row loads leave before work item `item`
+    (include/moe_nvfp4.h)."""
+    out, mo, args = _product_args(x, w, offsets, dtype, None, None)
+    _check(lib().moe_nvfp4_selftest_product_timeout(*args, item, mo.dtype, mo.data, mo.ld,
+                                                    _raw(None)),
+           "moe_nvfp4_selftest_product_timeout")
+    return out
+
+
+# ------------------------------------------------------------------ together
+
+class MxExperts:
+    """Routed experts in microscaled FP4 through which gradients pass: the weights stay frozen,
+    forward keeps the activations' input in 8 bits, and backward returns the gradients of the
+    tokens and of the routing weights.
+
+    fc1 [E, N1, H] ([gate; up] for "swiglu"), fc2 [E, H, I].  backward multiplies with the
+    transposed stacks, quantised along their other side (quantisation itself passes gradients
+    through unchanged).  y = combine(FC2(act(FC1(x)))).
+    """
+
+    def __init__(self, fc1, fc2, act, swiglu_limit=0.0, stream=None):
+        E, N1, H = fc1.shape
+        I = N1 // 2 if act == "swiglu" else N1
+        if fc2.shape != (E, H, I):
+            raise ValueError(f"fc2: expected {(E, H, I)}, got {tuple(fc2.shape)}")
+        self.E, self.H, self.I, self.act, self.limit = E, H, I, act, float(swiglu_limit)
+        self.fc1, self.fc2 = mx_quantize(fc1, stream=stream), mx_quantize(fc2, stream=stream)
+        self.fc1_t = mx_quantize_transposed(fc1, stream=stream)
+        self.fc2_t = mx_quantize_transposed(fc2, stream=stream)
+
+    def forward(self, x, topk_ids, topk_w, keep=True, stream=None):
+        """x [T, H], topk_ids [T, K], topk_w fp32 [T, K] -> (y [T, H], saved for backward)."""
+        plan = sort_routes(topk_ids, self.E, stream=stream)
+        n, dt = plan.n_rows, x.dtype
+        # a token's codes are the same on each of its routes: quantised once, then copied
+        xq = dispatch(mx_quantize(x, stream=stream), plan, stream=stream)
+        h = mx_product(xq, self.fc1, plan.offsets, dt, stream=stream)
+        a, kept = expert_act(h, self.act, self.limit, True, n_rows=n, stream=stream) if keep else (
+            expert_act(h, self.act, self.limit, n_rows=n, stream=stream), None)
+        rows = mx_product(mx_quantize(a, n_rows=n, stream=stream), self.fc2, plan.offsets, dt,
+                          stream=stream)
+        y = combine(rows, plan, topk_w, stream=stream)
+        return y, (plan, rows, kept, topk_w)
+
+    def backward(self, saved, dy, stream=None):
+        """dy [T, H] -> (dx [T, H], d_topk_w [T, K] fp32).  Uses saved rows' storage: once."""
+        plan, rows, kept, topk_w = saved
+        n, dt = plan.n_rows, dy.dtype
+        drows, dw = combine_grad(rows, plan, topk_w, dy, drows=rows, stream=stream)
+        da = mx_product(mx_quantize(drows, n_rows=n, stream=stream), self.fc2_t, plan.offsets, dt,
+                        stream=stream)
+        dh = expert_act_grad(kept, da, n_rows=n, stream=stream)
+        dxr = mx_product(mx_quantize(dh, n_rows=n, stream=stream), self.fc1_t, plan.offsets, dt,
+                         stream=stream)
+        return dispatch_grad(dxr, plan, stream=stream), dw
