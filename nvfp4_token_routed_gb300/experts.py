@@ -13,22 +13,23 @@ from collections import namedtuple
 import torch
 
 from . import (_DTYPE, _F32, _I32, _ID, _IDS64, ACT, MoeError, _arg, _check, _matrix, _out, _raw,
-               lib, moe_mx, padded)
+               lib, moe_logits, moe_mx, padded)
 
 _U8 = (torch.uint8,)
 
 
 def _like(t, name, shape, dtype, like, stream):
-    """An output matrix: `t` (rows may be strided) or a new one; and its moe_rows."""
+    """An output matrix: `t` (rows may be strided) or a new one; its address and row stride."""
     if t is None:
         t = _out(None, name, shape, dtype, like, stream)
-    elif t.shape != torch.Size(shape) or t.dtype != dtype:
+        return t, t.data_ptr(), shape[1]
+    if t.shape != torch.Size(shape) or t.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of "
                          f"{t.dtype}")
     m = _matrix(t, name)
     if t.get_device() != like.get_device():
         raise ValueError(f"{name}: expected a tensor on {like.device}, got {t.device}")
-    return t, m
+    return t, m.data, m.ld
 
 
 def _n_rows(t, like):
@@ -96,14 +97,16 @@ def dispatch(x, plan, rows=None, stream=None):
     if x.shape[0] != T:
         raise ValueError(f"x: expected {T} rows, got {x.shape[0]}")
     if isinstance(x, MxTensor):
-        out = rows if rows is not None else MxTensor.empty((T * K, x.shape[1]), x.codes, stream)
-        inv = _arg(plan.inv, "inv", (T, K), _I32, x.codes)
-        _check(lib().moe_nvfp4_mx_dispatch(x._c(), K, inv, out._c(), _raw(stream)),
+        inv = _arg(plan.inv, "inv", (T, K), _I32, x.on())
+        if rows is None:
+            rows = MxTensor.empty((T * K, x.shape[1]), x.on(), stream)
+        rows.on(x)
+        _check(lib().moe_nvfp4_mx_dispatch(x.c, K, inv, rows.c, _raw(stream)),
                "moe_nvfp4_mx_dispatch")
-        return out
+        return rows
     m = _matrix(x, "x")
-    rows, mo = _like(rows, "rows", (T * K, x.shape[1]), x.dtype, x, stream)
-    _check(lib().moe_nvfp4_dispatch(m, K, _arg(plan.inv, "inv", (T, K), _I32, x), mo.data, mo.ld,
+    rows, p, ld = _like(rows, "rows", (T * K, x.shape[1]), x.dtype, x, stream)
+    _check(lib().moe_nvfp4_dispatch(m, K, _arg(plan.inv, "inv", (T, K), _I32, x), p, ld,
                                     _raw(stream)), "moe_nvfp4_dispatch")
     return rows
 
@@ -112,9 +115,9 @@ def combine(rows, plan, topk_w=None, out=None, stream=None):
     """Route rows [T * K, H] back to their tokens [T, H], times topk_w fp32 [T, K] (None: 1)."""
     m = _matrix(rows, "rows")
     T, K = plan.inv.shape
-    out, mo = _like(out, "out", (T, rows.shape[1]), rows.dtype, rows, stream)
+    out, p, ld = _like(out, "out", (T, rows.shape[1]), rows.dtype, rows, stream)
     _check(lib().moe_nvfp4_combine(m, T, K, _arg(plan.inv, "inv", (T, K), _I32, rows),
-                                   _arg(topk_w, "topk_w", (T, K), _F32, rows), mo.data, mo.ld,
+                                   _arg(topk_w, "topk_w", (T, K), _F32, rows), p, ld,
                                    _raw(stream)), "moe_nvfp4_combine")
     return out
 
@@ -132,44 +135,105 @@ def combine_grad(rows, plan, topk_w, dout, drows=None, d_topk_w=None, stream=Non
     if dout.shape != (T, rows.shape[1]) or dout.dtype != rows.dtype:
         raise ValueError("dout: one row per token, of the rows' length and type")
     md = _matrix(dout, "dout")
-    drows, mo = _like(drows, "drows", rows.shape, rows.dtype, rows, stream)
+    drows, p, ld = _like(drows, "drows", rows.shape, rows.dtype, rows, stream)
     dw = _out(d_topk_w, "d_topk_w", (T, K), torch.float32, rows, stream)
     _check(lib().moe_nvfp4_combine_grad(m, T, K, _arg(plan.inv, "inv", (T, K), _I32, rows),
                                         _arg(topk_w, "topk_w", (T, K), _F32, rows), md.data, md.ld,
-                                        mo.data, mo.ld, dw.data_ptr(), _raw(stream)),
+                                        p, ld, dw.data_ptr(), _raw(stream)),
            "moe_nvfp4_combine_grad")
     return drows, dw
 
 
 # ------------------------------------------------------------------ 8 bits
 
-class Checkpoint(namedtuple("Checkpoint", "codes scales cols dtype act swiglu_limit")):
-    """Rows kept in 8 bits: codes [R, halves, W32] and scales [R, halves, W32 / 32] uint8, of
-    `cols` values a half.  act: None for checkpoint's, else the activation whose input it is."""
-    __slots__ = ()
+class _Held:
+    """Codes and scales on one device: two tensors, or one buffer that they are cut from when
+    asked for (an allocation and two views less a call)."""
+    __slots__ = ("_codes", "_scales", "_buf", "_cut", "device")
 
-    @staticmethod
-    def empty(R, cols, dtype, like, act=None, swiglu_limit=0.0, stream=None):
-        halves, w = 2 if act == "swiglu" else 1, (cols + 31) // 32 * 32
-        return Checkpoint(_out(None, "codes", (R, halves, w), torch.uint8, like, stream),
-                          _out(None, "scales", (R, halves, w // 32), torch.uint8, like, stream),
-                          cols, dtype, act, swiglu_limit)
+    def _set(self, codes, scales, codes_shape, scales_shape):
+        if not codes.is_cuda and not scales.is_cuda:
+            self.device = -1  # described, not used: the calls refuse it
+        else:
+            self.device = codes.get_device()
+        self._codes, self._scales, self._buf, self._cut = codes, scales, None, None
+        return (_arg(codes, "codes", torch.Size(codes_shape), _U8, codes),
+                _arg(scales, "scales", torch.Size(scales_shape), _U8, codes))
+
+    def _alloc(self, codes_shape, scales_shape, n_codes, n_scales, like, stream):
+        at = (n_codes + 255) // 256 * 256
+        self._buf = buf = _out(None, "codes", (at + n_scales,), torch.uint8, like, stream)
+        self._codes = self._scales = None
+        self._cut = codes_shape, scales_shape, n_codes, n_scales, at
+        self.device = like.get_device()
+        p = buf.data_ptr()
+        return p, p + at
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self._cut[2]].view(self._cut[0])
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buf[self._cut[4]:].view(self._cut[1])
+        return self._scales
 
     def nbytes(self):
         return self.codes.numel() + self.scales.numel()
 
-    def _ptrs(self, R, cols, halves, like):
+    def on(self, like=None):
+        """A tensor of it, on the current device (and on `like`'s)."""
+        t = self._buf if self._buf is not None else self._codes
+        if self.device != torch.cuda.current_device() or self.device < 0:
+            raise ValueError("codes: a tensor of the current CUDA device (no CPU path exists)")
+        if like is not None and self.device != (like.device if isinstance(like, _Held)
+                                                else like.get_device()):
+            raise ValueError(f"codes: on device {self.device}, other arguments on another")
+        return t
+
+
+class Checkpoint(_Held):
+    """Rows kept in 8 bits: codes [R, halves, W32] and scales [R, halves, W32 / 32] uint8, of
+    `cols` values a half.  act: None for checkpoint's, else the activation whose input it is."""
+    __slots__ = ("rows", "halves", "cols", "dtype", "act", "swiglu_limit", "c")
+
+    def __init__(self, codes, scales, cols, dtype, act=None, swiglu_limit=0.0):
+        self._about(codes.shape[0], cols, dtype, act, swiglu_limit)
         w = (cols + 31) // 32 * 32
-        return (_arg(self.codes, "codes", (R, halves, w), _U8, like),
-                _arg(self.scales, "scales", (R, halves, w // 32), _U8, like))
+        self.c = self._set(codes, scales, (self.rows, self.halves, w),
+                           (self.rows, self.halves, w // 32))
+
+    def _about(self, rows, cols, dtype, act, swiglu_limit):
+        self.rows, self.cols, self.dtype, self.act = rows, cols, dtype, act
+        self.halves, self.swiglu_limit = 2 if act == "swiglu" else 1, float(swiglu_limit)
+
+    @classmethod
+    def empty(cls, rows, cols, dtype, like, act=None, swiglu_limit=0.0, stream=None):
+        k = cls.__new__(cls)
+        k._about(rows, cols, dtype, act, swiglu_limit)
+        b, h = (cols + 31) // 32, k.halves
+        k.c = k._alloc((rows, h, 32 * b), (rows, h, b), 32 * rows * h * b, rows * h * b, like, stream)
+        return k
+
+    def _for(self, rows, cols, like):
+        if self.rows != rows or self.cols != cols:
+            raise ValueError(f"kept: holds {self.rows} rows of {self.cols}, got {rows} of {cols}")
+        self.on(like)
+        return self.c
 
 
 def checkpoint(x, kept=None, n_rows=None, stream=None):
     """Rows x [R, D] in 8 bits (E4M3, a power of two per 32 values): a Checkpoint."""
     m = _matrix(x, "x")
     R, D = x.shape
-    kept = kept if kept is not None else Checkpoint.empty(R, D, x.dtype, x, stream=stream)
-    codes, scales = kept._ptrs(R, D, 1, x)
+    if kept is None:
+        kept = Checkpoint.empty(R, D, x.dtype, x, stream=stream)
+    elif kept.act is not None:
+        raise ValueError("kept: made for an activation's input")
+    codes, scales = kept._for(R, D, x)
     _check(lib().moe_nvfp4_checkpoint(m, codes, scales, _n_rows(n_rows, x), _raw(stream)),
            "moe_nvfp4_checkpoint")
     return kept
@@ -179,11 +243,13 @@ def restore(kept, dtype=None, out=None, n_rows=None, stream=None):
     """The rows that checkpoint kept, of `dtype` (None: the type they had)."""
     if kept.act is not None:
         raise ValueError("kept: an activation's input is read by expert_act_grad")
-    R = kept.codes.shape[0]
-    out, mo = _like(out, "out", (R, kept.cols), dtype or kept.dtype, kept.codes, stream)
-    codes, scales = kept._ptrs(R, kept.cols, 1, out)
-    _check(lib().moe_nvfp4_restore(codes, scales, mo, _n_rows(n_rows, out), _raw(stream)),
-           "moe_nvfp4_restore")
+    R, D, dtype = kept.rows, kept.cols, dtype or kept.dtype
+    if dtype not in _DTYPE:
+        raise ValueError("dtype: float32, bfloat16 or float16")
+    out, p, ld = _like(out, "out", (R, D), dtype, kept.on(), stream)
+    codes, scales = kept.c
+    _check(lib().moe_nvfp4_restore(codes, scales, moe_logits(p, ld, R, D, _DTYPE[dtype]),
+                                   _n_rows(n_rows, out), _raw(stream)), "moe_nvfp4_restore")
     return out
 
 
@@ -195,15 +261,15 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
     m = _matrix(h, "h")
     halves = 2 if act == "swiglu" else 1
     R, I = h.shape[0], h.shape[1] // halves
-    y, my = _like(y, "y", (R, I), h.dtype, h, stream)
+    y, p, ld = _like(y, "y", (R, I), h.dtype, h, stream)
     codes = scales = None
     if kept is None and checkpoint:
-        kept = Checkpoint.empty(R, I, h.dtype, h, act, float(swiglu_limit), stream)
+        kept = Checkpoint.empty(R, I, h.dtype, h, act, swiglu_limit, stream)
     if kept is not None:
         if kept.act != act or kept.swiglu_limit != float(swiglu_limit):
             raise ValueError("kept: made for another activation")
-        codes, scales = kept._ptrs(R, I, halves, h)
-    _check(lib().moe_nvfp4_expert_act(m, ACT[act], swiglu_limit, my.data, my.ld, codes, scales,
+        codes, scales = kept._for(R, I, h)
+    _check(lib().moe_nvfp4_expert_act(m, ACT[act], swiglu_limit, p, ld, codes, scales,
                                       _n_rows(n_rows, h), _raw(stream)), "moe_nvfp4_expert_act")
     return y if kept is None else (y, kept)
 
@@ -215,42 +281,38 @@ def expert_act_grad(kept, dy, dh=None, n_rows=None, stream=None):
         raise ValueError("kept: expected what expert_act kept")
     m = _matrix(dy, "dy")
     R, I = dy.shape
-    if I != kept.cols:
-        raise ValueError(f"dy: expected rows of {kept.cols}, got {I}")
-    halves = 2 if kept.act == "swiglu" else 1
-    codes, scales = kept._ptrs(R, I, halves, dy)
-    dh, mo = _like(dh, "dh", (R, halves * I), dy.dtype, dy, stream)
+    codes, scales = kept._for(R, I, dy)
+    dh, p, ld = _like(dh, "dh", (R, kept.halves * I), dy.dtype, dy, stream)
     _check(lib().moe_nvfp4_expert_act_grad(codes, scales, ACT[kept.act], kept.swiglu_limit, m,
-                                           mo.data, mo.ld, _n_rows(n_rows, dy), _raw(stream)),
+                                           p, ld, _n_rows(n_rows, dy), _raw(stream)),
            "moe_nvfp4_expert_act_grad")
     return dh
 
 
 # ------------------------------------------------------------------ microscaled FP4
 
-class MxTensor(namedtuple("MxTensor", "codes scales shape")):
+class MxTensor(_Held):
     """A matrix [R, D], or a stack [E, N, D], in microscaled FP4: codes uint8 [rows, Dp / 2] and
     scales uint8 [Dp / 256, Rp, 8] (Dp: D rounded up to 256, rows: R or E * N, Rp: rows rounded
     up to even; layouts in include/moe_nvfp4.h)."""
-    __slots__ = ()
+    __slots__ = ("shape", "c")
 
-    @staticmethod
-    def empty(shape, like, stream=None):
+    def __init__(self, codes, scales, shape):
+        self.shape = shape = tuple(shape)
         rows, dp = _mx_rows(shape), padded(shape[-1])
-        return MxTensor(_out(None, "codes", (rows, dp // 2), torch.uint8, like, stream),
-                        _out(None, "scales", (dp // 256, (rows + 1) // 2 * 2, 8), torch.uint8,
-                             like, stream), tuple(shape))
+        p, q = self._set(codes, scales, (rows, dp // 2), (dp // 256, (rows + 1) // 2 * 2, 8))
+        self.c = moe_mx(p, q, rows, shape[-1])
 
-    def nbytes(self):
-        return self.codes.numel() + self.scales.numel()
-
-    def _c(self):
-        rows, dp = _mx_rows(self.shape), padded(self.shape[-1])
-        if not self.codes.is_cuda or self.codes.get_device() != torch.cuda.current_device():
-            raise ValueError("codes: a tensor of the current CUDA device (no CPU path exists)")
-        return moe_mx(_arg(self.codes, "codes", (rows, dp // 2), _U8, self.codes),
-                      _arg(self.scales, "scales", (dp // 256, (rows + 1) // 2 * 2, 8), _U8,
-                           self.codes), rows, self.shape[-1])
+    @classmethod
+    def empty(cls, shape, like, stream=None):
+        t = cls.__new__(cls)
+        t.shape = shape
+        rows, dp = _mx_rows(shape), padded(shape[-1])
+        rp = rows + (rows & 1)
+        p, q = t._alloc((rows, dp // 2), (dp // 256, rp, 8), rows * (dp // 2), rp * (dp // 32),
+                        like, stream)
+        t.c = moe_mx(p, q, rows, shape[-1])
+        return t
 
 
 def _mx_rows(shape):
@@ -259,19 +321,26 @@ def _mx_rows(shape):
     return shape[0] * shape[1] if len(shape) == 3 else shape[0]
 
 
+def _mx_out(out, shape, x, stream):
+    if out is None:
+        return MxTensor.empty(shape, x, stream)
+    if out.shape != shape:
+        raise ValueError(f"out: expected {shape}, got {out.shape}")
+    out.on(x)
+    return out
+
+
 def mx_quantize(x, out=None, n_rows=None, stream=None):
     """x [R, D] (rows may be strided) or [E, N, D] (contiguous) in microscaled FP4 (E2M1, a power
     of two per 32 values of a row): an MxTensor."""
     shape = tuple(x.shape)
-    if x.dim() == 3:
+    if len(shape) == 3:
         if not x.is_contiguous():
             raise ValueError("x: a stack must be contiguous")
         x = x.view(-1, shape[2])
     m = _matrix(x, "x")
-    out = out if out is not None else MxTensor.empty(shape, x, stream)
-    if out.shape != shape:
-        raise ValueError(f"out: expected {shape}, got {out.shape}")
-    _check(lib().moe_nvfp4_mx_quantize(m, out._c(), _n_rows(n_rows, x), _raw(stream)),
+    out = _mx_out(out, shape, x, stream)
+    _check(lib().moe_nvfp4_mx_quantize(m, out.c, _n_rows(n_rows, x), _raw(stream)),
            "moe_nvfp4_mx_quantize")
     return out
 
@@ -285,11 +354,9 @@ def mx_quantize_transposed(x, out=None, stream=None):
         raise ValueError("x: a tensor of the current CUDA device (no CPU path exists)")
     D, C = x.shape[-2:]
     shape = (x.shape[0], C, D) if x.dim() == 3 else (C, D)
-    out = out if out is not None else MxTensor.empty(shape, x, stream)
-    if out.shape != shape:
-        raise ValueError(f"out: expected {shape}, got {out.shape}")
+    out = _mx_out(out, shape, x, stream)
     _check(lib().moe_nvfp4_mx_quantize_transposed(x.shape[0] if x.dim() == 3 else 1, D, C,
-                                                  x.data_ptr(), _DTYPE[x.dtype], out._c(),
+                                                  x.data_ptr(), _DTYPE[x.dtype], out.c,
                                                   _raw(stream)),
            "moe_nvfp4_mx_quantize_transposed")
     return out
@@ -297,11 +364,13 @@ def mx_quantize_transposed(x, out=None, stream=None):
 
 def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
     """The values of an MxTensor, as a tensor of its shape."""
-    c = x._c()
-    out, mo = _like(out, "out", (c.rows, c.cols), dtype, x.codes, stream)
-    _check(lib().moe_nvfp4_mx_restore(c, mo, _n_rows(n_rows, out), _raw(stream)),
-           "moe_nvfp4_mx_restore")
-    return out.view(x.shape) if out.is_contiguous() else out
+    if dtype not in _DTYPE:
+        raise ValueError("dtype: float32, bfloat16 or float16")
+    rows, D = x.c.rows, x.c.cols
+    out, p, ld = _like(out, "out", (rows, D), dtype, x.on(), stream)
+    _check(lib().moe_nvfp4_mx_restore(x.c, moe_logits(p, ld, rows, D, _DTYPE[dtype]),
+                                      _n_rows(n_rows, out), _raw(stream)), "moe_nvfp4_mx_restore")
+    return out.view(x.shape) if len(x.shape) == 3 and out.is_contiguous() else out
 
 
 def _product_args(x, w, offsets, dtype, out, stream):
@@ -310,31 +379,32 @@ def _product_args(x, w, offsets, dtype, out, stream):
     E, N = (w.shape[0], w.shape[1]) if len(w.shape) == 3 else (1, w.shape[0])
     if E > 1 and offsets is None:
         raise ValueError("offsets: needed for a stack of weights")
-    cx, cw = x._c(), w._c()
-    off = None if offsets is None else _arg(offsets, "offsets", (E + 1,), _I32, x.codes)
-    if w.codes.get_device() != x.codes.get_device():
-        raise ValueError("w: expected a tensor on the rows' device")
-    out, mo = _like(out, "out", (x.shape[0], N), out.dtype if out is not None else dtype, x.codes,
-                    stream)
-    return out, mo, (cx, cw, E, off)
+    like = x.on()
+    w.on(x)
+    if out is not None:
+        dtype = out.dtype
+    dt = _DTYPE.get(dtype)
+    if dt is None:
+        raise ValueError("dtype: float32, bfloat16 or float16")
+    off = None if offsets is None else _arg(offsets, "offsets", (E + 1,), _I32, like)
+    out, p, ld = _like(out, "out", (x.shape[0], N), dtype, like, stream)
+    return out, (x.c, w.c, E, off), (dt, p, ld, _raw(stream))
 
 
 def mx_product(x, w, offsets=None, dtype=torch.bfloat16, out=None, stream=None):
     """x [R, D] times the weights of each row's expert: w [E, N, D] with offsets int32 [E + 1]
     (RoutePlan.offsets), or one matrix [N, D].  -> [R, N] of `dtype`; rows outside the groups
     are left as they were."""
-    out, mo, args = _product_args(x, w, offsets, dtype, out, stream)
-    _check(lib().moe_nvfp4_mx_product(*args, mo.dtype, mo.data, mo.ld, _raw(stream)),
-           "moe_nvfp4_mx_product")
+    out, args, rest = _product_args(x, w, offsets, dtype, out, stream)
+    _check(lib().moe_nvfp4_mx_product(*args, *rest), "moe_nvfp4_mx_product")
     return out
 
 
 def moe_nvfp4_selftest_product_timeout(x, w, offsets, item, dtype=torch.bfloat16):
     """mx_product by a kernel whose row loads leave before work item `item`
     (include/moe_nvfp4.h)."""
-    out, mo, args = _product_args(x, w, offsets, dtype, None, None)
-    _check(lib().moe_nvfp4_selftest_product_timeout(*args, item, mo.dtype, mo.data, mo.ld,
-                                                    _raw(None)),
+    out, args, rest = _product_args(x, w, offsets, dtype, None, None)
+    _check(lib().moe_nvfp4_selftest_product_timeout(*args, item, *rest),
            "moe_nvfp4_selftest_product_timeout")
     return out
 
