@@ -92,7 +92,7 @@ struct MxGemmArgs {
   void* out;               // [R][N], row stride ld
   int64_t ld;
   int dtype;
-  int wide;                // out rows lie on 16 bytes
+  int wide;                // 16-bit out in runs of 4 on 8 bytes
   int leave_item;          // self-test: the token producer leaves before this item; -1: never
 };
 cudaError_t launch_gemm_mx(const MxGemmArgs& a, const uint8_t* x_codes, const uint8_t* w_codes,

@@ -118,7 +118,7 @@ moe_status product_impl(const moe_mx* x, const moe_mx* w, int32_t E, const int32
   a.out = out;
   a.ld = ld_out;
   a.dtype = dtype;
-  a.wide = N % 2 == 0 && ld_out % 2 == 0 && aligned(out, 4);
+  a.wide = N % 4 == 0 && ld_out % 4 == 0 && aligned(out, 8);
   a.leave_item = leave;
   return cuda_status(launch_gemm_mx(a, x->codes, w->codes, sms, raw(stream)));
 }

@@ -22,8 +22,8 @@
 //     all four lane quadrants; one 32-bit column holds 128 values' four scales, and the
 //     instruction takes two of them by its scale id.
 //   * Warp 1 issues the MMAs, warps 2-5 drain the accumulators (two, or four where no
-//     tile passes 64 rows): a lane holds one output feature, lanes exchange pairs so that
-//     every store is 4 bytes of one row.
+//     tile passes 64 rows): a lane holds one output feature, four lanes exchange so that
+//     every store is 8 bytes of one row.
 //   * Waits are bounded.  A CTA in which one runs out drains its copies and MMAs, frees
 //     TMEM, and writes NaN to the items that it leaves.
 #include <cuda.h>
@@ -72,6 +72,16 @@ struct MxMaps {
   CUtensorMap x[4];  // 16, 32, 64, 128 rows
 };
 
+// Two values as 16-bit elements, a in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == kBf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint2 lds64(uint32_t saddr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr));
@@ -95,6 +105,35 @@ __device__ __forceinline__ void mma_mxf4_warp(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
+// Issue of a stage's copies by a converged warp with warp-uniform operands: the elected
+// lane announces the stage's bytes (expect) and copies a box of codes and a piece of scales.
+// In a branch of one lane each copy costs its thread a few hundred cycles.
+__device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void box_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                         int32_t c0, int32_t c1, uint64_t policy) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;\n}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void piece_warp(uint32_t dst, const void* src, uint32_t bytes,
+                                           uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2,"
+      " [%3];\n}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ bool wait_or_leave(uint32_t bar, uint32_t parity,
                                               volatile int* abort_flag) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -107,6 +146,17 @@ __device__ __forceinline__ bool wait_or_leave(uint32_t bar, uint32_t parity,
       return false;
     }
   }
+}
+
+// After an abort: wait (one shared time limit) for the last phases of the ring that this
+// warp has loaded, so that no copy lands in shared memory once the CTA is gone.  A phase
+// that the other producer never joined does not complete; the limit ends the wait, by which
+// time this warp's copies have landed.
+__device__ __forceinline__ void drain_ring(const Ring& R, int loaded, int n_stages) {
+  const uint64_t t0 = globaltimer();
+  for (int i = max(0, loaded - n_stages); i < loaded; ++i)
+    while (!mbar_try_wait_sleep(R.bar(kFull + i % n_stages), (uint32_t)(i / n_stages) & 1u))
+      if (globaltimer() - t0 > kWaitLimitNs) return;
 }
 
 // A CTA's walk over its items.
@@ -233,82 +283,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk{first_item, first_row, m_tiles, 0};
   if (warp == 0) {
     // ------------------------------------------------------------ weight producer
-    if (lane == 0) {
-      int last_par[kStages];
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) last_par[s] = -1;
-      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
-      const int64_t w_rows = ((int64_t)a.E * a.N + 1) & ~int64_t(1);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-        const Item it = walk.at(item);
-        // a weight tile of one row tile is not read again
-        const uint64_t pol =
-            first_item[it.e + 1] - first_item[it.e] == m_tiles ? once : keep;
-        const int64_t row = (int64_t)it.e * a.N + it.mt * 128, r0 = row & ~int64_t(1);
-        const uint32_t sf = 8u * (uint32_t)min((int64_t)(row != r0 ? 130 : 128), w_rows - r0);
-        for (int kb = 0; kb < a.kblocks; ++kb) {
-          if (!wait_or_leave(R.bar(kEmpty + stage), phase ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sb = stages + stage * stage_bytes;
-          const uint32_t full = R.bar(kFull + stage);
-          mbar_expect_tx(full, kABytes + sf);
-          tma_load_2d_hint(smem_u32(sb), &maps.w, full, kb * kRowBytes, (int)row, pol);
-          bulk_load(smem_u32(sb + off_sfa), a.sw + kb * a.sw_panel + 8 * r0, sf, full);
-          last_par[stage] = (int)phase;
-          if (++stage == n_stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+    const uint64_t once = policy_evict_first(), keep = policy_evict_last();
+    const int64_t w_rows = ((int64_t)a.E * a.N + 1) & ~int64_t(1);
+    int stage = 0, loaded = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+      const Item it = walk.at(item);
+      // a weight tile of one row tile is not read again
+      const uint64_t pol = first_item[it.e + 1] - first_item[it.e] == m_tiles ? once : keep;
+      const int64_t row = (int64_t)it.e * a.N + it.mt * 128, r0 = row & ~int64_t(1);
+      const uint32_t sf = 8u * (uint32_t)min((int64_t)(row != r0 ? 130 : 128), w_rows - r0);
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(kEmpty + stage), phase ^ 1, abort_flag));
+        if (!ok) break;
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes), full = R.bar(kFull + stage);
+        expect_warp(full, kABytes + sf);
+        box_warp(sb, &maps.w, full, kb * kRowBytes, (int)row, pol);
+        piece_warp(sb + off_sfa, a.sw + kb * a.sw_panel + 8 * r0, sf, full);
+        ++loaded;
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (!ok || *abort_flag) drain_stages(R, kFull, last_par, kStages);
     }
+    if (!ok || *abort_flag) drain_ring(R, loaded, n_stages);
   } else if (warp == 10) {
     // ------------------------------------------------------------ row producer
-    if (lane == 0) {
-      int last_par[kStages];
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) last_par[s] = -1;
-      const uint64_t pol = policy_evict_last();
-      const int rows_p = (a.R + 1) & ~1;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-        if (item == a.leave_item) break;
-        const Item it = walk.at(item);
-        const int n16 = (it.rows + 15) & ~15, r0 = it.row0 & ~1;
-        const uint32_t sf = 8u * (uint32_t)min(n16 + (it.row0 != r0 ? 2 : 0), rows_p - r0);
-        for (int kb = 0; kb < a.kblocks; ++kb) {
-          if (!wait_or_leave(R.bar(kEmpty + stage), phase ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sb = stages + stage * stage_bytes;
-          const uint32_t full = R.bar(kFull + stage);
-          mbar_expect_tx(full, n16 * kRowBytes + sf);
-          for (int r = 0; r < n16;) {
-            const int rem = n16 - r;
-            const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
-            tma_load_2d_hint(smem_u32(sb + off_b + r * kRowBytes), &maps.x[lg], full,
-                             kb * kRowBytes, it.row0 + r, pol);
-            r += 16 << lg;
-          }
-          bulk_load(smem_u32(sb + off_sfb), a.sx + kb * a.sx_panel + 8 * (int64_t)r0, sf, full);
-          last_par[stage] = (int)phase;
-          if (++stage == n_stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+    const uint64_t pol = policy_evict_last();
+    const int rows_p = (a.R + 1) & ~1;
+    int stage = 0, loaded = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+      if (item == a.leave_item) break;
+      const Item it = walk.at(item);
+      const int n16 = (it.rows + 15) & ~15, r0 = it.row0 & ~1;
+      const uint32_t sf = 8u * (uint32_t)min(n16 + (it.row0 != r0 ? 2 : 0), rows_p - r0);
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(kEmpty + stage), phase ^ 1, abort_flag));
+        if (!ok) break;
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes), full = R.bar(kFull + stage);
+        expect_warp(full, n16 * kRowBytes + sf);
+        for (int r = 0; r < n16;) {
+          const int rem = n16 - r;
+          const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
+          box_warp(sb + off_b + r * kRowBytes, &maps.x[lg], full, kb * kRowBytes, it.row0 + r,
+                   pol);
+          r += 16 << lg;
+        }
+        piece_warp(sb + off_sfb, a.sx + kb * a.sx_panel + 8 * (int64_t)r0, sf, full);
+        ++loaded;
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (!ok || *abort_flag) drain_stages(R, kFull, last_par, kStages);
     }
+    if (!ok || *abort_flag) drain_ring(R, loaded, n_stages);
   } else if (warp >= 6) {
     // ------------------------------------------------------------ scales to TMEM
     const uint32_t lane_q = (uint32_t)((warp & 3) * 32) << 16;
@@ -442,18 +475,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m = min(32, it.rows - c0);
         T* o = out + (int64_t)(it.row0 + c0) * a.ld;
         if (DT != kF32 && a.wide) {
-          // lanes 2i and 2i + 1 hold features f, f + 1: the even lane stores both of row j,
-          // the odd lane both of row j + 1
-          const bool odd = lane & 1;
-          const int f = n & ~1;
+          // A 4 x 4 transpose between four lanes, two rounds of exchange: lane i of a quad
+          // ends with features f .. f + 3 of row j + i, one store of 8 bytes.
+          const bool odd = lane & 1, upper = lane & 2;
+          const int f = n & ~3;
+          T* p = o + (int64_t)(lane & 3) * a.ld + f;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            if (j >= m) break;
-            const uint32_t b0 = float_to_elem<DT>(v[j]), b1 = float_to_elem<DT>(v[j + 1]);
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? b0 : b1, 1);
-            const uint32_t w = odd ? got | (b1 << 16) : b0 | (got << 16);
-            if (j + (int)odd < m && f < a.N)
-              *reinterpret_cast<uint32_t*>(o + (j + odd) * a.ld + f) = w;
+          for (int j = 0; j < 32; j += 4) {
+            const uint32_t w01 = pack2<DT>(v[j], v[j + 1]), w23 = pack2<DT>(v[j + 2], v[j + 3]);
+            const uint32_t x01 = __shfl_xor_sync(0xFFFFFFFFu, w01, 1);
+            const uint32_t x23 = __shfl_xor_sync(0xFFFFFFFFu, w23, 1);
+            const uint32_t a01 = odd ? __byte_perm(x01, w01, 0x7632) : __byte_perm(w01, x01, 0x5410);
+            const uint32_t a23 = odd ? __byte_perm(x23, w23, 0x7632) : __byte_perm(w23, x23, 0x5410);
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? a01 : a23, 2);
+            if (j + (lane & 3) < m && f < a.N)
+              *reinterpret_cast<uint2*>(p + j * a.ld) =
+                  upper ? make_uint2(got, a23) : make_uint2(a01, got);
           }
         } else if (n < a.N) {
 #pragma unroll
