@@ -36,6 +36,7 @@
 #include <cstdint>
 
 #include "block32.cuh"
+#include "cluster.cuh"
 #include "experts.h"
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -66,6 +67,8 @@ constexpr int kFlagsOff = 8 * kBars;           // tmem slot, abort flag, stop fl
 constexpr int kWarpSumOff = kFlagsOff + 32;    // two ints a warp
 constexpr int kGroupsOff = 512;                // first item [E + 1], first row [E + 1]
 static_assert(kWarpSumOff + 8 * (kThreads / 32) <= kGroupsOff, "barrier area");
+
+constexpr int64_t kPairRows = 128;             // rows an expert from which on CTAs work in pairs
 
 struct MxMaps {
   CUtensorMap w;
@@ -167,17 +170,61 @@ struct Item {
 struct Walk {
   const int* first_item;  // [E + 1]
   const int* first_row;   // [E + 1], the last one past the last group
-  int m_tiles, e;
-  // Row tiles of a group are equal and whole 16s.
+  int m_tiles, unit, e;
+  // Row tiles of a group are equal and whole units.
   __device__ __forceinline__ Item at(int item) {
     while (item >= first_item[e + 1]) ++e;
     const int tiles = (first_item[e + 1] - first_item[e]) / m_tiles;
     const int local = item - first_item[e], group = first_row[e + 1] - first_row[e];
-    const int h = ((group + tiles - 1) / tiles + 15) & ~15;
+    const int h = ((group + tiles - 1) / tiles + unit - 1) & -unit;
     const int tt = local % tiles;
     return Item{e, local / tiles, first_row[e] + tt * h, min(h, group - tt * h)};
   }
 };
+
+// First item and first row of each expert, by the whole block (blockDim.x = THREADS): row
+// tiles of at most tile_n rows in whole units of `unit`, m_tiles weight tiles each.  Also
+// folds the largest tile height into *s_most (set before).  s_sum: an int a warp.
+template <int THREADS>
+__device__ __forceinline__ void lay_out_groups(const MxGemmArgs& a, int tile_n, int unit,
+                                               int m_tiles, int* first_item, int* first_row,
+                                               int* s_sum, int* s_most) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (a.E + THREADS - 1) / THREADS;
+  const int e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
+  auto bound = [&](int e) {  // rows outside [0, R] are no rows
+    return a.offsets ? max(0, min(a.R, a.offsets[e])) : e ? a.R : 0;
+  };
+  int items = 0, most = unit;
+  for (int e = e0; e < e1; ++e) {
+    const int rows = max(0, bound(e + 1) - bound(e));
+    const int tiles = (rows + tile_n - 1) / tile_n;
+    items += tiles * m_tiles;
+    if (tiles) most = max(most, ((rows + tiles - 1) / tiles + unit - 1) / unit * unit);
+  }
+  int x = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  atomicMax(s_most, most);
+  __syncthreads();
+  int before = x - items;
+  for (int w = 0; w < warp; ++w) before += s_sum[w];
+  for (int e = e0; e < e1; ++e) {
+    const int b0 = bound(e), rows = max(0, bound(e + 1) - b0);
+    first_item[e] = before;
+    first_row[e] = b0;
+    before += (rows + tile_n - 1) / tile_n * m_tiles;
+    if (e == a.E - 1) {
+      first_item[a.E] = before;
+      first_row[a.E] = b0 + rows;
+    }
+  }
+  __syncthreads();
+}
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -226,43 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // ---- groups: first row and first item of each expert (thread i: kPer experts)
-  {
-    const int per = (a.E + kThreads - 1) / kThreads;
-    const int e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
-    auto bound = [&](int e) {  // rows outside [0, R] are no rows
-      return a.offsets ? max(0, min(a.R, a.offsets[e])) : e ? a.R : 0;
-    };
-    int items = 0, most = 16;
-    for (int e = e0; e < e1; ++e) {
-      const int rows = max(0, bound(e + 1) - bound(e));
-      const int tiles = (rows + kTileN - 1) / kTileN;
-      items += tiles * m_tiles;
-      if (tiles) most = max(most, ((rows + tiles - 1) / tiles + 15) & ~15);
-    }
-    int x = items;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_sum[warp] = x;
-    atomicMax(s_max16, most);
-    __syncthreads();
-    int before = x - items;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    for (int e = e0; e < e1; ++e) {
-      const int b0 = bound(e), rows = max(0, bound(e + 1) - b0);
-      first_item[e] = before;
-      first_row[e] = b0;
-      before += (rows + kTileN - 1) / kTileN * m_tiles;
-      if (e == a.E - 1) {
-        first_item[a.E] = before;
-        first_row[a.E] = b0 + rows;
-      }
-    }
-    __syncthreads();
-  }
+  lay_out_groups<kThreads>(a, kTileN, 16, m_tiles, first_item, first_row, s_sum, s_max16);
   const int n_items = first_item[a.E];
 
   // ---- geometry from the largest tile
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int n_stages = min(kStages, (kSmem - 1024 - head) / stage_bytes);
   n_stages = min(n_stages, (kTmemCols - sf_base) / slot_cols);
 
-  Walk walk{first_item, first_row, m_tiles, 0};
+  Walk walk{first_item, first_row, m_tiles, 16, 0};
   if (warp == 0) {
     // ------------------------------------------------------------ weight producer
     const uint64_t once = policy_evict_first(), keep = policy_evict_last();
@@ -511,13 +522,419 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// The same product where an expert has rows enough to fill the tensor cores: two CTAs of a
+// cluster share a tile of 256 weight rows x up to 256 rows (cta_group::2).  Each holds 128
+// weight rows, half of the rows' codes and 128 lanes of accumulators, and all the rows'
+// scales; rank 0 issues every MMA.  Against single CTAs a stage brings 32 KB for 256 x 256 x
+// 256 / 2 products in place of 40 KB for 128 x 192 x 256, and each role's work a stage (some
+// 250 to 500 cycles: waits, copies, scales to TMEM, issue) is spread over 512 cycles of MMA
+// in place of 384.  256 columns of accumulators leave no room for a second buffer beside the
+// scales: eight epilogue warps take them to registers as 16-bit pairs, free them, and store
+// while the next item's MMAs run.
+namespace pair {
+constexpr int kThreads = 512;  // 0 weights, 1 MMA, 2 rows, 3 scales, 4-7 scales to TMEM, 8-15 epilogue
+constexpr int kTileN = 256;
+constexpr int kStages = 8;
+constexpr int kFull = 0;
+constexpr int kEmpty = kStages;
+constexpr int kSfReady = 2 * kStages;  // rank 0's: 4 warps of both CTAs
+constexpr int kAccFull = 3 * kStages;
+constexpr int kAccEmpty = kAccFull + 1;  // rank 0's: 8 warps of both CTAs
+constexpr int kDrain = kAccEmpty + 1;
+constexpr int kBars = kDrain + 1;
+constexpr int kFlagsOff = 8 * kBars;
+constexpr int kWarpSumOff = kFlagsOff + 32;
+static_assert(kWarpSumOff + 4 * (kThreads / 32) <= kGroupsOff, "barrier area");
+
+__device__ __forceinline__ void alloc(uint32_t slot_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void mma_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+      " [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// Arrive on the barrier at this address in both CTAs once the MMAs so far are done.
+__device__ __forceinline__ void commit_warp(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], m;\n}" ::"r"(bar)
+      : "memory");
+}
+// Arrive on rank 0's barrier, with the instruction's default order (release, this CTA).
+// What is handed over lies in TMEM and shared memory, which have one copy, and is complete:
+// the caller has waited for its tcgen05.st or tcgen05.ld, and has seen the copies' mbarrier.
+// The order of a whole cluster's memory costs some 1000 cycles an arrival, two stages' MMAs.
+__device__ __forceinline__ void arrive_rank0(uint32_t bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
+}
+// As wait_or_leave, for a barrier that the other CTA arrives on too.
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (t0 == 0) {
+      t0 = globaltimer();
+    } else if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+}  // namespace pair
+
 template <int DT>
-cudaError_t launch_typed(const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t s) {
-  static std::atomic<uint64_t> configured{0};
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gemm_mx_kernel<DT>), kSmem,
-                                    configured);
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+    gemm_mx_pair_kernel(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmArgs a) {
+  using namespace pair;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const Ring R{smem};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + pair::kFlagsOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* epi_stop = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* s_most = reinterpret_cast<int*>(tmem_slot + 3);
+  int* s_sum = reinterpret_cast<int*>(smem + pair::kWarpSumOff);
+  int* first_item = reinterpret_cast<int*>(smem + kGroupsOff);
+  int* first_row = first_item + a.E + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int m_pairs = (a.N + 255) / 256;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < pair::kStages; ++s) {
+      mbar_init(R.bar(pair::kFull + s), 3);  // weights, rows, scales
+      mbar_init(R.bar(pair::kEmpty + s), 1);
+      mbar_init(R.bar(pair::kSfReady + s), 8);
+    }
+    mbar_init(R.bar(pair::kAccFull), 1);
+    mbar_init(R.bar(pair::kAccEmpty), 16);
+    mbar_init(R.bar(pair::kDrain), 1);
+    *abort_flag = 0;
+    *epi_stop = 0;
+    *s_most = 32;
+    fence_barrier_init();
+    prefetch_tmap(&maps.w);
+    for (int i = 0; i < 4; ++i) prefetch_tmap(&maps.x[i]);
+  }
+  __syncwarp();
+  if (warp == 1) pair::alloc(smem_u32(tmem_slot), kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // the other CTA's barriers and TMEM are there
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  lay_out_groups<pair::kThreads>(a, pair::kTileN, 32, m_pairs, first_item, first_row, s_sum,
+                                 s_most);
+  const int n_items = first_item[a.E];
+  const int item0 = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+
+  const int most = *s_most;                    // rows of the largest tile, whole 32s
+  const int sfb_bytes = (8 * (most + 2) + 127) & ~127;
+  const int off_b = kABytes, off_sfa = off_b + most / 2 * kRowBytes, off_sfb = off_sfa + kSfaBytes;
+  const int stage_bytes = (off_sfb + sfb_bytes + 1023) & ~1023;
+  const int nrb = most <= 128 ? 4 : 8;
+  const int slot_cols = 8 + 2 * nrb;
+  const int sf_base = (most + 31) & ~31;       // scales behind the accumulators
+  const int head = (kGroupsOff + 8 * (a.E + 1) + 1023) & ~1023;
+  uint8_t* stages = smem + head;
+  const int n_stages = min(pair::kStages, (kSmem - 1024 - head) / stage_bytes);
+  static_assert(pair::kTileN + pair::kStages * 24 <= kTmemCols, "TMEM columns");
+
+  Walk walk{first_item, first_row, m_pairs, 32, 0};
+  int stage = 0;
+  uint32_t phase = 0;
+  auto advance = [&] {
+    if (++stage == n_stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ producers
+    const uint64_t pol = policy_evict_last();
+    const int64_t w_rows = ((int64_t)a.E * a.N + 1) & ~int64_t(1);
+    const int x_rows = (a.R + 1) & ~1;
+    int loaded = 0;
+    bool ok = true;
+    for (int item = item0; ok && item < n_items; item += step) {
+      if (warp == 2 && item == a.leave_item) break;
+      const Item it = walk.at(item);
+      const int half = ((it.rows + 31) & ~31) / 2;
+      const int x0 = it.row0 + rank * half;
+      // a tile's last 128 weight rows may lie past the last weight: then no box is needed, but
+      // one of rows that exist keeps every stage alike
+      const int64_t w0 = min((int64_t)it.e * a.N + it.mt * 256 + rank * 128,
+                             (int64_t)a.E * a.N - 1);
+      const int64_t w_even = w0 & ~int64_t(1);
+      const int x_even = it.row0 & ~1;
+      const uint32_t sfa = 8u * (uint32_t)min((int64_t)(w0 != w_even ? 130 : 128), w_rows - w_even);
+      const uint32_t sfb = 8u * (uint32_t)min(2 * half + (it.row0 != x_even ? 2 : 0), x_rows - x_even);
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        wait_pair(R.bar(pair::kEmpty + stage), phase ^ 1, abort_flag));
+        if (!ok) break;
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
+        const uint32_t full = R.bar(pair::kFull + stage);
+        if (warp == 0) {
+          expect_warp(full, kABytes);
+          box_warp(sb, &maps.w, full, kb * kRowBytes, (int)w0, pol);
+        } else if (warp == 2) {
+          expect_warp(full, half * kRowBytes);
+          for (int r = 0; r < half;) {
+            const int rem = half - r;
+            const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
+            box_warp(sb + off_b + r * kRowBytes, &maps.x[lg], full, kb * kRowBytes, x0 + r, pol);
+            r += 16 << lg;
+          }
+        } else {
+          expect_warp(full, sfa + sfb);
+          piece_warp(sb + off_sfa, a.sw + kb * a.sw_panel + 8 * w_even, sfa, full);
+          piece_warp(sb + off_sfb, a.sx + kb * a.sx_panel + 8 * (int64_t)x_even, sfb, full);
+        }
+        ++loaded;
+        advance();
+      }
+    }
+    if (!ok || *abort_flag) drain_ring(R, loaded, n_stages);
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ scales to TMEM
+    const uint32_t lane_q = (uint32_t)((warp & 3) * 32) << 16;
+    bool ok = true;
+    for (int item = item0; ok && item < n_items; item += step) {
+      const Item it = walk.at(item);
+      const int64_t w0 = min((int64_t)it.e * a.N + it.mt * 256 + rank * 128,
+                             (int64_t)a.E * a.N - 1);
+      const int odd_w = (int)(w0 & 1), odd_x = it.row0 & 1;
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        if (!wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
+        const uint32_t col = tmem + lane_q + sf_base + stage * slot_cols;
+        const uint32_t sa = sb + off_sfa + 8 * (odd_w + lane), sx = sb + off_sfb + 8 * (odd_x + lane);
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint2 p = lds64(sa + 256 * j);
+          v[j] = p.x, v[4 + j] = p.y;
+        }
+        pair::st8(col, v);
+        if (nrb == 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint2 p = 32 * j < it.rows ? lds64(sx + 256 * j) : make_uint2(0u, 0u);
+            v[j] = p.x, v[4 + j] = p.y;
+          }
+          pair::st8(col + 8, v);
+        } else {
+          uint32_t u[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint2 p = 32 * j < it.rows ? lds64(sx + 256 * j) : make_uint2(0u, 0u);
+            u[j] = p.x, u[8 + j] = p.y;
+          }
+          tmem_st16(col + 8, u);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_rank0(R.bar(pair::kSfReady + stage));
+        advance();
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (rank 0)
+    bool ok = rank == 0, issued = false;
+    uint32_t acc_phase = 1;
+    for (int item = item0; ok && item < n_items; item += step) {
+      const Item it = walk.at(item);
+      const uint32_t idesc = idesc_mxf4(256, (it.rows + 31) & ~31);
+      ok = __all_sync(0xFFFFFFFFu, wait_pair(R.bar(pair::kAccEmpty), acc_phase, abort_flag));
+      if (!ok) break;
+      acc_phase ^= 1;
+      tc_fence_after();
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        wait_pair(R.bar(pair::kSfReady + stage), phase, abort_flag) &&
+                            wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
+        const uint32_t col = tmem + sf_base + stage * slot_cols;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t id = 2u * (ks & 1);
+          pair::mma_warp(tmem, smem_desc(sb + ks * 32, 16, 1024, 2),
+                         smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
+                         idesc | (id << 4) | (id << 29), col + 4 * (ks >> 1),
+                         col + 8 + nrb * (ks >> 1), (kb | ks) != 0 ? 1u : 0u);
+        }
+        issued = true;
+        pair::commit_warp(R.bar(pair::kEmpty + stage));
+        advance();
+      }
+      if (!ok) break;
+      pair::commit_warp(R.bar(pair::kAccFull));
+    }
+    if (issued && (!ok || *abort_flag)) {
+      pair::commit_warp(R.bar(pair::kDrain));
+      mbar_wait(R.bar(pair::kDrain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    using T = typename Elem<DT>::type;
+    const int q = warp & 3, h = (warp - 8) >> 2;  // lanes 32q ..., first or second half of the rows
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    T* out = static_cast<T*>(a.out);
+    uint32_t acc_phase = 0;
+    for (int item = item0; item < n_items; item += step) {
+      const Item it = walk.at(item);
+      const int n = it.mt * 256 + rank * 128 + q * 32 + lane;
+      const int half = ((it.rows + 31) & ~31) / 2;
+      if (!wait_pair(R.bar(pair::kAccFull), acc_phase, abort_flag)) *epi_stop = 1;
+      named_bar_sync(1, 256);
+      const bool stop = *epi_stop != 0;
+      named_bar_sync(1, 256);
+      if (stop) {
+        for (; item < n_items; item += step) {
+          const Item left = walk.at(item);
+          const int f = left.mt * 256 + rank * 128 + ((int)threadIdx.x & 127);
+          for (int j = h; f < a.N && j < left.rows; j += 2)
+            out[(left.row0 + j) * a.ld + f] = (T)float_to_elem<DT>(__int_as_float(0x7FC00000));
+        }
+        break;
+      }
+      acc_phase ^= 1;
+      tc_fence_after();
+      const uint32_t acc = tmem + lane_addr + h * half;
+      const int m = min(half, it.rows - h * half);  // rows of this half
+      T* o = out + (int64_t)(it.row0 + h * half) * a.ld;
+      if constexpr (DT != kF32) {
+        uint32_t w[64];  // 128 rows in pairs
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          if (16 * g >= half) continue;
+          float v[16];
+          tmem_ld16(acc + 16 * g, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[8 * g + i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_rank0(R.bar(pair::kAccEmpty));
+        if (a.wide) {
+          // the 4 x 4 exchange of the single CTAs
+          const bool odd = lane & 1, upper = lane & 2;
+          const int f = n & ~3;
+          T* p = o + (int64_t)(lane & 3) * a.ld + f;
+#pragma unroll
+          for (int j = 0; j < 128; j += 4) {
+            if (j >= half) continue;
+            const uint32_t w01 = w[j / 2], w23 = w[j / 2 + 1];
+            const uint32_t x01 = __shfl_xor_sync(0xFFFFFFFFu, w01, 1);
+            const uint32_t x23 = __shfl_xor_sync(0xFFFFFFFFu, w23, 1);
+            const uint32_t a01 = odd ? __byte_perm(x01, w01, 0x7632) : __byte_perm(w01, x01, 0x5410);
+            const uint32_t a23 = odd ? __byte_perm(x23, w23, 0x7632) : __byte_perm(w23, x23, 0x5410);
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? a01 : a23, 2);
+            if (j + (lane & 3) < m && f < a.N)
+              *reinterpret_cast<uint2*>(p) = upper ? make_uint2(got, a23) : make_uint2(a01, got);
+            p += 4 * a.ld;
+          }
+        } else if (n < a.N) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j < m) o[j * a.ld + n] = (T)(w[j / 2] >> (16 * (j & 1)));
+        }
+      } else {
+        for (int c = 0; c < half; c += 16) {
+          float v[16];
+          tmem_ld16(acc + c, v);
+          tmem_wait_ld();
+          if (n < a.N)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < m) o[(c + j) * a.ld + n] = (T)float_to_elem<DT>(v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_rank0(R.bar(pair::kAccEmpty));
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // neither CTA's shared memory or TMEM is used any more
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    pair::dealloc(tmem, kTmemCols);
+  }
+}
+
+// Pairs where the rows an expert has on average are enough and there are two weight tiles.
+bool use_pairs(const MxGemmArgs& a) { return a.N > 128 && a.R >= (int64_t)a.E * kPairRows; }
+
+template <typename K>
+cudaError_t launch_kernel(K kernel, int threads, std::atomic<uint64_t>& configured,
+                          const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t s) {
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmem, configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gemm_mx_kernel<DT>, dim3(grid), dim3(kThreads), (size_t)kSmem, s, maps, a);
+  return launch_pdl(kernel, dim3(grid), dim3(threads), (size_t)kSmem, s, maps, a);
+}
+
+template <int DT>
+cudaError_t launch_typed(const MxMaps& maps, const MxGemmArgs& a, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> single_set{0}, pair_set{0};
+  if (use_pairs(a)) {
+    const int64_t tiles = (int64_t)a.R / pair::kTileN + a.E;
+    const int64_t pairs = std::min<int64_t>(sms / 2, tiles * ((a.N + 255) / 256));
+    return launch_kernel(gemm_mx_pair_kernel<DT>, pair::kThreads, pair_set, maps, a,
+                         (int)pairs * 2, s);
+  }
+  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kTileN + a.E);
+  const int grid = (int)std::min<int64_t>(sms, tiles * ((a.N + 127) / 128));
+  return launch_kernel(gemm_mx_kernel<DT>, kThreads, single_set, maps, a, grid, s);
 }
 
 }  // namespace
@@ -529,11 +946,9 @@ cudaError_t launch_gemm_mx(const MxGemmArgs& a, const uint8_t* x_codes, const ui
   if (!byte_map(&maps.w, w_codes, row_bytes, (uint64_t)a.E * a.N, 128)) return cudaErrorInvalidValue;
   for (int i = 0; i < 4; ++i)
     if (!byte_map(&maps.x[i], x_codes, row_bytes, a.R, 16u << i)) return cudaErrorInvalidValue;
-  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kTileN + a.E);
-  const int grid = (int)std::min<int64_t>(sms, tiles * ((a.N + 127) / 128));
-  return a.dtype == kF32    ? launch_typed<kF32>(maps, a, grid, s)
-         : a.dtype == kBf16 ? launch_typed<kBf16>(maps, a, grid, s)
-                            : launch_typed<kF16>(maps, a, grid, s);
+  return a.dtype == kF32    ? launch_typed<kF32>(maps, a, sms, s)
+         : a.dtype == kBf16 ? launch_typed<kBf16>(maps, a, sms, s)
+                            : launch_typed<kF16>(maps, a, sms, s);
 }
 
 }  // namespace moe
