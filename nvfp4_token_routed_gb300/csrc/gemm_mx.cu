@@ -151,6 +151,18 @@ __device__ __forceinline__ bool wait_or_leave(uint32_t bar, uint32_t parity,
   }
 }
 
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // After an abort: wait (one shared time limit) for the last phases of the ring that this
 // warp has loaded, so that no copy lands in shared memory once the CTA is gone.  A phase
 // that the other producer never joined does not complete; the limit ends the wait, by which
@@ -402,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     int stage = 0, local = 0;
     uint32_t phase = 0;
-    bool ok = true, issued = false;
+    bool ok = true, issued = false, ready = false;
     for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
       const Item it = walk.at(item);
       const uint32_t idesc = idesc_mxf4(128, (it.rows + 15) & ~15);
@@ -413,15 +425,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem + buf * acc_stride;
       for (int kb = 0; kb < a.kblocks; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu,
-                        wait_or_leave(R.bar(kSfReady + stage), phase, abort_flag) &&
-                            wait_or_leave(R.bar(kFull + stage), phase, abort_flag));
+        if (!ready)
+          ok = __all_sync(0xFFFFFFFFu,
+                          wait_or_leave(R.bar(kSfReady + stage), phase, abort_flag) &&
+                              wait_or_leave(R.bar(kFull + stage), phase, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
-        const uint32_t col = tmem + sf_base + stage * slot_cols;
+        const int s = stage;
+        const uint32_t sb = smem_u32(stages + s * stage_bytes);
+        const uint32_t col = tmem + sf_base + s * slot_cols;
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
+          // the next stage is looked at while this one's first MMAs run
+          if (ks == 2)
+            ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(kSfReady + stage), phase) &&
+                                                phase_done(R.bar(kFull + stage), phase));
           const uint32_t id = 2u * (ks & 1);  // which two of a column's four scales
           mma_mxf4_warp(acc, smem_desc(sb + ks * 32, 16, 1024, 2),
                         smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
@@ -429,11 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         col + 8 + nrb * (ks >> 1), (kb | ks) != 0 ? 1u : 0u);
         }
         issued = true;
-        tc_commit_warp(R.bar(kEmpty + stage));
-        if (++stage == n_stages) {
-          stage = 0;
-          phase ^= 1;
-        }
+        tc_commit_warp(R.bar(kEmpty + s));
       }
       if (!ok) break;
       tc_commit_warp(R.bar(kAccFull + buf));
@@ -782,7 +800,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (rank 0)
-    bool ok = rank == 0, issued = false;
+    bool ok = rank == 0, issued = false, ready = false;
     uint32_t acc_phase = 1;
     for (int item = item0; ok && item < n_items; item += step) {
       const Item it = walk.at(item);
@@ -792,15 +810,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       acc_phase ^= 1;
       tc_fence_after();
       for (int kb = 0; kb < a.kblocks; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu,
-                        wait_pair(R.bar(pair::kSfReady + stage), phase, abort_flag) &&
-                            wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag));
+        if (!ready)
+          ok = __all_sync(0xFFFFFFFFu,
+                          wait_or_leave(R.bar(pair::kSfReady + stage), phase, abort_flag) &&
+                              wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sb = smem_u32(stages + stage * stage_bytes);
-        const uint32_t col = tmem + sf_base + stage * slot_cols;
+        const int s = stage;
+        const uint32_t sb = smem_u32(stages + s * stage_bytes);
+        const uint32_t col = tmem + sf_base + s * slot_cols;
+        advance();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
+          if (ks == 2)
+            ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(pair::kSfReady + stage), phase) &&
+                                                phase_done(R.bar(pair::kFull + stage), phase));
           const uint32_t id = 2u * (ks & 1);
           pair::mma_warp(tmem, smem_desc(sb + ks * 32, 16, 1024, 2),
                          smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
@@ -808,8 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                          col + 8 + nrb * (ks >> 1), (kb | ks) != 0 ? 1u : 0u);
         }
         issued = true;
-        pair::commit_warp(R.bar(pair::kEmpty + stage));
-        advance();
+        pair::commit_warp(R.bar(pair::kEmpty + s));
       }
       if (!ok) break;
       pair::commit_warp(R.bar(pair::kAccFull));
