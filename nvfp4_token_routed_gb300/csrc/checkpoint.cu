@@ -11,8 +11,9 @@
 //   relu2    y = max(h, 0)^2, dh = 2 dy max(h, 0)
 // y comes from the unrounded input, the gradient from the kept values.
 //
-// A thread takes a run of 8 values (of both halves), four lanes a block; nothing is
-// shared between blocks, so the kernels are bound by HBM.
+// A warp takes U times 256 consecutive values of a row (of both halves), 8 a lane and four
+// lanes a block of 32; its loads are issued together.  Nothing is shared between blocks, so
+// the kernels are bound by HBM.
 #include <algorithm>
 
 #include "block32.cuh"
@@ -25,40 +26,38 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSpan = 256;  // values of a row that a warp takes at once
 
-// A thread's run: row, first value, and how many of its 8 values the row has.
-struct Place {
-  int64_t r;
-  int c;
-  int n;       // <= 0: padding of the last block
-  bool live;   // the row counts
-};
-__device__ __forceinline__ Place place_of(const KeepArgs& a, int64_t i, int runs) {
-  Place p;
-  p.r = i <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)runs) : i / runs;
-  p.c = (int)(i - p.r * runs) * 8;
-  const int rows = a.n_rows ? min(a.R, *a.n_rows) : a.R;
-  p.live = p.r < rows;
-  p.n = p.live ? a.W - p.c : 0;
-  return p;
+// A warp's row and first span; false: nothing to do.
+__device__ __forceinline__ bool place_of(const KeepArgs& a, int segs, int u, int64_t& r, int& c) {
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  r = i <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)segs) : i / segs;
+  c = (int)(i - r * segs) * (u * kSpan) + (threadIdx.x & 31) * 8;
+  return r < (a.n_rows ? min(a.R, *a.n_rows) : a.R);
 }
 
 // Writes a run's codes and its block's scale.  All lanes take part.
-__device__ __forceinline__ void keep_run(const KeepArgs& a, const Place& p, int halves, int half,
-                                         const Run8& r) {
+__device__ __forceinline__ void keep_run(const KeepArgs& a, int64_t r, int c, int halves, int half,
+                                         const Run8& v) {
   const int Wp = (a.W + 31) & ~31;
-  const uint32_t byte = block_scale_byte<E4m3>(quad_max(r.amax_bits()));
-  if (!p.live) return;
-  const int64_t at = (p.r * halves + half) * Wp + p.c;
+  const uint32_t byte = block_scale_byte<E4m3>(quad_max(v.amax_bits()));
+  if (c >= Wp) return;
+  const int64_t at = (r * halves + half) * Wp + c;
   *reinterpret_cast<uint2*>(a.codes + at) =
-      byte == 255u ? make_uint2(0u, 0u) : e4m3x8(r, block_inverse(byte));
+      byte == 255u ? make_uint2(0u, 0u) : e4m3x8(v, block_inverse(byte));
   if ((threadIdx.x & 3) == 0) a.scales[at >> 5] = (uint8_t)byte;
 }
-__device__ __forceinline__ void kept_run(const KeepArgs& a, const Place& p, int halves, int half,
-                                         Run8& r) {
+// A run's codes and scale byte, zeros past the row.
+struct Kept {
+  uint2 codes;
+  uint32_t byte;
+};
+__device__ __forceinline__ Kept kept_run(const KeepArgs& a, int64_t r, int c, int halves,
+                                         int half) {
   const int Wp = (a.W + 31) & ~31;
-  const int64_t at = (p.r * halves + half) * Wp + p.c;
-  e4m3x8_to_float(*reinterpret_cast<const uint2*>(a.codes + at), block_scale(a.scales[at >> 5]), r);
+  if (c >= a.W) return Kept{make_uint2(0u, 0u), 0u};
+  const int64_t at = (r * halves + half) * Wp + c;
+  return Kept{*reinterpret_cast<const uint2*>(a.codes + at), a.scales[at >> 5]};
 }
 
 template <int DT>
@@ -70,27 +69,41 @@ __device__ __forceinline__ void* elem_ptr(void* p, int64_t i) {
   return static_cast<typename Elem<DT>::type*>(p) + i;
 }
 
-template <int DT, int VB>
-__global__ void __launch_bounds__(kThreads) checkpoint_kernel(const KeepArgs a, int runs) {
+template <int DT, int VB, int U>
+__global__ void __launch_bounds__(kThreads) checkpoint_kernel(const KeepArgs a, int segs) {
   pdl_trigger();
   pdl_wait();
-  const Place p = place_of(a, (int64_t)blockIdx.x * kThreads + threadIdx.x, runs);
-  uint32_t w[kRunWords<DT>];
-  run_load_raw<DT, VB>(elem_ptr<DT>(a.x, p.r * a.ld_x + p.c), p.n, w);
-  Run8 r;
-  run_unpack<DT>(w, r);
-  keep_run(a, p, 1, 0, r);
+  int64_t r;
+  int c;
+  if (!place_of(a, segs, U, r, c)) return;
+  uint32_t w[U][kRunWords<DT>];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    run_load_raw<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + c + u * kSpan), a.W - c - u * kSpan, w[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    Run8 v;
+    run_unpack<DT>(w[u], v);
+    keep_run(a, r, c + u * kSpan, 1, 0, v);
+  }
 }
 
-template <int DT, int VB>
-__global__ void __launch_bounds__(kThreads) restore_kernel(const KeepArgs a, int runs) {
+template <int DT, int VB, int U>
+__global__ void __launch_bounds__(kThreads) restore_kernel(const KeepArgs a, int segs) {
   pdl_trigger();
   pdl_wait();
-  const Place p = place_of(a, (int64_t)blockIdx.x * kThreads + threadIdx.x, runs);
-  if (p.n <= 0) return;
-  Run8 r;
-  kept_run(a, p, 1, 0, r);
-  run_store<DT, VB>(elem_ptr<DT>(a.out, p.r * a.ld_out + p.c), p.n, r);
+  int64_t r;
+  int c;
+  if (!place_of(a, segs, U, r, c)) return;
+  Kept k[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) k[u] = kept_run(a, r, c + u * kSpan, 1, 0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    Run8 v;
+    e4m3x8_to_float(k[u].codes, block_scale(k[u].byte), v);
+    run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + c + u * kSpan), a.W - c - u * kSpan, v);
+  }
 }
 
 // s(g): correctly to fp32's last bits for fp32 rows, by the fast exponential (2^-21 of
@@ -104,67 +117,88 @@ __device__ __forceinline__ float sigmoid(float g) {
 __device__ __forceinline__ float cap(float g, float L) { return g > L ? L : g; }
 __device__ __forceinline__ float clip(float u, float L) { return u > L ? L : u < -L ? -L : u; }
 
-template <int DT, int VB, int ACT>
-__global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int runs) {
+template <int DT, int VB, int U, int ACT>
+__global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int segs) {
+  constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
   pdl_trigger();
   pdl_wait();
-  const Place p = place_of(a, (int64_t)blockIdx.x * kThreads + threadIdx.x, runs);
-  uint32_t wg[kRunWords<DT>], wu[kRunWords<DT>];
-  run_load_raw<DT, VB>(elem_ptr<DT>(a.x, p.r * a.ld_x + p.c), p.n, wg);
-  if (ACT == kActSwiglu) run_load_raw<DT, VB>(elem_ptr<DT>(a.x, p.r * a.ld_x + a.W + p.c), p.n, wu);
-  Run8 g, u, y;
-  run_unpack<DT>(wg, g);
-  if (ACT == kActSwiglu) {
-    run_unpack<DT>(wu, u);
-    const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
+  int64_t r;
+  int c;
+  if (!place_of(a, segs, U, r, c)) return;
+  uint32_t w[U][kHalves][kRunWords<DT>];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float gc = cap(g.v[i], L);
-      y.v[i] = gc * sigmoid<DT>(gc) * clip(u.v[i], L);
-    }
-  } else {
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float h = g.v[i] < 0.0f ? 0.0f : g.v[i];
-      y.v[i] = h * h;
+    for (int h = 0; h < kHalves; ++h)
+      run_load_raw<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + h * a.W + c + u * kSpan),
+                           a.W - c - u * kSpan, w[u][h]);
+  const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    Run8 g, up, y;
+    run_unpack<DT>(w[u][0], g);
+    if constexpr (ACT == kActSwiglu) {
+      run_unpack<DT>(w[u][kHalves - 1], up);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float gc = cap(g.v[i], L);
+        y.v[i] = gc * sigmoid<DT>(gc) * clip(up.v[i], L);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = g.v[i] < 0.0f ? 0.0f : g.v[i];
+        y.v[i] = h * h;
+      }
     }
+    const int cu = c + u * kSpan;
+    run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, y);
+    if (!a.codes) continue;
+    keep_run(a, r, cu, kHalves, 0, g);
+    if constexpr (ACT == kActSwiglu) keep_run(a, r, cu, kHalves, 1, up);
   }
-  run_store<DT, VB>(elem_ptr<DT>(a.out, p.r * a.ld_out + p.c), p.n, y);
-  if (!a.codes) return;
-  constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
-  keep_run(a, p, kHalves, 0, g);
-  if (ACT == kActSwiglu) keep_run(a, p, kHalves, 1, u);
 }
 
-template <int DT, int VB, int ACT>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, int runs) {
+template <int DT, int VB, int U, int ACT>
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, int segs) {
+  constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
   pdl_trigger();
   pdl_wait();
-  const Place p = place_of(a, (int64_t)blockIdx.x * kThreads + threadIdx.x, runs);
-  if (p.n <= 0) return;
-  uint32_t wd[kRunWords<DT>];
-  run_load_raw<DT, VB>(elem_ptr<DT>(a.x, p.r * a.ld_x + p.c), p.n, wd);
-  constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
-  Run8 g, u, d;
-  kept_run(a, p, kHalves, 0, g);
-  if (ACT == kActSwiglu) kept_run(a, p, kHalves, 1, u);
-  run_unpack<DT>(wd, d);
-  if (ACT == kActSwiglu) {
-    const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
+  int64_t r;
+  int c;
+  if (!place_of(a, segs, U, r, c)) return;
+  uint32_t w[U][kRunWords<DT>];
+  Kept k[U][kHalves];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float gk = g.v[i], uk = u.v[i];
-      const float gc = cap(gk, L), uc = clip(uk, L), s = sigmoid<DT>(gc);
-      g.v[i] = gk > L ? 0.0f : d.v[i] * uc * (s * (1.0f + gc * (1.0f - s)));
-      u.v[i] = fabsf(uk) > L ? 0.0f : d.v[i] * (gc * s);
-    }
-  } else {
+  for (int u = 0; u < U; ++u) {
+    const int cu = c + u * kSpan;
+    run_load_raw<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + cu), a.W - cu, w[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * d.v[i] * (g.v[i] < 0.0f ? 0.0f : g.v[i]);
+    for (int h = 0; h < kHalves; ++h) k[u][h] = kept_run(a, r, cu, kHalves, h);
   }
-  run_store<DT, VB>(elem_ptr<DT>(a.out, p.r * a.ld_out + p.c), p.n, g);
-  if (ACT == kActSwiglu)
-    run_store<DT, VB>(elem_ptr<DT>(a.out, p.r * a.ld_out + a.W + p.c), p.n, u);
+  const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int cu = c + u * kSpan;
+    Run8 g, up, d;
+    run_unpack<DT>(w[u], d);
+    e4m3x8_to_float(k[u][0].codes, block_scale(k[u][0].byte), g);
+    if constexpr (ACT == kActSwiglu) {
+      e4m3x8_to_float(k[u][kHalves - 1].codes, block_scale(k[u][kHalves - 1].byte), up);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float gk = g.v[i], uk = up.v[i];
+        const float gc = cap(gk, L), uc = clip(uk, L), s = sigmoid<DT>(gc);
+        g.v[i] = gk > L ? 0.0f : d.v[i] * uc * (s * (1.0f + gc * (1.0f - s)));
+        up.v[i] = fabsf(uk) > L ? 0.0f : d.v[i] * (gc * s);
+      }
+      run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + a.W + cu), a.W - cu, up);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * d.v[i] * (g.v[i] < 0.0f ? 0.0f : g.v[i]);
+    }
+    run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, g);
+  }
 }
 
 int size_of(int dtype) { return dtype == kF32 ? 4 : 2; }
@@ -175,40 +209,49 @@ int width(const void* p, int64_t ld, int W, int dtype) {
 }
 
 template <typename K>
-cudaError_t go(K kernel, const KeepArgs& a, cudaStream_t s) {
-  const int runs = (a.W + 31) / 32 * 4;
-  const int64_t blocks = ((int64_t)a.R * runs + kThreads - 1) / kThreads;
-  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, runs);
+cudaError_t go(K kernel, const KeepArgs& a, int u, cudaStream_t s) {
+  const int segs = (a.W + u * kSpan - 1) / (u * kSpan);
+  const int64_t blocks = ((int64_t)a.R * segs + kThreads / 32 - 1) / (kThreads / 32);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, segs);
 }
 
-#define MOE_BY_WIDTH(KERNEL, DT, vb, ...)                                   \
-  switch (vb) {                                                             \
-    case 16: return go(KERNEL<DT, 16 __VA_ARGS__>, a, s);                   \
-    case 8: return go(KERNEL<DT, 8 __VA_ARGS__>, a, s);                     \
-    case 4: return go(KERNEL<DT, 4 __VA_ARGS__>, a, s);                     \
-    default: break;                                                         \
-  }                                                                         \
-  if constexpr (DT != kF32) return go(KERNEL<DT, 2 __VA_ARGS__>, a, s);     \
+// U spans a warp where that leaves the device enough warps, else one.
+constexpr int64_t kManyWarps = 152 * 16;
+int spans(const KeepArgs& a, int u) {
+  return (int64_t)a.R * ((a.W + u * kSpan - 1) / (u * kSpan)) >= kManyWarps ? u : 1;
+}
+
+#define MOE_BY_WIDTH(KERNEL, DT, U, vb, ...)                                                      \
+  const bool many = spans(a, U) == U;                                                             \
+  switch (vb) {                                                                                   \
+    case 16:                                                                                      \
+      return many ? go(KERNEL<DT, 16, U __VA_ARGS__>, a, U, s)                                    \
+                  : go(KERNEL<DT, 16, 1 __VA_ARGS__>, a, 1, s);                                   \
+    case 8: return go(KERNEL<DT, 8, 1 __VA_ARGS__>, a, 1, s);                                     \
+    case 4: return go(KERNEL<DT, 4, 1 __VA_ARGS__>, a, 1, s);                                     \
+    default: break;                                                                               \
+  }                                                                                               \
+  if constexpr (DT != kF32) return go(KERNEL<DT, 2, 1 __VA_ARGS__>, a, 1, s);                     \
   return cudaErrorInvalidValue;
 #define MOE_COMMA ,
 
 template <int DT>
 cudaError_t checkpoint_typed(const KeepArgs& a, cudaStream_t s) {
-  MOE_BY_WIDTH(checkpoint_kernel, DT, width(a.x, a.ld_x, a.W, DT))
+  MOE_BY_WIDTH(checkpoint_kernel, DT, 4, width(a.x, a.ld_x, a.W, DT))
 }
 template <int DT>
 cudaError_t restore_typed(const KeepArgs& a, cudaStream_t s) {
-  MOE_BY_WIDTH(restore_kernel, DT, width(a.out, a.ld_out, a.W, DT))
+  MOE_BY_WIDTH(restore_kernel, DT, 4, width(a.out, a.ld_out, a.W, DT))
 }
 template <int DT, int ACT>
 cudaError_t act_typed(const KeepArgs& a, cudaStream_t s) {
   const int vb = std::min(width(a.x, a.ld_x, a.W, DT), width(a.out, a.ld_out, a.W, DT));
-  MOE_BY_WIDTH(act_kernel, DT, vb, MOE_COMMA ACT)
+  MOE_BY_WIDTH(act_kernel, DT, 2, vb, MOE_COMMA ACT)
 }
 template <int DT, int ACT>
 cudaError_t act_grad_typed(const KeepArgs& a, cudaStream_t s) {
   const int vb = std::min(width(a.x, a.ld_x, a.W, DT), width(a.out, a.ld_out, a.W, DT));
-  MOE_BY_WIDTH(act_grad_kernel, DT, vb, MOE_COMMA ACT)
+  MOE_BY_WIDTH(act_grad_kernel, DT, 2, vb, MOE_COMMA ACT)
 }
 #undef MOE_BY_WIDTH
 #undef MOE_COMMA

@@ -31,41 +31,53 @@ __device__ __forceinline__ void write_panel(const MxQuantArgs& a, int64_t r, int
   uint32_t lo = byte | (__shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8);
   lo |= __shfl_down_sync(0xFFFFFFFFu, lo, 8) << 16;
   const uint32_t hi = __shfl_sync(0xFFFFFFFFu, lo, 16);
-  const int64_t rows_p = (a.R + 1) & ~1;
+  const int64_t rows_p = ((int64_t)a.R + 1) & ~int64_t(1);
   if (lane == 0)
     *reinterpret_cast<uint2*>(a.scales + (panel * rows_p + r) * 8) = make_uint2(lo, hi);
 }
 
-template <int DT, int VB>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const MxQuantArgs a, int panels) {
+// A warp's row and first of U panels; false: nothing to do.
+__device__ __forceinline__ bool place_of(const MxQuantArgs& a, int segs, int u, int64_t& r,
+                                         int& panel) {
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  r = i <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)segs) : i / segs;
+  panel = (int)(i - r * segs) * u;
+  return r < (a.n_rows ? min(a.R, *a.n_rows) : a.R);
+}
+
+// U panels a warp, their loads issued together.
+template <int DT, int VB, int U>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const MxQuantArgs a, int segs) {
   pdl_trigger();
   pdl_wait();
-  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t r = i / panels;
-  const int panel = (int)(i - r * panels);
-  const int rows = a.n_rows ? min(a.R, *a.n_rows) : a.R;
-  if (r >= rows) return;  // the whole warp
+  int64_t r;
+  int panel;
+  if (!place_of(a, segs, U, r, panel)) return;
   const int c = panel * kMxPanel + (threadIdx.x & 31) * 8;
-  uint32_t w[kRunWords<DT>];
-  run_load_raw<DT, VB>(static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ld_x + c, a.D - c,
-                       w);
-  Run8 v;
-  run_unpack<DT>(w, v);
-  write_panel(a, r, panel, v);
+  const auto* x = static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ld_x + c;
+  uint32_t w[U][kRunWords<DT>];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    run_load_raw<DT, VB>(x + u * kMxPanel, a.D - c - u * kMxPanel, w[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (U > 1 && (panel + u) * kMxPanel >= a.Dp) break;
+    Run8 v;
+    run_unpack<DT>(w[u], v);
+    write_panel(a, r, panel + u, v);
+  }
 }
 
 template <int DT, int VB>
 __global__ void __launch_bounds__(kThreads) restore_kernel(const MxQuantArgs a, int panels) {
   pdl_trigger();
   pdl_wait();
-  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t r = i / panels;
-  const int panel = (int)(i - r * panels);
-  const int rows = a.n_rows ? min(a.R, *a.n_rows) : a.R;
-  if (r >= rows) return;
+  int64_t r;
+  int panel;
+  if (!place_of(a, panels, 1, r, panel)) return;
   const int lane = threadIdx.x & 31, c = panel * kMxPanel + lane * 8;
   if (c >= a.D) return;
-  const int64_t rows_p = (a.R + 1) & ~1;
+  const int64_t rows_p = ((int64_t)a.R + 1) & ~int64_t(1);
   const uint32_t code =
       reinterpret_cast<const uint32_t*>(a.codes + r * (a.Dp / 2) + panel * (kMxPanel / 2))[lane];
   Run8 v;
@@ -103,33 +115,36 @@ __global__ void __launch_bounds__(kThreads) quantize_t_kernel(const MxQuantArgs 
 int size_of(int dtype) { return dtype == kF32 ? 4 : 2; }
 
 template <typename K>
-cudaError_t go(K kernel, const MxQuantArgs& a, cudaStream_t s) {
-  const int panels = a.Dp / kMxPanel;
-  const int64_t warps = (int64_t)a.R * panels;
-  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, panels);
+cudaError_t go(K kernel, const MxQuantArgs& a, int u, cudaStream_t s) {
+  const int segs = (a.Dp / kMxPanel + u - 1) / u;
+  const int64_t blocks = ((int64_t)a.R * segs + kThreads / 32 - 1) / (kThreads / 32);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, segs);
 }
 
 template <int DT>
 cudaError_t quantize_typed(const MxQuantArgs& a, cudaStream_t s) {
   switch (access_bytes(a.x, a.ld_x * size_of(DT), (int64_t)a.D * size_of(DT))) {
-    case 16: return go(quantize_kernel<DT, 16>, a, s);
-    case 8: return go(quantize_kernel<DT, 8>, a, s);
-    case 4: return go(quantize_kernel<DT, 4>, a, s);
+    case 16:
+      // four panels a warp where that leaves the device enough warps
+      return (int64_t)a.R * (a.Dp / kMxPanel) >= 4 * 152 * 16
+                 ? go(quantize_kernel<DT, 16, 4>, a, 4, s)
+                 : go(quantize_kernel<DT, 16, 1>, a, 1, s);
+    case 8: return go(quantize_kernel<DT, 8, 1>, a, 1, s);
+    case 4: return go(quantize_kernel<DT, 4, 1>, a, 1, s);
     default: break;
   }
-  if constexpr (DT != kF32) return go(quantize_kernel<DT, 2>, a, s);
+  if constexpr (DT != kF32) return go(quantize_kernel<DT, 2, 1>, a, 1, s);
   return cudaErrorInvalidValue;
 }
 template <int DT>
 cudaError_t restore_typed(const MxQuantArgs& a, cudaStream_t s) {
   switch (access_bytes(a.out, a.ld_out * size_of(DT), (int64_t)a.D * size_of(DT))) {
-    case 16: return go(restore_kernel<DT, 16>, a, s);
-    case 8: return go(restore_kernel<DT, 8>, a, s);
-    case 4: return go(restore_kernel<DT, 4>, a, s);
+    case 16: return go(restore_kernel<DT, 16>, a, 1, s);
+    case 8: return go(restore_kernel<DT, 8>, a, 1, s);
+    case 4: return go(restore_kernel<DT, 4>, a, 1, s);
     default: break;
   }
-  if constexpr (DT != kF32) return go(restore_kernel<DT, 2>, a, s);
+  if constexpr (DT != kF32) return go(restore_kernel<DT, 2>, a, 1, s);
   return cudaErrorInvalidValue;
 }
 

@@ -364,8 +364,10 @@ struct RowVec {
   }
 };
 
-// One thread a vector of a token's output; four rows in flight at a time.
-template <int DT, int VB, bool WEIGHTS>
+// One thread a vector of a token's output.  ROWS routes at a time: their row numbers, then
+// their vectors, then the sum, so that ROWS reads are in flight (ROWS = K where K has a
+// kernel of its own: one round).
+template <int DT, int VB, int ROWS>
 __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int64_t ld_in,
                                                       int64_t ld_out, int vecs) {
   using RV = RowVec<DT, VB>;
@@ -379,27 +381,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int64_t l
   float acc[RV::kN];
 #pragma unroll
   for (int j = 0; j < RV::kN; ++j) acc[j] = 0.0f;
-  for (int k0 = 0; k0 < a.K; k0 += 4) {
-    V y[4];
-    float w[4];
-    bool live[4];
+  for (int k0 = 0; k0 < a.K; k0 += ROWS) {
+    const int64_t route = (int64_t)t * a.K + k0;
+    int r[ROWS];
+    float w[ROWS];
+    V y[ROWS];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t route = (int64_t)t * a.K + k0 + u;
-      const int r = k0 + u < a.K ? route_row(a, route) : -1;
-      live[u] = r >= 0;
-      if (live[u]) {
-        y[u] = in[r * ld_in];
-        w[u] = WEIGHTS ? a.w[route] : 1.0f;
-      }
+    for (int u = 0; u < ROWS; ++u) r[u] = k0 + u < a.K ? route_row(a, route + u) : -1;
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      w[u] = a.w && r[u] >= 0 ? a.w[route + u] : 1.0f;
+      if (r[u] >= 0) y[u] = in[r[u] * ld_in];
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (!live[u]) continue;
+    for (int u = 0; u < ROWS; ++u) {
       float f[RV::kN];
       RV::unpack(y[u], f);
+      if (r[u] >= 0) {
 #pragma unroll
-      for (int j = 0; j < RV::kN; ++j) acc[j] = WEIGHTS ? fmaf(w[u], f[j], acc[j]) : acc[j] + f[j];
+        for (int j = 0; j < RV::kN; ++j) acc[j] = fmaf(w[u], f[j], acc[j]);
+      }
     }
   }
   reinterpret_cast<V*>(a.out)[t * ld_out + v] = RV::pack(acc);
@@ -548,19 +549,21 @@ cudaError_t combine_typed(const RowArgs& a, cudaStream_t s) {
                           access_bytes(a.out, a.ld_out * sz, row));
   const int vecs = (int)(row / vb);
   const dim3 grid((unsigned)blocks_of((int64_t)a.T * vecs));
-  auto go = [&](auto with, auto without) {
-    const int64_t li = a.ld_x * sz / vb, lo = a.ld_out * sz / vb;
-    return a.w ? launch_pdl(with, grid, dim3(256), 0, s, a, li, lo, vecs)
-               : launch_pdl(without, grid, dim3(256), 0, s, a, li, lo, vecs);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, dim3(256), 0, s, a, a.ld_x * sz / vb, a.ld_out * sz / vb, vecs);
   };
-  switch (vb) {
-    case 16: return go(combine_kernel<DT, 16, true>, combine_kernel<DT, 16, false>);
-    case 8: return go(combine_kernel<DT, 8, true>, combine_kernel<DT, 8, false>);
-    case 4: return go(combine_kernel<DT, 4, true>, combine_kernel<DT, 4, false>);
-    default: break;
+  if (vb == 16) {
+    switch (a.K) {
+      case 1: return go(combine_kernel<DT, 16, 1>);
+      case 2: return go(combine_kernel<DT, 16, 2>);
+      case 6: return go(combine_kernel<DT, 16, 6>);
+      case 8: return go(combine_kernel<DT, 16, 8>);
+      default: return go(combine_kernel<DT, 16, 4>);
+    }
   }
-  if constexpr (DT != kF32)
-    return go(combine_kernel<DT, 2, true>, combine_kernel<DT, 2, false>);
+  if (vb == 8) return go(combine_kernel<DT, 8, 4>);
+  if (vb == 4) return go(combine_kernel<DT, 4, 4>);
+  if constexpr (DT != kF32) return go(combine_kernel<DT, 2, 4>);
   return cudaErrorInvalidValue;
 }
 
