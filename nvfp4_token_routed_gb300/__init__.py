@@ -548,7 +548,8 @@ def _matrix(t, name):
     dt = _DTYPE.get(t.dtype)
     if dt is None or t.dim() != 2:
         raise ValueError(f"{name}: a 2-D float32, bfloat16 or float16 tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()  # -1 on the CPU
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: a tensor of the current CUDA device (no CPU path exists)")
     rows, cols = t.shape
     ld, one = t.stride()
@@ -598,7 +599,7 @@ def _dlogits(t, logits, stream):
 def _raw(stream):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def token_logp(logits, actions, temperature=1.0, logp=None, stream=None):

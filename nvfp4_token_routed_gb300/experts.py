@@ -65,28 +65,31 @@ def sort_routes(topk_ids, E, plan=None, ws=None, stream=None):
     """Stable counting sort of the routes topk_ids [T, K] (int32 or int64, -1: empty slot) by
     expert: a RoutePlan.  Ids outside [-1, E) are empty slots too; moe_nvfp4_read_status(ws)
     reports them."""
-    if topk_ids.dim() != 2 or not topk_ids.is_cuda:
-        raise ValueError("topk_ids: a 2-D tensor of the current CUDA device (no CPU path exists)")
-    ids = _arg(topk_ids, "topk_ids", topk_ids.shape, _ID, topk_ids)
-    if topk_ids.get_device() != torch.cuda.current_device():
-        raise ValueError("topk_ids: a tensor of the current CUDA device")
-    T, K = topk_ids.shape
-    if plan is None:
-        plan = RoutePlan(_out(None, "offsets", (E + 1,), torch.int32, topk_ids, stream),
-                         _out(None, "perm", (T * K,), torch.int32, topk_ids, stream),
-                         _out(None, "inv", (T, K), torch.int32, topk_ids, stream))
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids: one row of expert ids per token")
+    dev = topk_ids.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("topk_ids: a tensor of the current CUDA device (no CPU path exists)")
+    shape = T, K = topk_ids.shape
+    ids = _arg(topk_ids, "topk_ids", shape, _ID, topk_ids)
     L = lib()
+    if plan is None:
+        plan = RoutePlan(_out(None, "offsets", E + 1, torch.int32, topk_ids, stream),
+                         _out(None, "perm", T * K, torch.int32, topk_ids, stream),
+                         _out(None, "inv", shape, torch.int32, topk_ids, stream))
+        ptrs = plan.offsets.data_ptr(), plan.perm.data_ptr(), plan.inv.data_ptr()
+    else:
+        ptrs = (_arg(plan.offsets, "offsets", (E + 1,), _I32, topk_ids),
+                _arg(plan.perm, "perm", (T * K,), _I32, topk_ids),
+                _arg(plan.inv, "inv", shape, _I32, topk_ids))
     if ws is None:
         n = L.moe_nvfp4_sort_routes_workspace_bytes(T, K, E)
-        ws = _out(None, "ws", (n,), torch.uint8, topk_ids, stream)
+        ws = _out(None, "ws", n, torch.uint8, topk_ids, stream)
+        wp = ws.data_ptr()
     else:
-        n = ws.numel()
-    _check(L.moe_nvfp4_sort_routes(
-        T, K, E, ids, _IDS64[topk_ids.dtype],
-        _arg(plan.offsets, "offsets", (E + 1,), _I32, topk_ids),
-        _arg(plan.perm, "perm", (T * K,), _I32, topk_ids),
-        _arg(plan.inv, "inv", topk_ids.shape, _I32, topk_ids),
-        _arg(ws, "ws", ws.shape, _U8, topk_ids), n, _raw(stream)), "moe_nvfp4_sort_routes")
+        n, wp = ws.numel(), _arg(ws, "ws", ws.shape, _U8, topk_ids)
+    _check(L.moe_nvfp4_sort_routes(T, K, E, ids, _IDS64[topk_ids.dtype], *ptrs, wp, n,
+                                   _raw(stream)), "moe_nvfp4_sort_routes")
     return plan
 
 
@@ -100,7 +103,7 @@ def dispatch(x, plan, rows=None, stream=None):
         inv = _arg(plan.inv, "inv", (T, K), _I32, x.on())
         if rows is None:
             rows = MxTensor.empty((T * K, x.shape[1]), x.on(), stream)
-        rows.on(x)
+        rows.on()
         _check(lib().moe_nvfp4_mx_dispatch(x.c, K, inv, rows.c, _raw(stream)),
                "moe_nvfp4_mx_dispatch")
         return rows
@@ -162,9 +165,9 @@ class _Held:
 
     def _alloc(self, codes_shape, scales_shape, n_codes, n_scales, like, stream):
         at = (n_codes + 255) // 256 * 256
-        self._buf = buf = _out(None, "codes", (at + n_scales,), torch.uint8, like, stream)
+        self._buf = buf = _out(None, "codes", at + n_scales, torch.uint8, like, stream)
         self._codes = self._scales = None
-        self._cut = codes_shape, scales_shape, n_codes, n_scales, at
+        self._cut = codes_shape, scales_shape, n_codes, at
         self.device = like.get_device()
         p = buf.data_ptr()
         return p, p + at
@@ -178,20 +181,17 @@ class _Held:
     @property
     def scales(self):
         if self._scales is None:
-            self._scales = self._buf[self._cut[4]:].view(self._cut[1])
+            self._scales = self._buf[self._cut[3]:].view(self._cut[1])
         return self._scales
 
     def nbytes(self):
         return self.codes.numel() + self.scales.numel()
 
-    def on(self, like=None):
-        """A tensor of it, on the current device (and on `like`'s)."""
+    def on(self):
+        """A tensor of it, which has to lie on the current device (as every matrix of rows)."""
         t = self._buf if self._buf is not None else self._codes
-        if self.device != torch.cuda.current_device() or self.device < 0:
+        if self.device < 0 or self.device != torch._C._cuda_getDevice():
             raise ValueError("codes: a tensor of the current CUDA device (no CPU path exists)")
-        if like is not None and self.device != (like.device if isinstance(like, _Held)
-                                                else like.get_device()):
-            raise ValueError(f"codes: on device {self.device}, other arguments on another")
         return t
 
 
@@ -218,10 +218,10 @@ class Checkpoint(_Held):
         k.c = k._alloc((rows, h, 32 * b), (rows, h, b), 32 * rows * h * b, rows * h * b, like, stream)
         return k
 
-    def _for(self, rows, cols, like):
+    def _for(self, rows, cols):
         if self.rows != rows or self.cols != cols:
             raise ValueError(f"kept: holds {self.rows} rows of {self.cols}, got {rows} of {cols}")
-        self.on(like)
+        self.on()
         return self.c
 
 
@@ -233,7 +233,7 @@ def checkpoint(x, kept=None, n_rows=None, stream=None):
         kept = Checkpoint.empty(R, D, x.dtype, x, stream=stream)
     elif kept.act is not None:
         raise ValueError("kept: made for an activation's input")
-    codes, scales = kept._for(R, D, x)
+    codes, scales = kept._for(R, D)
     _check(lib().moe_nvfp4_checkpoint(m, codes, scales, _n_rows(n_rows, x), _raw(stream)),
            "moe_nvfp4_checkpoint")
     return kept
@@ -268,7 +268,7 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
     if kept is not None:
         if kept.act != act or kept.swiglu_limit != float(swiglu_limit):
             raise ValueError("kept: made for another activation")
-        codes, scales = kept._for(R, I, h)
+        codes, scales = kept._for(R, I)
     _check(lib().moe_nvfp4_expert_act(m, ACT[act], swiglu_limit, p, ld, codes, scales,
                                       _n_rows(n_rows, h), _raw(stream)), "moe_nvfp4_expert_act")
     return y if kept is None else (y, kept)
@@ -281,7 +281,7 @@ def expert_act_grad(kept, dy, dh=None, n_rows=None, stream=None):
         raise ValueError("kept: expected what expert_act kept")
     m = _matrix(dy, "dy")
     R, I = dy.shape
-    codes, scales = kept._for(R, I, dy)
+    codes, scales = kept._for(R, I)
     dh, p, ld = _like(dh, "dh", (R, kept.halves * I), dy.dtype, dy, stream)
     _check(lib().moe_nvfp4_expert_act_grad(codes, scales, ACT[kept.act], kept.swiglu_limit, m,
                                            p, ld, _n_rows(n_rows, dy), _raw(stream)),
@@ -326,7 +326,7 @@ def _mx_out(out, shape, x, stream):
         return MxTensor.empty(shape, x, stream)
     if out.shape != shape:
         raise ValueError(f"out: expected {shape}, got {out.shape}")
-    out.on(x)
+    out.on()
     return out
 
 
@@ -380,7 +380,7 @@ def _product_args(x, w, offsets, dtype, out, stream):
     if E > 1 and offsets is None:
         raise ValueError("offsets: needed for a stack of weights")
     like = x.on()
-    w.on(x)
+    w.on()
     if out is not None:
         dtype = out.dtype
     dt = _DTYPE.get(dtype)
