@@ -75,6 +75,10 @@ struct MxMaps {
   CUtensorMap x[4];  // 16, 32, 64, 128 rows
 };
 
+// A value that is the same in every lane, and that the compiler then knows to be: what
+// depends on it (branches, descriptors, addresses of copies) stays in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // Two values as 16-bit elements, a in the low half.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -174,7 +178,7 @@ __device__ __forceinline__ void drain_ring(const Ring& R, int loaded, int n_stag
       if (globaltimer() - t0 > kWaitLimitNs) return;
 }
 
-// A CTA's walk over its items.
+// A CTA's walk over its items, by a whole warp.
 struct Item {
   int e, mt;
   int row0, rows;  // first row of the tile, rows
@@ -185,12 +189,13 @@ struct Walk {
   int m_tiles, unit, e;
   // Row tiles of a group are equal and whole units.
   __device__ __forceinline__ Item at(int item) {
-    while (item >= first_item[e + 1]) ++e;
-    const int tiles = (first_item[e + 1] - first_item[e]) / m_tiles;
-    const int local = item - first_item[e], group = first_row[e + 1] - first_row[e];
+    while (item >= uniform(first_item[e + 1])) ++e;
+    const int i0 = uniform(first_item[e]), r0 = uniform(first_row[e]);
+    const int tiles = (uniform(first_item[e + 1]) - i0) / m_tiles;
+    const int group = uniform(first_row[e + 1]) - r0;
     const int h = ((group + tiles - 1) / tiles + unit - 1) & -unit;
-    const int tt = local % tiles;
-    return Item{e, local / tiles, first_row[e] + tt * h, min(h, group - tt * h)};
+    const int mt = (item - i0) / tiles, tt = item - i0 - mt * tiles;
+    return Item{e, mt, r0 + tt * h, min(h, group - tt * h)};
   }
 };
 
@@ -247,13 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Ring R{smem};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kFlagsOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* epi_stop = reinterpret_cast<volatile int*>(tmem_slot + 2);
   int* s_max16 = reinterpret_cast<int*>(tmem_slot + 3);
   int* s_sum = reinterpret_cast<int*>(smem + kWarpSumOff);
   int* first_item = reinterpret_cast<int*>(smem + kGroupsOff);
   int* first_row = first_item + a.E + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int m_tiles = (a.N + 127) / 128;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -267,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(R.bar(kDrain), 1);
     *abort_flag = 0;
-    *epi_stop = 0;
     *s_max16 = 16;
     fence_barrier_init();
     prefetch_tmap(&maps.w);
@@ -281,15 +284,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   pdl_wait();
   pdl_trigger();
 
   lay_out_groups<kThreads>(a, kTileN, 16, m_tiles, first_item, first_row, s_sum, s_max16);
-  const int n_items = first_item[a.E];
+  const int n_items = uniform(first_item[a.E]);
 
   // ---- geometry from the largest tile
-  const int max16 = *s_max16;
+  const int max16 = uniform(*s_max16);
   const int acc_stride = (max16 + 31) & ~31;
   const int sfb_bytes = (8 * (acc_stride + 2) + 127) & ~127;  // a warp reads whole 32s, from an odd row on
   const int off_b = kABytes, off_sfa = off_b + max16 * kRowBytes, off_sfb = off_sfa + kSfaBytes;
@@ -427,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < a.kblocks; ++kb) {
         if (!ready)
           ok = __all_sync(0xFFFFFFFFu,
-                          wait_or_leave(R.bar(kSfReady + stage), phase, abort_flag) &&
-                              wait_or_leave(R.bar(kFull + stage), phase, abort_flag));
+                          wait_or_leave(R.bar(kSfReady + stage), phase, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const int s = stage;
@@ -442,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ks = 0; ks < 4; ++ks) {
           // the next stage is looked at while this one's first MMAs run
           if (ks == 2)
-            ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(kSfReady + stage), phase) &&
-                                                phase_done(R.bar(kFull + stage), phase));
+            ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(kSfReady + stage), phase));
           const uint32_t id = 2u * (ks & 1);  // which two of a column's four scales
           mma_mxf4_warp(acc, smem_desc(sb + ks * 32, 16, 1024, 2),
                         smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
@@ -465,7 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     using T = typename Elem<DT>::type;
     const int q = warp & 3;
-    const int et = threadIdx.x - 64;
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     T* out = static_cast<T*>(a.out);
     int local = 0;
@@ -474,16 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = it.mt * 128 + q * 32 + lane;  // this lane's feature
       const int n16 = (it.rows + 15) & ~15;
       const int buf = local % nbuf;
-      if (!wait_or_leave(R.bar(kAccFull + buf), (uint32_t)(local / nbuf) & 1u, abort_flag))
-        *epi_stop = 1;
-      named_bar_sync(1, 128);
-      const bool stop = *epi_stop != 0;
-      named_bar_sync(1, 128);
-      if (stop) {
-        // what this CTA leaves: NaN, by one thread a feature
+      if (!__all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(kAccFull + buf),
+                                                 (uint32_t)(local / nbuf) & 1u, abort_flag))) {
+        // what this warp leaves: NaN in its features
         for (; item < n_items; item += gridDim.x) {
           const Item left = walk.at(item);
-          const int f = left.mt * 128 + et;
+          const int f = left.mt * 128 + q * 32 + lane;
           for (int j = 0; f < a.N && j < left.rows; ++j)
             out[(left.row0 + j) * a.ld + f] = (T)float_to_elem<DT>(__int_as_float(0x7FC00000));
         }
@@ -602,28 +598,6 @@ __device__ __forceinline__ void arrive_rank0(uint32_t bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
 }
-// As wait_or_leave, for a barrier that the other CTA arrives on too.
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  uint64_t t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    if (ok) return true;
-    if (*abort_flag) return false;
-    if (t0 == 0) {
-      t0 = globaltimer();
-    } else if (globaltimer() - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -642,13 +616,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   const Ring R{smem};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + pair::kFlagsOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* epi_stop = reinterpret_cast<volatile int*>(tmem_slot + 2);
   int* s_most = reinterpret_cast<int*>(tmem_slot + 3);
   int* s_sum = reinterpret_cast<int*>(smem + pair::kWarpSumOff);
   int* first_item = reinterpret_cast<int*>(smem + kGroupsOff);
   int* first_row = first_item + a.E + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int m_pairs = (a.N + 255) / 256;
   if (threadIdx.x == 0) {
@@ -661,7 +634,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     mbar_init(R.bar(pair::kAccEmpty), 16);
     mbar_init(R.bar(pair::kDrain), 1);
     *abort_flag = 0;
-    *epi_stop = 0;
     *s_most = 32;
     fence_barrier_init();
     prefetch_tmap(&maps.w);
@@ -674,15 +646,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   cluster_arrive();  // the other CTA's barriers and TMEM are there
   cluster_wait();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   pdl_wait();
   pdl_trigger();
   lay_out_groups<pair::kThreads>(a, pair::kTileN, 32, m_pairs, first_item, first_row, s_sum,
                                  s_most);
-  const int n_items = first_item[a.E];
+  const int n_items = uniform(first_item[a.E]);
   const int item0 = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
-  const int most = *s_most;                    // rows of the largest tile, whole 32s
+  const int most = uniform(*s_most);                // rows of the largest tile, whole 32s
   const int sfb_bytes = (8 * (most + 2) + 127) & ~127;
   const int off_b = kABytes, off_sfa = off_b + most / 2 * kRowBytes, off_sfb = off_sfa + kSfaBytes;
   const int stage_bytes = (off_sfb + sfb_bytes + 1023) & ~1023;
@@ -725,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const uint32_t sfb = 8u * (uint32_t)min(2 * half + (it.row0 != x_even ? 2 : 0), x_rows - x_even);
       for (int kb = 0; kb < a.kblocks; ++kb) {
         ok = __all_sync(0xFFFFFFFFu,
-                        wait_pair(R.bar(pair::kEmpty + stage), phase ^ 1, abort_flag));
+                        wait_or_leave(R.bar(pair::kEmpty + stage), phase ^ 1, abort_flag));
         if (!ok) break;
         const uint32_t sb = smem_u32(stages + stage * stage_bytes);
         const uint32_t full = R.bar(pair::kFull + stage);
@@ -805,15 +777,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     for (int item = item0; ok && item < n_items; item += step) {
       const Item it = walk.at(item);
       const uint32_t idesc = idesc_mxf4(256, (it.rows + 31) & ~31);
-      ok = __all_sync(0xFFFFFFFFu, wait_pair(R.bar(pair::kAccEmpty), acc_phase, abort_flag));
+      ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(pair::kAccEmpty), acc_phase, abort_flag));
       if (!ok) break;
       acc_phase ^= 1;
       tc_fence_after();
       for (int kb = 0; kb < a.kblocks; ++kb) {
         if (!ready)
           ok = __all_sync(0xFFFFFFFFu,
-                          wait_or_leave(R.bar(pair::kSfReady + stage), phase, abort_flag) &&
-                              wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag));
+                          wait_or_leave(R.bar(pair::kSfReady + stage), phase, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const int s = stage;
@@ -823,8 +794,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           if (ks == 2)
-            ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(pair::kSfReady + stage), phase) &&
-                                                phase_done(R.bar(pair::kFull + stage), phase));
+            ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(pair::kSfReady + stage), phase));
           const uint32_t id = 2u * (ks & 1);
           pair::mma_warp(tmem, smem_desc(sb + ks * 32, 16, 1024, 2),
                          smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
@@ -852,14 +822,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const Item it = walk.at(item);
       const int n = it.mt * 256 + rank * 128 + q * 32 + lane;
       const int half = ((it.rows + 31) & ~31) / 2;
-      if (!wait_pair(R.bar(pair::kAccFull), acc_phase, abort_flag)) *epi_stop = 1;
-      named_bar_sync(1, 256);
-      const bool stop = *epi_stop != 0;
-      named_bar_sync(1, 256);
-      if (stop) {
+      if (!__all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(pair::kAccFull), acc_phase, abort_flag))) {
         for (; item < n_items; item += step) {
           const Item left = walk.at(item);
-          const int f = left.mt * 256 + rank * 128 + ((int)threadIdx.x & 127);
+          const int f = left.mt * 256 + rank * 128 + q * 32 + lane;
           for (int j = h; f < a.N && j < left.rows; j += 2)
             out[(left.row0 + j) * a.ld + f] = (T)float_to_elem<DT>(__int_as_float(0x7FC00000));
         }
@@ -873,13 +839,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       if constexpr (DT != kF32) {
         uint32_t w[64];  // 128 rows in pairs
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          if (16 * g >= half) continue;
-          float v[16];
-          tmem_ld16(acc + 16 * g, v);
+        for (int g = 0; g < 4; ++g) {  // two loads of 16 columns in flight
+          if (32 * g >= half) continue;
+          float v[32];
+          tmem_ld16(acc + 32 * g, *reinterpret_cast<float(*)[16]>(v));
+          if (32 * g + 16 < half)
+            tmem_ld16(acc + 32 * g + 16, *reinterpret_cast<float(*)[16]>(v + 16));
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[8 * g + i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+          for (int i = 0; i < 16; ++i) w[16 * g + i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
         }
         tc_fence_before();
         __syncwarp();
