@@ -81,28 +81,60 @@ __device__ __forceinline__ uint32_t float_to_elem(float v) {
 template <int DT>
 constexpr int kRunWords = DT == kF32 ? 8 : 4;
 
-// Reads elements [0, n) of a run of 8 (n <= 0: none, the rest zeros) by accesses of VB
-// bytes; with VB over the element's size n is 0 or 8 or a multiple of VB's elements.
+// A span: 256 consecutive elements of a row by one warp, run l (elements 8l ... 8l + 7) in
+// lane l.  With rows on 16 bytes (VB = 16) a lane reads and writes its run; else accesses of
+// VB bytes go by consecutive lanes (a run a lane, its accesses would lie 16 bytes apart and
+// each touch 16 sectors) and the runs are put together in shared memory, kSpanBytes a warp.
+// n: elements of the row from the span's first on (any number; those past n read as zero and
+// are not written).  All lanes take part.
+constexpr int kSpan = 256;
 template <int DT, int VB>
-__device__ __forceinline__ void run_load_raw(const void* p, int n, uint32_t (&w)[kRunWords<DT>]) {
+constexpr int kSpanBytes = VB == 16 ? 16 : kSpan * (DT == kF32 ? 4 : 2);  // 16: not used
+
+template <int DT, int VB>
+struct NarrowType {
+  using type = uint16_t;
+};
+template <int DT>
+struct NarrowType<DT, 4> {
+  using type = uint32_t;
+};
+template <int DT>
+struct NarrowType<DT, 8> {
+  using type = uint2;
+};
+
+template <int DT, int VB>
+__device__ __forceinline__ void span_load(const void* p, int n, void* stage,
+                                          uint32_t (&w)[kRunWords<DT>]) {
   constexpr int kSize = DT == kF32 ? 4 : 2;
-  constexpr int kPer = VB / kSize;  // elements an access
-  const char* c = static_cast<const char*>(p);
+  const int lane = threadIdx.x & 31;
+  if constexpr (VB == 16) {
+    constexpr int kPer = 16 / kSize;
+    const uint4* c = reinterpret_cast<const uint4*>(p) + lane * (8 / kPer);
 #pragma unroll
-  for (int i = 0; i < kRunWords<DT>; ++i) w[i] = 0u;
-#pragma unroll
-  for (int i = 0; i < 8 / kPer; ++i) {
-    if (i * kPer >= n) continue;
-    if constexpr (VB == 16) {
-      const uint4 t = *reinterpret_cast<const uint4*>(c + 16 * i);
+    for (int i = 0; i < 8 / kPer; ++i) {
+      const uint4 t = lane * 8 + i * kPer < n ? c[i] : make_uint4(0u, 0u, 0u, 0u);
       w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
-    } else if constexpr (VB == 8) {
-      const uint2 t = *reinterpret_cast<const uint2*>(c + 8 * i);
-      w[2 * i] = t.x, w[2 * i + 1] = t.y;
-    } else if constexpr (VB == 4) {
-      w[i] = *reinterpret_cast<const uint32_t*>(c + 4 * i);
-    } else {
-      w[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(c + 2 * i) << (16 * (i & 1));
+    }
+  } else {
+    using V = typename NarrowType<DT, VB>::type;
+    constexpr int kPer = VB / kSize, kN = kSpan / kPer / 32;
+    const V* c = reinterpret_cast<const V*>(p);
+    V t[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      t[i] = V{};
+      if ((32 * i + lane) * kPer < n) t[i] = c[32 * i + lane];
+    }
+    __syncwarp();  // an earlier use of the stage is over
+#pragma unroll
+    for (int i = 0; i < kN; ++i) reinterpret_cast<V*>(stage)[32 * i + lane] = t[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRunWords<DT> / 4; ++i) {
+      const uint4 q = reinterpret_cast<const uint4*>(stage)[lane * (kRunWords<DT> / 4) + i];
+      w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
   }
 }
@@ -117,28 +149,35 @@ __device__ __forceinline__ void run_unpack(const uint32_t (&w)[kRunWords<DT>], R
   }
 }
 template <int DT, int VB>
-__device__ __forceinline__ void run_store(void* p, int n, const Run8& r) {
+__device__ __forceinline__ void span_store(void* p, int n, void* stage, const Run8& r) {
   constexpr int kSize = DT == kF32 ? 4 : 2;
-  constexpr int kPer = VB / kSize;
+  const int lane = threadIdx.x & 31;
   uint32_t w[kRunWords<DT>];
 #pragma unroll
   for (int i = 0; i < kRunWords<DT>; ++i)
     w[i] = DT == kF32 ? float_to_elem<DT>(r.v[i])
                       : float_to_elem<DT>(r.v[(2 * i) & 7]) |
                             (float_to_elem<DT>(r.v[(2 * i + 1) & 7]) << 16);
-  char* c = static_cast<char*>(p);
+  if constexpr (VB == 16) {
+    constexpr int kPer = 16 / kSize;
+    uint4* c = reinterpret_cast<uint4*>(p) + lane * (8 / kPer);
 #pragma unroll
-  for (int i = 0; i < 8 / kPer; ++i) {
-    if (i * kPer >= n) continue;
-    if constexpr (VB == 16)
-      *reinterpret_cast<uint4*>(c + 16 * i) =
+    for (int i = 0; i < 8 / kPer; ++i)
+      if (lane * 8 + i * kPer < n)
+        c[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  } else {
+    using V = typename NarrowType<DT, VB>::type;
+    constexpr int kPer = VB / kSize, kN = kSpan / kPer / 32;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRunWords<DT> / 4; ++i)
+      reinterpret_cast<uint4*>(stage)[lane * (kRunWords<DT> / 4) + i] =
           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    else if constexpr (VB == 8)
-      *reinterpret_cast<uint2*>(c + 8 * i) = make_uint2(w[2 * i], w[2 * i + 1]);
-    else if constexpr (VB == 4)
-      *reinterpret_cast<uint32_t*>(c + 4 * i) = w[i];
-    else
-      *reinterpret_cast<uint16_t*>(c + 2 * i) = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    __syncwarp();
+    V* c = reinterpret_cast<V*>(p);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if ((32 * i + lane) * kPer < n) c[32 * i + lane] = reinterpret_cast<const V*>(stage)[32 * i + lane];
   }
 }
 

@@ -26,20 +26,28 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSpan = 256;  // values of a row that a warp takes at once
 
-// A warp's row and first span; false: nothing to do.
+// A warp's stage for spans of rows that do not lie on 16 bytes.
+template <int DT, int VB>
+__device__ __forceinline__ void* warp_stage() {
+  __shared__ __align__(16) uint8_t stage[kThreads / 32][kSpanBytes<DT, VB>];
+  return stage[threadIdx.x >> 5];
+}
+
+// A warp's row and its first span's first value; false: nothing to do.
 __device__ __forceinline__ bool place_of(const KeepArgs& a, int segs, int u, int64_t& r, int& c) {
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   r = i <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)segs) : i / segs;
-  c = (int)(i - r * segs) * (u * kSpan) + (threadIdx.x & 31) * 8;
+  c = (int)(i - r * segs) * (u * kSpan);
   return r < (a.n_rows ? min(a.R, *a.n_rows) : a.R);
 }
 
-// Writes a run's codes and its block's scale.  All lanes take part.
+// Writes a run's codes and its block's scale; c: the span's first value.  All lanes take
+// part.
 __device__ __forceinline__ void keep_run(const KeepArgs& a, int64_t r, int c, int halves, int half,
                                          const Run8& v) {
   const int Wp = (a.W + 31) & ~31;
+  c += (threadIdx.x & 31) * 8;
   const uint32_t byte = block_scale_byte<E4m3>(quad_max(v.amax_bits()));
   if (c >= Wp) return;
   const int64_t at = (r * halves + half) * Wp + c;
@@ -55,6 +63,7 @@ struct Kept {
 __device__ __forceinline__ Kept kept_run(const KeepArgs& a, int64_t r, int c, int halves,
                                          int half) {
   const int Wp = (a.W + 31) & ~31;
+  c += (threadIdx.x & 31) * 8;
   if (c >= a.W) return Kept{make_uint2(0u, 0u), 0u};
   const int64_t at = (r * halves + half) * Wp + c;
   return Kept{*reinterpret_cast<const uint2*>(a.codes + at), a.scales[at >> 5]};
@@ -76,10 +85,12 @@ __global__ void __launch_bounds__(kThreads) checkpoint_kernel(const KeepArgs a, 
   int64_t r;
   int c;
   if (!place_of(a, segs, U, r, c)) return;
+  void* stage = warp_stage<DT, VB>();
   uint32_t w[U][kRunWords<DT>];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    run_load_raw<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + c + u * kSpan), a.W - c - u * kSpan, w[u]);
+    span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + c + u * kSpan), a.W - c - u * kSpan, stage,
+                      w[u]);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     Run8 v;
@@ -95,6 +106,7 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const KeepArgs a, int
   int64_t r;
   int c;
   if (!place_of(a, segs, U, r, c)) return;
+  void* stage = warp_stage<DT, VB>();
   Kept k[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) k[u] = kept_run(a, r, c + u * kSpan, 1, 0);
@@ -102,7 +114,8 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const KeepArgs a, int
   for (int u = 0; u < U; ++u) {
     Run8 v;
     e4m3x8_to_float(k[u].codes, block_scale(k[u].byte), v);
-    run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + c + u * kSpan), a.W - c - u * kSpan, v);
+    span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + c + u * kSpan), a.W - c - u * kSpan,
+                       stage, v);
   }
 }
 
@@ -125,13 +138,14 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
   int64_t r;
   int c;
   if (!place_of(a, segs, U, r, c)) return;
+  void* stage = warp_stage<DT, VB>();
   uint32_t w[U][kHalves][kRunWords<DT>];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
-      run_load_raw<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + h * a.W + c + u * kSpan),
-                           a.W - c - u * kSpan, w[u][h]);
+      span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + h * a.W + c + u * kSpan),
+                        a.W - c - u * kSpan, stage, w[u][h]);
   const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -152,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
       }
     }
     const int cu = c + u * kSpan;
-    run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, y);
+    span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, stage, y);
     if (!a.codes) continue;
     keep_run(a, r, cu, kHalves, 0, g);
     if constexpr (ACT == kActSwiglu) keep_run(a, r, cu, kHalves, 1, up);
@@ -167,12 +181,13 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, in
   int64_t r;
   int c;
   if (!place_of(a, segs, U, r, c)) return;
+  void* stage = warp_stage<DT, VB>();
   uint32_t w[U][kRunWords<DT>];
   Kept k[U][kHalves];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int cu = c + u * kSpan;
-    run_load_raw<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + cu), a.W - cu, w[u]);
+    span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + cu), a.W - cu, stage, w[u]);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) k[u][h] = kept_run(a, r, cu, kHalves, h);
   }
@@ -192,12 +207,12 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, in
         g.v[i] = gk > L ? 0.0f : d.v[i] * uc * (s * (1.0f + gc * (1.0f - s)));
         up.v[i] = fabsf(uk) > L ? 0.0f : d.v[i] * (gc * s);
       }
-      run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + a.W + cu), a.W - cu, up);
+      span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + a.W + cu), a.W - cu, stage, up);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * d.v[i] * (g.v[i] < 0.0f ? 0.0f : g.v[i]);
     }
-    run_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, g);
+    span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, stage, g);
   }
 }
 

@@ -19,6 +19,13 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+static_assert(kMxPanel == kSpan, "a panel is a warp's span");
+
+template <int DT, int VB>
+__device__ __forceinline__ void* warp_stage() {
+  __shared__ __align__(16) uint8_t stage[kThreads / 32][kSpanBytes<DT, VB>];
+  return stage[threadIdx.x >> 5];
+}
 
 // A warp's 256 values (lane l holds 8l ... 8l+7): 4 bytes of codes a lane, 8 of scales.
 __device__ __forceinline__ void write_panel(const MxQuantArgs& a, int64_t r, int panel,
@@ -53,12 +60,13 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const MxQuantArgs a,
   int64_t r;
   int panel;
   if (!place_of(a, segs, U, r, panel)) return;
-  const int c = panel * kMxPanel + (threadIdx.x & 31) * 8;
+  void* stage = warp_stage<DT, VB>();
+  const int c = panel * kMxPanel;
   const auto* x = static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ld_x + c;
   uint32_t w[U][kRunWords<DT>];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    run_load_raw<DT, VB>(x + u * kMxPanel, a.D - c - u * kMxPanel, w[u]);
+    span_load<DT, VB>(x + u * kMxPanel, a.D - c - u * kMxPanel, stage, w[u]);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (U > 1 && (panel + u) * kMxPanel >= a.Dp) break;
@@ -75,14 +83,14 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const MxQuantArgs a, 
   int64_t r;
   int panel;
   if (!place_of(a, panels, 1, r, panel)) return;
-  const int lane = threadIdx.x & 31, c = panel * kMxPanel + lane * 8;
-  if (c >= a.D) return;
+  const int lane = threadIdx.x & 31, c = panel * kMxPanel;
   const int64_t rows_p = ((int64_t)a.R + 1) & ~int64_t(1);
   const uint32_t code =
       reinterpret_cast<const uint32_t*>(a.codes + r * (a.Dp / 2) + panel * (kMxPanel / 2))[lane];
   Run8 v;
   e2m1x8_to_float(code, block_scale(a.scales[(panel * rows_p + r) * 8 + (lane >> 2)]), v);
-  run_store<DT, VB>(static_cast<typename Elem<DT>::type*>(a.out) + r * a.ld_out + c, a.D - c, v);
+  span_store<DT, VB>(static_cast<typename Elem<DT>::type*>(a.out) + r * a.ld_out + c, a.D - c,
+                     warp_stage<DT, VB>(), v);
 }
 
 // Columns of a stack of matrices as rows: 256 values of 32 columns a block, through

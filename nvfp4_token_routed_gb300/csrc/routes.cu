@@ -364,46 +364,53 @@ struct RowVec {
   }
 };
 
-// One thread a vector of a token's output.  ROWS routes at a time: their row numbers, then
-// their vectors, then the sum, so that ROWS reads are in flight (ROWS = K where K has a
-// kernel of its own: one round).
-template <int DT, int VB, int ROWS>
+// TPT threads a token, each a vector of its output at a time.  ROWS routes at a time: their
+// row numbers and weights (once a token where K <= ROWS), then their vectors, all in flight,
+// then the sum.  ROWS = K has kernels of its own where rows lie on 16 bytes.
+template <int DT, int VB, int ROWS, int TPT>
 __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int64_t ld_in,
                                                       int64_t ld_out, int vecs) {
   using RV = RowVec<DT, VB>;
   using V = typename RV::V;
+  const int t = blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
   pdl_trigger();
-  int v;
-  const int t = split_index((int64_t)blockIdx.x * 256 + threadIdx.x, vecs, v);
   if (t >= a.T) return;
   pdl_wait();
-  const V* in = reinterpret_cast<const V*>(a.x) + v;
-  float acc[RV::kN];
-#pragma unroll
-  for (int j = 0; j < RV::kN; ++j) acc[j] = 0.0f;
-  for (int k0 = 0; k0 < a.K; k0 += ROWS) {
-    const int64_t route = (int64_t)t * a.K + k0;
-    int r[ROWS];
-    float w[ROWS];
-    V y[ROWS];
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) r[u] = k0 + u < a.K ? route_row(a, route + u) : -1;
+  int r[ROWS];
+  float w[ROWS];
+  auto routes = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
-      w[u] = a.w && r[u] >= 0 ? a.w[route + u] : 1.0f;
-      if (r[u] >= 0) y[u] = in[r[u] * ld_in];
+      const int64_t route = (int64_t)t * a.K + k0 + u;
+      r[u] = k0 + u < a.K ? route_row(a, route) : -1;
+      w[u] = 1.0f;
+      if (a.w && r[u] >= 0) w[u] = a.w[route];
     }
+  };
+  routes(0);
+  for (int v = threadIdx.x % TPT; v < vecs; v += TPT) {
+    const V* in = reinterpret_cast<const V*>(a.x) + v;
+    float acc[RV::kN];
 #pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-      float f[RV::kN];
-      RV::unpack(y[u], f);
-      if (r[u] >= 0) {
+    for (int j = 0; j < RV::kN; ++j) acc[j] = 0.0f;
+    for (int k0 = 0; k0 < a.K; k0 += ROWS) {
+      if (a.K > ROWS) routes(k0);
+      V y[ROWS];
 #pragma unroll
-        for (int j = 0; j < RV::kN; ++j) acc[j] = fmaf(w[u], f[j], acc[j]);
+      for (int u = 0; u < ROWS; ++u)
+        if (r[u] >= 0) y[u] = in[r[u] * ld_in];
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+        float f[RV::kN];
+        RV::unpack(y[u], f);
+        if (r[u] >= 0) {
+#pragma unroll
+          for (int j = 0; j < RV::kN; ++j) acc[j] = fmaf(w[u], f[j], acc[j]);
+        }
       }
     }
+    reinterpret_cast<V*>(a.out)[t * ld_out + v] = RV::pack(acc);
   }
-  reinterpret_cast<V*>(a.out)[t * ld_out + v] = RV::pack(acc);
 }
 
 // Gradient of combine.  A block holds kTokens tokens of TPT threads each.  A thread keeps
@@ -541,29 +548,38 @@ cudaError_t launch_dispatch_scales(int T, int K, int panels, const int32_t* inv,
 
 namespace {
 
+template <int DT, int VB, int ROWS>
+cudaError_t combine_rows(const RowArgs& a, cudaStream_t s) {
+  const int sz = dtype_size(DT);
+  const int vecs = (int)((int64_t)a.H * sz / VB);
+  auto go = [&](auto kernel, int tpt) {
+    const int tokens = 256 / tpt;
+    return launch_pdl(kernel, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(256), 0, s, a,
+                      a.ld_x * sz / VB, a.ld_out * sz / VB, vecs);
+  };
+  // a block a token where its row fills one, or where tokens are too few to fill the device
+  if (vecs > 128 || (vecs > 32 && a.T < 152 * 8)) return go(combine_kernel<DT, VB, ROWS, 256>, 256);
+  return go(combine_kernel<DT, VB, ROWS, 32>, 32);
+}
+
 template <int DT>
 cudaError_t combine_typed(const RowArgs& a, cudaStream_t s) {
   const int sz = dtype_size(DT);
   const int64_t row = (int64_t)a.H * sz;
   const int vb = std::min(access_bytes(a.x, a.ld_x * sz, row),
                           access_bytes(a.out, a.ld_out * sz, row));
-  const int vecs = (int)(row / vb);
-  const dim3 grid((unsigned)blocks_of((int64_t)a.T * vecs));
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(256), 0, s, a, a.ld_x * sz / vb, a.ld_out * sz / vb, vecs);
-  };
   if (vb == 16) {
     switch (a.K) {
-      case 1: return go(combine_kernel<DT, 16, 1>);
-      case 2: return go(combine_kernel<DT, 16, 2>);
-      case 6: return go(combine_kernel<DT, 16, 6>);
-      case 8: return go(combine_kernel<DT, 16, 8>);
-      default: return go(combine_kernel<DT, 16, 4>);
+      case 1: return combine_rows<DT, 16, 1>(a, s);
+      case 2: return combine_rows<DT, 16, 2>(a, s);
+      case 6: return combine_rows<DT, 16, 6>(a, s);
+      case 8: return combine_rows<DT, 16, 8>(a, s);
+      default: return combine_rows<DT, 16, 4>(a, s);
     }
   }
-  if (vb == 8) return go(combine_kernel<DT, 8, 4>);
-  if (vb == 4) return go(combine_kernel<DT, 4, 4>);
-  if constexpr (DT != kF32) return go(combine_kernel<DT, 2, 4>);
+  if (vb == 8) return combine_rows<DT, 8, 4>(a, s);
+  if (vb == 4) return combine_rows<DT, 4, 4>(a, s);
+  if constexpr (DT != kF32) return combine_rows<DT, 2, 4>(a, s);
   return cudaErrorInvalidValue;
 }
 
