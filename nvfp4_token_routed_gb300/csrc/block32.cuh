@@ -47,13 +47,6 @@ __device__ __forceinline__ float block_scale(uint32_t byte) {
 // 8 values of a row in fp32.
 struct Run8 {
   float v[8];
-  // Bits of the largest magnitude; infinities and NaN above every finite value.
-  __device__ __forceinline__ uint32_t amax_bits() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
-  }
 };
 
 template <int DT>
@@ -181,35 +174,72 @@ __device__ __forceinline__ void span_store(void* p, int n, void* stage, const Ru
   }
 }
 
+// Largest of two magnitudes' bits in each half of a word, one instruction.
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Bits (of fp32) of the largest magnitude of a block of 32 values, from the words of the four
+// lanes' runs; infinities and NaN come out above every finite value.  16-bit types compare as
+// unsigned halves, two at a time; all lanes take part.
+template <int DT>
+__device__ __forceinline__ uint32_t block_amax(const uint32_t (&w)[kRunWords<DT>]) {
+  uint32_t m;
+  if constexpr (DT == kF32) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  } else {
+    m = max16x2(max16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                max16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    m = max16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    m = max(m & 0xFFFFu, m >> 16);
+    return __float_as_uint(elem_to_float<DT>(m));
+  }
+}
+
 // E4M3 codes of 8 values times `inv` (|v inv| <= 448), value i in byte i.
 __device__ __forceinline__ uint2 e4m3x8(const Run8& r, float inv) {
-  uint32_t h[4];
+  uint32_t h[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint16_t o;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(o)
-        : "f"(r.v[2 * i + 1] * inv), "f"(r.v[2 * i] * inv));
-    h[i] = o;
-  }
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  for (int i = 0; i < 2; ++i)
+    asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n mov.b32 %0, {a, b};\n}"
+        : "=r"(h[i])
+        : "f"(r.v[4 * i] * inv), "f"(r.v[4 * i + 1] * inv), "f"(r.v[4 * i + 2] * inv),
+          "f"(r.v[4 * i + 3] * inv));
+  return make_uint2(h[0], h[1]);
 }
 __device__ __forceinline__ void e4m3x8_to_float(const uint2& c, float scale, Run8& r) {
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
-    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-    r.v[2 * i] = f.x * scale;
-    r.v[2 * i + 1] = f.y * scale;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[2];
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(w[i]));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[j]));
+      r.v[4 * i + 2 * j] = f.x * scale;
+      r.v[4 * i + 2 * j + 1] = f.y * scale;
+    }
   }
 }
 // E2M1 codes of 8 values times `inv`, value i in nibble i.
 __device__ __forceinline__ uint32_t e2m1x8(const Run8& r, float inv) {
-  uint32_t o = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o |= cvt_e2m1x2(r.v[2 * i] * inv, r.v[2 * i + 1] * inv) << (8 * i);
+  uint32_t o;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(o)
+      : "f"(r.v[0] * inv), "f"(r.v[1] * inv), "f"(r.v[2] * inv), "f"(r.v[3] * inv),
+        "f"(r.v[4] * inv), "f"(r.v[5] * inv), "f"(r.v[6] * inv), "f"(r.v[7] * inv));
   return o;
 }
 __device__ __forceinline__ void e2m1x8_to_float(uint32_t c, float scale, Run8& r) {
@@ -225,12 +255,6 @@ __device__ __forceinline__ void e2m1x8_to_float(uint32_t c, float scale, Run8& r
     r.v[2 * i] = f.x * scale;
     r.v[2 * i + 1] = f.y * scale;
   }
-}
-
-// Largest over the 4 lanes that hold a block of 32 values.
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
 // Widest access (bytes, at most 16) by which rows of `row_bytes` at base, stride

@@ -44,11 +44,12 @@ __device__ __forceinline__ bool place_of(const KeepArgs& a, int segs, int u, int
 
 // Writes a run's codes and its block's scale; c: the span's first value.  All lanes take
 // part.
+template <int DT>
 __device__ __forceinline__ void keep_run(const KeepArgs& a, int64_t r, int c, int halves, int half,
-                                         const Run8& v) {
+                                         const uint32_t (&w)[kRunWords<DT>], const Run8& v) {
   const int Wp = (a.W + 31) & ~31;
   c += (threadIdx.x & 31) * 8;
-  const uint32_t byte = block_scale_byte<E4m3>(quad_max(v.amax_bits()));
+  const uint32_t byte = block_scale_byte<E4m3>(block_amax<DT>(w));
   if (c >= Wp) return;
   const int64_t at = (r * halves + half) * Wp + c;
   *reinterpret_cast<uint2*>(a.codes + at) =
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_kernel(const KeepArgs a, 
   for (int u = 0; u < U; ++u) {
     Run8 v;
     run_unpack<DT>(w[u], v);
-    keep_run(a, r, c + u * kSpan, 1, 0, v);
+    keep_run<DT>(a, r, c + u * kSpan, 1, 0, w[u], v);
   }
 }
 
@@ -119,18 +120,35 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const KeepArgs a, int
   }
 }
 
-// s(g): correctly to fp32's last bits for fp32 rows, by the fast exponential (2^-21 of
-// the result) where y is rounded to 16 bits.
+// s(g): to fp32's last bits for fp32 rows; by the hardware's exponential and reciprocal
+// (2^-21 of the result, results below 2^-126 are 0) where y is rounded to 16 bits.
 template <int DT>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (DT == kF32) return 1.0f / (1.0f + expf(-g));
-  return __fdividef(1.0f, 1.0f + __expf(-g));
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return s;
 }
-// Comparisons, not fminf: a NaN stays one.
-__device__ __forceinline__ float cap(float g, float L) { return g > L ? L : g; }
-__device__ __forceinline__ float clip(float u, float L) { return u > L ? L : u < -L ? -L : u; }
+// min and max that keep a NaN.
+__device__ __forceinline__ float cap(float g, float L) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(g), "f"(L));
+  return y;
+}
+__device__ __forceinline__ float clip(float u, float L) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(cap(u, L)), "f"(-L));
+  return y;
+}
+// h where it is positive (or NaN), else 0.
+__device__ __forceinline__ float positive(float h) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(h));
+  return y;
+}
 
-template <int DT, int VB, int U, int ACT>
+template <int DT, int VB, int U, int ACT, bool LIMIT>
 __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int segs) {
   constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
   pdl_trigger();
@@ -146,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
     for (int h = 0; h < kHalves; ++h)
       span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + h * a.W + c + u * kSpan),
                         a.W - c - u * kSpan, stage, w[u][h]);
-  const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
+  const float L = a.limit;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     Run8 g, up, y;
@@ -155,25 +173,25 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
       run_unpack<DT>(w[u][kHalves - 1], up);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float gc = cap(g.v[i], L);
-        y.v[i] = gc * sigmoid<DT>(gc) * clip(up.v[i], L);
+        const float gc = LIMIT ? cap(g.v[i], L) : g.v[i];
+        y.v[i] = gc * sigmoid<DT>(gc) * (LIMIT ? clip(up.v[i], L) : up.v[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h = g.v[i] < 0.0f ? 0.0f : g.v[i];
+        const float h = positive(g.v[i]);
         y.v[i] = h * h;
       }
     }
     const int cu = c + u * kSpan;
     span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, stage, y);
     if (!a.codes) continue;
-    keep_run(a, r, cu, kHalves, 0, g);
-    if constexpr (ACT == kActSwiglu) keep_run(a, r, cu, kHalves, 1, up);
+    keep_run<DT>(a, r, cu, kHalves, 0, w[u][0], g);
+    if constexpr (ACT == kActSwiglu) keep_run<DT>(a, r, cu, kHalves, 1, w[u][kHalves - 1], up);
   }
 }
 
-template <int DT, int VB, int U, int ACT>
+template <int DT, int VB, int U, int ACT, bool LIMIT>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, int segs) {
   constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
   pdl_trigger();
@@ -191,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, in
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) k[u][h] = kept_run(a, r, cu, kHalves, h);
   }
-  const float L = a.limit > 0.0f ? a.limit : __int_as_float(0x7F800000);
+  const float L = a.limit;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int cu = c + u * kSpan;
@@ -203,14 +221,17 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, in
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float gk = g.v[i], uk = up.v[i];
-        const float gc = cap(gk, L), uc = clip(uk, L), s = sigmoid<DT>(gc);
-        g.v[i] = gk > L ? 0.0f : d.v[i] * uc * (s * (1.0f + gc * (1.0f - s)));
-        up.v[i] = fabsf(uk) > L ? 0.0f : d.v[i] * (gc * s);
+        const float gc = LIMIT ? cap(gk, L) : gk, uc = LIMIT ? clip(uk, L) : uk;
+        const float s = sigmoid<DT>(gc), gs = gc * s;
+        // s (1 + g (1 - s)) = s + g s (1 - s)
+        const float dg = d.v[i] * uc * fmaf(gs, 1.0f - s, s), du = d.v[i] * gs;
+        g.v[i] = LIMIT && gk > L ? 0.0f : dg;
+        up.v[i] = LIMIT && fabsf(uk) > L ? 0.0f : du;
       }
       span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + a.W + cu), a.W - cu, stage, up);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * d.v[i] * (g.v[i] < 0.0f ? 0.0f : g.v[i]);
+      for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * d.v[i] * positive(g.v[i]);
     }
     span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, stage, g);
   }
@@ -258,15 +279,15 @@ template <int DT>
 cudaError_t restore_typed(const KeepArgs& a, cudaStream_t s) {
   MOE_BY_WIDTH(restore_kernel, DT, 4, width(a.out, a.ld_out, a.W, DT))
 }
-template <int DT, int ACT>
+template <int DT, int ACT, bool LIMIT>
 cudaError_t act_typed(const KeepArgs& a, cudaStream_t s) {
   const int vb = std::min(width(a.x, a.ld_x, a.W, DT), width(a.out, a.ld_out, a.W, DT));
-  MOE_BY_WIDTH(act_kernel, DT, 2, vb, MOE_COMMA ACT)
+  MOE_BY_WIDTH(act_kernel, DT, 2, vb, MOE_COMMA ACT MOE_COMMA LIMIT)
 }
-template <int DT, int ACT>
+template <int DT, int ACT, bool LIMIT>
 cudaError_t act_grad_typed(const KeepArgs& a, cudaStream_t s) {
   const int vb = std::min(width(a.x, a.ld_x, a.W, DT), width(a.out, a.ld_out, a.W, DT));
-  MOE_BY_WIDTH(act_grad_kernel, DT, 2, vb, MOE_COMMA ACT)
+  MOE_BY_WIDTH(act_grad_kernel, DT, 2, vb, MOE_COMMA ACT MOE_COMMA LIMIT)
 }
 #undef MOE_BY_WIDTH
 #undef MOE_COMMA
@@ -283,23 +304,32 @@ cudaError_t launch_restore(const KeepArgs& a, int dtype, cudaStream_t s) {
          : dtype == kBf16 ? restore_typed<kBf16>(a, s)
                           : restore_typed<kF16>(a, s);
 }
+namespace {
+
+template <int DT>
+cudaError_t act_any(const KeepArgs& a, int act, cudaStream_t s) {
+  if (act == kActRelu2) return act_typed<DT, kActRelu2, false>(a, s);
+  return a.limit > 0.0f ? act_typed<DT, kActSwiglu, true>(a, s)
+                        : act_typed<DT, kActSwiglu, false>(a, s);
+}
+template <int DT>
+cudaError_t act_grad_any(const KeepArgs& a, int act, cudaStream_t s) {
+  if (act == kActRelu2) return act_grad_typed<DT, kActRelu2, false>(a, s);
+  return a.limit > 0.0f ? act_grad_typed<DT, kActSwiglu, true>(a, s)
+                        : act_grad_typed<DT, kActSwiglu, false>(a, s);
+}
+
+}  // namespace
+
 cudaError_t launch_expert_act(const KeepArgs& a, int act, int dtype, cudaStream_t s) {
-  if (act == kActSwiglu)
-    return dtype == kF32    ? act_typed<kF32, kActSwiglu>(a, s)
-           : dtype == kBf16 ? act_typed<kBf16, kActSwiglu>(a, s)
-                            : act_typed<kF16, kActSwiglu>(a, s);
-  return dtype == kF32    ? act_typed<kF32, kActRelu2>(a, s)
-         : dtype == kBf16 ? act_typed<kBf16, kActRelu2>(a, s)
-                          : act_typed<kF16, kActRelu2>(a, s);
+  return dtype == kF32    ? act_any<kF32>(a, act, s)
+         : dtype == kBf16 ? act_any<kBf16>(a, act, s)
+                          : act_any<kF16>(a, act, s);
 }
 cudaError_t launch_expert_act_grad(const KeepArgs& a, int act, int dtype, cudaStream_t s) {
-  if (act == kActSwiglu)
-    return dtype == kF32    ? act_grad_typed<kF32, kActSwiglu>(a, s)
-           : dtype == kBf16 ? act_grad_typed<kBf16, kActSwiglu>(a, s)
-                            : act_grad_typed<kF16, kActSwiglu>(a, s);
-  return dtype == kF32    ? act_grad_typed<kF32, kActRelu2>(a, s)
-         : dtype == kBf16 ? act_grad_typed<kBf16, kActRelu2>(a, s)
-                          : act_grad_typed<kF16, kActRelu2>(a, s);
+  return dtype == kF32    ? act_grad_any<kF32>(a, act, s)
+         : dtype == kBf16 ? act_grad_any<kBf16>(a, act, s)
+                          : act_grad_any<kF16>(a, act, s);
 }
 
 }  // namespace moe

@@ -28,10 +28,13 @@ __device__ __forceinline__ void* warp_stage() {
 }
 
 // A warp's 256 values (lane l holds 8l ... 8l+7): 4 bytes of codes a lane, 8 of scales.
+template <int DT>
 __device__ __forceinline__ void write_panel(const MxQuantArgs& a, int64_t r, int panel,
-                                            const Run8& v) {
+                                            const uint32_t (&w)[kRunWords<DT>]) {
   const int lane = threadIdx.x & 31;
-  const uint32_t byte = block_scale_byte<E2m1>(quad_max(v.amax_bits()));
+  const uint32_t byte = block_scale_byte<E2m1>(block_amax<DT>(w));
+  Run8 v;
+  run_unpack<DT>(w, v);
   reinterpret_cast<uint32_t*>(a.codes + r * (a.Dp / 2) + panel * (kMxPanel / 2))[lane] =
       byte == 255u ? 0u : e2m1x8(v, block_inverse(byte));
   // lane 4b holds block b's byte; lanes 0 and 16 gather four each
@@ -70,9 +73,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const MxQuantArgs a,
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (U > 1 && (panel + u) * kMxPanel >= a.Dp) break;
-    Run8 v;
-    run_unpack<DT>(w[u], v);
-    write_panel(a, r, panel + u, v);
+    write_panel<DT>(a, r, panel + u, w[u]);
   }
 }
 
@@ -113,10 +114,10 @@ __global__ void __launch_bounds__(kThreads) quantize_t_kernel(const MxQuantArgs 
   }
   __syncthreads();
   for (int j = warp; j < kColsT && c0 + j < C; j += kThreads / 32) {
-    Run8 v;
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v.v[i] = tile[j * kStrideT + lane * 8 + i];
-    write_panel(a, b * C + c0 + j, panel, v);
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(tile[j * kStrideT + lane * 8 + i]);
+    write_panel<kF32>(a, b * C + c0 + j, panel, w);
   }
 }
 
