@@ -13,6 +13,7 @@
 
 #include <cstdint>
 
+#include "logits.cuh"
 #include "loss.h"
 #include "ptx.cuh"
 
@@ -202,16 +203,27 @@ __device__ __forceinline__ uint32_t block_amax(const uint32_t (&w)[kRunWords<DT>
   }
 }
 
+__device__ __forceinline__ Run8 scaled(const Run8& r, float f) {
+  Run8 o;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 t = unpack2(mul2(pack2(r.v[i], r.v[i + 1]), pack2(f, f)));
+    o.v[i] = t.x;
+    o.v[i + 1] = t.y;
+  }
+  return o;
+}
+
 // E4M3 codes of 8 values times `inv` (|v inv| <= 448), value i in byte i.
 __device__ __forceinline__ uint2 e4m3x8(const Run8& r, float inv) {
   uint32_t h[2];
+  const Run8 v = scaled(r, inv);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n"
         " cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n mov.b32 %0, {a, b};\n}"
         : "=r"(h[i])
-        : "f"(r.v[4 * i] * inv), "f"(r.v[4 * i + 1] * inv), "f"(r.v[4 * i + 2] * inv),
-          "f"(r.v[4 * i + 3] * inv));
+        : "f"(v.v[4 * i]), "f"(v.v[4 * i + 1]), "f"(v.v[4 * i + 2]), "f"(v.v[4 * i + 3]));
   return make_uint2(h[0], h[1]);
 }
 __device__ __forceinline__ void e4m3x8_to_float(const uint2& c, float scale, Run8& r) {
@@ -225,21 +237,23 @@ __device__ __forceinline__ void e4m3x8_to_float(const uint2& c, float scale, Run
         : "r"(w[i]));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[j]));
-      r.v[4 * i + 2 * j] = f.x * scale;
-      r.v[4 * i + 2 * j + 1] = f.y * scale;
+      const float2 f = unpack2(mul2(pack2(__half22float2(*reinterpret_cast<__half2*>(&h[j]))),
+                                    pack2(scale, scale)));
+      r.v[4 * i + 2 * j] = f.x;
+      r.v[4 * i + 2 * j + 1] = f.y;
     }
   }
 }
 // E2M1 codes of 8 values times `inv`, value i in nibble i.
 __device__ __forceinline__ uint32_t e2m1x8(const Run8& r, float inv) {
   uint32_t o;
+  const Run8 v = scaled(r, inv);
   asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
       " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}"
       : "=r"(o)
-      : "f"(r.v[0] * inv), "f"(r.v[1] * inv), "f"(r.v[2] * inv), "f"(r.v[3] * inv),
-        "f"(r.v[4] * inv), "f"(r.v[5] * inv), "f"(r.v[6] * inv), "f"(r.v[7] * inv));
+      : "f"(v.v[0]), "f"(v.v[1]), "f"(v.v[2]), "f"(v.v[3]), "f"(v.v[4]), "f"(v.v[5]), "f"(v.v[6]),
+        "f"(v.v[7]));
   return o;
 }
 __device__ __forceinline__ void e2m1x8_to_float(uint32_t c, float scale, Run8& r) {

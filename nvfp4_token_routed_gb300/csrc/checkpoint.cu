@@ -19,6 +19,7 @@
 #include "block32.cuh"
 #include "experts.h"
 #include "internal.h"
+#include "logits.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -122,13 +123,19 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const KeepArgs a, int
 
 // s(g): to fp32's last bits for fp32 rows; by the hardware's exponential and reciprocal
 // (2^-21 of the result, results below 2^-126 are 0) where y is rounded to 16 bits.
+// Two at a time: a multiplication or addition of two fp32 is one instruction.
 template <int DT>
-__device__ __forceinline__ float sigmoid(float g) {
-  if constexpr (DT == kF32) return 1.0f / (1.0f + expf(-g));
-  float e, s;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-  return s;
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 g) {
+  if constexpr (DT == kF32) {
+    const float2 f = unpack2(g);
+    return pack2(1.0f / (1.0f + expf(-f.x)), 1.0f / (1.0f + expf(-f.y)));
+  }
+  const float2 k = unpack2(mul2(g, pack2(-kLog2e, -kLog2e)));
+  const float2 t = unpack2(add2(pack2(ex2(k.x), ex2(k.y)), pack2(1.0f, 1.0f)));
+  float s0, s1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(t.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(t.y));
+  return pack2(s0, s1);
 }
 // min and max that keep a NaN.
 __device__ __forceinline__ float cap(float g, float L) {
@@ -172,9 +179,15 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
     if constexpr (ACT == kActSwiglu) {
       run_unpack<DT>(w[u][kHalves - 1], up);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float gc = LIMIT ? cap(g.v[i], L) : g.v[i];
-        y.v[i] = gc * sigmoid<DT>(gc) * (LIMIT ? clip(up.v[i], L) : up.v[i]);
+      for (int i = 0; i < 8; i += 2) {
+        f32x2 gc = pack2(g.v[i], g.v[i + 1]), uc = pack2(up.v[i], up.v[i + 1]);
+        if (LIMIT) {
+          gc = pack2(cap(g.v[i], L), cap(g.v[i + 1], L));
+          uc = pack2(clip(up.v[i], L), clip(up.v[i + 1], L));
+        }
+        const float2 f = unpack2(mul2(mul2(gc, sigmoid2<DT>(gc)), uc));
+        y.v[i] = f.x;
+        y.v[i + 1] = f.y;
       }
     } else {
 #pragma unroll
@@ -219,14 +232,23 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, in
     if constexpr (ACT == kActSwiglu) {
       e4m3x8_to_float(k[u][kHalves - 1].codes, block_scale(k[u][kHalves - 1].byte), up);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float gk = g.v[i], uk = up.v[i];
-        const float gc = LIMIT ? cap(gk, L) : gk, uc = LIMIT ? clip(uk, L) : uk;
-        const float s = sigmoid<DT>(gc), gs = gc * s;
+      for (int i = 0; i < 8; i += 2) {
+        const f32x2 gk = pack2(g.v[i], g.v[i + 1]), uk = pack2(up.v[i], up.v[i + 1]);
+        f32x2 gc = gk, uc = uk;
+        if (LIMIT) {
+          gc = pack2(cap(g.v[i], L), cap(g.v[i + 1], L));
+          uc = pack2(clip(up.v[i], L), clip(up.v[i + 1], L));
+        }
+        const f32x2 dd = pack2(d.v[i], d.v[i + 1]), s = sigmoid2<DT>(gc), gs = mul2(gc, s);
         // s (1 + g (1 - s)) = s + g s (1 - s)
-        const float dg = d.v[i] * uc * fmaf(gs, 1.0f - s, s), du = d.v[i] * gs;
-        g.v[i] = LIMIT && gk > L ? 0.0f : dg;
-        up.v[i] = LIMIT && fabsf(uk) > L ? 0.0f : du;
+        const f32x2 rest = fma2(s, pack2(-1.0f, -1.0f), pack2(1.0f, 1.0f));
+        const float2 dg = unpack2(mul2(mul2(dd, uc), fma2(gs, rest, s)));
+        const float2 du = unpack2(mul2(dd, gs));
+        const float2 gf = unpack2(gk), uf = unpack2(uk);
+        g.v[i] = LIMIT && gf.x > L ? 0.0f : dg.x;
+        g.v[i + 1] = LIMIT && gf.y > L ? 0.0f : dg.y;
+        up.v[i] = LIMIT && fabsf(uf.x) > L ? 0.0f : du.x;
+        up.v[i + 1] = LIMIT && fabsf(uf.y) > L ? 0.0f : du.y;
       }
       span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + a.W + cu), a.W - cu, stage, up);
     } else {
