@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "block32.cuh"
+#include "cluster.cuh"
 #include "experts.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -23,12 +24,13 @@ namespace {
 
 // ---------------------------------------------------------------- sort
 // A chunk of routes is one block's: each warp takes a contiguous part, 32 routes at a
-// time; match.any ranks equal experts within the 32, a count per warp and expert in
+// time; votes rank equal experts within the 32, a count per warp and expert in
 // shared memory carries the rank on, and a prefix over the warps makes it the chunk's.
 constexpr int kChunk = 2048;      // routes a block of many
 constexpr int kChunkWarps = 8;
-constexpr int kOneBlock = 4096;   // routes of the only block of a small batch
+constexpr int kOneBlock = 4096;   // routes a block of a batch that one cluster sorts
 constexpr int kOneWarps = 32;
+constexpr int kCluster = 8;       // blocks of the largest cluster: 32768 routes
 
 int64_t chunks_of(int64_t TK) { return (TK + kChunk - 1) / kChunk; }
 
@@ -78,6 +80,7 @@ __device__ __forceinline__ void rank_chunk(const SortArgs& a, int c0, int c1, ui
   uint16_t* mine = cnt + warp * a.E;
   for (int e = lane; e < a.E; e += 32) mine[e] = 0;
   const int w0 = c0 + warp * (32 * ITERS);
+  const int bits = 32 - __clz(a.E);  // E < 2^bits: keys 0 .. E - 1 and 2^bits - 1
   any_bad = false;
 #pragma unroll
   for (int j = 0; j < ITERS; ++j) {
@@ -89,7 +92,14 @@ __device__ __forceinline__ void rank_chunk(const SortArgs& a, int c0, int c1, ui
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < ITERS; ++j) {
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, key[j]);
+    // lanes with this lane's key, a vote a bit (match.any takes a step for each of the up to
+    // 32 different keys); key -1 has every bit set, and no expert has
+    unsigned same = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+      const bool set = (key[j] >> b) & 1;
+      const unsigned vote = __ballot_sync(0xFFFFFFFFu, set);
+      same &= set ? vote : ~vote;
+    }
     const int first = __ffs(same) - 1;
     int before = 0;
     if (lane == first && key[j] >= 0) {
@@ -107,51 +117,88 @@ __device__ __forceinline__ void write_route(const SortArgs& a, int i, int row) {
   if (row >= 0) a.perm[row] = i;
 }
 
-// The whole sort by one block.
-__global__ void __launch_bounds__(kOneWarps * 32) sort_small_kernel(const SortArgs a) {
+// Value of another block of the cluster at this block's shared address p.
+__device__ __forceinline__ int load_cluster(const int* p, int rank) {
+  uint32_t r;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+  return v;
+}
+
+// The whole sort by one cluster: block c ranks routes [c kOneBlock, ...), reads the other
+// blocks' counts in their shared memory, and adds up for itself where its routes go.
+__global__ void __launch_bounds__(kOneWarps * 32) sort_cluster_kernel(const SortArgs a) {
   constexpr int kIters = kOneBlock / (kOneWarps * 32);
   extern __shared__ uint16_t cnt[];
   __shared__ int s_warp[kOneWarps];
-  __shared__ int s_off[1024];
-  __shared__ int s_bad;
+  __shared__ int s_count[1025];  // this block's routes of each expert; [E]: a bad id
+  __shared__ int s_base[1024];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int TK = a.T * a.K;
-  if (threadIdx.x == 0) s_bad = 0;
+  const int rank = (int)cluster_rank(), blocks = (int)cluster_size();
+  const int TK = a.T * a.K, c0 = rank * kOneBlock;
+  if (threadIdx.x == 0) s_count[a.E] = 0;
   pdl_trigger();
   pdl_wait();
   __syncthreads();
-  int key[kIters], rank[kIters];
+  int key[kIters], row[kIters];
   bool bad;
-  rank_chunk<kOneWarps, kIters>(a, 0, TK, cnt, key, rank, bad);
-  if (bad) s_bad = 1;
+  rank_chunk<kOneWarps, kIters>(a, c0, min(TK, c0 + kOneBlock), cnt, key, row, bad);
+  if (bad) s_count[a.E] = 1;
   __syncthreads();
-  // thread e: expert e's routes in each warp's part, then its first row
-  int sum = 0;
-  if ((int)threadIdx.x < a.E)
+  // thread e: expert e's routes in each warp's part
+  const int e = threadIdx.x;
+  if (e < a.E) {
+    int c[kOneWarps], sum = 0;  // all reads before the writes: they overlap
+#pragma unroll
+    for (int w = 0; w < kOneWarps; ++w) c[w] = cnt[w * a.E + e];
+#pragma unroll
     for (int w = 0; w < kOneWarps; ++w) {
-      const int c = cnt[w * a.E + threadIdx.x];
-      cnt[w * a.E + threadIdx.x] = (uint16_t)sum;
-      sum += c;
+      cnt[w * a.E + e] = (uint16_t)sum;
+      sum += c[w];
     }
-  int n;
-  const int off = block_exclusive(sum, s_warp, n);
-  if ((int)threadIdx.x < a.E) {
-    s_off[threadIdx.x] = off;
-    a.offsets[threadIdx.x] = off;
+    s_count[e] = sum;
   }
-  if (threadIdx.x == 0) {
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  int before = 0, total = 0;
+  if (e < a.E) {
+    int v[kCluster];
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) v[c] = c < blocks ? load_cluster(s_count + e, c) : 0;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      if (c < rank) before += v[c];
+      total += v[c];
+    }
+  }
+  int any_bad = 0;
+  if (rank == 0 && threadIdx.x == 0)
+    for (int c = 0; c < blocks; ++c) any_bad |= load_cluster(s_count + a.E, c);
+  __syncwarp();
+  cluster_arrive();  // no more reads of other blocks
+  int n;
+  const int off = block_exclusive(total, s_warp, n);
+  if (e < a.E) {
+    s_base[e] = off + before;
+    if (rank == 0) a.offsets[e] = off;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
     a.offsets[a.E] = n;
-    a.status[kStatusFlags] = s_bad ? kFlagBadExpertId : 0;
+    a.status[kStatusFlags] = any_bad ? kFlagBadExpertId : 0;
   }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kIters; ++j) {
-    const int i = warp * (32 * kIters) + 32 * j + lane;
+    const int i = c0 + warp * (32 * kIters) + 32 * j + lane;
     if (i >= TK) continue;
-    const int e = key[j];
-    write_route(a, i, e < 0 ? -1 : s_off[e] + cnt[warp * a.E + e] + rank[j]);
+    const int k = key[j];
+    write_route(a, i, k < 0 ? -1 : s_base[k] + cnt[warp * a.E + k] + row[j]);
     if (i >= n) a.perm[i] = -1;
   }
+  __syncwarp();
+  cluster_wait();
 }
 
 // Counts of each chunk, and whether it held a bad id.
@@ -498,19 +545,32 @@ int dtype_size(int dtype) { return dtype == kF32 ? 4 : 2; }
 
 size_t sort_routes_ws_bytes(int64_t TK, int E) {
   const size_t head = 256;  // status words
-  if (TK <= kOneBlock) return head;
+  if (TK <= kCluster * kOneBlock) return head;
   return head + sizeof(int32_t) * ((size_t)chunks_of(TK) * (E + 1) + E);
 }
 
 cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t s) {
   const int64_t TK = (int64_t)a.T * a.K;
-  if (TK <= kOneBlock) {
+  if (TK <= kCluster * kOneBlock) {
     static std::atomic<uint64_t> configured{0};
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(sort_small_kernel),
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(sort_cluster_kernel),
                                       kOneWarps * 1024 * 2, configured);
     if (e != cudaSuccess) return e;
-    return launch_pdl(sort_small_kernel, dim3(1), dim3(kOneWarps * 32),
-                      (size_t)kOneWarps * a.E * 2, s, a);
+    const unsigned blocks = (unsigned)((TK + kOneBlock - 1) / kOneBlock);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kOneWarps * 32);
+    cfg.dynamicSmemBytes = (size_t)kOneWarps * a.E * 2;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, a);
   }
   const int n = (int)chunks_of(TK);
   cudaError_t e = launch_pdl(sort_count_kernel, dim3(n), dim3(kChunkWarps * 32), 0, s, a);

@@ -39,7 +39,8 @@ def _check_plan(plan, ids, E):
 
 @pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 1024, 32), (5, 8, 8), (33, 60, 4), (512, 256, 8),
                                    (513, 256, 8), (128, 1000, 32), (4097, 1, 1), (4096, 384, 6),
-                                   (5000, 1024, 3), (20000, 33, 10)])
+                                   (5000, 1024, 3), (20000, 33, 10), (4096, 8, 8),
+                                   (4097, 8, 8), (32768, 64, 1), (32767, 40, 1), (32769, 2, 1)])
 @pytest.mark.parametrize("empty", [0.0, 0.3])
 def test_sort(T, E, K, empty):
     for dtype in (torch.int32, torch.int64):
@@ -55,7 +56,7 @@ def test_definitions_agree():
     assert torch.equal(plan.inv.cpu(), inv)
 
 
-@pytest.mark.parametrize("T", [7, 3000])
+@pytest.mark.parametrize("T", [7, 3000, 9000])
 def test_sort_bad_repeated_and_missing_ids(T):
     E, K = 16, 4
     ids = torch.randint(0, E, (T, K), generator=torch.Generator().manual_seed(2))  # repeats
