@@ -21,7 +21,8 @@ _U8 = (torch.uint8,)
 def _like(t, name, shape, dtype, like, stream):
     """An output matrix: `t` (rows may be strided) or a new one; its address and row stride."""
     if t is None:
-        t = _out(None, name, shape, dtype, like, stream)
+        t = (torch.empty(shape, dtype=dtype, device=like.device) if stream is None
+             else _out(None, name, shape, dtype, like, stream))
         return t, t.data_ptr(), shape[1]
     if t.shape != torch.Size(shape) or t.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of "
@@ -154,20 +155,20 @@ class _Held:
     asked for (an allocation and two views less a call)."""
     __slots__ = ("_codes", "_scales", "_buf", "_cut", "device")
 
-    def _set(self, codes, scales, codes_shape, scales_shape):
-        if not codes.is_cuda and not scales.is_cuda:
-            self.device = -1  # described, not used: the calls refuse it
-        else:
-            self.device = codes.get_device()
+    def _set(self, codes, scales):
+        self.device = codes.get_device()  # -1 on the CPU: described, but no call takes it
         self._codes, self._scales, self._buf, self._cut = codes, scales, None, None
-        return (_arg(codes, "codes", torch.Size(codes_shape), _U8, codes),
-                _arg(scales, "scales", torch.Size(scales_shape), _U8, codes))
+        shapes = self._shapes()
+        return (_arg(codes, "codes", shapes[0], _U8, codes),
+                _arg(scales, "scales", shapes[1], _U8, codes))
 
-    def _alloc(self, codes_shape, scales_shape, n_codes, n_scales, like, stream):
-        at = (n_codes + 255) // 256 * 256
-        self._buf = buf = _out(None, "codes", at + n_scales, torch.uint8, like, stream)
+    def _alloc(self, n_codes, n_scales, like, stream):
+        at = (n_codes + 255) & -256
+        self._buf = buf = (
+            torch.empty(at + n_scales, dtype=torch.uint8, device=like.device) if stream is None
+            else _out(None, "codes", at + n_scales, torch.uint8, like, stream))
         self._codes = self._scales = None
-        self._cut = codes_shape, scales_shape, n_codes, at
+        self._cut = n_codes, at
         self.device = like.get_device()
         p = buf.data_ptr()
         return p, p + at
@@ -175,13 +176,13 @@ class _Held:
     @property
     def codes(self):
         if self._codes is None:
-            self._codes = self._buf[:self._cut[2]].view(self._cut[0])
+            self._codes = self._buf[:self._cut[0]].view(self._shapes()[0])
         return self._codes
 
     @property
     def scales(self):
         if self._scales is None:
-            self._scales = self._buf[self._cut[3]:].view(self._cut[1])
+            self._scales = self._buf[self._cut[1]:].view(self._shapes()[1])
         return self._scales
 
     def nbytes(self):
@@ -201,22 +202,22 @@ class Checkpoint(_Held):
     __slots__ = ("rows", "halves", "cols", "dtype", "act", "swiglu_limit", "c")
 
     def __init__(self, codes, scales, cols, dtype, act=None, swiglu_limit=0.0):
-        self._about(codes.shape[0], cols, dtype, act, swiglu_limit)
-        w = (cols + 31) // 32 * 32
-        self.c = self._set(codes, scales, (self.rows, self.halves, w),
-                           (self.rows, self.halves, w // 32))
-
-    def _about(self, rows, cols, dtype, act, swiglu_limit):
-        self.rows, self.cols, self.dtype, self.act = rows, cols, dtype, act
+        self.rows, self.cols, self.dtype, self.act = codes.shape[0], cols, dtype, act
         self.halves, self.swiglu_limit = 2 if act == "swiglu" else 1, float(swiglu_limit)
+        self.c = self._set(codes, scales)
 
     @classmethod
     def empty(cls, rows, cols, dtype, like, act=None, swiglu_limit=0.0, stream=None):
         k = cls.__new__(cls)
-        k._about(rows, cols, dtype, act, swiglu_limit)
-        b, h = (cols + 31) // 32, k.halves
-        k.c = k._alloc((rows, h, 32 * b), (rows, h, b), 32 * rows * h * b, rows * h * b, like, stream)
+        k.rows, k.cols, k.dtype, k.act = rows, cols, dtype, act
+        k.halves, k.swiglu_limit = 2 if act == "swiglu" else 1, float(swiglu_limit)
+        n = rows * k.halves * ((cols + 31) >> 5)
+        k.c = k._alloc(32 * n, n, like, stream)
         return k
+
+    def _shapes(self):
+        b = (self.cols + 31) // 32
+        return (self.rows, self.halves, 32 * b), (self.rows, self.halves, b)
 
     def _for(self, rows, cols):
         if self.rows != rows or self.cols != cols:
@@ -259,13 +260,16 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
     ("relu2") -> y [R, I].  With checkpoint (or `kept`, a Checkpoint to fill) h is kept in 8
     bits for expert_act_grad: (y, kept), else y."""
     m = _matrix(h, "h")
-    halves = 2 if act == "swiglu" else 1
-    R, I = h.shape[0], h.shape[1] // halves
+    R, I = h.shape
+    if act == "swiglu":
+        I //= 2
     y, p, ld = _like(y, "y", (R, I), h.dtype, h, stream)
     codes = scales = None
-    if kept is None and checkpoint:
-        kept = Checkpoint.empty(R, I, h.dtype, h, act, swiglu_limit, stream)
-    if kept is not None:
+    if kept is None:
+        if checkpoint:
+            kept = Checkpoint.empty(R, I, h.dtype, h, act, swiglu_limit, stream)
+            codes, scales = kept.c
+    else:
         if kept.act != act or kept.swiglu_limit != float(swiglu_limit):
             raise ValueError("kept: made for another activation")
         codes, scales = kept._for(R, I)
@@ -299,20 +303,22 @@ class MxTensor(_Held):
 
     def __init__(self, codes, scales, shape):
         self.shape = shape = tuple(shape)
-        rows, dp = _mx_rows(shape), padded(shape[-1])
-        p, q = self._set(codes, scales, (rows, dp // 2), (dp // 256, (rows + 1) // 2 * 2, 8))
-        self.c = moe_mx(p, q, rows, shape[-1])
+        p, q = self._set(codes, scales)
+        self.c = moe_mx(p, q, _mx_rows(shape), shape[-1])
 
     @classmethod
     def empty(cls, shape, like, stream=None):
         t = cls.__new__(cls)
         t.shape = shape
-        rows, dp = _mx_rows(shape), padded(shape[-1])
-        rp = rows + (rows & 1)
-        p, q = t._alloc((rows, dp // 2), (dp // 256, rp, 8), rows * (dp // 2), rp * (dp // 32),
-                        like, stream)
-        t.c = moe_mx(p, q, rows, shape[-1])
+        rows, d = _mx_rows(shape), shape[-1]
+        dp = (d + 255) & -256
+        p, q = t._alloc(rows * dp >> 1, (rows + 1 & -2) * dp >> 5, like, stream)
+        t.c = moe_mx(p, q, rows, d)
         return t
+
+    def _shapes(self):
+        rows, dp = _mx_rows(self.shape), padded(self.shape[-1])
+        return (rows, dp // 2), (dp // 256, (rows + 1) // 2 * 2, 8)
 
 
 def _mx_rows(shape):
