@@ -259,6 +259,8 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
     """The experts' activation of FC1 rows h: [R, 2I] = [gate | up] ("swiglu") or [R, I]
     ("relu2") -> y [R, I].  With checkpoint (or `kept`, a Checkpoint to fill) h is kept in 8
     bits for expert_act_grad: (y, kept), else y."""
+    if act not in ACT:
+        raise ValueError(f"act: one of {sorted(ACT)}")
     m = _matrix(h, "h")
     R, I = h.shape
     if act == "swiglu":
@@ -428,6 +430,8 @@ class MxExperts:
     """
 
     def __init__(self, fc1, fc2, act, swiglu_limit=0.0, stream=None):
+        if act not in ACT:
+            raise ValueError(f"act: one of {sorted(ACT)}")
         E, N1, H = fc1.shape
         I = N1 // 2 if act == "swiglu" else N1
         if fc2.shape != (E, H, I):

@@ -149,6 +149,41 @@ def test_special_values_stay_in_their_block():
     assert torch.equal(M.expert_act(low, "relu2"), torch.zeros(1, 64, device=DEV))
 
 
+def test_rows_more_than_32_bits_apart():
+    R_, ld = 300, 8_000_000
+    store = torch.empty(R_ * ld, dtype=torch.bfloat16, device=DEV)
+    for W in (128, 66):
+        _, x = _values(R_, W, "bf16", W)
+        far = torch.as_strided(store, (R_, W), (ld, 1))
+        far.copy_(x)
+        kept, want = M.checkpoint(far), M.checkpoint(x)
+        assert torch.equal(kept.codes, want.codes) and torch.equal(kept.scales, want.scales)
+        assert torch.equal(M.restore(kept, out=far), M.restore(want))
+        far.copy_(x)
+        y, k1 = M.expert_act(far, "swiglu", checkpoint=True)
+        y2, k2 = M.expert_act(x, "swiglu", checkpoint=True)
+        assert torch.equal(y, y2) and torch.equal(k1.codes, k2.codes)
+        assert torch.equal(M.expert_act_grad(k1, y, dh=far), M.expert_act_grad(k2, y2))
+
+
+def test_many_short_and_long_rows():
+    """Spans several to a warp and one, many rows to a block and many blocks to a row."""
+    for R_, W in ((5000, 40), (3000, 1031), (40, 20000), (1, 300000)):
+        _, x = _values(R_, 2 * W, "bf16", W)
+        y, kept = M.expert_act(x, "swiglu", checkpoint=True)
+        gate, up = x[:, :W].float(), x[:, W:].float()
+        want = (gate.double() * torch.sigmoid(gate.double()) * up.double())
+        g = gate.abs().double()
+        tol = (R.half_step(torch.bfloat16) + (8 + 1.2 * g) * 2.0 ** -23) * want.abs() + 2.0 ** -125 * g * up.abs()
+        assert torch.all((y.double() - want).abs() <= tol + R.tiny(torch.bfloat16))
+        halves = torch.cat([M.restore(M.checkpoint(h.contiguous()), torch.float32)
+                            for h in (x[:, :W], x[:, W:])], 1).double()
+        dh = M.expert_act_grad(kept, y).double()
+        want, weight = R.act_grad(halves, "swiglu", 0.0, y)
+        tol = R.half_step(torch.bfloat16) * want.abs() + 2.0 ** -23 * weight
+        assert torch.all((dh - want).abs() <= tol + R.tiny(torch.bfloat16))
+
+
 @pytest.mark.parametrize("n", [0, 1, 5, 9, 50])
 def test_rows_behind_the_last(n):
     """n_rows on the device: rows from there on are neither read nor written."""
@@ -181,7 +216,7 @@ def test_no_rows_and_refusals():
                 lambda: M.expert_act_grad(M.checkpoint(h), h),
                 lambda: M.expert_act_grad(kept, h), lambda: M.expert_act_grad(kept, h[:3, :32]),
                 lambda: M.expert_act(h, "swiglu", kept=M.checkpoint(h)),
-                lambda: M.expert_act(h, "relu2", kept=kept),
+                lambda: M.expert_act(h, "relu2", kept=kept), lambda: M.expert_act(h, "gelu"),
                 lambda: M.expert_act(h, "swiglu", n_rows=torch.zeros(1, device=DEV))):
         with pytest.raises(ValueError):
             bad()

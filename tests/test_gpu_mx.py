@@ -243,6 +243,63 @@ def test_no_rows_and_refusals():
         M.mx_product(M.mx_quantize(torch.randn(4, 65, device=DEV)), w, off)
 
 
+def test_long_rows():
+    """The longest reduction (256 stages) and rows of the most outputs."""
+    x, _ = _values(3, 65536, "bf16", 11)
+    w = torch.randn(1, 130, 65536, generator=torch.Generator().manual_seed(1)) / 256
+    _product(x, w, None, torch.bfloat16)
+    x, _ = _values(5, 40, "bf16", 12)
+    _product(x, torch.randn(1, 65536, 40, generator=torch.Generator().manual_seed(2)) / 6, None,
+             torch.float16)
+
+
+def test_outputs_more_than_32_bits_apart():
+    """Rows of an output whose last elements lie past 2^31 elements (and 2^32 bytes)."""
+    R_, N, ld = 300, 260, 8_000_000
+    x, xc = _values(R_, 256, "bf16", 13)
+    w = M.mx_quantize(torch.randn(N, 256, device=DEV) / 16)
+    q = M.mx_quantize(xc)
+    want = M.mx_product(q, w)
+    store = torch.empty(R_ * ld, dtype=torch.bfloat16, device=DEV)
+    for shift in (0, 1):  # stores of 8 bytes, and by the element
+        out = torch.as_strided(store, (R_, N), (ld, 1), shift)
+        assert torch.equal(M.mx_product(q, w, out=out), want)
+    few = M.mx_product(M.mx_quantize(xc[:40].contiguous()), w,
+                       out=torch.as_strided(store, (40, N), (50_000_000, 1)))
+    assert torch.equal(few, want[:40])
+    far = torch.as_strided(store, (R_, 256), (ld, 1))
+    far.copy_(xc)
+    again = M.mx_quantize(far)
+    assert torch.equal(again.codes, q.codes) and torch.equal(again.scales, q.scales)
+    assert torch.equal(M.mx_restore(q, out=far), M.mx_restore(q))
+
+
+@pytest.mark.parametrize("E,N,D", [(2, 300, 512), (3, 129, 300), (1, 515, 1024)])
+@pytest.mark.parametrize("rows", [128, 129, 160, 255, 256, 257, 288, 512, 545, 1000])
+def test_product_by_pairs_of_blocks(E, N, D, rows):
+    """Groups of `rows` rows (and one of a few) around the tiles' heights, odd starts."""
+    offsets = [0] + [3 + rows * (i + 1) for i in range(E)]
+    offsets[-1] += 200
+    x, _ = _values(offsets[-1], D, "bf16", rows)
+    w = torch.randn(E, N, D, generator=torch.Generator().manual_seed(N)) * D ** -0.5
+    for dtype in ("bf16", "f32"):
+        _product(x, w, offsets, R.TYPES[dtype])
+
+
+def test_expired_waits_give_nan_in_pairs():
+    x, xc = _values(600, 512, "bf16", 14)
+    w = M.mx_quantize(torch.randn(2, 384, 512, device=DEV) / 22)
+    off = torch.tensor([0, 301, 600], dtype=torch.int32, device=DEV)
+    q = M.mx_quantize(xc)
+    want = M.mx_product(q, w, off)
+    # expert 1 (items 4 .. 7): its first row tile (160 rows), outputs 256 .. 383
+    got = M.moe_nvfp4_selftest_product_timeout(q, w, off, 6)
+    lost = torch.isnan(got)
+    assert torch.all(lost[301:461, 256:]) and int(lost.sum()) == 160 * 128
+    assert torch.equal(got[~lost], want[~lost])
+    assert torch.equal(M.mx_product(q, w, off), want)
+
+
 def test_expired_waits_give_nan():
     """Row loads that leave before an item: its block's items from there on get NaN, the
     rest their results, and the context stays usable."""

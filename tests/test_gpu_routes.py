@@ -211,6 +211,24 @@ def test_a_plan_that_is_none():
     assert dw[1].tolist() == [0.0, 0.0] and dw[0, 1] == 0
 
 
+def test_rows_more_than_32_bits_apart():
+    """Rows whose last elements lie past 2^31 elements (and 2^32 bytes)."""
+    T, E, K, ld = 90, 16, 4, 8_000_000
+    for H in (64, 33):  # by 16 bytes, by the element
+        plan = M.sort_routes(_ids(T, E, K, 0.1, 3).to(DEV), E)
+        n = int(plan.n_rows)
+        x = torch.randn(T, H, device=DEV).bfloat16()
+        w = torch.rand(T, K, device=DEV)
+        store = torch.empty(T * K * ld, dtype=torch.bfloat16, device=DEV)
+        far = torch.as_strided(store, (T * K, H), (ld, 1))
+        rows = M.dispatch(x, plan)
+        assert torch.equal(M.dispatch(x, plan, rows=far)[:n], rows[:n])
+        assert torch.equal(M.combine(far, plan, w), M.combine(rows, plan, w))
+        drows, dw = M.combine_grad(rows, plan, w, x)
+        got, dw2 = M.combine_grad(far, plan, w, x, drows=far)
+        assert torch.equal(got[:n], drows[:n]) and torch.equal(dw2, dw)
+
+
 def test_graph_stream_and_repeat():
     T, E, K, H = 700, 64, 8, 512
     ids = _ids(T, E, K, 0.1, 8).to(DEV)
