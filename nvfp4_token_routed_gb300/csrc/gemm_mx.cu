@@ -68,7 +68,13 @@ constexpr int kWarpSumOff = kFlagsOff + 32;    // two ints a warp
 constexpr int kGroupsOff = 512;                // first item [E + 1], first row [E + 1]
 static_assert(kWarpSumOff + 8 * (kThreads / 32) <= kGroupsOff, "barrier area");
 
-constexpr int64_t kPairRows = 128;             // rows an expert from which on CTAs work in pairs
+// CTAs work in pairs from this many rows an expert and stages a row on (both measured, us,
+// single / pair): N4096 D7168, 8 experts of 192 rows 27.9 / 32.2, of 256 39.5 / 33.2, of 1024
+// 108 / 76; N7168 D2048, 32 experts of 256 77 / 64, of 1024 239 / 191; N2048 D1024, 8 experts
+// of 256 9.2 / 9.9, of 1024 19.4 / 19.6.  Few items leave pairs idle: one matrix N4096 D7168,
+// 256 rows 11.5 / 15.0 (16 items of pairs), 512 15.1 / 15.4, 1024 24.3 / 16.5.
+constexpr int64_t kPairRows = 224;
+constexpr int kPairStages = 8;
 
 struct MxMaps {
   CUtensorMap w;
@@ -548,14 +554,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // while the next item's MMAs run.
 namespace pair {
 constexpr int kThreads = 512;  // 0 weights, 1 MMA, 2 rows, 3 scales, 4-7 scales to TMEM, 8-15 epilogue
-constexpr int kTileN = 256;
+constexpr int kTileN = 256;       // rows of the largest tile
 constexpr int kStages = 8;
 constexpr int kFull = 0;
 constexpr int kEmpty = kStages;
 constexpr int kSfReady = 2 * kStages;  // rank 0's: 4 warps of both CTAs
 constexpr int kAccFull = 3 * kStages;
-constexpr int kAccEmpty = kAccFull + 1;  // rank 0's: 8 warps of both CTAs
-constexpr int kDrain = kAccEmpty + 1;
+constexpr int kAccEmpty = kAccFull + 2;  // rank 0's: 8 warps of both CTAs
+constexpr int kDrain = kAccEmpty + 2;
 constexpr int kBars = kDrain + 1;
 constexpr int kFlagsOff = 8 * kBars;
 constexpr int kWarpSumOff = kFlagsOff + 32;
@@ -630,8 +636,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       mbar_init(R.bar(pair::kEmpty + s), 1);
       mbar_init(R.bar(pair::kSfReady + s), 8);
     }
-    mbar_init(R.bar(pair::kAccFull), 1);
-    mbar_init(R.bar(pair::kAccEmpty), 16);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(R.bar(pair::kAccFull + b), 1);
+      mbar_init(R.bar(pair::kAccEmpty + b), 16);
+    }
     mbar_init(R.bar(pair::kDrain), 1);
     *abort_flag = 0;
     *s_most = 32;
@@ -660,11 +668,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   const int stage_bytes = (off_sfb + sfb_bytes + 1023) & ~1023;
   const int nrb = most <= 128 ? 4 : 8;
   const int slot_cols = 8 + 2 * nrb;
-  const int sf_base = (most + 31) & ~31;       // scales behind the accumulators
+  // two accumulator buffers where they leave room for the scales of five stages
+  const int nbuf = 2 * most + 5 * slot_cols <= kTmemCols ? 2 : 1;
+  const int sf_base = nbuf * most;             // scales behind the accumulators
   const int head = (kGroupsOff + 8 * (a.E + 1) + 1023) & ~1023;
   uint8_t* stages = smem + head;
-  const int n_stages = min(pair::kStages, (kSmem - 1024 - head) / stage_bytes);
-  static_assert(pair::kTileN + pair::kStages * 24 <= kTmemCols, "TMEM columns");
+  const int n_stages = min(min(pair::kStages, (kSmem - 1024 - head) / stage_bytes),
+                           (kTmemCols - sf_base) / slot_cols);
 
   Walk walk{first_item, first_row, m_pairs, 32, 0};
   int stage = 0;
@@ -773,14 +783,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (rank 0)
     bool ok = rank == 0, issued = false, ready = false;
-    uint32_t acc_phase = 1;
-    for (int item = item0; ok && item < n_items; item += step) {
+    int local = 0;
+    for (int item = item0; ok && item < n_items; item += step, ++local) {
       const Item it = walk.at(item);
       const uint32_t idesc = idesc_mxf4(256, (it.rows + 31) & ~31);
-      ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(pair::kAccEmpty), acc_phase, abort_flag));
+      const int buf = nbuf == 2 ? local & 1 : 0;
+      const uint32_t acc_par = ((uint32_t)(nbuf == 2 ? local >> 1 : local) & 1u) ^ 1u;
+      ok = __all_sync(0xFFFFFFFFu,
+                      wait_or_leave(R.bar(pair::kAccEmpty + buf), acc_par, abort_flag));
       if (!ok) break;
-      acc_phase ^= 1;
       tc_fence_after();
+      const uint32_t acc = tmem + buf * most;
       for (int kb = 0; kb < a.kblocks; ++kb) {
         if (!ready)
           ok = __all_sync(0xFFFFFFFFu,
@@ -796,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           if (ks == 2)
             ready = __all_sync(0xFFFFFFFFu, phase_done(R.bar(pair::kSfReady + stage), phase));
           const uint32_t id = 2u * (ks & 1);
-          pair::mma_warp(tmem, smem_desc(sb + ks * 32, 16, 1024, 2),
+          pair::mma_warp(acc, smem_desc(sb + ks * 32, 16, 1024, 2),
                          smem_desc(sb + off_b + ks * 32, 16, 1024, 2),
                          idesc | (id << 4) | (id << 29), col + 4 * (ks >> 1),
                          col + 8 + nrb * (ks >> 1), (kb | ks) != 0 ? 1u : 0u);
@@ -805,7 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         pair::commit_warp(R.bar(pair::kEmpty + s));
       }
       if (!ok) break;
-      pair::commit_warp(R.bar(pair::kAccFull));
+      pair::commit_warp(R.bar(pair::kAccFull + buf));
     }
     if (issued && (!ok || *abort_flag)) {
       pair::commit_warp(R.bar(pair::kDrain));
@@ -817,12 +830,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const int q = warp & 3, h = (warp - 8) >> 2;  // lanes 32q ..., first or second half of the rows
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     T* out = static_cast<T*>(a.out);
-    uint32_t acc_phase = 0;
-    for (int item = item0; item < n_items; item += step) {
+    int local = 0;
+    for (int item = item0; item < n_items; item += step, ++local) {
       const Item it = walk.at(item);
       const int n = it.mt * 256 + rank * 128 + q * 32 + lane;
       const int half = ((it.rows + 31) & ~31) / 2;
-      if (!__all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(pair::kAccFull), acc_phase, abort_flag))) {
+      const int buf = nbuf == 2 ? local & 1 : 0;
+      const uint32_t acc_par = (uint32_t)(nbuf == 2 ? local >> 1 : local) & 1u;
+      if (!__all_sync(0xFFFFFFFFu,
+                      wait_or_leave(R.bar(pair::kAccFull + buf), acc_par, abort_flag))) {
         for (; item < n_items; item += step) {
           const Item left = walk.at(item);
           const int f = left.mt * 256 + rank * 128 + q * 32 + lane;
@@ -831,9 +847,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         break;
       }
-      acc_phase ^= 1;
       tc_fence_after();
-      const uint32_t acc = tmem + lane_addr + h * half;
+      const uint32_t acc = tmem + lane_addr + buf * most + h * half;
       const int m = min(half, it.rows - h * half);  // rows of this half
       T* o = out + (int64_t)(it.row0 + h * half) * a.ld;
       if constexpr (DT != kF32) {
@@ -851,24 +866,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_rank0(R.bar(pair::kAccEmpty));
+        if (lane == 0) arrive_rank0(R.bar(pair::kAccEmpty + buf));
         if (a.wide) {
           // the 4 x 4 exchange of the single CTAs
           const bool odd = lane & 1, upper = lane & 2;
           const int f = n & ~3;
           T* p = o + (int64_t)(lane & 3) * a.ld + f;
 #pragma unroll
-          for (int j = 0; j < 128; j += 4) {
-            if (j >= half) continue;
-            const uint32_t w01 = w[j / 2], w23 = w[j / 2 + 1];
-            const uint32_t x01 = __shfl_xor_sync(0xFFFFFFFFu, w01, 1);
-            const uint32_t x23 = __shfl_xor_sync(0xFFFFFFFFu, w23, 1);
-            const uint32_t a01 = odd ? __byte_perm(x01, w01, 0x7632) : __byte_perm(w01, x01, 0x5410);
-            const uint32_t a23 = odd ? __byte_perm(x23, w23, 0x7632) : __byte_perm(w23, x23, 0x5410);
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? a01 : a23, 2);
-            if (j + (lane & 3) < m && f < a.N)
-              *reinterpret_cast<uint2*>(p) = upper ? make_uint2(got, a23) : make_uint2(a01, got);
-            p += 4 * a.ld;
+          for (int g = 0; g < 8; ++g) {
+            if (16 * g >= half) break;  // a branch for 16 rows: their exchanges overlap
+#pragma unroll
+            for (int j = 16 * g; j < 16 * g + 16; j += 4) {
+              const uint32_t w01 = w[j / 2], w23 = w[j / 2 + 1];
+              const uint32_t x01 = __shfl_xor_sync(0xFFFFFFFFu, w01, 1);
+              const uint32_t x23 = __shfl_xor_sync(0xFFFFFFFFu, w23, 1);
+              const uint32_t a01 = odd ? __byte_perm(x01, w01, 0x7632) : __byte_perm(w01, x01, 0x5410);
+              const uint32_t a23 = odd ? __byte_perm(x23, w23, 0x7632) : __byte_perm(w23, x23, 0x5410);
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? a01 : a23, 2);
+              if (j + (lane & 3) < m && f < a.N)
+                *reinterpret_cast<uint2*>(p) = upper ? make_uint2(got, a23) : make_uint2(a01, got);
+              p += 4 * a.ld;
+            }
           }
         } else if (n < a.N) {
 #pragma unroll
@@ -887,7 +905,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_rank0(R.bar(pair::kAccEmpty));
+        if (lane == 0) arrive_rank0(R.bar(pair::kAccEmpty + buf));
       }
     }
   }
@@ -903,8 +921,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   }
 }
 
-// Pairs where the rows an expert has on average are enough and there are two weight tiles.
-bool use_pairs(const MxGemmArgs& a) { return a.N > 128 && a.R >= (int64_t)a.E * kPairRows; }
+bool use_pairs(const MxGemmArgs& a, int sms) {
+  const int64_t items = (int64_t)a.R / pair::kTileN * ((a.N + 255) / 256);
+  return a.kblocks >= kPairStages && a.R >= a.E * kPairRows && items >= sms / 4;
+}
 
 template <typename K>
 cudaError_t launch_kernel(K kernel, int threads, std::atomic<uint64_t>& configured,
@@ -917,7 +937,7 @@ cudaError_t launch_kernel(K kernel, int threads, std::atomic<uint64_t>& configur
 template <int DT>
 cudaError_t launch_typed(const MxMaps& maps, const MxGemmArgs& a, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> single_set{0}, pair_set{0};
-  if (use_pairs(a)) {
+  if (use_pairs(a, sms)) {
     const int64_t tiles = (int64_t)a.R / pair::kTileN + a.E;
     const int64_t pairs = std::min<int64_t>(sms / 2, tiles * ((a.N + 255) / 256));
     return launch_kernel(gemm_mx_pair_kernel<DT>, pair::kThreads, pair_set, maps, a,

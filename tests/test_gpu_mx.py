@@ -274,28 +274,49 @@ def test_outputs_more_than_32_bits_apart():
     assert torch.equal(M.mx_restore(q, out=far), M.mx_restore(q))
 
 
-@pytest.mark.parametrize("E,N,D", [(2, 300, 512), (3, 129, 300), (1, 515, 1024)])
-@pytest.mark.parametrize("rows", [128, 129, 160, 255, 256, 257, 288, 512, 545, 1000])
-def test_product_by_pairs_of_blocks(E, N, D, rows):
-    """Groups of `rows` rows (and one of a few) around the tiles' heights, odd starts."""
+# rows an expert, experts, outputs, length: pairs of blocks take these (stages from 8 on, 38
+# items or more of 256 rows and outputs); row tiles of 32 to 256 rows, one and two accumulators
+@pytest.mark.parametrize("rows,E,N,D", [(229, 5, 2436, 2048), (256, 4, 2560, 2100),
+                                        (257, 4, 2561, 2048), (288, 4, 2499, 1999),
+                                        (500, 2, 3301, 2305), (1023, 1, 2818, 4001),
+                                        (160, 9, 2305, 1900)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_product_by_pairs_of_blocks(rows, E, N, D, dtype):
     offsets = [0] + [3 + rows * (i + 1) for i in range(E)]
-    offsets[-1] += 200
+    offsets[-1] += 224 * E - min(224 * E, offsets[-1])
     x, _ = _values(offsets[-1], D, "bf16", rows)
     w = torch.randn(E, N, D, generator=torch.Generator().manual_seed(N)) * D ** -0.5
-    for dtype in ("bf16", "f32"):
-        _product(x, w, offsets, R.TYPES[dtype])
+    _product(x, w, offsets, R.TYPES[dtype])
+
+
+def test_ragged_groups_by_pairs_of_blocks():
+    offsets = [0, 1, 1, 700, 731, 1060, 1500, 1500, 2001]
+    x, _ = _values(2001, 2048, "bf16", 4)
+    w = torch.randn(8, 1400, 2048, generator=torch.Generator().manual_seed(4)) / 45
+    store = torch.full((2001, 1401), 7.0, dtype=torch.bfloat16, device=DEV)
+    for out in (None, store[:, 1:], torch.as_strided(store, (2001, 1400), (1401, 1))):
+        _product(x, w, offsets, torch.bfloat16, out=out)
+
+
+def test_a_row_has_the_same_bits_in_pairs():
+    x, _ = _values(2000, 2048, "bf16", 15)
+    w = M.mx_quantize(torch.randn(1, 1300, 2048, device=DEV) / 45)
+    whole = M.mx_product(M.mx_quantize(x.to(DEV)), w)
+    for a, b in ((0, 1), (777, 900), (1990, 2000)):
+        part = M.mx_product(M.mx_quantize(x[a:b].contiguous().to(DEV)), w)
+        assert torch.equal(part, whole[a:b])
 
 
 def test_expired_waits_give_nan_in_pairs():
-    x, xc = _values(600, 512, "bf16", 14)
-    w = M.mx_quantize(torch.randn(2, 384, 512, device=DEV) / 22)
-    off = torch.tensor([0, 301, 600], dtype=torch.int32, device=DEV)
+    x, xc = _values(1000, 2048, "bf16", 14)
+    w = M.mx_quantize(torch.randn(2, 3328, 2048, device=DEV) / 45)
+    off = torch.tensor([0, 501, 1000], dtype=torch.int32, device=DEV)
     q = M.mx_quantize(xc)
     want = M.mx_product(q, w, off)
-    # expert 1 (items 4 .. 7): its first row tile (160 rows), outputs 256 .. 383
-    got = M.moe_nvfp4_selftest_product_timeout(q, w, off, 6)
+    # expert 1 has items 26 .. 51: its second row tile of outputs 256 .. 511
+    got = M.moe_nvfp4_selftest_product_timeout(q, w, off, 29)
     lost = torch.isnan(got)
-    assert torch.all(lost[301:461, 256:]) and int(lost.sum()) == 160 * 128
+    assert torch.all(lost[757:, 256:512]) and int(lost.sum()) == 243 * 256
     assert torch.equal(got[~lost], want[~lost])
     assert torch.equal(M.mx_product(q, w, off), want)
 
