@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
   }
 }
 
+// (16-bit rows: five blocks an SM, 48 registers a thread)
 template <int DT, int VB, int U, int ACT, bool LIMIT>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const KeepArgs a, int segs) {
+__global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 5) act_grad_kernel(const KeepArgs a, int segs) {
   constexpr int kHalves = ACT == kActSwiglu ? 2 : 1;
   pdl_trigger();
   pdl_wait();

@@ -93,6 +93,7 @@ struct MxGemmArgs {
   int64_t ld;
   int dtype;
   int wide;                // 16-bit out in runs of 4 on 8 bytes
+  int tile_rows;           // pairs: rows of the largest tile
   int leave_item;          // self-test: the token producer leaves before this item; -1: never
 };
 cudaError_t launch_gemm_mx(const MxGemmArgs& a, const uint8_t* x_codes, const uint8_t* w_codes,

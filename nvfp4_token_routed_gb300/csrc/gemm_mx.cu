@@ -15,7 +15,7 @@
 //     groups up for itself and takes items blockIdx.x, + gridDim.x, ...: no counter, no
 //     workspace, nothing to reset between launches.
 //   * Warp 0 loads weight tiles (TMA, 128-byte swizzle) and their scales, warp 10 row
-//     tiles (boxes of 128 / 64 / 32 / 16 rows) and theirs; a stage is 256 values deep.
+//     tiles (a box, two above 128 rows: a map for each height) and theirs; a stage is 256 values deep.
 //     A stage's scales are one contiguous piece of a panel (mx_quant.cu), which starts on
 //     an even row: 8 bytes a row, 16 a bulk copy's boundary.
 //   * Warps 6-9 move a stage's scales to TMEM: row r at lane r % 32, column r / 32, in
@@ -78,7 +78,7 @@ constexpr int kPairStages = 8;
 
 struct MxMaps {
   CUtensorMap w;
-  CUtensorMap x[4];  // 16, 32, 64, 128 rows
+  CUtensorMap x[8];  // 16, 32, ... 128 rows
 };
 
 // A value that is the same in every lane, and that the compiler then knows to be: what
@@ -205,6 +205,11 @@ struct Walk {
   }
 };
 
+// First row of expert e; rows outside [0, R] are no rows.
+__device__ __forceinline__ int group_bound(const MxGemmArgs& a, int e) {
+  return a.offsets ? max(0, min(a.R, a.offsets[e])) : e ? a.R : 0;
+}
+
 // First item and first row of each expert, by the whole block (blockDim.x = THREADS): row
 // tiles of at most tile_n rows in whole units of `unit`, m_tiles weight tiles each.  Also
 // folds the largest tile height into *s_most (set before).  s_sum: an int a warp.
@@ -215,12 +220,9 @@ __device__ __forceinline__ void lay_out_groups(const MxGemmArgs& a, int tile_n, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (a.E + THREADS - 1) / THREADS;
   const int e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
-  auto bound = [&](int e) {  // rows outside [0, R] are no rows
-    return a.offsets ? max(0, min(a.R, a.offsets[e])) : e ? a.R : 0;
-  };
   int items = 0, most = unit;
   for (int e = e0; e < e1; ++e) {
-    const int rows = max(0, bound(e + 1) - bound(e));
+    const int rows = max(0, group_bound(a, e + 1) - group_bound(a, e));
     const int tiles = (rows + tile_n - 1) / tile_n;
     items += tiles * m_tiles;
     if (tiles) most = max(most, ((rows + tiles - 1) / tiles + unit - 1) / unit * unit);
@@ -237,7 +239,7 @@ __device__ __forceinline__ void lay_out_groups(const MxGemmArgs& a, int tile_n, 
   int before = x - items;
   for (int w = 0; w < warp; ++w) before += s_sum[w];
   for (int e = e0; e < e1; ++e) {
-    const int b0 = bound(e), rows = max(0, bound(e + 1) - b0);
+    const int b0 = group_bound(a, e), rows = max(0, group_bound(a, e + 1) - b0);
     first_item[e] = before;
     first_row[e] = b0;
     before += (rows + tile_n - 1) / tile_n * m_tiles;
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *s_max16 = 16;
     fence_barrier_init();
     prefetch_tmap(&maps.w);
-    for (int i = 0; i < 4; ++i) prefetch_tmap(&maps.x[i]);
+    for (int i = 0; i < 8; ++i) prefetch_tmap(&maps.x[i]);
   }
   __syncwarp();
   if (warp == 1) {
@@ -358,13 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const uint32_t sb = smem_u32(stages + stage * stage_bytes), full = R.bar(kFull + stage);
         expect_warp(full, n16 * kRowBytes + sf);
-        for (int r = 0; r < n16;) {
-          const int rem = n16 - r;
-          const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
-          box_warp(sb + off_b + r * kRowBytes, &maps.x[lg], full, kb * kRowBytes, it.row0 + r,
-                   pol);
-          r += 16 << lg;
-        }
+        const int first = min(n16, 128);
+        box_warp(sb + off_b, &maps.x[first / 16 - 1], full, kb * kRowBytes, it.row0, pol);
+        if (n16 > 128)
+          box_warp(sb + off_b + 128 * kRowBytes, &maps.x[(n16 - 128) / 16 - 1], full,
+                   kb * kRowBytes, it.row0 + 128, pol);
         piece_warp(sb + off_sfb, a.sx + kb * a.sx_panel + 8 * (int64_t)r0, sf, full);
         ++loaded;
         if (++stage == n_stages) {
@@ -645,7 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     *s_most = 32;
     fence_barrier_init();
     prefetch_tmap(&maps.w);
-    for (int i = 0; i < 4; ++i) prefetch_tmap(&maps.x[i]);
+    for (int i = 0; i < 8; ++i) prefetch_tmap(&maps.x[i]);
   }
   __syncwarp();
   if (warp == 1) pair::alloc(smem_u32(tmem_slot), kTmemCols);
@@ -657,10 +657,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   pdl_wait();
   pdl_trigger();
-  lay_out_groups<pair::kThreads>(a, pair::kTileN, 32, m_pairs, first_item, first_row, s_sum,
+  const int item0 = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+  lay_out_groups<pair::kThreads>(a, a.tile_rows, 32, m_pairs, first_item, first_row, s_sum,
                                  s_most);
   const int n_items = uniform(first_item[a.E]);
-  const int item0 = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
   const int most = uniform(*s_most);                // rows of the largest tile, whole 32s
   const int sfb_bytes = (8 * (most + 2) + 127) & ~127;
@@ -716,12 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           box_warp(sb, &maps.w, full, kb * kRowBytes, (int)w0, pol);
         } else if (warp == 2) {
           expect_warp(full, half * kRowBytes);
-          for (int r = 0; r < half;) {
-            const int rem = half - r;
-            const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
-            box_warp(sb + off_b + r * kRowBytes, &maps.x[lg], full, kb * kRowBytes, x0 + r, pol);
-            r += 16 << lg;
-          }
+          box_warp(sb + off_b, &maps.x[half / 16 - 1], full, kb * kRowBytes, x0, pol);
         } else {
           expect_warp(full, sfa + sfb);
           piece_warp(sb + off_sfa, a.sw + kb * a.sw_panel + 8 * w_even, sfa, full);
@@ -926,6 +921,21 @@ bool use_pairs(const MxGemmArgs& a, int sms) {
   return a.kblocks >= kPairStages && a.R >= a.E * kPairRows && items >= sms / 4;
 }
 
+// Rows of the largest tile of pairs: 256; of a single matrix less where the items then come
+// out in fuller rounds of the pairs.  A stage of an item takes some 316 + rows cycles.  R4096
+// N4096 D7168 by 76 pairs: 256 items are 4 rounds, the last a third full, and so are 304 items
+// of 224 rows (41.7 -> 40.0 us); R8192 stays at 256.
+int tile_rows(const MxGemmArgs& a, int pairs) {
+  int best = pair::kTileN;
+  int64_t best_cost = INT64_MAX;
+  for (int h = pair::kTileN; h >= 192 && !a.offsets; h -= 32) {
+    const int64_t items = (int64_t)((a.R + h - 1) / h) * ((a.N + 255) / 256);
+    const int64_t cost = (items + pairs - 1) / pairs * (316 + h);
+    if (cost < best_cost) best = h, best_cost = cost;
+  }
+  return best;
+}
+
 template <typename K>
 cudaError_t launch_kernel(K kernel, int threads, std::atomic<uint64_t>& configured,
                           const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t s) {
@@ -938,9 +948,11 @@ template <int DT>
 cudaError_t launch_typed(const MxMaps& maps, const MxGemmArgs& a, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> single_set{0}, pair_set{0};
   if (use_pairs(a, sms)) {
-    const int64_t tiles = (int64_t)a.R / pair::kTileN + a.E;
+    MxGemmArgs p = a;
+    p.tile_rows = tile_rows(a, sms / 2);
+    const int64_t tiles = (int64_t)a.R / p.tile_rows + a.E;
     const int64_t pairs = std::min<int64_t>(sms / 2, tiles * ((a.N + 255) / 256));
-    return launch_kernel(gemm_mx_pair_kernel<DT>, pair::kThreads, pair_set, maps, a,
+    return launch_kernel(gemm_mx_pair_kernel<DT>, pair::kThreads, pair_set, maps, p,
                          (int)pairs * 2, s);
   }
   const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kTileN + a.E);
@@ -955,8 +967,8 @@ cudaError_t launch_gemm_mx(const MxGemmArgs& a, const uint8_t* x_codes, const ui
   MxMaps maps;
   const uint64_t row_bytes = (uint64_t)a.kblocks * kRowBytes;
   if (!byte_map(&maps.w, w_codes, row_bytes, (uint64_t)a.E * a.N, 128)) return cudaErrorInvalidValue;
-  for (int i = 0; i < 4; ++i)
-    if (!byte_map(&maps.x[i], x_codes, row_bytes, a.R, 16u << i)) return cudaErrorInvalidValue;
+  for (int i = 0; i < 8; ++i)
+    if (!byte_map(&maps.x[i], x_codes, row_bytes, a.R, 16u * (i + 1))) return cudaErrorInvalidValue;
   return a.dtype == kF32    ? launch_typed<kF32>(maps, a, sms, s)
          : a.dtype == kBf16 ? launch_typed<kBf16>(maps, a, sms, s)
                             : launch_typed<kF16>(maps, a, sms, s);
