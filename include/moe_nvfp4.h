@@ -546,7 +546,8 @@ size_t moe_nvfp4_sort_routes_workspace_bytes(int32_t T, int32_t K, int32_t E);
  *   perm [T*K]     route t*K+k of each row; -1 from offsets[E] on
  *   inv [T][K]     row of each route, -1 for an empty slot
  * 1 <= E <= 1024, 1 <= K <= min(32, E), T*K <= 2^26.  ws: 256-byte aligned, one per stream;
- * its contents before the call do not matter.  T == 0 writes offsets (zeros) only. */
+ * its contents before the call do not matter.  NULL where no more than 256 bytes are needed
+ * (T*K <= 32768): bad ids then go unreported.  T == 0 writes offsets (zeros) only. */
 moe_status moe_nvfp4_sort_routes(int32_t T, int32_t K, int32_t E, const void* topk_ids,
                                  int32_t ids_int64, int32_t* offsets, int32_t* perm, int32_t* inv,
                                  void* ws, size_t ws_bytes, moe_stream_t stream);

@@ -18,9 +18,10 @@ struct SortArgs {
   int32_t* offsets;  // [E + 1]
   int32_t* perm;     // [T*K]
   int32_t* inv;      // [T][K]
-  int32_t* status;   // kStatusWords words at the workspace's start
+  int32_t* status;   // kStatusWords words at the workspace's start, or null (one cluster)
   int32_t* chunks;   // [chunks][E + 1] then totals [E]
 };
+constexpr size_t kSortStatusBytes = 256;  // head of the workspace, all of it up to 32768 routes
 size_t sort_routes_ws_bytes(int64_t TK, int E);
 cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t s);
 

@@ -139,15 +139,18 @@ moe_status moe_nvfp4_sort_routes(int32_t T, int32_t K, int32_t E, const void* to
   if (st != MOE_OK) return st;
   if (E < 1 || !bool_ok(ids_int64)) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || K > E) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (!offsets || !ws || (T > 0 && (!topk_ids || !perm || !inv))) return MOE_ERR_INVALID_ARG;
+  const size_t need = sort_routes_ws_bytes((int64_t)T * K, E);
+  if (!offsets || (!ws && need > kSortStatusBytes) || (T > 0 && (!topk_ids || !perm || !inv)))
+    return MOE_ERR_INVALID_ARG;
   if (!aligned(offsets, 4) || !aligned(ws, 256) || !aligned(perm, 4) || !aligned(inv, 4) ||
       (T > 0 && !aligned(topk_ids, ids_int64 ? 8 : 4)))
     return MOE_ERR_MISALIGNED;
-  if (ws_bytes < sort_routes_ws_bytes((int64_t)T * K, E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws && ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if ((st = (moe_status)device_status(nullptr)) != MOE_OK) return st;
   if (T == 0) {
     cudaError_t e = cudaMemsetAsync(offsets, 0, ((size_t)E + 1) * sizeof(int32_t), raw(stream));
-    if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, kStatusWords * sizeof(int32_t), raw(stream));
+    if (e == cudaSuccess && ws)
+      e = cudaMemsetAsync(ws, 0, kStatusWords * sizeof(int32_t), raw(stream));
     return cuda_status(e);
   }
   SortArgs a = {};
@@ -160,7 +163,7 @@ moe_status moe_nvfp4_sort_routes(int32_t T, int32_t K, int32_t E, const void* to
   a.perm = perm;
   a.inv = inv;
   a.status = static_cast<int32_t*>(ws);
-  a.chunks = static_cast<int32_t*>(ws) + 64;
+  a.chunks = ws ? static_cast<int32_t*>(ws) + kSortStatusBytes / sizeof(int32_t) : nullptr;
   return cuda_status(launch_sort_routes(a, raw(stream)));
 }
 

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kOneWarps * 32) sort_cluster_kernel(const Sort
   }
   if (rank == 0 && threadIdx.x == 0) {
     a.offsets[a.E] = n;
-    a.status[kStatusFlags] = any_bad ? kFlagBadExpertId : 0;
+    if (a.status) a.status[kStatusFlags] = any_bad ? kFlagBadExpertId : 0;
   }
   __syncthreads();
 #pragma unroll
@@ -544,9 +544,8 @@ int dtype_size(int dtype) { return dtype == kF32 ? 4 : 2; }
 }  // namespace
 
 size_t sort_routes_ws_bytes(int64_t TK, int E) {
-  const size_t head = 256;  // status words
-  if (TK <= kCluster * kOneBlock) return head;
-  return head + sizeof(int32_t) * ((size_t)chunks_of(TK) * (E + 1) + E);
+  if (TK <= kCluster * kOneBlock) return kSortStatusBytes;
+  return kSortStatusBytes + sizeof(int32_t) * ((size_t)chunks_of(TK) * (E + 1) + E);
 }
 
 cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t s) {

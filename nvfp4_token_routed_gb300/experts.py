@@ -64,8 +64,8 @@ def sort_routes_workspace(T_max, K, E, device="cuda"):
 
 def sort_routes(topk_ids, E, plan=None, ws=None, stream=None):
     """Stable counting sort of the routes topk_ids [T, K] (int32 or int64, -1: empty slot) by
-    expert: a RoutePlan.  Ids outside [-1, E) are empty slots too; moe_nvfp4_read_status(ws)
-    reports them."""
+    expert: a RoutePlan.  Ids outside [-1, E) are empty slots too; with a workspace of the
+    caller's (sort_routes_workspace) moe_nvfp4_read_status(ws) reports them."""
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids: one row of expert ids per token")
     dev = topk_ids.get_device()
@@ -84,9 +84,9 @@ def sort_routes(topk_ids, E, plan=None, ws=None, stream=None):
                 _arg(plan.perm, "perm", (T * K,), _I32, topk_ids),
                 _arg(plan.inv, "inv", shape, _I32, topk_ids))
     if ws is None:
-        n = L.moe_nvfp4_sort_routes_workspace_bytes(T, K, E)
-        ws = _out(None, "ws", n, torch.uint8, topk_ids, stream)
-        wp = ws.data_ptr()
+        n = 0 if T * K <= 32768 else L.moe_nvfp4_sort_routes_workspace_bytes(T, K, E)
+        ws = _out(None, "ws", n, torch.uint8, topk_ids, stream) if n else None
+        wp = ws.data_ptr() if n else None
     else:
         n, wp = ws.numel(), _arg(ws, "ws", ws.shape, _U8, topk_ids)
     _check(L.moe_nvfp4_sort_routes(T, K, E, ids, _IDS64[topk_ids.dtype], *ptrs, wp, n,

@@ -33,7 +33,7 @@ def test_sort_checks(lib):
     for kw, code in ((dict(T=-1), 1), (dict(K=0), 1), (dict(E=0), 1), (dict(i64=2), 1),
                      (dict(K=33, E=64), 2), (dict(K=9), 2), (dict(E=1025), 2),
                      (dict(T=1 << 26), 2), (dict(ids=None), 1), (dict(off=None), 1),
-                     (dict(perm=None), 1), (dict(inv=None), 1), (dict(ws=None), 1),
+                     (dict(perm=None), 1), (dict(inv=None), 1), (dict(T=16385, ws=None), 1),
                      (dict(ids=P + 2), 3), (dict(ids=P + 4, i64=1), 3), (dict(off=P + 1), 3),
                      (dict(perm=P + 2), 3), (dict(inv=P + 2), 3), (dict(ws=P + 16), 3),
                      (dict(n=255), 4), (dict(T=100000, n=3815), 4)):
