@@ -12,8 +12,12 @@
 // y comes from the unrounded input, the gradient from the kept values.
 //
 // A warp takes U times 256 consecutive values of a row (of both halves), 8 a lane and four
-// lanes a block of 32; its loads are issued together.  Nothing is shared between blocks, so
-// the kernels are bound by HBM.
+// lanes a block of 32; its loads are issued together (U = 1: clamped SwiGLU 86 us, 2: 75).
+// Nothing is shared between blocks: the kernels are bound by HBM once the instructions fit
+// beside it, for which 16-bit maxima and fp32 arithmetic go two at a time (75 -> 61 us).
+// Measured (bf16; copy rate 6686 GB/s): clamped SwiGLU 24576 x 2048 forward 61 us (0.99 of the
+// copy rate), gradient 65 us (0.93), rows of 4096 x 7168 kept 13.6 us and restored 12.5 us;
+// squared ReLU 5001 x 1407 f16, rows off 4 bytes, 10.4 and 11.0 us (0.5; by a run a lane 20).
 #include <algorithm>
 
 #include "block32.cuh"
@@ -274,7 +278,8 @@ cudaError_t go(K kernel, const KeepArgs& a, int u, cudaStream_t s) {
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, segs);
 }
 
-// U spans a warp where that leaves the device enough warps, else one.
+// U spans a warp where that leaves the device enough warps (16 an SM), else one: 128 rows of
+// 1024 take 3.2 us with one span a warp.
 constexpr int64_t kManyWarps = 152 * 16;
 int spans(const KeepArgs& a, int u) {
   return (int64_t)a.R * ((a.W + u * kSpan - 1) / (u * kSpan)) >= kManyWarps ? u : 1;

@@ -8,7 +8,9 @@
 // are one contiguous piece, which one bulk copy brings, and a run of rows may start at any
 // row: experts' groups need no padding.
 //
-// A warp takes 256 values of a row, 8 a lane; bound by HBM.
+// A warp takes 256 values of a row, 8 a lane, four such spans where there are rows enough
+// (one: 80 us, four: 53; maxima of 16-bit halves two at a time: 48).  Measured (bf16, 16384 x
+// 7168; copy rate 6686 GB/s): 48 us, 0.94 of the copy rate, with 75 % of the issue slots used.
 #include "block32.cuh"
 #include "experts.h"
 #include "internal.h"

@@ -9,7 +9,10 @@
 //
 // All row kernels go by tokens, not by rows: a token's row is read (or written) once and
 // its K rows stay independent accesses in flight, and no sum meets another thread's, so
-// equal inputs give equal bits.  They are bound by HBM; the sort by launch latency.
+// equal inputs give equal bits.  They are bound by HBM, the sort by latency.  Measured (bf16,
+// T4096 K6 H7168, 384 experts; copy rate 6686 GB/s): dispatch 59 us (1.05 of the copy rate,
+// as its last writes are still in L2), combine 66 us (0.94), its gradient 122 us (0.93), the
+// sort of the 24576 routes 11 us in one launch (three launches of many blocks: 18.5).
 #include <algorithm>
 
 #include "block32.cuh"
