@@ -575,8 +575,9 @@ moe_status moe_nvfp4_combine_grad(const moe_rows* rows, int32_t T, int32_t K, co
 
 /* Rows kept in 8 bits: E4M3 times a power of two 2^e per 32 consecutive values, e the
  * smallest with which no value passes 448, -127 <= e <= 127, stored as e + 127.  A value is
- * rounded to nearest even: off by at most 2^-4 of itself or half of 2^(e-9).  A block with an
- * infinity or a NaN (byte 255) reads as NaN.
+ * rounded to nearest even, downwards where that would leave its type's range: off by at
+ * most 2^-4 of itself or half of 2^(e-9).  A block with an infinity or a NaN (byte 255)
+ * reads as NaN.
  *   codes  [R][W32], W32 = cols rounded up to 32, zeros behind the row; 8-byte aligned
  *   scales [R][W32 / 32]
  * cols <= 2^20. */

@@ -51,11 +51,19 @@ __device__ __forceinline__ bool place_of(const KeepArgs& a, int segs, int u, int
 // part.
 template <int DT>
 __device__ __forceinline__ void keep_run(const KeepArgs& a, int64_t r, int c, int halves, int half,
-                                         const uint32_t (&w)[kRunWords<DT>], const Run8& v) {
+                                         const uint32_t (&w)[kRunWords<DT>], Run8& v) {
   const int Wp = (a.W + 31) & ~31;
   c += (threadIdx.x & 31) * 8;
   const uint32_t byte = block_scale_byte<E4m3>(block_amax<DT>(w));
   if (c >= Wp) return;
+  // from 248 2^e on a value rounds to 256 2^e: where the type ends before that it takes 240 2^e,
+  // which is still within 2^-4 of it, and not an infinity
+  constexpr uint32_t kLastByte = DT == kF16 ? 8 + 127 : 120 + 127;
+  if (byte == kLastByte) {
+    const float most = 240.0f * block_scale(kLastByte);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.v[i] = fminf(fmaxf(v.v[i], -most), most);
+  }
   const int64_t at = (r * halves + half) * Wp + c;
   *reinterpret_cast<uint2*>(a.codes + at) =
       byte == 255u ? make_uint2(0u, 0u) : e4m3x8(v, block_inverse(byte));

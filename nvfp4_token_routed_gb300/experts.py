@@ -101,6 +101,8 @@ def dispatch(x, plan, rows=None, stream=None):
     if x.shape[0] != T:
         raise ValueError(f"x: expected {T} rows, got {x.shape[0]}")
     if isinstance(x, MxTensor):
+        if len(x.shape) != 2:
+            raise ValueError("x: an MxTensor of rows [T, H]")
         inv = _arg(plan.inv, "inv", (T, K), _I32, x.on())
         if rows is None:
             rows = MxTensor.empty((T * K, x.shape[1]), x.on(), stream)
@@ -241,10 +243,11 @@ def checkpoint(x, kept=None, n_rows=None, stream=None):
 
 
 def restore(kept, dtype=None, out=None, n_rows=None, stream=None):
-    """The rows that checkpoint kept, of `dtype` (None: the type they had)."""
+    """The rows that checkpoint kept, of `dtype` (None: the type they had), or of out's."""
     if kept.act is not None:
         raise ValueError("kept: an activation's input is read by expert_act_grad")
-    R, D, dtype = kept.rows, kept.cols, dtype or kept.dtype
+    R, D = kept.rows, kept.cols
+    dtype = out.dtype if out is not None else dtype or kept.dtype
     if dtype not in _DTYPE:
         raise ValueError("dtype: float32, bfloat16 or float16")
     out, p, ld = _like(out, "out", (R, D), dtype, kept.on(), stream)
@@ -371,7 +374,9 @@ def mx_quantize_transposed(x, out=None, stream=None):
 
 
 def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
-    """The values of an MxTensor, as a tensor of its shape."""
+    """The values of an MxTensor, as a tensor of its shape (into `out`: as rows, of out's type)."""
+    if out is not None:
+        dtype = out.dtype
     if dtype not in _DTYPE:
         raise ValueError("dtype: float32, bfloat16 or float16")
     rows, D = x.c.rows, x.c.cols
@@ -419,6 +424,23 @@ def moe_nvfp4_selftest_product_timeout(x, w, offsets, item, dtype=torch.bfloat16
 
 # ------------------------------------------------------------------ together
 
+class SavedPass:
+    """What MxExperts.backward needs of a forward.  The experts' rows are overwritten by their
+    gradient, so it can be taken once."""
+    __slots__ = ("plan", "rows", "kept", "topk_w")
+
+    def __init__(self, plan, rows, kept, topk_w):
+        self.plan, self.rows, self.kept, self.topk_w = plan, rows, kept, topk_w
+
+    def take(self):
+        if self.kept is None:
+            raise ValueError("saved: from a forward with keep=False")
+        if self.rows is None:
+            raise ValueError("saved: backward has used it already")
+        rows, self.rows = self.rows, None
+        return self.plan, rows, self.kept, self.topk_w
+
+
 class MxExperts:
     """Routed experts in microscaled FP4 through which gradients pass: the weights stay frozen,
     forward keeps the activations' input in 8 bits, and backward returns the gradients of the
@@ -453,11 +475,11 @@ class MxExperts:
         rows = mx_product(mx_quantize(a, n_rows=n, stream=stream), self.fc2, plan.offsets, dt,
                           stream=stream)
         y = combine(rows, plan, topk_w, stream=stream)
-        return y, (plan, rows, kept, topk_w)
+        return y, SavedPass(plan, rows, kept, topk_w)
 
     def backward(self, saved, dy, stream=None):
-        """dy [T, H] -> (dx [T, H], d_topk_w [T, K] fp32).  Uses saved rows' storage: once."""
-        plan, rows, kept, topk_w = saved
+        """dy [T, H] -> (dx [T, H], d_topk_w [T, K] fp32), once for each forward."""
+        plan, rows, kept, topk_w = saved.take()
         n, dt = plan.n_rows, dy.dtype
         drows, dw = combine_grad(rows, plan, topk_w, dy, drows=rows, stream=stream)
         da = mx_product(mx_quantize(drows, n_rows=n, stream=stream), self.fc2_t, plan.offsets, dt,

@@ -89,8 +89,9 @@ def blocks(x, largest):
     return pad, exps
 
 
-def held(x, largest, fraction_bits, least_exp):
-    """(values that the format holds of x [R, D], scale bytes [R, B])."""
+def held(x, largest, fraction_bits, least_exp, most=math.inf):
+    """(values that the format holds of x [R, D], scale bytes [R, B]); a value that would round
+    past `most` rounds down."""
     pad, exps = blocks(x, largest)
     unit = torch.tensor([[math.nan if e is None else 2.0 ** e for e in row] for row in exps],
                         dtype=torch.float64).unsqueeze(2)
@@ -99,11 +100,13 @@ def held(x, largest, fraction_bits, least_exp):
     e = torch.floor(torch.log2(v.abs().clamp_min(2.0 ** (least_exp - 1))))
     e = torch.where(2.0 ** (e + 1) <= v.abs(), e + 1, torch.where(2.0 ** e > v.abs(), e - 1, e))
     step = 2.0 ** (e.clamp_min(least_exp) - fraction_bits)
-    return (torch.round(v / step) * step * unit).flatten(1)[:, :x.shape[1]], byte.to(torch.uint8)
+    q = torch.round(v / step) * step
+    q = torch.where((q * unit).abs() > most, torch.sign(v) * (torch.floor(v.abs() / step) * step), q)
+    return (q * unit).flatten(1)[:, :x.shape[1]], byte.to(torch.uint8)
 
 
 def held8(x):
-    return held(x, E4M3_MAX, 3, -6)
+    return held(x, E4M3_MAX, 3, -6, torch.finfo(x.dtype).max)
 
 
 def held4(x):

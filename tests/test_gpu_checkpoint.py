@@ -64,10 +64,36 @@ def test_block_borders_and_special_values():
     assert torch.equal(kept.scales.cpu()[:, 0], byte)
     got = M.restore(kept).cpu()
     assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.isnan(want).sum() == 64
-    # the value next to the type's largest rounds to 2^128, which fp32 writes as infinity
-    same = torch.equal(got.nan_to_num(), want.float().nan_to_num())
+    same = torch.equal(got.nan_to_num().double(), want.nan_to_num())
     assert same
-    assert float(got[0, 0]) == 448.0 and float(got[11, 0]) == -448.0 and float(got[7, 0]) > 3.2e38
+    assert float(got[0, 0]) == 448.0 and float(got[11, 0]) == -448.0 and float(got[7, 0]) == 240.0 * 2.0 ** 120
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_the_types_largest_values_stay_finite(dtype):
+    info = torch.finfo(R.TYPES[dtype])
+    x = torch.tensor([info.max, info.min, 0.98 * info.max, 0.9 * info.max, -1.0, 0.5 * info.max])
+    x = x.to(R.TYPES[dtype]).repeat(2, 12)  # blocks of 32 and a part
+    want, byte = R.held8(x)
+    kept = M.checkpoint(x.to(DEV))
+    got = M.restore(kept).cpu()
+    assert torch.all(torch.isfinite(got)) and torch.equal(got.double(), want)
+    assert torch.all((got.double() - x.double()).abs() <= x.double().abs() / 16 + 2.0 ** -10 *
+                     torch.exp2(byte.double().max() - 127))
+    h = torch.cat([x, torch.ones_like(x)], 1).to(DEV)  # the lowest gate gives 0, and no gradient
+    y, kept = M.expert_act(h, "swiglu", checkpoint=True)
+    dh = M.expert_act_grad(kept, torch.ones_like(y))
+    assert torch.all(y[:, 1::6] == 0) and torch.all(dh[:, 1:72:6] == 0)
+    assert torch.all(torch.isfinite(dh))
+
+
+def test_outputs_of_another_type():
+    x = torch.randn(3, 40, device=DEV).bfloat16()
+    out = torch.empty(3, 40, device=DEV)
+    assert M.restore(M.checkpoint(x), out=out) is out
+    assert torch.equal(out.bfloat16(), M.restore(M.checkpoint(x)))
+    assert M.mx_restore(M.mx_quantize(x), out=out) is out
+    assert torch.equal(out.bfloat16(), M.mx_restore(M.mx_quantize(x)))
 
 
 ACTS = [("swiglu", 0.0), ("swiglu", 1.5), ("relu2", 0.0)]

@@ -95,6 +95,14 @@ def test_forward_without_a_backward_keeps_nothing():
     ids = torch.zeros(5, 1, dtype=torch.int32, device=DEV)
     w = torch.ones(5, 1, device=DEV)
     y, saved = layer.forward(x, ids, w, keep=False)
-    assert saved[2] is None and torch.equal(y, layer.forward(x, ids, w)[0])
+    again, kept = layer.forward(x, ids, w)
+    assert saved.kept is None and torch.equal(y, again)
+    with pytest.raises(ValueError):
+        layer.backward(saved, y)
+    layer.backward(kept, y)
+    with pytest.raises(ValueError):  # its rows hold their gradient now
+        layer.backward(kept, y)
+    with pytest.raises(ValueError):
+        M.dispatch(layer.fc1, M.sort_routes(ids, 4))
     with pytest.raises(ValueError):
         M.MxExperts(torch.randn(4, 64, 64, device=DEV), torch.randn(4, 64, 32, device=DEV), "relu2")
