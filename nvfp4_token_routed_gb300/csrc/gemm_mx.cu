@@ -15,21 +15,20 @@
 //     groups up for itself and takes items blockIdx.x, + gridDim.x, ...: no counter, no
 //     workspace, nothing to reset between launches.
 //   * Warp 0 loads weight tiles (TMA, 128-byte swizzle) and their scales, warp 10 row
-//     tiles (a box, two above 128 rows: a map for each height) and theirs; a stage is 256 values deep.
-//     A stage's scales are one contiguous piece of a panel (mx_quant.cu), which starts on
-//     an even row: 8 bytes a row, 16 a bulk copy's boundary.
+//     tiles (a box, two above 128 rows: a map for each height) and theirs; a stage is 256
+//     values deep.  A stage's scales are one contiguous piece of a panel (mx_quant.cu), which
+//     starts on an even row: 8 bytes a row, 16 a bulk copy's boundary.
 //   * Warps 6-9 move a stage's scales to TMEM: row r at lane r % 32, column r / 32, in
 //     all four lane quadrants; one 32-bit column holds 128 values' four scales, and the
 //     instruction takes two of them by its scale id.
 //   * Warp 1 issues the MMAs, warps 2-5 drain the accumulators (two, or four where no
 //     tile passes 64 rows): a lane holds one output feature, four lanes exchange so that
 //     every store is 8 bytes of one row.
+//   * Waits are bounded.  A CTA in which one runs out drains its copies and MMAs, frees
+//     TMEM, and writes NaN to the items that it leaves.
 // Measured (bf16 out): 128 rows on 64 experts N2048 D2048 22.2 us (0.97 of the copy rate,
 // 6686 GB/s), on 256 experts N4096 D7168 223 us (1.0); 2048 rows on 32 experts N4096 D7168 83
 // us (0.95).  Where rows bound it, see the pairs below.
-//
-//   * Waits are bounded.  A CTA in which one runs out drains its copies and MMAs, frees
-//     TMEM, and writes NaN to the items that it leaves.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -67,16 +66,17 @@ constexpr int kAccFull = 3 * kStages;
 constexpr int kAccEmpty = kAccFull + kAccs;
 constexpr int kDrain = kAccEmpty + kAccs;
 constexpr int kBars = kDrain + 1;
-constexpr int kFlagsOff = 8 * kBars;           // tmem slot, abort flag, stop flag, tile height
-constexpr int kWarpSumOff = kFlagsOff + 32;    // two ints a warp
+constexpr int kFlagsOff = 8 * kBars;           // tmem slot, abort flag, -, tile height
+constexpr int kWarpSumOff = kFlagsOff + 32;    // an int a warp
 constexpr int kGroupsOff = 512;                // first item [E + 1], first row [E + 1]
-static_assert(kWarpSumOff + 8 * (kThreads / 32) <= kGroupsOff, "barrier area");
+static_assert(kWarpSumOff + 4 * (kThreads / 32) <= kGroupsOff, "barrier area");
 
 // CTAs work in pairs from this many rows an expert and stages a row on (both measured, us,
 // single / pair): N4096 D7168, 8 experts of 192 rows 27.9 / 32.2, of 256 39.5 / 33.2, of 1024
 // 108 / 76; N7168 D2048, 32 experts of 256 77 / 64, of 1024 239 / 191; N2048 D1024, 8 experts
 // of 256 9.2 / 9.9, of 1024 19.4 / 19.6.  Few items leave pairs idle: one matrix N4096 D7168,
-// 256 rows 11.5 / 15.0 (16 items of pairs), 512 15.1 / 15.4, 1024 24.3 / 16.5.
+// 256 rows 11.5 / 15.0 (16 items of pairs), 512 15.1 / 15.4, 1024 24.3 / 16.5.  One weight
+// tile leaves half of a pair idle: R16384 D2048 N128 9.0 / 10.6, N256 12.0 / 10.5.
 constexpr int64_t kPairRows = 224;
 constexpr int kPairStages = 8;
 
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- geometry from the largest tile
   const int max16 = uniform(*s_max16);
   const int acc_stride = (max16 + 31) & ~31;
-  const int sfb_bytes = (8 * (acc_stride + 2) + 127) & ~127;  // a warp reads whole 32s, from an odd row on
+  const int sfb_bytes = (8 * (acc_stride + 2) + 127) & ~127;  // read in whole 32s, from an odd row on
   const int off_b = kABytes, off_sfa = off_b + max16 * kRowBytes, off_sfb = off_sfa + kSfaBytes;
   const int stage_bytes = (off_sfb + sfb_bytes + 1023) & ~1023;
   const int nbuf = max16 <= 64 ? 4 : 2;
@@ -388,10 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = walk.at(item);
       const int odd_w = (int)(((int64_t)it.e * a.N) & 1), odd_x = it.row0 & 1;
       for (int kb = 0; kb < a.kblocks; ++kb) {
-        if (!wait_or_leave(R.bar(kFull + stage), phase, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(kFull + stage), phase, abort_flag));
+        if (!ok) break;
         const uint32_t sb = smem_u32(stages + stage * stage_bytes);
         const uint32_t col = tmem + lane_q + sf_base + stage * slot_cols;
         const uint32_t sa = sb + off_sfa + 8 * (odd_w + lane), sx = sb + off_sfb + 8 * (odd_x + lane);
@@ -421,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1;
         }
       }
-      ok = __all_sync(0xFFFFFFFFu, ok);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -746,10 +743,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                              (int64_t)a.E * a.N - 1);
       const int odd_w = (int)(w0 & 1), odd_x = it.row0 & 1;
       for (int kb = 0; kb < a.kblocks; ++kb) {
-        if (!wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag));
+        if (!ok) break;
         const uint32_t sb = smem_u32(stages + stage * stage_bytes);
         const uint32_t col = tmem + lane_q + sf_base + stage * slot_cols;
         const uint32_t sa = sb + off_sfa + 8 * (odd_w + lane), sx = sb + off_sfb + 8 * (odd_x + lane);
@@ -782,7 +777,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         if (lane == 0) arrive_rank0(R.bar(pair::kSfReady + stage));
         advance();
       }
-      ok = __all_sync(0xFFFFFFFFu, ok);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (rank 0)
@@ -927,7 +921,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
 bool use_pairs(const MxGemmArgs& a, int sms) {
   const int64_t items = (int64_t)a.R / pair::kTileN * ((a.N + 255) / 256);
-  return a.kblocks >= kPairStages && a.R >= a.E * kPairRows && items >= sms / 4;
+  return a.N > 128 && a.kblocks >= kPairStages && a.R >= a.E * kPairRows && items >= sms / 4;
 }
 
 // Rows of the largest tile of pairs: 256; of a single matrix less where the items then come
