@@ -11,6 +11,8 @@
 
 namespace moe {
 
+constexpr int kMxPanel = 256;  // values of a row per scale panel, and per GEMM stage
+
 // ---------------------------------------------------------------- routes (routes.cu)
 struct SortArgs {
   int T, K, E, ids64;
@@ -38,13 +40,12 @@ struct RowArgs {
   int64_t ld_out;
   float* dw;           // combine's gradient: [T][K], or null
 };
-// The codes of a microscaled matrix move as rows of 2-byte words (dtype kBf16), its
-// scales by a launch of their own.
 cudaError_t launch_dispatch(const RowArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_combine(const RowArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_combine_grad(const RowArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_dispatch_scales(int T, int K, int panels, const int32_t* inv,
-                                   const uint8_t* in, uint8_t* out, cudaStream_t s);
+// A microscaled matrix of T rows of H values (a multiple of kMxPanel): codes in x and out.
+cudaError_t launch_dispatch_mx(const RowArgs& a, const uint8_t* scales, uint8_t* out_scales,
+                               cudaStream_t s);
 
 // ---------------------------------------------------------------- 8 bits (checkpoint.cu)
 struct KeepArgs {
@@ -65,7 +66,6 @@ cudaError_t launch_expert_act(const KeepArgs& a, int act, int dtype, cudaStream_
 cudaError_t launch_expert_act_grad(const KeepArgs& a, int act, int dtype, cudaStream_t s);
 
 // ---------------------------------------------------------------- microscaled FP4 (mx_quant.cu)
-constexpr int kMxPanel = 256;  // values of a row per scale panel, and per GEMM stage
 struct MxQuantArgs {
   int R, D, Dp;          // Dp = D rounded up to kMxPanel
   const int32_t* n_rows; // as KeepArgs

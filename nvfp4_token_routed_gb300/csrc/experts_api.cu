@@ -372,20 +372,14 @@ moe_status moe_nvfp4_mx_dispatch(const moe_mx* x, int32_t K, const int32_t* inv,
   if (!inv) return MOE_ERR_INVALID_ARG;
   if (!aligned(inv, 4)) return MOE_ERR_MISALIGNED;
   if ((st = (moe_status)device_status(nullptr)) != MOE_OK) return st;
-  const int Dp = padded(x->cols);
   RowArgs a = {};
   a.T = x->rows;
   a.K = K;
-  a.H = Dp / 4;  // 2-byte words of a row's codes
+  a.H = padded(x->cols);
   a.inv = inv;
   a.x = x->codes;
-  a.ld_x = a.ld_out = Dp / 4;
   a.out = out->codes;
-  cudaError_t e = launch_dispatch(a, kBf16, raw(stream));
-  if (e == cudaSuccess)
-    e = launch_dispatch_scales(x->rows, K, Dp / kMxPanel, inv, x->scales, out->scales,
-                               raw(stream));
-  return cuda_status(e);
+  return cuda_status(launch_dispatch_mx(a, x->scales, out->scales, raw(stream)));
 }
 
 moe_status moe_nvfp4_mx_product(const moe_mx* x, const moe_mx* w, int32_t E,

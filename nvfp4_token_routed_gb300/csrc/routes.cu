@@ -33,6 +33,7 @@ constexpr int kChunk = 2048;      // routes a block of many
 constexpr int kChunkWarps = 8;
 constexpr int kOneBlock = 4096;   // routes a block of a batch that one cluster sorts
 constexpr int kOneWarps = 32;
+constexpr int kSmall = 1024;      // routes of the only block of a small batch
 constexpr int kCluster = 8;       // blocks of the largest cluster: 32768 routes
 
 int64_t chunks_of(int64_t TK) { return (TK + kChunk - 1) / kChunk; }
@@ -118,6 +119,69 @@ __device__ __forceinline__ void rank_chunk(const SortArgs& a, int c0, int c1, ui
 __device__ __forceinline__ void write_route(const SortArgs& a, int i, int row) {
   a.inv[i] = row;
   if (row >= 0) a.perm[row] = i;
+}
+
+// The whole sort of a few routes by one block of 8 warps: no cluster, and a quarter of the
+// counters (128 routes of 256 experts 4.0 us, by the cluster's kernel 8.1).
+__global__ void __launch_bounds__(kChunkWarps * 32) sort_small_kernel(const SortArgs a) {
+  constexpr int kIters = kSmall / (kChunkWarps * 32);
+  constexpr int kPer = 1024 / (kChunkWarps * 32);  // experts a thread
+  __shared__ uint16_t cnt[kChunkWarps * 1024];
+  __shared__ int s_base[1024];
+  __shared__ int s_warp[kChunkWarps];
+  __shared__ int s_bad;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int TK = a.T * a.K;
+  if (threadIdx.x == 0) s_bad = 0;
+  pdl_trigger();
+  pdl_wait();
+  __syncthreads();
+  int key[kIters], rank[kIters];
+  bool bad;
+  rank_chunk<kChunkWarps, kIters>(a, 0, TK, cnt, key, rank, bad);
+  if (bad) s_bad = 1;
+  __syncthreads();
+  int tot[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    tot[i] = 0;
+    if (e < a.E) {
+      int c[kChunkWarps];
+#pragma unroll
+      for (int w = 0; w < kChunkWarps; ++w) c[w] = cnt[w * a.E + e];
+#pragma unroll
+      for (int w = 0; w < kChunkWarps; ++w) {
+        cnt[w * a.E + e] = (uint16_t)tot[i];
+        tot[i] += c[w];
+      }
+    }
+    sum += tot[i];
+  }
+  int n;
+  int off = block_exclusive(sum, s_warp, n);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    if (e < a.E) {
+      s_base[e] = off;
+      a.offsets[e] = off;
+    }
+    off += tot[i];
+  }
+  if (threadIdx.x == 0) {
+    a.offsets[a.E] = n;
+    if (a.status) a.status[kStatusFlags] = s_bad ? kFlagBadExpertId : 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kIters; ++j) {
+    const int i = warp * (32 * kIters) + 32 * j + lane;
+    if (i >= TK) continue;
+    const int e = key[j];
+    write_route(a, i, e < 0 ? -1 : s_base[e] + cnt[warp * a.E + e] + rank[j]);
+    if (i >= n) a.perm[i] = -1;
+  }
 }
 
 // Value of another block of the cluster at this block's shared address p.
@@ -365,21 +429,32 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a, int64_t 
   }
 }
 
-// Scale panels of a microscaled matrix: 8 bytes a row and panel.
-__global__ void __launch_bounds__(256) dispatch_scales_kernel(int T, int K, int panels,
-                                                              const int32_t* inv, const uint2* in,
-                                                              uint2* out) {
+// A microscaled matrix: a row's codes as vectors of 16 bytes, then its 8 bytes of each scale
+// panel, one thread each.
+__global__ void __launch_bounds__(256) dispatch_mx_kernel(const RowArgs a, int code_vecs,
+                                                          int panels, const uint2* scales,
+                                                          uint2* out_scales) {
   pdl_trigger();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t TK = (int64_t)T * K;
-  const int p = (int)(i / TK);
-  if (p >= panels) return;
-  const int64_t route = i - p * TK;
+  int v;
+  const int t = split_index((int64_t)blockIdx.x * 256 + threadIdx.x, code_vecs + panels, v);
+  if (t >= a.T) return;
   pdl_wait();
-  const int r = inv[route];
-  if ((unsigned)r >= (unsigned)TK) return;
-  const int64_t in_rows = (T + 1) & ~1, out_rows = (TK + 1) & ~int64_t(1);
-  out[p * out_rows + r] = in[p * in_rows + route / K];
+  if (v < code_vecs) {
+    const uint4 x = reinterpret_cast<const uint4*>(a.x)[(int64_t)t * code_vecs + v];
+    uint4* out = reinterpret_cast<uint4*>(a.out) + v;
+    for (int k = 0; k < a.K; ++k) {
+      const int r = route_row(a, (int64_t)t * a.K + k);
+      if (r >= 0) out[(int64_t)r * code_vecs] = x;
+    }
+    return;
+  }
+  const int64_t p = v - code_vecs;
+  const int64_t in_rows = (a.T + 1) & ~1, out_rows = ((int64_t)a.T * a.K + 1) & ~int64_t(1);
+  const uint2 x = scales[p * in_rows + t];
+  for (int k = 0; k < a.K; ++k) {
+    const int r = route_row(a, (int64_t)t * a.K + k);
+    if (r >= 0) out_scales[p * out_rows + r] = x;
+  }
 }
 
 template <int DT, int VB>
@@ -553,6 +628,8 @@ size_t sort_routes_ws_bytes(int64_t TK, int E) {
 
 cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t s) {
   const int64_t TK = (int64_t)a.T * a.K;
+  if (TK <= kSmall)
+    return launch_pdl(sort_small_kernel, dim3(1), dim3(kChunkWarps * 32), 0, s, a);
   if (TK <= kCluster * kOneBlock) {
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(sort_cluster_kernel),
@@ -601,11 +678,12 @@ cudaError_t launch_dispatch(const RowArgs& a, int dtype, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_dispatch_scales(int T, int K, int panels, const int32_t* inv,
-                                   const uint8_t* in, uint8_t* out, cudaStream_t s) {
-  return launch_pdl(dispatch_scales_kernel, dim3((unsigned)blocks_of((int64_t)T * K * panels)),
-                    dim3(256), 0, s, T, K, panels, inv, reinterpret_cast<const uint2*>(in),
-                    reinterpret_cast<uint2*>(out));
+cudaError_t launch_dispatch_mx(const RowArgs& a, const uint8_t* scales, uint8_t* out_scales,
+                               cudaStream_t s) {
+  const int code_vecs = a.H / 32, panels = a.H / kMxPanel;
+  const dim3 grid((unsigned)blocks_of((int64_t)a.T * (code_vecs + panels)));
+  return launch_pdl(dispatch_mx_kernel, grid, dim3(256), 0, s, a, code_vecs, panels,
+                    reinterpret_cast<const uint2*>(scales), reinterpret_cast<uint2*>(out_scales));
 }
 
 namespace {

@@ -40,7 +40,7 @@ def _check_plan(plan, ids, E):
 @pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 1024, 32), (5, 8, 8), (33, 60, 4), (512, 256, 8),
                                    (513, 256, 8), (128, 1000, 32), (4097, 1, 1), (4096, 384, 6),
                                    (5000, 1024, 3), (20000, 33, 10), (4096, 8, 8),
-                                   (4097, 8, 8), (32768, 64, 1), (32767, 40, 1), (32769, 2, 1)])
+                                   (4097, 8, 8), (128, 8, 8), (129, 1024, 8), (1025, 7, 1), (32768, 64, 1), (32767, 40, 1), (32769, 2, 1)])
 @pytest.mark.parametrize("empty", [0.0, 0.3])
 def test_sort(T, E, K, empty):
     for dtype in (torch.int32, torch.int64):
