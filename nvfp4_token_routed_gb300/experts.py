@@ -389,19 +389,21 @@ def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
 def _product_args(x, w, offsets, dtype, out, stream):
     if len(x.shape) != 2:
         raise ValueError("x: an MxTensor of rows [R, D]")
-    E, N = (w.shape[0], w.shape[1]) if len(w.shape) == 3 else (1, w.shape[0])
-    if E > 1 and offsets is None:
-        raise ValueError("offsets: needed for a stack of weights")
+    E, N = w.shape[:2] if len(w.shape) == 3 else (1, w.shape[0])
     like = x.on()
-    w.on()
+    if w.device != x.device:
+        raise ValueError(f"w: on device {w.device}, the rows on {x.device}")
     if out is not None:
         dtype = out.dtype
     dt = _DTYPE.get(dtype)
     if dt is None:
         raise ValueError("dtype: float32, bfloat16 or float16")
-    off = None if offsets is None else _arg(offsets, "offsets", (E + 1,), _I32, like)
+    if offsets is not None:
+        offsets = _arg(offsets, "offsets", (E + 1,), _I32, like)
+    elif E > 1:
+        raise ValueError("offsets: needed for a stack of weights")
     out, p, ld = _like(out, "out", (x.shape[0], N), dtype, like, stream)
-    return out, (x.c, w.c, E, off), (dt, p, ld, _raw(stream))
+    return out, (x.c, w.c, E, offsets), (dt, p, ld, _raw(stream))
 
 
 def mx_product(x, w, offsets=None, dtype=torch.bfloat16, out=None, stream=None):
