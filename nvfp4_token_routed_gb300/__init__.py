@@ -180,6 +180,8 @@ def lib():
                   "moe_nvfp4_profile_spans", "moe_nvfp4_forward_noalloc"]:
             getattr(L, f).restype = C.c_int
         _lib = L
+        from . import experts
+        experts._attach(L)
     return _lib
 
 

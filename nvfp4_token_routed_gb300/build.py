@@ -2,19 +2,23 @@
 
 Each .cu file under csrc/ compiles to its own object in parallel, then one
 shared library is linked next to this file.  No cmake, no torch extension
-machinery: the library has a plain C ABI (include/moe_nvfp4.h).
+machinery: the library has a plain C ABI (include/moe_nvfp4.h).  calls.c, a
+CPython extension that shortens the binding's ordinary calls, is compiled by
+the host compiler where Python's headers are installed.
 """
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_nvfp4.so")
+CALLS = os.path.join(PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,9 +38,27 @@ def _deps():
         os.path.join(ROOT, "include", "moe_nvfp4.h")]
 
 
+def build_calls():
+    """The CPython extension; without Python's headers the binding does without it."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write("calls.c not built: no Python.h\n")
+        return None
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-std=c11", "-O2", "-Wall", "-fPIC", "-shared", "-I", include, "-I",
+           os.path.join(ROOT, "include"), os.path.join(CSRC, "calls.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for calls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force=False, verbose=False):
     os.makedirs(OBJ, exist_ok=True)
     newest = max(os.path.getmtime(p) for p in _deps())
+    if force or not os.path.exists(CALLS) or os.path.getmtime(CALLS) < newest:
+        build_calls()
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB
     cc = nvcc()

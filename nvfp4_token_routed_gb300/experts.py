@@ -8,6 +8,7 @@ returned, else allocated on the stream of the call.  With `stream`, the inputs m
 on that stream.  Nothing is recorded for autograd: the gradients are what the *_grad calls
 return.
 """
+import ctypes as C
 from collections import namedtuple
 
 import torch
@@ -16,6 +17,37 @@ from . import (_DTYPE, _F32, _I32, _ID, _IDS64, ACT, MoeError, _arg, _check, _ma
                lib, moe_logits, moe_mx, padded)
 
 _U8 = (torch.uint8,)
+
+
+class _Interpreted:
+    """In place of the compiled calls (csrc/calls.c): no call is theirs."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+_fast = _Interpreted()
+_FAST = ["sort_routes", "dispatch", "combine", "combine_grad", "checkpoint", "restore",
+         "expert_act", "expert_act_grad", "mx_quantize", "mx_product"]
+
+
+def _attach(L):
+    """Give the compiled calls the library's entry points, and use them from now on: each
+    returns None for a call that is not an ordinary one, which then goes the interpreted way
+    with its checks and errors."""
+    global _fast
+    try:
+        from . import _calls
+    except ImportError:  # not built (no Python headers): every call is interpreted
+        return
+    if not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        return
+    _calls.attach((torch.Tensor, torch.empty, torch._C._cuda_getDevice,
+                   torch._C._cuda_getCurrentRawStream),
+                  (torch.float32, torch.bfloat16, torch.float16, torch.uint8, torch.int32,
+                   torch.int64), (MxTensor, Checkpoint, RoutePlan),
+                  tuple(C.cast(getattr(L, "moe_nvfp4_" + n), C.c_void_p).value for n in _FAST))
+    _fast = _calls
 
 
 def _like(t, name, shape, dtype, like, stream):
@@ -66,6 +98,10 @@ def sort_routes(topk_ids, E, plan=None, ws=None, stream=None):
     """Stable counting sort of the routes topk_ids [T, K] (int32 or int64, -1: empty slot) by
     expert: a RoutePlan.  Ids outside [-1, E) are empty slots too; with a workspace of the
     caller's (sort_routes_workspace) moe_nvfp4_read_status(ws) reports them."""
+    if plan is None and ws is None and stream is None:
+        r = _fast.sort_routes(topk_ids, E)
+        if r is not None:
+            return r
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids: one row of expert ids per token")
     dev = topk_ids.get_device()
@@ -97,6 +133,10 @@ def sort_routes(topk_ids, E, plan=None, ws=None, stream=None):
 def dispatch(x, plan, rows=None, stream=None):
     """Token rows x [T, H] to their routes' rows [T * K, H]; x may be an MxTensor.  Rows behind
     the last route are left as they were (a new tensor's: undefined)."""
+    if stream is None:
+        r = _fast.dispatch(x, plan, rows)
+        if r is not None:
+            return r
     T, K = plan.inv.shape
     if x.shape[0] != T:
         raise ValueError(f"x: expected {T} rows, got {x.shape[0]}")
@@ -119,6 +159,10 @@ def dispatch(x, plan, rows=None, stream=None):
 
 def combine(rows, plan, topk_w=None, out=None, stream=None):
     """Route rows [T * K, H] back to their tokens [T, H], times topk_w fp32 [T, K] (None: 1)."""
+    if out is None and stream is None:
+        r = _fast.combine(rows, plan, topk_w)
+        if r is not None:
+            return r
     m = _matrix(rows, "rows")
     T, K = plan.inv.shape
     out, p, ld = _like(out, "out", (T, rows.shape[1]), rows.dtype, rows, stream)
@@ -136,6 +180,10 @@ def dispatch_grad(drows, plan, dx=None, stream=None):
 def combine_grad(rows, plan, topk_w, dout, drows=None, d_topk_w=None, stream=None):
     """Gradients of combine: (drows [T * K, H], d_topk_w [T, K] fp32).  drows may be the rows
     tensor itself; its rows behind the last route are left as they were."""
+    if d_topk_w is None and stream is None:
+        r = _fast.combine_grad(rows, plan, topk_w, dout, drows)
+        if r is not None:
+            return r
     m = _matrix(rows, "rows")
     T, K = plan.inv.shape
     if dout.shape != (T, rows.shape[1]) or dout.dtype != rows.dtype:
@@ -230,6 +278,10 @@ class Checkpoint(_Held):
 
 def checkpoint(x, kept=None, n_rows=None, stream=None):
     """Rows x [R, D] in 8 bits (E4M3, a power of two per 32 values): a Checkpoint."""
+    if kept is None and n_rows is None and stream is None:
+        r = _fast.checkpoint(x)
+        if r is not None:
+            return r
     m = _matrix(x, "x")
     R, D = x.shape
     if kept is None:
@@ -244,6 +296,10 @@ def checkpoint(x, kept=None, n_rows=None, stream=None):
 
 def restore(kept, dtype=None, out=None, n_rows=None, stream=None):
     """The rows that checkpoint kept, of `dtype` (None: the type they had), or of out's."""
+    if dtype is None and out is None and n_rows is None and stream is None:
+        r = _fast.restore(kept)
+        if r is not None:
+            return r
     if kept.act is not None:
         raise ValueError("kept: an activation's input is read by expert_act_grad")
     R, D = kept.rows, kept.cols
@@ -262,6 +318,10 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
     """The experts' activation of FC1 rows h: [R, 2I] = [gate | up] ("swiglu") or [R, I]
     ("relu2") -> y [R, I].  With checkpoint (or `kept`, a Checkpoint to fill) h is kept in 8
     bits for expert_act_grad: (y, kept), else y."""
+    if y is None and kept is None and n_rows is None and stream is None:
+        r = _fast.expert_act(h, act, swiglu_limit, checkpoint)
+        if r is not None:
+            return r
     if act not in ACT:
         raise ValueError(f"act: one of {sorted(ACT)}")
     m = _matrix(h, "h")
@@ -286,6 +346,10 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
 def expert_act_grad(kept, dy, dh=None, n_rows=None, stream=None):
     """Gradient of expert_act at the values that `kept` holds: dy [R, I] -> dh [R, 2I] (swiglu)
     or [R, I], of dy's type."""
+    if dh is None and n_rows is None and stream is None:
+        r = _fast.expert_act_grad(kept, dy)
+        if r is not None:
+            return r
     if kept.act is None:
         raise ValueError("kept: expected what expert_act kept")
     m = _matrix(dy, "dy")
@@ -304,12 +368,16 @@ class MxTensor(_Held):
     """A matrix [R, D], or a stack [E, N, D], in microscaled FP4: codes uint8 [rows, Dp / 2] and
     scales uint8 [Dp / 256, Rp, 8] (Dp: D rounded up to 256, rows: R or E * N, Rp: rows rounded
     up to even; layouts in include/moe_nvfp4.h)."""
-    __slots__ = ("shape", "c")
+    __slots__ = ("shape", "raw")  # raw: the bytes of its moe_mx
 
     def __init__(self, codes, scales, shape):
         self.shape = shape = tuple(shape)
         p, q = self._set(codes, scales)
-        self.c = moe_mx(p, q, _mx_rows(shape), shape[-1])
+        self.raw = bytes(moe_mx(p, q, _mx_rows(shape), shape[-1]))
+
+    @property
+    def c(self):
+        return moe_mx.from_buffer_copy(self.raw)
 
     @classmethod
     def empty(cls, shape, like, stream=None):
@@ -318,7 +386,7 @@ class MxTensor(_Held):
         rows, d = _mx_rows(shape), shape[-1]
         dp = (d + 255) & -256
         p, q = t._alloc(rows * dp >> 1, (rows + 1 & -2) * dp >> 5, like, stream)
-        t.c = moe_mx(p, q, rows, d)
+        t.raw = bytes(moe_mx(p, q, rows, d))
         return t
 
     def _shapes(self):
@@ -344,6 +412,10 @@ def _mx_out(out, shape, x, stream):
 def mx_quantize(x, out=None, n_rows=None, stream=None):
     """x [R, D] (rows may be strided) or [E, N, D] (contiguous) in microscaled FP4 (E2M1, a power
     of two per 32 values of a row): an MxTensor."""
+    if out is None and n_rows is None and stream is None:
+        r = _fast.mx_quantize(x)
+        if r is not None:
+            return r
     shape = tuple(x.shape)
     if len(shape) == 3:
         if not x.is_contiguous():
@@ -410,6 +482,10 @@ def mx_product(x, w, offsets=None, dtype=torch.bfloat16, out=None, stream=None):
     """x [R, D] times the weights of each row's expert: w [E, N, D] with offsets int32 [E + 1]
     (RoutePlan.offsets), or one matrix [N, D].  -> [R, N] of `dtype`; rows outside the groups
     are left as they were."""
+    if out is None and stream is None:
+        r = _fast.mx_product(x, w, offsets, dtype)
+        if r is not None:
+            return r
     out, args, rest = _product_args(x, w, offsets, dtype, out, stream)
     _check(lib().moe_nvfp4_mx_product(*args, *rest), "moe_nvfp4_mx_product")
     return out

@@ -174,6 +174,33 @@ def test_product_checks(lib):
     assert lib.moe_nvfp4_selftest_product_timeout(x, w, 2, P, -1, 0, P, 8, None) == 1
 
 
+def test_compiled_calls_take_no_call_that_is_not_theirs(lib):
+    """They answer None, with no error left, to whatever is not an ordinary call."""
+    from nvfp4_token_routed_gb300 import experts
+    _calls = pytest.importorskip("nvfp4_token_routed_gb300._calls")
+    assert experts._fast is _calls
+    x, ids = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    plan = M.RoutePlan(torch.zeros(4, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), ids)
+    q = M.MxTensor(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(1, 4, 8, dtype=torch.uint8),
+                   (4, 8))
+    kept = M.Checkpoint(torch.zeros(4, 1, 32, dtype=torch.uint8),
+                        torch.zeros(4, 1, 1, dtype=torch.uint8), 8, x.dtype)
+    odd = [x, ids, plan, q, kept, None, 3, "swiglu", (1, 2, 3), object(), x[0], x.t(), [x]]
+    arity = {"sort_routes": 2, "dispatch": 3, "combine": 3, "combine_grad": 5, "checkpoint": 1,
+             "restore": 1, "expert_act": 4, "expert_act_grad": 2, "mx_quantize": 1,
+             "mx_product": 4}
+    for name, n in arity.items():
+        f = getattr(_calls, name)
+        assert f() is None and f(*odd[:7]) is None
+        for i in range(len(odd)):
+            for j in range(len(odd)):
+                args = [odd[i], odd[j]] + odd[2:5]
+                assert f(*args[:n]) is None, (name, i, j)
+    for bad in ((), (1,), ((1, 2, 3, 4), (1,) * 6, (1, 2, 3), (0,) * 10)):
+        with pytest.raises(TypeError):
+            _calls.attach(*bad)
+
+
 def test_binding_refuses_cpu_tensors():
     x, ids = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
     plan = M.RoutePlan(torch.zeros(4, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), ids)
