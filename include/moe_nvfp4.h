@@ -636,7 +636,8 @@ moe_status moe_nvfp4_mx_dispatch(const moe_mx* x, int32_t K, const int32_t* inv,
  *   out[r][n] = sum_d x[r][d] * w[e * N + n][d], e the expert with offsets[e] <= r <
  *   offsets[e+1]; w->rows = E * N, w->cols = x->cols.
  * offsets: device [E+1] ascending, 1 <= E <= 1024; or NULL with E == 1: every row.  Rows
- * outside all groups are left as they were.  1 <= N <= 65536.  out: row stride ld_out >= N,
+ * outside all groups are left as they were.  1 <= N <= 65536, E * ceil(x->rows / 192) *
+ * ceil(N / 128) < 2^31 (numbers of tiles, whatever offsets holds).  out: row stride ld_out >= N,
  * `dtype`; accumulated in fp32 on the tensor cores, rounded once.  A row's bits do not
  * depend on the other rows.  Waits inside the kernel are bounded (2 s); should one run out,
  * what is left unfinished gets NaN. */

@@ -99,6 +99,10 @@ moe_status product_impl(const moe_mx* x, const moe_mx* w, int32_t E, const int32
     return MOE_ERR_INVALID_ARG;
   const int N = w->rows / E;
   if (E > 1024 || N > kMaxHidden) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // offsets that do not ascend may put all rows into each of the groups: the kernels count
+  // their tiles in 32 bits
+  if (((int64_t)x->rows + 191) / 192 * ((N + 127) / 128) * E > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (ld_out < N) return MOE_ERR_INVALID_ARG;
   if (x->rows == 0) return MOE_OK;
   if ((st = check_ptr(out, dtype)) != MOE_OK) return st;

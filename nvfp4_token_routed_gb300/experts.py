@@ -559,7 +559,11 @@ class MxExperts:
         """dy [T, H] -> (dx [T, H], d_topk_w [T, K] fp32), once for each forward."""
         plan, rows, kept, topk_w = saved.take()
         n, dt = plan.n_rows, dy.dtype
-        drows, dw = combine_grad(rows, plan, topk_w, dy, drows=rows, stream=stream)
+        try:
+            drows, dw = combine_grad(rows, plan, topk_w, dy, drows=rows, stream=stream)
+        except Exception:  # refused (dy's type, shape or device): the rows are as they were
+            saved.rows = rows
+            raise
         da = mx_product(mx_quantize(drows, n_rows=n, stream=stream), self.fc2_t, plan.offsets, dt,
                         stream=stream)
         dh = expert_act_grad(kept, da, n_rows=n, stream=stream)

@@ -166,7 +166,9 @@ def test_product_checks(lib):
                      (dict(w=_mx(rows=16, cols=65)), 1), (dict(w=_mx(0, 64)), 1), (dict(ld=7), 1),
                      (dict(out=None), 1), (dict(out=P + 2), 3), (dict(off=P + 2), 3),
                      (dict(x=_mx(codes=None)), 1), (dict(w=_mx(rows=16, scales=P + 8)), 3),
-                     (dict(w=_mx(rows=2050), E=1025), 2), (dict(w=_mx(rows=65537), E=1, ld=65537), 2)):
+                     (dict(w=_mx(rows=2050), E=1025), 2), (dict(w=_mx(rows=65537), E=1, ld=65537), 2),
+                     (dict(x=_mx(rows=1 << 26), w=_mx(rows=1 << 16), E=128, ld=512, out=P + 2), 3),
+                     (dict(x=_mx(rows=1 << 26), w=_mx(rows=1 << 24), E=1024, ld=1 << 14), 2)):
         assert call(**kw) == code, kw
     assert call(x=_mx(0, 64, None, None), out=None) == 0
     assert lib.moe_nvfp4_mx_product(None, _mx(), 1, None, 0, P, 8, None) == 1

@@ -149,6 +149,23 @@ def test_rows_outside_the_groups_and_between_rows():
     assert torch.equal(M.mx_product(q, qw, bad), M.mx_product(q, qw, good))
 
 
+@pytest.mark.parametrize("rows,N,D,offsets", [(50, 40, 256, [3, 20, 5, 33]),
+                                              (2048, 1300, 2048, [100, 1500, 200, 2000])])
+def test_offsets_that_do_not_ascend(rows, N, D, offsets):
+    """Rows of one group alone are its product, and no row is written outside the groups."""
+    x, _ = _values(rows, D, "bf16", N)
+    w = torch.randn(3, N, D, generator=torch.Generator().manual_seed(D)) / D ** 0.5
+    q, qw = M.mx_quantize(x.to(DEV)), M.mx_quantize(w.to(DEV))
+    out = torch.full((rows + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    M.mx_product(q, qw, torch.tensor(offsets, dtype=torch.int32, device=DEV), out=out[1:-1])
+    a, b, c, d = offsets
+    first, last = (M.mx_product(q, qw, torch.tensor(o, dtype=torch.int32, device=DEV))
+                   for o in ([a, b, b, b], [c, c, c, d]))
+    got = out[1:-1]
+    assert torch.equal(got[a:c], first[a:c]) and torch.equal(got[b:d], last[b:d])
+    assert torch.all(out[:a + 1] == 7.0) and torch.all(out[d + 1:] == 7.0)
+
+
 def test_a_row_does_not_depend_on_its_batch():
     x, _ = _values(300, 1024, "bf16", 6)
     w = torch.randn(2, 200, 1024) / 32

@@ -99,6 +99,8 @@ def test_forward_without_a_backward_keeps_nothing():
     assert saved.kept is None and torch.equal(y, again)
     with pytest.raises(ValueError):
         layer.backward(saved, y)
+    with pytest.raises(ValueError):  # refused before the saved rows are touched
+        layer.backward(kept, y.half())
     layer.backward(kept, y)
     with pytest.raises(ValueError):  # its rows hold their gradient now
         layer.backward(kept, y)
