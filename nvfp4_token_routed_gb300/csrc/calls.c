@@ -1,7 +1,7 @@
 /* calls.c -- the routed-row calls of the binding in their ordinary form, as a CPython
  * extension: new outputs, the current stream, every row.  A call of a few microseconds of GPU
- * time otherwise waits for the interpreter: sort_routes and dispatch of 16 tokens take 17 us
- * here, 22 interpreted; what is left is allocation and launch.
+ * time otherwise waits for the interpreter: sort_routes and dispatch of 16 tokens take 10.5 us
+ * here, 22 interpreted; what is left is allocation (1.2 us each) and launch (2 us).
  *
  * Each function takes the positional arguments of its namesake in experts.py and returns its
  * result, or None where the call is not an ordinary one: other types, shapes, devices or
@@ -38,7 +38,8 @@ typedef moe_status (*product_fn)(const moe_mx*, const moe_mx*, int32_t, const in
 
 /* Set once by attach() and kept. */
 static struct {
-  PyObject *tensor, *empty, *get_device, *get_stream; /* torch.Tensor, functions */
+  PyObject *tensor, *empty, *get_device, *get_stream; /* torch.Tensor, functions; empty: of
+                                                         (size, stride, type), current device */
   PyObject *f32, *bf16, *f16, *u8, *i32, *i64;        /* torch types */
   PyObject *mx, *kept, *plan;                         /* MxTensor, Checkpoint, RoutePlan */
   void* fn[10];
@@ -47,7 +48,7 @@ enum { SORT, DISPATCH, COMBINE, COMBINE_GRAD, CHECKPOINT, RESTORE, ACT, ACT_GRAD
 
 static PyObject *s_dtype, *s_shape, *s_stride, *s_device_of, *s_data_ptr, *s_contiguous;
 static PyObject *s_raw, *s_codes, *s_scales, *s_buf, *s_cut, *s_device, *s_rows, *s_cols, *s_act;
-static PyObject *s_halves, *s_limit, *s_c, *kw_empty, *empty_tuple;
+static PyObject *s_halves, *s_limit, *s_c, *empty_tuple;
 
 /* None, with any error of a failed look-up cleared. */
 static PyObject* not_ordinary(void) {
@@ -152,22 +153,22 @@ static int arg_of(PyObject* t, int64_t* dev, PyObject* type0, PyObject* type1, i
 }
 
 /* A new tensor on the current device and its address. */
-static PyObject* new_tensor(int n, const int64_t* shape, PyObject* type, int64_t dev, void** p) {
-  PyObject* size = n == 1 ? PyLong_FromLongLong(shape[0]) : Py_BuildValue("(LL)", shape[0], shape[1]);
-  PyObject* d = PyLong_FromLongLong(dev);
-  PyObject* args[3] = {size, type, d};
-  PyObject* t = size && d ? PyObject_Vectorcall(g.empty, args, 1, kw_empty) : NULL;
+static PyObject* new_tensor(int n, const int64_t* shape, PyObject* type, void** p) {
+  PyObject* size = n == 1 ? Py_BuildValue("(L)", shape[0]) : Py_BuildValue("(LL)", shape[0], shape[1]);
+  PyObject* stride = n == 1 ? Py_BuildValue("(i)", 1) : Py_BuildValue("(Li)", shape[1], 1);
+  PyObject* args[3] = {size, stride, type};
+  PyObject* t = size && stride ? PyObject_Vectorcall(g.empty, args, 3, NULL) : NULL;
   Py_XDECREF(size);
-  Py_XDECREF(d);
+  Py_XDECREF(stride);
   if (t && !address(t, p)) Py_CLEAR(t);
   return t;
 }
 /* Codes and scales of an MxTensor or Checkpoint, cut from one new buffer. */
-static PyObject* new_buffer(int64_t codes, int64_t scales, int64_t dev, uint8_t** p, int64_t* at) {
+static PyObject* new_buffer(int64_t codes, int64_t scales, uint8_t** p, int64_t* at) {
   void* q;
   *at = (codes + 255) & ~(int64_t)255;
   const int64_t n = *at + scales;
-  PyObject* t = new_tensor(1, &n, g.u8, dev, &q);
+  PyObject* t = new_tensor(1, &n, g.u8, &q);
   *p = (uint8_t*)q;
   return t;
 }
@@ -258,7 +259,7 @@ static PyObject* new_kept(int64_t rows, int64_t cols, int halves, PyObject* type
   const int64_t blocks = rows * halves * ((cols + 31) / 32);
   int64_t at;
   uint8_t* p;
-  PyObject* buf = new_buffer(32 * blocks, blocks, dev, &p, &at);
+  PyObject* buf = new_buffer(32 * blocks, blocks, &p, &at);
   PyObject* k = buf ? new_object(g.kept) : NULL;
   if (k && !(set_held(k, buf, 32 * blocks, at, dev) && set_steal(k, s_rows, PyLong_FromLongLong(rows)) &&
              set_steal(k, s_cols, PyLong_FromLongLong(cols)) && PyObject_SetAttr(k, s_dtype, type) == 0 &&
@@ -297,7 +298,7 @@ static PyObject* matrix_out(PyObject* given, int64_t rows, int64_t cols, int dty
   if (given == Py_None) {
     const int64_t sh[2] = {rows, cols};
     *ld = cols;
-    return new_tensor(2, sh, type_object(dtype), *dev, p);
+    return new_tensor(2, sh, type_object(dtype), p);
   }
   moe_rows m;
   if (!rows_of(given, dev, &m) || m.rows != rows || m.cols != cols || m.dtype != dtype) return NULL;
@@ -329,9 +330,9 @@ static PyObject* sort_routes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   ORDINARY(sh[0] >= 1 && sh[0] <= 32768 && sh[1] >= 1 && sh[1] <= 32 && sh[0] * sh[1] <= 32768 &&
            arg_of(a[0], &dev, g.i32, g.i64, 2, sh, &ids, &is64) && stream_of(dev, &s));
   const int64_t no = E + 1, np = sh[0] * sh[1];
-  PyObject* offsets = new_tensor(1, &no, g.i32, dev, &po);
-  PyObject* perm = offsets ? new_tensor(1, &np, g.i32, dev, &pp) : NULL;
-  PyObject* inv = perm ? new_tensor(2, sh, g.i32, dev, &pi) : NULL;
+  PyObject* offsets = new_tensor(1, &no, g.i32, &po);
+  PyObject* perm = offsets ? new_tensor(1, &np, g.i32, &pp) : NULL;
+  PyObject* inv = perm ? new_tensor(2, sh, g.i32, &pi) : NULL;
   PyObject* plan = NULL;
   if (inv && CALL(SORT, sort_fn)((int32_t)sh[0], (int32_t)sh[1], (int32_t)E, ids, is64, po, pp, pi,
                                  NULL, 0, s) == MOE_OK) {
@@ -385,7 +386,7 @@ static PyObject* combine_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) 
            x.rows == T * K && stream_of(dev, &s));
   const int64_t sh[2] = {T, K};
   PyObject* drows = matrix_out(a[4], x.rows, x.cols, x.dtype, &dev, &p, &ld);
-  PyObject* dw = drows ? new_tensor(2, sh, g.f32, dev, &pw) : NULL;
+  PyObject* dw = drows ? new_tensor(2, sh, g.f32, &pw) : NULL;
   PyObject* r = NULL;
   if (dw && CALL(COMBINE_GRAD, combine_grad_fn)(&x, (int32_t)T, (int32_t)K, inv, w, d.data, d.ld, p,
                                                 ld, pw, s) == MOE_OK)
@@ -425,7 +426,7 @@ static PyObject* restore(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Py_DECREF(dt);
   ORDINARY(type >= 0);
   const int64_t sh[2] = {k.rows, k.cols};
-  PyObject* out = new_tensor(2, sh, type_object(type), dev, &p);
+  PyObject* out = new_tensor(2, sh, type_object(type), &p);
   if (out) {
     const moe_rows m = {p, k.cols, (int32_t)k.rows, (int32_t)k.cols, type};
     if (CALL(RESTORE, restore_fn)(k.codes, k.scales, &m, NULL, s) != MOE_OK) Py_CLEAR(out);
@@ -446,7 +447,7 @@ static PyObject* expert_act(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int keep = PyObject_IsTrue(a[3]);
   ORDINARY(act >= 0 && !PyErr_Occurred() && keep >= 0 && h.cols % halves == 0);
   const int64_t sh[2] = {h.rows, h.cols / halves};
-  PyObject* y = new_tensor(2, sh, type_object(h.dtype), dev, &p);
+  PyObject* y = new_tensor(2, sh, type_object(h.dtype), &p);
   PyObject* k = y && keep ? new_kept(sh[0], sh[1], halves, type_object(h.dtype), a[1], limit, dev,
                                      &codes, &scales)
                           : NULL;
@@ -469,7 +470,7 @@ static PyObject* expert_act_grad(PyObject* self, PyObject* const* a, Py_ssize_t 
   ORDINARY(n == 2 && kept_of(a[0], &dev, &k) && k.act >= 0 && rows_of(a[1], &dev, &dy) &&
            dy.rows == k.rows && dy.cols == k.cols && stream_of(dev, &s));
   const int64_t sh[2] = {dy.rows, dy.cols * k.halves};
-  PyObject* dh = new_tensor(2, sh, type_object(dy.dtype), dev, &p);
+  PyObject* dh = new_tensor(2, sh, type_object(dy.dtype), &p);
   if (dh && CALL(ACT_GRAD, act_grad_fn)(k.codes, k.scales, k.act, (float)k.limit, &dy, p, sh[1],
                                         NULL, s) != MOE_OK)
     Py_CLEAR(dh);
@@ -484,7 +485,7 @@ static PyObject* mx_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   moe_stream_t s;
   ORDINARY(n == 1 && rows_of(a[0], &dev, &x) && stream_of(dev, &s));
   const int64_t dp = ((int64_t)x.cols + 255) & ~(int64_t)255, codes = x.rows * dp / 2;
-  PyObject* buf = new_buffer(codes, (((int64_t)x.rows + 1) & ~(int64_t)1) * dp / 32, dev, &p, &at);
+  PyObject* buf = new_buffer(codes, (((int64_t)x.rows + 1) & ~(int64_t)1) * dp / 32, &p, &at);
   PyObject* q = NULL;
   if (buf) {
     moe_mx m;
@@ -526,7 +527,7 @@ static PyObject* mx_product(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   ORDINARY(a[2] == Py_None ? E == 1 : arg_of(a[2], &dev, g.i32, g.i32, 1, &groups, &off, NULL));
   const int64_t sh[2] = {sx[0], N};
   ORDINARY(sx[0] >= 1);
-  PyObject* out = new_tensor(2, sh, a[3], dev, &p);
+  PyObject* out = new_tensor(2, sh, a[3], &p);
   if (out && CALL(PRODUCT, product_fn)(&x, &w, (int32_t)E, off, type, p, N, s) != MOE_OK)
     Py_CLEAR(out);
   return out ? out : not_ordinary();
@@ -583,7 +584,6 @@ PyMODINIT_FUNC PyInit__calls(void) {
                {&s_limit, "swiglu_limit"}, {&s_c, "c"}};
   for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
     if (!(*names[i].name = PyUnicode_InternFromString(names[i].text))) return NULL;
-  if (!(kw_empty = Py_BuildValue("(ss)", "dtype", "device")) || !(empty_tuple = PyTuple_New(0)))
-    return NULL;
+  if (!(empty_tuple = PyTuple_New(0))) return NULL;
   return PyModule_Create(&module);
 }

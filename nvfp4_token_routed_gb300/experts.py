@@ -42,7 +42,7 @@ def _attach(L):
         return
     if not hasattr(torch._C, "_cuda_getCurrentRawStream"):
         return
-    _calls.attach((torch.Tensor, torch.empty, torch._C._cuda_getDevice,
+    _calls.attach((torch.Tensor, _empty, torch._C._cuda_getDevice,
                    torch._C._cuda_getCurrentRawStream),
                   (torch.float32, torch.bfloat16, torch.float16, torch.uint8, torch.int32,
                    torch.int64), (MxTensor, Checkpoint, RoutePlan),
@@ -50,10 +50,27 @@ def _attach(L):
     _fast = _calls
 
 
+def _empty_by_torch(size, stride, dtype):
+    return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+# New tensors on the current device by (size, stride, dtype).  After a launch torch.empty takes
+# 4.2 us on the host and the allocation that torch's compiled programs make 1.2.
+_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
+                 "_empty_strided_cuda", _empty_by_torch)
+
+
+def _new(shape, dtype, like):
+    """A new tensor of one or two dimensions on like's device."""
+    if like.get_device() != torch._C._cuda_getDevice():
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _empty(tuple(shape), (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+
+
 def _like(t, name, shape, dtype, like, stream):
     """An output matrix: `t` (rows may be strided) or a new one; its address and row stride."""
     if t is None:
-        t = (torch.empty(shape, dtype=dtype, device=like.device) if stream is None
+        t = (_new(shape, dtype, like) if stream is None
              else _out(None, name, shape, dtype, like, stream))
         return t, t.data_ptr(), shape[1]
     if t.shape != torch.Size(shape) or t.dtype != dtype:
@@ -215,7 +232,7 @@ class _Held:
     def _alloc(self, n_codes, n_scales, like, stream):
         at = (n_codes + 255) & -256
         self._buf = buf = (
-            torch.empty(at + n_scales, dtype=torch.uint8, device=like.device) if stream is None
+            _new((at + n_scales,), torch.uint8, like) if stream is None
             else _out(None, "codes", at + n_scales, torch.uint8, like, stream))
         self._codes = self._scales = None
         self._cut = n_codes, at

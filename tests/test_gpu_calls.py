@@ -67,6 +67,23 @@ def test_the_same_results(compiled, monkeypatch, seed, dtype):
         assert torch.equal(a, b)
 
 
+def test_without_the_short_allocation(compiled, monkeypatch):
+    """Both ways allocate by torch.empty_strided where torch lacks its shorter form."""
+    c = _case(1)
+    want = _all(c)
+    with monkeypatch.context() as m:
+        m.setattr(experts, "_empty", experts._empty_by_torch)
+        experts._attach(M.lib())
+        fast = _all(c)
+        m.setattr(experts, "_fast", experts._Interpreted())
+        slow = _all(c)
+    experts._attach(M.lib())
+    assert experts._fast is compiled
+    for a, b, d in zip(want, fast, slow):
+        assert torch.equal(a, b) and torch.equal(a, d)
+        assert a.stride() == b.stride() == d.stride()
+
+
 def test_the_same_attributes(compiled, monkeypatch):
     c = _case(0)
 
@@ -135,7 +152,7 @@ def test_references_and_memory(compiled):
     _, k = M.expert_act(c["h"], "swiglu", checkpoint=True)
     watched = [c["x"], c["rows"], c["w"], c["dout"], c["h"], c["ids"], *plan, plan, q, w, k,
                q.shape, k.c, torch.bfloat16, torch.uint8, M.MxTensor, M.Checkpoint, M.RoutePlan,
-               torch.empty]
+               experts._empty]
 
     def some(n):
         for _ in range(n):
