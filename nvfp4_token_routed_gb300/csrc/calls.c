@@ -3,8 +3,8 @@
  * time otherwise waits for the interpreter: sort_routes and dispatch of 16 tokens take 10.5 us
  * here, 22 interpreted; what is left is allocation (1.2 us each) and launch (2 us).
  *
- * Each function takes the positional arguments of its namesake in experts.py and returns its
- * result, or None where the call is not an ordinary one: other types, shapes, devices or
+ * Each function takes the positional arguments of its namesake in experts.py (mx_raw: of
+ * MxTensor) and returns its result, or None where the call is not an ordinary one: other types, shapes, devices or
  * layouts than expected, or a status other than MOE_OK.  experts.py then goes its own way,
  * which makes every check and raises every error; so nothing here reports one. */
 #define PY_SSIZE_T_CLEAN
@@ -133,10 +133,10 @@ static int rows_of(PyObject* t, int64_t* dev, moe_rows* m) {
   m->cols = (int32_t)sh[1];
   return 1;
 }
-/* A contiguous tensor of one of two types (0 or 1 in *which) and of a shape. */
+/* A contiguous tensor of one of two types (0 or 1 in *which) and of a shape of up to 3 sizes. */
 static int arg_of(PyObject* t, int64_t* dev, PyObject* type0, PyObject* type1, int n,
                   const int64_t* shape, void** p, int* which) {
-  int64_t sh[2];
+  int64_t sh[3];
   if (!on_device(t, dev)) return 0;
   PyObject* dt = PyObject_GetAttr(t, s_dtype);
   if (!dt) return 0;
@@ -504,6 +504,32 @@ static PyObject* mx_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return q ? q : not_ordinary();
 }
 
+/* The moe_mx of an MxTensor of these codes, scales and shape, as bytes. */
+static PyObject* mx_raw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int64_t dev = -1, sh[3];
+  void *codes, *scales;
+  ORDINARY(n == 3 && PyTuple_Check(a[2]));
+  const int dims = (int)PyTuple_GET_SIZE(a[2]);
+  ORDINARY(dims == 2 || dims == 3);
+  Py_INCREF(a[2]);
+  ORDINARY(sizes(a[2], dims, sh)); /* takes the reference */
+  const int64_t cols = sh[dims - 1], e = dims == 3 ? sh[0] : 1, each = sh[dims - 2];
+  ORDINARY(cols >= 1 && cols <= INT32_MAX && e >= 1 && e <= INT32_MAX && each >= 1 &&
+           each <= INT32_MAX / e);
+  const int64_t rows = e * each, dp = (cols + 255) & ~(int64_t)255;
+  const int64_t c[2] = {rows, dp / 2}, s[3] = {dp / 256, (rows + 1) & ~(int64_t)1, 8};
+  ORDINARY(arg_of(a[0], &dev, g.u8, g.u8, 2, c, &codes, NULL) &&
+           arg_of(a[1], &dev, g.u8, g.u8, 3, s, &scales, NULL));
+  moe_mx m;
+  memset(&m, 0, sizeof(m));
+  m.codes = codes;
+  m.scales = scales;
+  m.rows = (int32_t)rows;
+  m.cols = (int32_t)cols;
+  PyObject* raw = PyBytes_FromStringAndSize((const char*)&m, sizeof(m));
+  return raw ? raw : not_ordinary();
+}
+
 /* mx_product(x, w, offsets, dtype) */
 static PyObject* mx_product(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t dev = -1, sx[2], sw[3];
@@ -567,6 +593,7 @@ static PyMethodDef methods[] = {{"attach", attach, METH_VARARGS, NULL},
                                 FAST(expert_act),
                                 FAST(expert_act_grad),
                                 FAST(mx_quantize),
+                                FAST(mx_raw),
                                 FAST(mx_product),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods,

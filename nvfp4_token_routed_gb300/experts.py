@@ -389,6 +389,11 @@ class MxTensor(_Held):
 
     def __init__(self, codes, scales, shape):
         self.shape = shape = tuple(shape)
+        raw = _fast.mx_raw(codes, scales, shape)
+        if raw is not None:
+            self.device, self.raw = codes.get_device(), raw
+            self._codes, self._scales, self._buf, self._cut = codes, scales, None, None
+            return
         p, q = self._set(codes, scales)
         self.raw = bytes(moe_mx(p, q, _mx_rows(shape), shape[-1]))
 

@@ -190,7 +190,7 @@ def test_compiled_calls_take_no_call_that_is_not_theirs(lib):
     odd = [x, ids, plan, q, kept, None, 3, "swiglu", (1, 2, 3), object(), x[0], x.t(), [x]]
     arity = {"sort_routes": 2, "dispatch": 3, "combine": 3, "combine_grad": 5, "checkpoint": 1,
              "restore": 1, "expert_act": 4, "expert_act_grad": 2, "mx_quantize": 1,
-             "mx_product": 4}
+             "mx_raw": 3, "mx_product": 4}
     for name, n in arity.items():
         f = getattr(_calls, name)
         assert f() is None and f(*odd[:7]) is None

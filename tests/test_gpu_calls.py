@@ -47,9 +47,10 @@ def _all(c):
         out += [y, M.expert_act(c["h"], act, limit), k.codes, k.scales, M.expert_act_grad(k, dy)]
     q = M.mx_quantize(rows)
     w, one = M.mx_quantize(c["fc"]), M.mx_quantize(c["one"])
+    stack = M.MxTensor(w.codes, w.scales, list(w.shape))
     out += [q.codes, q.scales, w.codes, w.scales]
     out += [M.mx_product(q, w, plan.offsets, torch.float32), M.mx_product(q, w, plan.offsets),
-            M.mx_product(q, one), M.mx_product(M.MxTensor(q.codes, q.scales, q.shape), one),
+            M.mx_product(q, stack, plan.offsets), M.mx_product(q, one), M.mx_product(M.MxTensor(q.codes, q.scales, q.shape), one),
             M.restore(M.Checkpoint(kept.codes, kept.scales, kept.cols, kept.dtype))]
     return out
 
@@ -138,6 +139,14 @@ def test_other_calls_are_not(compiled):
                     (compiled.expert_act_grad, (k, c["h"])),
                     (compiled.expert_act_grad, (M.checkpoint(c["x"]), c["x"])),
                     (compiled.mx_quantize, (c["fc"],)), (compiled.mx_product, (q, w, None, q)),
+                    (compiled.mx_raw, (w.codes, w.scales, (8, 41, 264))),
+                    (compiled.mx_raw, (w.codes, w.scales, [8, 40, 264])),
+                    (compiled.mx_raw, (w.codes, w.scales, (0, 40, 264))),
+                    (compiled.mx_raw, (w.codes, w.scales, (8, 8, 5, 264))),
+                    (compiled.mx_raw, (w.codes, w.scales, (2 ** 40, 40, 264))),
+                    (compiled.mx_raw, (w.codes[:, ::2], w.scales, (8, 40, 264))),
+                    (compiled.mx_raw, (w.codes.cpu(), w.scales, w.shape)),
+                    (compiled.mx_raw, (w.scales, w.codes, w.shape)),
                     (compiled.mx_product, (q, w, None, torch.float32)),
                     (compiled.mx_product, (q, w, bad, torch.float32)),
                     (compiled.mx_product, (w, w, plan.offsets, torch.float32)),
