@@ -17,6 +17,7 @@
 
 typedef moe_status (*sort_fn)(int32_t, int32_t, int32_t, const void*, int32_t, int32_t*, int32_t*,
                               int32_t*, void*, size_t, moe_stream_t);
+typedef size_t (*sort_ws_fn)(int32_t, int32_t, int32_t);
 typedef moe_status (*dispatch_fn)(const moe_rows*, int32_t, const int32_t*, void*, int64_t,
                                   moe_stream_t);
 typedef moe_status (*combine_fn)(const moe_rows*, int32_t, int32_t, const int32_t*, const float*,
@@ -42,9 +43,10 @@ static struct {
                                                          (size, stride, type), current device */
   PyObject *f32, *bf16, *f16, *u8, *i32, *i64;        /* torch types */
   PyObject *mx, *kept, *plan;                         /* MxTensor, Checkpoint, RoutePlan */
-  void* fn[10];
+  void* fn[11];
 } g;
-enum { SORT, DISPATCH, COMBINE, COMBINE_GRAD, CHECKPOINT, RESTORE, ACT, ACT_GRAD, QUANTIZE, PRODUCT };
+enum { SORT, DISPATCH, COMBINE, COMBINE_GRAD, CHECKPOINT, RESTORE, ACT, ACT_GRAD, QUANTIZE, PRODUCT,
+       SORT_WS };
 
 static PyObject *s_dtype, *s_shape, *s_stride, *s_device_of, *s_data_ptr, *s_contiguous;
 static PyObject *s_raw, *s_codes, *s_scales, *s_buf, *s_cut, *s_device, *s_rows, *s_cols, *s_act;
@@ -321,21 +323,26 @@ static int weights_of(PyObject* w, int64_t T, int64_t K, int64_t* dev, void** p)
 /* sort_routes(topk_ids, E) */
 static PyObject* sort_routes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t dev = -1, sh[2];
-  void *ids, *po, *pp, *pi;
+  void *ids, *po, *pp, *pi, *pw = NULL;
   int is64;
   moe_stream_t s;
   ORDINARY(n == 2 && PyObject_TypeCheck(a[0], (PyTypeObject*)g.tensor) && PyLong_Check(a[1]));
   const int64_t E = PyLong_AsLongLong(a[1]);
   ORDINARY(E >= 1 && E <= 1024 && sizes(PyObject_GetAttr(a[0], s_shape), 2, sh));
-  ORDINARY(sh[0] >= 1 && sh[0] <= 32768 && sh[1] >= 1 && sh[1] <= 32 && sh[0] * sh[1] <= 32768 &&
+  ORDINARY(sh[0] >= 1 && sh[0] <= INT32_MAX && sh[1] >= 1 && sh[1] <= 32 &&
            arg_of(a[0], &dev, g.i32, g.i64, 2, sh, &ids, &is64) && stream_of(dev, &s));
-  const int64_t no = E + 1, np = sh[0] * sh[1];
+  const int64_t ws = (int64_t)CALL(SORT_WS, sort_ws_fn)((int32_t)sh[0], (int32_t)sh[1], (int32_t)E);
+  ORDINARY(ws > 0);
+  // a workspace only where the sort needs more than the status that nobody reads here
+  const int64_t no = E + 1, np = sh[0] * sh[1], nw = np > 32768 ? ws : 0;
   PyObject* offsets = new_tensor(1, &no, g.i32, &po);
   PyObject* perm = offsets ? new_tensor(1, &np, g.i32, &pp) : NULL;
   PyObject* inv = perm ? new_tensor(2, sh, g.i32, &pi) : NULL;
+  PyObject* work = inv && nw ? new_tensor(1, &nw, g.u8, &pw) : NULL;
   PyObject* plan = NULL;
-  if (inv && CALL(SORT, sort_fn)((int32_t)sh[0], (int32_t)sh[1], (int32_t)E, ids, is64, po, pp, pi,
-                                 NULL, 0, s) == MOE_OK) {
+  if (inv && (work || !nw) &&
+      CALL(SORT, sort_fn)((int32_t)sh[0], (int32_t)sh[1], (int32_t)E, ids, is64, po, pp, pi, pw,
+                          (size_t)nw, s) == MOE_OK) {
     PyObject* items = Py_BuildValue("((OOO))", offsets, perm, inv);
     if (items) plan = PyTuple_Type.tp_new((PyTypeObject*)g.plan, items, NULL);
     Py_XDECREF(items);
@@ -343,6 +350,7 @@ static PyObject* sort_routes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Py_XDECREF(offsets);
   Py_XDECREF(perm);
   Py_XDECREF(inv);
+  Py_XDECREF(work); /* its memory is used next by work behind this on the stream */
   return plan ? plan : not_ordinary();
 }
 
@@ -560,13 +568,13 @@ static PyObject* mx_product(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* attach((Tensor, empty, current device, current stream), (f32, bf16, f16, u8, i32, i64),
- *        (MxTensor, Checkpoint, RoutePlan), ten entry points' addresses) */
+ *        (MxTensor, Checkpoint, RoutePlan), eleven entry points' addresses) */
 static PyObject* attach(PyObject* self, PyObject* args) {
   PyObject* o[13];
-  unsigned long long fn[10];
-  if (!PyArg_ParseTuple(args, "(OOOO)(OOOOOO)(OOO)(KKKKKKKKKK)", &o[0], &o[1], &o[2], &o[3], &o[4],
+  unsigned long long fn[11];
+  if (!PyArg_ParseTuple(args, "(OOOO)(OOOOOO)(OOO)(KKKKKKKKKKK)", &o[0], &o[1], &o[2], &o[3], &o[4],
                         &o[5], &o[6], &o[7], &o[8], &o[9], &o[10], &o[11], &o[12], &fn[0], &fn[1],
-                        &fn[2], &fn[3], &fn[4], &fn[5], &fn[6], &fn[7], &fn[8], &fn[9]))
+                        &fn[2], &fn[3], &fn[4], &fn[5], &fn[6], &fn[7], &fn[8], &fn[9], &fn[10]))
     return NULL;
   PyObject** slot[13] = {&g.tensor, &g.empty, &g.get_device, &g.get_stream, &g.f32, &g.bf16, &g.f16,
                          &g.u8, &g.i32, &g.i64, &g.mx, &g.kept, &g.plan};
@@ -578,7 +586,7 @@ static PyObject* attach(PyObject* self, PyObject* args) {
     Py_INCREF(o[i]);
     Py_XSETREF(*slot[i], o[i]);
   }
-  for (int i = 0; i < 10; ++i) g.fn[i] = (void*)(uintptr_t)fn[i];
+  for (int i = 0; i < 11; ++i) g.fn[i] = (void*)(uintptr_t)fn[i];
   Py_RETURN_NONE;
 }
 

@@ -28,7 +28,8 @@ class _Interpreted:
 
 _fast = _Interpreted()
 _FAST = ["sort_routes", "dispatch", "combine", "combine_grad", "checkpoint", "restore",
-         "expert_act", "expert_act_grad", "mx_quantize", "mx_product"]
+         "expert_act", "expert_act_grad", "mx_quantize", "mx_product",
+         "sort_routes_workspace_bytes"]
 
 
 def _attach(L):

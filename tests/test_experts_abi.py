@@ -198,7 +198,7 @@ def test_compiled_calls_take_no_call_that_is_not_theirs(lib):
             for j in range(len(odd)):
                 args = [odd[i], odd[j]] + odd[2:5]
                 assert f(*args[:n]) is None, (name, i, j)
-    for bad in ((), (1,), ((1, 2, 3, 4), (1,) * 6, (1, 2, 3), (0,) * 10)):
+    for bad in ((), (1,), ((1, 2, 3, 4), (1,) * 6, (1, 2, 3), (0,) * 11)):
         with pytest.raises(TypeError):
             _calls.attach(*bad)
 

@@ -115,6 +115,16 @@ def test_ordinary_calls_are_compiled(compiled):
         assert r is not None
 
 
+@pytest.mark.parametrize("T,K", [(16384, 2), (16385, 2), (40000, 3)])
+def test_sorts_with_a_workspace(compiled, monkeypatch, T, K):
+    ids = torch.randint(-2, 70, (T, K), generator=torch.Generator().manual_seed(T)).to(DEV)
+    fast = [compiled.sort_routes(ids, 64), compiled.sort_routes(ids.int(), 64)]
+    monkeypatch.setattr(experts, "_fast", experts._Interpreted())
+    for got in fast:
+        for a, b in zip(got, M.sort_routes(ids, 64)):
+            assert a.shape == b.shape and torch.equal(a, b)
+
+
 def test_other_calls_are_not(compiled):
     c = _case(0)
     plan = M.sort_routes(c["ids"], c["E"])
