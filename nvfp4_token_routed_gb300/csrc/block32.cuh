@@ -98,29 +98,24 @@ struct NarrowType<DT, 8> {
   using type = uint2;
 };
 
+// A span as it was read, and the runs made of it: several spans are read before the first is
+// put together.
 template <int DT, int VB>
-__device__ __forceinline__ void span_load(const void* p, int n, void* stage,
-                                          uint32_t (&w)[kRunWords<DT>]) {
-  constexpr int kSize = DT == kF32 ? 4 : 2;
-  const int lane = threadIdx.x & 31;
-  if constexpr (VB == 16) {
-    constexpr int kPer = 16 / kSize;
-    const uint4* c = reinterpret_cast<const uint4*>(p) + lane * (8 / kPer);
-#pragma unroll
-    for (int i = 0; i < 8 / kPer; ++i) {
-      const uint4 t = lane * 8 + i * kPer < n ? c[i] : make_uint4(0u, 0u, 0u, 0u);
-      w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
-    }
-  } else {
-    using V = typename NarrowType<DT, VB>::type;
-    constexpr int kPer = VB / kSize, kN = kSpan / kPer / 32;
+struct Span {
+  using V = typename NarrowType<DT, VB>::type;
+  static constexpr int kPer = VB / (DT == kF32 ? 4 : 2), kN = kSpan / kPer / 32;
+  V t[kN];
+  __device__ __forceinline__ void load(const void* p, int n) {
+    const int lane = threadIdx.x & 31;
     const V* c = reinterpret_cast<const V*>(p);
-    V t[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       t[i] = V{};
       if ((32 * i + lane) * kPer < n) t[i] = c[32 * i + lane];
     }
+  }
+  __device__ __forceinline__ void runs(void* stage, uint32_t (&w)[kRunWords<DT>]) const {
+    const int lane = threadIdx.x & 31;
     __syncwarp();  // an earlier use of the stage is over
 #pragma unroll
     for (int i = 0; i < kN; ++i) reinterpret_cast<V*>(stage)[32 * i + lane] = t[i];
@@ -131,7 +126,25 @@ __device__ __forceinline__ void span_load(const void* p, int n, void* stage,
       w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
   }
-}
+};
+template <int DT>
+struct Span<DT, 16> {
+  uint32_t t[kRunWords<DT>];
+  __device__ __forceinline__ void load(const void* p, int n) {
+    constexpr int kPer = 16 / (DT == kF32 ? 4 : 2);
+    const int lane = threadIdx.x & 31;
+    const uint4* c = reinterpret_cast<const uint4*>(p) + lane * (8 / kPer);
+#pragma unroll
+    for (int i = 0; i < 8 / kPer; ++i) {
+      const uint4 q = lane * 8 + i * kPer < n ? c[i] : make_uint4(0u, 0u, 0u, 0u);
+      t[4 * i] = q.x, t[4 * i + 1] = q.y, t[4 * i + 2] = q.z, t[4 * i + 3] = q.w;
+    }
+  }
+  __device__ __forceinline__ void runs(void*, uint32_t (&w)[kRunWords<DT>]) const {
+#pragma unroll
+    for (int i = 0; i < kRunWords<DT>; ++i) w[i] = t[i];
+  }
+};
 template <int DT>
 __device__ __forceinline__ void run_unpack(const uint32_t (&w)[kRunWords<DT>], Run8& r) {
 #pragma unroll

@@ -17,7 +17,9 @@
 // beside it, for which 16-bit maxima and fp32 arithmetic go two at a time (75 -> 61 us).
 // Measured (bf16; copy rate 6686 GB/s): clamped SwiGLU 24576 x 2048 forward 61 us (0.99 of the
 // copy rate), gradient 65 us (0.93), rows of 4096 x 7168 kept 13.6 us and restored 12.5 us;
-// squared ReLU 5001 x 1407 f16, rows off 4 bytes, 10.4 and 11.0 us (0.5; by a run a lane 20).
+// squared ReLU 5001 x 1407 f16, rows off 4 bytes, 16.7 us for both (by a run a lane 31); rows
+// off 16 bytes of 3719 x 6662 kept 12.2 us (L2 warm; one span a warp 17.1) and restored 10.2
+// (15.4).
 #include <algorithm>
 
 #include "block32.cuh"
@@ -100,16 +102,17 @@ __global__ void __launch_bounds__(kThreads) checkpoint_kernel(const KeepArgs a, 
   int c;
   if (!place_of(a, segs, U, r, c)) return;
   void* stage = warp_stage<DT, VB>();
-  uint32_t w[U][kRunWords<DT>];
+  Span<DT, VB> x[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + c + u * kSpan), a.W - c - u * kSpan, stage,
-                      w[u]);
+    x[u].load(elem_ptr<DT>(a.x, r * a.ld_x + c + u * kSpan), a.W - c - u * kSpan);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    uint32_t w[kRunWords<DT>];
+    x[u].runs(stage, w);
     Run8 v;
-    run_unpack<DT>(w[u], v);
-    keep_run<DT>(a, r, c + u * kSpan, 1, 0, w[u], v);
+    run_unpack<DT>(w, v);
+    keep_run<DT>(a, r, c + u * kSpan, 1, 0, w, v);
   }
 }
 
@@ -176,20 +179,22 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
   int c;
   if (!place_of(a, segs, U, r, c)) return;
   void* stage = warp_stage<DT, VB>();
-  uint32_t w[U][kHalves][kRunWords<DT>];
+  Span<DT, VB> x[U][kHalves];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
-      span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + h * a.W + c + u * kSpan),
-                        a.W - c - u * kSpan, stage, w[u][h]);
+      x[u][h].load(elem_ptr<DT>(a.x, r * a.ld_x + h * a.W + c + u * kSpan), a.W - c - u * kSpan);
   const float L = a.limit;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    uint32_t w[kHalves][kRunWords<DT>];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) x[u][h].runs(stage, w[h]);
     Run8 g, up, y;
-    run_unpack<DT>(w[u][0], g);
+    run_unpack<DT>(w[0], g);
     if constexpr (ACT == kActSwiglu) {
-      run_unpack<DT>(w[u][kHalves - 1], up);
+      run_unpack<DT>(w[kHalves - 1], up);
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         f32x2 gc = pack2(g.v[i], g.v[i + 1]), uc = pack2(up.v[i], up.v[i + 1]);
@@ -211,8 +216,8 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const KeepArgs a, int seg
     const int cu = c + u * kSpan;
     span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, stage, y);
     if (!a.codes) continue;
-    keep_run<DT>(a, r, cu, kHalves, 0, w[u][0], g);
-    if constexpr (ACT == kActSwiglu) keep_run<DT>(a, r, cu, kHalves, 1, w[u][kHalves - 1], up);
+    keep_run<DT>(a, r, cu, kHalves, 0, w[0], g);
+    if constexpr (ACT == kActSwiglu) keep_run<DT>(a, r, cu, kHalves, 1, w[kHalves - 1], up);
   }
 }
 
@@ -226,12 +231,12 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 5) act_grad_kernel(
   int c;
   if (!place_of(a, segs, U, r, c)) return;
   void* stage = warp_stage<DT, VB>();
-  uint32_t w[U][kRunWords<DT>];
+  Span<DT, VB> x[U];
   Kept k[U][kHalves];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int cu = c + u * kSpan;
-    span_load<DT, VB>(elem_ptr<DT>(a.x, r * a.ld_x + cu), a.W - cu, stage, w[u]);
+    x[u].load(elem_ptr<DT>(a.x, r * a.ld_x + cu), a.W - cu);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) k[u][h] = kept_run(a, r, cu, kHalves, h);
   }
@@ -239,8 +244,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 5) act_grad_kernel(
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int cu = c + u * kSpan;
+    uint32_t w[kRunWords<DT>];
+    x[u].runs(stage, w);
     Run8 g, up, d;
-    run_unpack<DT>(w[u], d);
+    run_unpack<DT>(w, d);
     e4m3x8_to_float(k[u][0].codes, block_scale(k[u][0].byte), g);
     if constexpr (ACT == kActSwiglu) {
       e4m3x8_to_float(k[u][kHalves - 1].codes, block_scale(k[u][kHalves - 1].byte), up);
@@ -287,7 +294,8 @@ cudaError_t go(K kernel, const KeepArgs& a, int u, cudaStream_t s) {
 }
 
 // U spans a warp where that leaves the device enough warps (16 an SM), else one: 128 rows of
-// 1024 take 3.2 us with one span a warp.
+// 1024 take 3.2 us with one span a warp.  (Rows of a few spans gain least: 5001 x 1407 of fp32,
+// six spans a row, are kept in 7.4 us, by one span a warp in 6.5; of 16 bits both in 6.5.)
 constexpr int64_t kManyWarps = 152 * 16;
 int spans(const KeepArgs& a, int u) {
   return (int64_t)a.R * ((a.W + u * kSpan - 1) / (u * kSpan)) >= kManyWarps ? u : 1;
@@ -299,11 +307,17 @@ int spans(const KeepArgs& a, int u) {
     case 16:                                                                                      \
       return many ? go(KERNEL<DT, 16, U __VA_ARGS__>, a, U, s)                                    \
                   : go(KERNEL<DT, 16, 1 __VA_ARGS__>, a, 1, s);                                   \
-    case 8: return go(KERNEL<DT, 8, 1 __VA_ARGS__>, a, 1, s);                                     \
-    case 4: return go(KERNEL<DT, 4, 1 __VA_ARGS__>, a, 1, s);                                     \
+    case 8:                                                                                       \
+      return many ? go(KERNEL<DT, 8, U __VA_ARGS__>, a, U, s)                                     \
+                  : go(KERNEL<DT, 8, 1 __VA_ARGS__>, a, 1, s);                                    \
+    case 4:                                                                                       \
+      return many ? go(KERNEL<DT, 4, U __VA_ARGS__>, a, U, s)                                     \
+                  : go(KERNEL<DT, 4, 1 __VA_ARGS__>, a, 1, s);                                    \
     default: break;                                                                               \
   }                                                                                               \
-  if constexpr (DT != kF32) return go(KERNEL<DT, 2, 1 __VA_ARGS__>, a, 1, s);                     \
+  if constexpr (DT != kF32)                                                                       \
+    return many ? go(KERNEL<DT, 2, U __VA_ARGS__>, a, U, s)                                       \
+                : go(KERNEL<DT, 2, 1 __VA_ARGS__>, a, 1, s);                                      \
   return cudaErrorInvalidValue;
 #define MOE_COMMA ,
 
