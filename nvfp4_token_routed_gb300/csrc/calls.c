@@ -1,7 +1,7 @@
 /* calls.c -- the routed-row calls of the binding in their ordinary form, as a CPython
  * extension: new outputs, the current stream, every row.  A call of a few microseconds of GPU
  * time otherwise waits for the interpreter: sort_routes and dispatch of 16 tokens take 10.5 us
- * here, 22 interpreted; what is left is allocation (1.2 us each) and launch (2 us).
+ * here, 20 interpreted; what is left is allocation (1.2 us each) and launch (2 us).
  *
  * Each function takes the positional arguments of its namesake in experts.py (mx_raw: of
  * MxTensor) and returns its result, or None where the call is not an ordinary one: other types, shapes, devices or

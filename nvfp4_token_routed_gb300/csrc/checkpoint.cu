@@ -325,9 +325,10 @@ template <int DT>
 cudaError_t checkpoint_typed(const KeepArgs& a, cudaStream_t s) {
   MOE_BY_WIDTH(checkpoint_kernel, DT, 4, width(a.x, a.ld_x, a.W, DT))
 }
+// (fp32: two spans 5001 x 1407 6.1 us, 4096 x 7168 30.1; four 6.8 and 30.9)
 template <int DT>
 cudaError_t restore_typed(const KeepArgs& a, cudaStream_t s) {
-  MOE_BY_WIDTH(restore_kernel, DT, 4, width(a.out, a.ld_out, a.W, DT))
+  MOE_BY_WIDTH(restore_kernel, DT, (DT == kF32 ? 2 : 4), width(a.out, a.ld_out, a.W, DT))
 }
 template <int DT, int ACT, bool LIMIT>
 cudaError_t act_typed(const KeepArgs& a, cudaStream_t s) {

@@ -145,10 +145,12 @@ cudaError_t go(K kernel, const MxQuantArgs& a, int u, cudaStream_t s) {
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, segs);
 }
 
-// Four panels a warp where that leaves the device enough warps.
-template <typename K>
-cudaError_t go_many(K one, K four, const MxQuantArgs& a, cudaStream_t s) {
-  return (int64_t)a.R * (a.Dp / kMxPanel) >= 4 * 152 * 16 ? go(four, a, 4, s) : go(one, a, 1, s);
+// U panels a warp where that leaves the device enough warps.  Restored fp32 rows take two:
+// 5001 x 1407 5.9 us (by four 6.6, by one 6.6), 20000 x 3001 43 (43, 50), 4096 x 7168 28.5 (30.1,
+// 26.1).
+template <int U = 4, typename K>
+cudaError_t go_many(K one, K many, const MxQuantArgs& a, cudaStream_t s) {
+  return (int64_t)a.R * (a.Dp / kMxPanel) >= 4 * 152 * 16 ? go(many, a, U, s) : go(one, a, 1, s);
 }
 template <int DT>
 cudaError_t quantize_typed(const MxQuantArgs& a, cudaStream_t s) {
@@ -164,14 +166,15 @@ cudaError_t quantize_typed(const MxQuantArgs& a, cudaStream_t s) {
 }
 template <int DT>
 cudaError_t restore_typed(const MxQuantArgs& a, cudaStream_t s) {
+  constexpr int kMany = DT == kF32 ? 2 : 4;
   switch (access_bytes(a.out, a.ld_out * size_of(DT), (int64_t)a.D * size_of(DT))) {
-    case 16: return go_many(restore_kernel<DT, 16, 1>, restore_kernel<DT, 16, 4>, a, s);
-    case 8: return go_many(restore_kernel<DT, 8, 1>, restore_kernel<DT, 8, 4>, a, s);
-    case 4: return go_many(restore_kernel<DT, 4, 1>, restore_kernel<DT, 4, 4>, a, s);
+    case 16: return go_many<kMany>(restore_kernel<DT, 16, 1>, restore_kernel<DT, 16, kMany>, a, s);
+    case 8: return go_many<kMany>(restore_kernel<DT, 8, 1>, restore_kernel<DT, 8, kMany>, a, s);
+    case 4: return go_many<kMany>(restore_kernel<DT, 4, 1>, restore_kernel<DT, 4, kMany>, a, s);
     default: break;
   }
   if constexpr (DT != kF32)
-    return go_many(restore_kernel<DT, 2, 1>, restore_kernel<DT, 2, 4>, a, s);
+    return go_many<kMany>(restore_kernel<DT, 2, 1>, restore_kernel<DT, 2, kMany>, a, s);
   return cudaErrorInvalidValue;
 }
 
