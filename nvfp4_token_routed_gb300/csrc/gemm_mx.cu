@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < a.kblocks; ++kb) {
         ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(kFull + stage), phase, abort_flag));
         if (!ok) break;
+        tc_fence_after();  // behind the MMAs that read this stage's columns (kEmpty, then kFull)
         const uint32_t sb = smem_u32(stages + stage * stage_bytes);
         const uint32_t col = tmem + lane_q + sf_base + stage * slot_cols;
         const uint32_t sa = sb + off_sfa + 8 * (odd_w + lane), sx = sb + off_sfb + 8 * (odd_x + lane);
@@ -745,6 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       for (int kb = 0; kb < a.kblocks; ++kb) {
         ok = __all_sync(0xFFFFFFFFu, wait_or_leave(R.bar(pair::kFull + stage), phase, abort_flag));
         if (!ok) break;
+        tc_fence_after();  // as the single CTAs
         const uint32_t sb = smem_u32(stages + stage * stage_bytes);
         const uint32_t col = tmem + lane_q + sf_base + stage * slot_cols;
         const uint32_t sa = sb + off_sfa + 8 * (odd_w + lane), sx = sb + off_sfb + 8 * (odd_x + lane);
