@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(w4a4::kThreads, 1)
           ok = false;
           break;
         }
+        tc_fence_after();  // behind the MMAs that read this slot before (empty, then full barrier)
         const uint32_t sb = smem_u32(stages + stage * stage_bytes);
         const uint32_t col0 = tmem + lane_q + sf_base + stage * slot_cols;
 #pragma unroll
