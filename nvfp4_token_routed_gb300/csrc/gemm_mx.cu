@@ -188,6 +188,16 @@ __device__ __forceinline__ void drain_ring(const Ring& R, int loaded, int n_stag
       if (globaltimer() - t0 > kWaitLimitNs) return;
 }
 
+// At the end of a walk, by the warp that loads weights: the last use of each stage has been given
+// back, so that no arrival of a commit is on its way to this CTA's barriers when it leaves (the
+// commit behind them, on the accumulator's barrier, promises that of the MMAs alone).
+__device__ __forceinline__ void await_ring(const Ring& R, int empty, int loaded, int n_stages,
+                                           volatile int* abort_flag) {
+  for (int i = max(0, loaded - n_stages); i < loaded; ++i)
+    if (!wait_or_leave(R.bar(empty + i % n_stages), (uint32_t)(i / n_stages) & 1u, abort_flag))
+      return;
+}
+
 // A CTA's walk over its items, by a whole warp.
 struct Item {
   int e, mt;
@@ -346,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (ok) await_ring(R, kEmpty, loaded, n_stages, abort_flag);
     if (!ok || *abort_flag) drain_ring(R, loaded, n_stages);
   } else if (warp == 10) {
     // ------------------------------------------------------------ row producer
@@ -733,6 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         advance();
       }
     }
+    if (ok && warp == 0) await_ring(R, pair::kEmpty, loaded, n_stages, abort_flag);
     if (!ok || *abort_flag) drain_ring(R, loaded, n_stages);
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ scales to TMEM

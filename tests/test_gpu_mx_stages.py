@@ -37,3 +37,24 @@ def test_scales_of_reused_stages(rows, E, N, D):
     for _ in range(5):
         got = M.mx_product(q, qw, offsets, torch.float32)
         assert torch.equal(got.double(), want)
+
+
+def test_products_one_behind_the_other():
+    """Launches of pairs and of single blocks in turn, hundreds without a pause: what one leaves
+    in flight at its end would meet the next one's barriers."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    E, N, D = 4, 2560, 2048
+    qw = M.mx_quantize(_powers(E * N, D, g).view(E, N, D))
+    many, few = M.mx_quantize(_powers(1024, D, g)), M.mx_quantize(_powers(20, D, g))
+    cut = [torch.tensor(o, dtype=torch.int32, device=DEV) for o in ([0, 256, 512, 768, 1024],
+                                                                   [0, 9, 9, 19, 20])]
+    want = [M.mx_product(many, qw, cut[0]), M.mx_product(few, qw, cut[1])]
+    outs = [torch.empty_like(w) for w in want]
+    for _ in range(300):
+        for o in outs:
+            o.fill_(7.0)
+        M.mx_product(many, qw, cut[0], out=outs[0])
+        M.mx_product(few, qw, cut[1], out=outs[1])
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
