@@ -317,6 +317,16 @@ static int weights_of(PyObject* w, int64_t T, int64_t K, int64_t* dev, void** p)
 }
 
 #define CALL(NAME, TYPE) ((TYPE)g.fn[NAME])
+/* `status` of an entry point, called without the interpreter's lock: a launch waits where the
+ * stream's queue is full, and what the queue waits for may need another Python thread.  (0.1 us.)
+ * The arguments are plain values; their tensors are the caller's, or new and held here. */
+#define LAUNCH(status, NAME, TYPE, ...)       \
+  do {                                        \
+    const TYPE entry = CALL(NAME, TYPE);      \
+    Py_BEGIN_ALLOW_THREADS                    \
+    status = entry(__VA_ARGS__);              \
+    Py_END_ALLOW_THREADS                      \
+  } while (0)
 #define ORDINARY(cond) \
   if (!(cond)) return not_ordinary()
 
@@ -340,9 +350,11 @@ static PyObject* sort_routes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject* inv = perm ? new_tensor(2, sh, g.i32, &pi) : NULL;
   PyObject* work = inv && nw ? new_tensor(1, &nw, g.u8, &pw) : NULL;
   PyObject* plan = NULL;
-  if (inv && (work || !nw) &&
-      CALL(SORT, sort_fn)((int32_t)sh[0], (int32_t)sh[1], (int32_t)E, ids, is64, po, pp, pi, pw,
-                          (size_t)nw, s) == MOE_OK) {
+  moe_status st = MOE_ERR_CUDA;
+  if (inv && (work || !nw))
+    LAUNCH(st, SORT, sort_fn, (int32_t)sh[0], (int32_t)sh[1], (int32_t)E, ids, is64, po, pp, pi, pw,
+           (size_t)nw, s);
+  if (st == MOE_OK) {
     PyObject* items = Py_BuildValue("((OOO))", offsets, perm, inv);
     if (items) plan = PyTuple_Type.tp_new((PyTypeObject*)g.plan, items, NULL);
     Py_XDECREF(items);
@@ -363,7 +375,9 @@ static PyObject* dispatch(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   ORDINARY(n == 3 && rows_of(a[0], &dev, &x) && inv_of(a[1], x.rows, &dev, &inv, &K) &&
            stream_of(dev, &s));
   PyObject* out = matrix_out(a[2], x.rows * K, x.cols, x.dtype, &dev, &p, &ld);
-  if (out && CALL(DISPATCH, dispatch_fn)(&x, (int32_t)K, inv, p, ld, s) != MOE_OK) Py_CLEAR(out);
+  moe_status st = MOE_OK;
+  if (out) LAUNCH(st, DISPATCH, dispatch_fn, &x, (int32_t)K, inv, p, ld, s);
+  if (st != MOE_OK) Py_CLEAR(out);
   return out ? out : not_ordinary();
 }
 
@@ -377,8 +391,9 @@ static PyObject* combine(PyObject* self, PyObject* const* a, Py_ssize_t n) {
            inv_of(a[1], T, &dev, &inv, &K) && weights_of(a[2], T, K, &dev, &w) &&
            stream_of(dev, &s));
   PyObject* out = matrix_out(Py_None, T, x.cols, x.dtype, &dev, &p, &ld);
-  if (out && CALL(COMBINE, combine_fn)(&x, (int32_t)T, (int32_t)K, inv, w, p, ld, s) != MOE_OK)
-    Py_CLEAR(out);
+  moe_status st = MOE_OK;
+  if (out) LAUNCH(st, COMBINE, combine_fn, &x, (int32_t)T, (int32_t)K, inv, w, p, ld, s);
+  if (st != MOE_OK) Py_CLEAR(out);
   return out ? out : not_ordinary();
 }
 
@@ -396,9 +411,11 @@ static PyObject* combine_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   PyObject* drows = matrix_out(a[4], x.rows, x.cols, x.dtype, &dev, &p, &ld);
   PyObject* dw = drows ? new_tensor(2, sh, g.f32, &pw) : NULL;
   PyObject* r = NULL;
-  if (dw && CALL(COMBINE_GRAD, combine_grad_fn)(&x, (int32_t)T, (int32_t)K, inv, w, d.data, d.ld, p,
-                                                ld, pw, s) == MOE_OK)
-    r = PyTuple_Pack(2, drows, dw);
+  moe_status st = MOE_ERR_CUDA;
+  if (dw)
+    LAUNCH(st, COMBINE_GRAD, combine_grad_fn, &x, (int32_t)T, (int32_t)K, inv, w, d.data, d.ld, p,
+           ld, pw, s);
+  if (st == MOE_OK) r = PyTuple_Pack(2, drows, dw);
   Py_XDECREF(drows);
   Py_XDECREF(dw);
   return r ? r : not_ordinary();
@@ -412,7 +429,9 @@ static PyObject* checkpoint(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   moe_stream_t s;
   ORDINARY(n == 1 && rows_of(a[0], &dev, &x) && stream_of(dev, &s));
   PyObject* k = new_kept(x.rows, x.cols, 1, type_object(x.dtype), Py_None, 0.0, dev, &codes, &scales);
-  if (k && CALL(CHECKPOINT, checkpoint_fn)(&x, codes, scales, NULL, s) != MOE_OK) Py_CLEAR(k);
+  moe_status st = MOE_OK;
+  if (k) LAUNCH(st, CHECKPOINT, checkpoint_fn, &x, codes, scales, NULL, s);
+  if (st != MOE_OK) Py_CLEAR(k);
   return k ? k : not_ordinary();
 }
 
@@ -437,7 +456,9 @@ static PyObject* restore(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject* out = new_tensor(2, sh, type_object(type), &p);
   if (out) {
     const moe_rows m = {p, k.cols, (int32_t)k.rows, (int32_t)k.cols, type};
-    if (CALL(RESTORE, restore_fn)(k.codes, k.scales, &m, NULL, s) != MOE_OK) Py_CLEAR(out);
+    moe_status st;
+    LAUNCH(st, RESTORE, restore_fn, k.codes, k.scales, &m, NULL, s);
+    if (st != MOE_OK) Py_CLEAR(out);
   }
   return out ? out : not_ordinary();
 }
@@ -460,9 +481,10 @@ static PyObject* expert_act(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                                      &codes, &scales)
                           : NULL;
   PyObject* r = NULL;
-  if (y && (k || !keep) &&
-      CALL(ACT, act_fn)(&h, act, (float)limit, p, sh[1], codes, scales, NULL, s) == MOE_OK)
-    r = keep ? PyTuple_Pack(2, y, k) : Py_NewRef(y);
+  moe_status st = MOE_ERR_CUDA;
+  if (y && (k || !keep))
+    LAUNCH(st, ACT, act_fn, &h, act, (float)limit, p, sh[1], codes, scales, NULL, s);
+  if (st == MOE_OK) r = keep ? PyTuple_Pack(2, y, k) : Py_NewRef(y);
   Py_XDECREF(y);
   Py_XDECREF(k);
   return r ? r : not_ordinary();
@@ -479,9 +501,11 @@ static PyObject* expert_act_grad(PyObject* self, PyObject* const* a, Py_ssize_t 
            dy.rows == k.rows && dy.cols == k.cols && stream_of(dev, &s));
   const int64_t sh[2] = {dy.rows, dy.cols * k.halves};
   PyObject* dh = new_tensor(2, sh, type_object(dy.dtype), &p);
-  if (dh && CALL(ACT_GRAD, act_grad_fn)(k.codes, k.scales, k.act, (float)k.limit, &dy, p, sh[1],
-                                        NULL, s) != MOE_OK)
-    Py_CLEAR(dh);
+  moe_status st = MOE_OK;
+  if (dh)
+    LAUNCH(st, ACT_GRAD, act_grad_fn, k.codes, k.scales, k.act, (float)k.limit, &dy, p, sh[1], NULL,
+           s);
+  if (st != MOE_OK) Py_CLEAR(dh);
   return dh ? dh : not_ordinary();
 }
 
@@ -502,7 +526,9 @@ static PyObject* mx_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     m.scales = p + at;
     m.rows = x.rows;
     m.cols = x.cols;
-    if (CALL(QUANTIZE, quantize_fn)(&x, &m, NULL, s) == MOE_OK && (q = new_object(g.mx)) &&
+    moe_status st;
+    LAUNCH(st, QUANTIZE, quantize_fn, &x, &m, NULL, s);
+    if (st == MOE_OK && (q = new_object(g.mx)) &&
         !(set_held(q, buf, codes, at, dev) &&
           set_steal(q, s_shape, Py_BuildValue("(ii)", x.rows, x.cols)) &&
           set_steal(q, s_raw, PyBytes_FromStringAndSize((const char*)&m, sizeof(m)))))
@@ -562,8 +588,9 @@ static PyObject* mx_product(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int64_t sh[2] = {sx[0], N};
   ORDINARY(sx[0] >= 1);
   PyObject* out = new_tensor(2, sh, a[3], &p);
-  if (out && CALL(PRODUCT, product_fn)(&x, &w, (int32_t)E, off, type, p, N, s) != MOE_OK)
-    Py_CLEAR(out);
+  moe_status st = MOE_OK;
+  if (out) LAUNCH(st, PRODUCT, product_fn, &x, &w, (int32_t)E, off, type, p, N, s);
+  if (st != MOE_OK) Py_CLEAR(out);
   return out ? out : not_ordinary();
 }
 
