@@ -205,6 +205,21 @@ static int held_device(PyObject* o, int64_t* dev) {
   }
   return v == *dev;
 }
+/* Whether codes and scales still lie where they did (0.1 us): the tensors of a caller may have
+ * been given other storage, a buffer is the object's own. */
+static int still_at(PyObject* o, const void* codes, const void* scales) {
+  PyObject* buf = PyObject_GetAttr(o, s_buf);
+  if (!buf) return 0;
+  const int own = buf != Py_None;
+  Py_DECREF(buf);
+  if (own) return 1;
+  PyObject *c = PyObject_GetAttr(o, s_codes), *s = c ? PyObject_GetAttr(o, s_scales) : NULL;
+  void *p, *q;
+  const int ok = s && address(c, &p) && address(s, &q) && p == codes && q == scales;
+  Py_XDECREF(c);
+  Py_XDECREF(s);
+  return ok;
+}
 static int mx_of(PyObject* o, int64_t* dev, moe_mx* m) {
   if ((PyObject*)Py_TYPE(o) != g.mx || !held_device(o, dev)) return 0;
   PyObject* raw = PyObject_GetAttr(o, s_raw);
@@ -212,7 +227,7 @@ static int mx_of(PyObject* o, int64_t* dev, moe_mx* m) {
   const int ok = PyBytes_Check(raw) && PyBytes_GET_SIZE(raw) == sizeof(*m);
   if (ok) memcpy(m, PyBytes_AS_STRING(raw), sizeof(*m));
   Py_DECREF(raw);
-  return ok;
+  return ok && still_at(o, m->codes, m->scales);
 }
 typedef struct {
   void *codes, *scales;
@@ -242,7 +257,7 @@ static int kept_of(PyObject* o, int64_t* dev, Kept* k) {
   if (ok) {
     k->codes = PyLong_AsVoidPtr(PyTuple_GET_ITEM(c, 0));
     k->scales = PyLong_AsVoidPtr(PyTuple_GET_ITEM(c, 1));
-    ok = k->codes && k->scales;
+    ok = k->codes && k->scales && still_at(o, k->codes, k->scales);
   }
   Py_DECREF(c);
   PyObject* act = ok ? PyObject_GetAttr(o, s_act) : NULL;

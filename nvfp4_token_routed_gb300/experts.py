@@ -9,6 +9,7 @@ on that stream.  Nothing is recorded for autograd: the gradients are what the *_
 return.
 """
 import ctypes as C
+import math
 from collections import namedtuple
 
 import torch
@@ -220,15 +221,26 @@ def combine_grad(rows, plan, topk_w, dout, drows=None, d_topk_w=None, stream=Non
 
 class _Held:
     """Codes and scales on one device: two tensors, or one buffer that they are cut from when
-    asked for (an allocation and two views less a call)."""
+    asked for (an allocation and two views less a call).  Their addresses are kept; a call looks
+    whether the tensors still lie there, as a program may give them other storage (`codes.data =
+    ...`; offloading does), and takes the new ones."""
     __slots__ = ("_codes", "_scales", "_buf", "_cut", "device")
 
     def _set(self, codes, scales):
+        shapes = self._shapes()
+        for t in (codes, scales):
+            if t.numel() and t.untyped_storage().nbytes() < t.storage_offset() + t.numel():
+                raise ValueError("codes, scales: their storage has been freed")
+        at = (_arg(codes, "codes", shapes[0], _U8, codes),
+              _arg(scales, "scales", shapes[1], _U8, codes))
         self.device = codes.get_device()  # -1 on the CPU: described, but no call takes it
         self._codes, self._scales, self._buf, self._cut = codes, scales, None, None
-        shapes = self._shapes()
-        return (_arg(codes, "codes", shapes[0], _U8, codes),
-                _arg(scales, "scales", shapes[1], _U8, codes))
+        return at
+
+    def _moved(self, codes, scales):
+        """Whether the tensors lie elsewhere than at these addresses (a buffer is nobody else's)."""
+        return self._buf is None and (self._codes.data_ptr() != (codes or 0) or
+                                      self._scales.data_ptr() != (scales or 0))
 
     def _alloc(self, n_codes, n_scales, like, stream):
         at = (n_codes + 255) & -256
@@ -241,23 +253,30 @@ class _Held:
         p = buf.data_ptr()
         return p, p + at
 
+    def _views(self):
+        buf = self._buf
+        if buf is not None:
+            shapes = self._shapes()
+            self._codes = buf[:self._cut[0]].view(shapes[0])
+            self._scales = buf[self._cut[1]:].view(shapes[1])
+            self._buf = None  # the views hold it, and are what counts from now on
+
     @property
     def codes(self):
-        if self._codes is None:
-            self._codes = self._buf[:self._cut[0]].view(self._shapes()[0])
+        self._views()
         return self._codes
 
     @property
     def scales(self):
-        if self._scales is None:
-            self._scales = self._buf[self._cut[1]:].view(self._shapes()[1])
+        self._views()
         return self._scales
 
     def nbytes(self):
-        return self.codes.numel() + self.scales.numel()
+        return sum(math.prod(s) for s in self._shapes())
 
     def on(self):
         """A tensor of it, which has to lie on the current device (as every matrix of rows)."""
+        self._look()
         t = self._buf if self._buf is not None else self._codes
         if self.device < 0 or self.device != torch._C._cuda_getDevice():
             raise ValueError("codes: a tensor of the current CUDA device (no CPU path exists)")
@@ -282,6 +301,10 @@ class Checkpoint(_Held):
         n = rows * k.halves * ((cols + 31) >> 5)
         k.c = k._alloc(32 * n, n, like, stream)
         return k
+
+    def _look(self):
+        if self._moved(*self.c):
+            self.c = self._set(self._codes, self._scales)
 
     def _shapes(self):
         b = (self.cols + 31) // 32
@@ -400,7 +423,14 @@ class MxTensor(_Held):
 
     @property
     def c(self):
+        self._look()
         return moe_mx.from_buffer_copy(self.raw)
+
+    def _look(self):
+        m = moe_mx.from_buffer_copy(self.raw)
+        if self._moved(m.codes, m.scales):
+            p, q = self._set(self._codes, self._scales)
+            self.raw = bytes(moe_mx(p, q, m.rows, m.cols))
 
     @classmethod
     def empty(cls, shape, like, stream=None):
@@ -486,6 +516,7 @@ def _product_args(x, w, offsets, dtype, out, stream):
         raise ValueError("x: an MxTensor of rows [R, D]")
     E, N = w.shape[:2] if len(w.shape) == 3 else (1, w.shape[0])
     like = x.on()
+    w._look()
     if w.device != x.device:
         raise ValueError(f"w: on device {w.device}, the rows on {x.device}")
     if out is not None:
