@@ -302,6 +302,10 @@ class Checkpoint(_Held):
         k.c = k._alloc(32 * n, n, like, stream)
         return k
 
+    def __reduce__(self):  # copies and pickles: the addresses are not theirs
+        return Checkpoint, (self.codes, self.scales, self.cols, self.dtype, self.act,
+                            self.swiglu_limit)
+
     def _look(self):
         if self._moved(*self.c):
             self.c = self._set(self._codes, self._scales)
@@ -425,6 +429,9 @@ class MxTensor(_Held):
     def c(self):
         self._look()
         return moe_mx.from_buffer_copy(self.raw)
+
+    def __reduce__(self):  # as Checkpoint's
+        return MxTensor, (self.codes, self.scales, self.shape)
 
     def _look(self):
         m = moe_mx.from_buffer_copy(self.raw)

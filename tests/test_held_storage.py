@@ -1,4 +1,8 @@
-"""Codes and scales whose tensors are given other storage, as offloading does."""
+"""Codes and scales whose tensors are given other storage, as offloading does; and copies."""
+import copy
+import io
+import pickle
+
 import pytest
 import torch
 
@@ -67,3 +71,52 @@ def test_calls_follow_the_tensors(monkeypatch, compiled):
     for i in (0, 2, 3, 4, 5):
         with pytest.raises(ValueError):
             calls[i]()
+
+
+def _copies(t):
+    with io.BytesIO() as f:
+        torch.save(t, f)
+        f.seek(0)
+        loaded = torch.load(f, weights_only=False)
+    return [copy.deepcopy(t), copy.copy(t), pickle.loads(pickle.dumps(t)), loaded]
+
+
+def test_copies_describe_their_own_tensors():
+    for t in (M.MxTensor(_u8(4, 128), _u8(1, 4, 8), (4, 8)),
+              M.Checkpoint(_u8(4, 2, 32), _u8(4, 2, 1), 8, torch.float16, "swiglu", 2.0)):
+        for other in _copies(t):
+            at = other.c if type(t) is M.Checkpoint else (other.c.codes, other.c.scales)
+            assert at == (other.codes.data_ptr(), other.scales.data_ptr())
+            assert torch.equal(other.codes, t.codes) and torch.equal(other.scales, t.scales)
+            for name in ("shape", "rows", "cols", "halves", "dtype", "act", "swiglu_limit"):
+                assert getattr(other, name, None) == getattr(t, name, None)
+
+
+@pytest.mark.gpu
+def test_copies_have_addresses_of_their_own():
+    x = torch.randn(6, 300, device="cuda")
+    h = torch.randn(6, 128, device="cuda")
+    y, kept = M.expert_act(h, "swiglu", 2.0, checkpoint=True)
+    w = M.mx_quantize(torch.randn(2, 40, 300, device="cuda"))
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    for t, call in ((M.mx_quantize(x), lambda t: M.mx_product(t, w, off)),
+                    (w, lambda t: M.mx_product(M.mx_quantize(x), t, off)),
+                    (kept, lambda t: M.expert_act_grad(t, y)), (M.checkpoint(h), M.restore)):
+        want = call(t)
+        fresh = copy.deepcopy(t)  # of an object whose tensors nobody has asked for
+        assert torch.equal(call(fresh), want)
+        for other in _copies(t) + _copies(fresh):
+            assert type(other) is type(t) and torch.equal(call(other), want)
+            assert torch.equal(other.codes, t.codes) and torch.equal(other.scales, t.scales)
+        deep = copy.deepcopy(t)
+        t.codes.fill_(0)
+        assert torch.equal(call(deep), want)
+    layer = M.MxExperts(torch.randn(4, 64, 96, device="cuda"), torch.randn(4, 96, 64, device="cuda"),
+                        "relu2")
+    ids = torch.zeros(5, 1, dtype=torch.int32, device="cuda")
+    args = torch.randn(5, 96, device="cuda"), ids, torch.ones(5, 1, device="cuda")
+    want = layer.forward(*args)[0]
+    again = copy.deepcopy(layer)
+    layer.fc1.codes.fill_(0), layer.fc2.codes.fill_(0)
+    del layer
+    assert torch.equal(again.forward(*args)[0], want)
