@@ -603,8 +603,12 @@ moe_status moe_nvfp4_expert_act_grad(const uint8_t* codes, const uint8_t* scales
                                      int64_t ld_dh, const int32_t* n_rows, moe_stream_t stream);
 
 /* A matrix in microscaled FP4: E2M1 times a power of two 2^e per 32 consecutive values of a
- * row, e the smallest with which no value passes 6, -127 <= e <= 127; rounding, e's byte and
- * non-finite blocks as above.  Dp = cols rounded up to 256, Rp = rows rounded up to 2.
+ * row, e the smallest with which no value passes 6, -127 <= e <= 127; e's byte and non-finite
+ * blocks as above.  A value is rounded to nearest even: off by at most a quarter of itself or of
+ * 2^e.  That also holds at the end of its type, unlike above, as rounding down there would
+ * cost a quarter of the value: f16 values from 57344 on stand for 65536, bf16 and fp32
+ * values from 3.5 * 2^126 on for 2^128.  Products take them as that; restored to a type that
+ * ends before, they are infinite.  Dp = cols rounded up to 256, Rp = rows rounded up to 2.
  *   codes  [rows][Dp / 2], value 2j in the low nibble of byte j, zeros behind the row
  *   scales [Dp / 256][Rp][8]: the 8 scales of a row's 256 values, rows one after another
  * Both 16-byte aligned.  1 <= cols <= 65536, rows <= 2^26. */
@@ -625,7 +629,8 @@ moe_status moe_nvfp4_mx_quantize(const moe_rows* x, const moe_mx* out, const int
 moe_status moe_nvfp4_mx_quantize_transposed(int32_t batch, int32_t D, int32_t C, const void* x,
                                             int32_t dtype, const moe_mx* out,
                                             moe_stream_t stream);
-/* The values that `x` stands for, rounded once to out's type (out->data is written). */
+/* The values that `x` stands for, rounded once to out's type, past its end to an infinity
+ * (out->data is written). */
 moe_status moe_nvfp4_mx_restore(const moe_mx* x, const moe_rows* out, const int32_t* n_rows,
                                 moe_stream_t stream);
 /* moe_nvfp4_dispatch of a microscaled matrix: out has x->rows * K rows. */

@@ -471,7 +471,8 @@ def _mx_out(out, shape, x, stream):
 
 def mx_quantize(x, out=None, n_rows=None, stream=None):
     """x [R, D] (rows may be strided) or [E, N, D] (contiguous) in microscaled FP4 (E2M1, a power
-    of two per 32 values of a row): an MxTensor."""
+    of two per 32 values of a row): an MxTensor.  Values about the type's largest round to the
+    power of two behind it (f16 from 57344 on: 65536), which products take as it is."""
     if out is None and n_rows is None and stream is None:
         r = _fast.mx_quantize(x)
         if r is not None:
@@ -506,7 +507,8 @@ def mx_quantize_transposed(x, out=None, stream=None):
 
 
 def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
-    """The values of an MxTensor, as a tensor of its shape (into `out`: as rows, of out's type)."""
+    """The values of an MxTensor, as a tensor of its shape (into `out`: as rows, of out's type);
+    infinite where one passes the type's largest."""
     if out is not None:
         dtype = out.dtype
     if dtype not in _DTYPE:
