@@ -514,10 +514,11 @@ def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
     if dtype not in _DTYPE:
         raise ValueError("dtype: float32, bfloat16 or float16")
     rows, D = x.c.rows, x.c.cols
+    given = out is not None
     out, p, ld = _like(out, "out", (rows, D), dtype, x.on(), stream)
     _check(lib().moe_nvfp4_mx_restore(x.c, moe_logits(p, ld, rows, D, _DTYPE[dtype]),
                                       _n_rows(n_rows, out), _raw(stream)), "moe_nvfp4_mx_restore")
-    return out.view(x.shape) if len(x.shape) == 3 and out.is_contiguous() else out
+    return out if given or len(x.shape) == 2 else out.view(x.shape)
 
 
 def _product_args(x, w, offsets, dtype, out, stream):
