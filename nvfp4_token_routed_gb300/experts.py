@@ -84,6 +84,15 @@ def _like(t, name, shape, dtype, like, stream):
     return t, m.data, m.ld
 
 
+def _type_of(dtype, out, default):
+    """The result's type: `dtype`, out's or the default; a given out has to agree."""
+    if out is None:
+        return dtype or default
+    if dtype is not None and dtype != out.dtype:
+        raise ValueError(f"dtype: {dtype}, but out is of {out.dtype}")
+    return out.dtype
+
+
 def _n_rows(t, like):
     return _arg(t, "n_rows", (1,), _I32, like) if t is not None else None
 
@@ -340,7 +349,7 @@ def checkpoint(x, kept=None, n_rows=None, stream=None):
 
 
 def restore(kept, dtype=None, out=None, n_rows=None, stream=None):
-    """The rows that checkpoint kept, of `dtype` (None: the type they had), or of out's."""
+    """The rows that checkpoint kept, of `dtype` (None: out's, else the type they had)."""
     if dtype is None and out is None and n_rows is None and stream is None:
         r = _fast.restore(kept)
         if r is not None:
@@ -348,7 +357,7 @@ def restore(kept, dtype=None, out=None, n_rows=None, stream=None):
     if kept.act is not None:
         raise ValueError("kept: an activation's input is read by expert_act_grad")
     R, D = kept.rows, kept.cols
-    dtype = out.dtype if out is not None else dtype or kept.dtype
+    dtype = _type_of(dtype, out, kept.dtype)
     if dtype not in _DTYPE:
         raise ValueError("dtype: float32, bfloat16 or float16")
     out, p, ld = _like(out, "out", (R, D), dtype, kept.on(), stream)
@@ -506,11 +515,10 @@ def mx_quantize_transposed(x, out=None, stream=None):
     return out
 
 
-def mx_restore(x, dtype=torch.bfloat16, out=None, n_rows=None, stream=None):
-    """The values of an MxTensor, as a tensor of its shape (into `out`: as rows, of out's type);
-    infinite where one passes the type's largest."""
-    if out is not None:
-        dtype = out.dtype
+def mx_restore(x, dtype=None, out=None, n_rows=None, stream=None):
+    """The values of an MxTensor, as a tensor of its shape (into `out`: as rows), of `dtype` (None:
+    out's, else bfloat16); infinite where one passes the type's largest."""
+    dtype = _type_of(dtype, out, torch.bfloat16)
     if dtype not in _DTYPE:
         raise ValueError("dtype: float32, bfloat16 or float16")
     rows, D = x.c.rows, x.c.cols
@@ -529,8 +537,7 @@ def _product_args(x, w, offsets, dtype, out, stream):
     w._look()
     if w.device != x.device:
         raise ValueError(f"w: on device {w.device}, the rows on {x.device}")
-    if out is not None:
-        dtype = out.dtype
+    dtype = _type_of(dtype, out, torch.bfloat16)
     dt = _DTYPE.get(dtype)
     if dt is None:
         raise ValueError("dtype: float32, bfloat16 or float16")
@@ -542,12 +549,12 @@ def _product_args(x, w, offsets, dtype, out, stream):
     return out, (x.c, w.c, E, offsets), (dt, p, ld, _raw(stream))
 
 
-def mx_product(x, w, offsets=None, dtype=torch.bfloat16, out=None, stream=None):
+def mx_product(x, w, offsets=None, dtype=None, out=None, stream=None):
     """x [R, D] times the weights of each row's expert: w [E, N, D] with offsets int32 [E + 1]
-    (RoutePlan.offsets), or one matrix [N, D].  -> [R, N] of `dtype`; rows outside the groups
-    are left as they were."""
+    (RoutePlan.offsets), or one matrix [N, D].  -> [R, N] of `dtype` (None: out's, else
+    bfloat16); rows outside the groups are left as they were."""
     if out is None and stream is None:
-        r = _fast.mx_product(x, w, offsets, dtype)
+        r = _fast.mx_product(x, w, offsets, dtype or torch.bfloat16)
         if r is not None:
             return r
     out, args, rest = _product_args(x, w, offsets, dtype, out, stream)
