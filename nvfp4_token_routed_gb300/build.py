@@ -39,17 +39,24 @@ def _deps():
 
 
 def build_calls():
-    """The CPython extension; without Python's headers the binding does without it."""
+    """The CPython extension; the binding does without it where it cannot be built."""
+    def none(why):
+        if os.path.exists(CALLS):
+            os.remove(CALLS)  # of other sources
+        sys.stderr.write(f"calls.c not built, every call is interpreted: {why}\n")
+
     include = sysconfig.get_paths()["include"]
     if not os.path.exists(os.path.join(include, "Python.h")):
-        sys.stderr.write("calls.c not built: no Python.h\n")
-        return None
+        return none("no Python.h")
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["gcc", "-std=c11", "-O2", "-Wall", "-fPIC", "-shared", "-I", include, "-I",
            os.path.join(ROOT, "include"), os.path.join(CSRC, "calls.c"), "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return none(e)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for calls.c:\n{r.stdout}\n{r.stderr}")
+        return none(f"\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
     return CALLS
 

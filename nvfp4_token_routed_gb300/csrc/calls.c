@@ -499,7 +499,8 @@ static PyObject* expert_act(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   moe_status st = MOE_ERR_CUDA;
   if (y && (k || !keep))
     LAUNCH(st, ACT, act_fn, &h, act, (float)limit, p, sh[1], codes, scales, NULL, s);
-  if (st == MOE_OK) r = keep ? PyTuple_Pack(2, y, k) : Py_NewRef(y);
+  if (st == MOE_OK && !keep) Py_INCREF(r = y);
+  if (st == MOE_OK && keep) r = PyTuple_Pack(2, y, k);
   Py_XDECREF(y);
   Py_XDECREF(k);
   return r ? r : not_ordinary();
