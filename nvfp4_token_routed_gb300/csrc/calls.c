@@ -489,7 +489,8 @@ static PyObject* expert_act(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int act = act_of(a[1]), halves = act == MOE_ACT_SWIGLU ? 2 : 1;
   const double limit = PyFloat_AsDouble(a[2]);
   const int keep = PyObject_IsTrue(a[3]);
-  ORDINARY(act >= 0 && !PyErr_Occurred() && keep >= 0 && h.cols % halves == 0);
+  ORDINARY(act >= 0 && !PyErr_Occurred() && keep >= 0 && h.cols % halves == 0 &&
+           (limit == 0.0 || (float)limit != 0.0f));
   const int64_t sh[2] = {h.rows, h.cols / halves};
   PyObject* y = new_tensor(2, sh, type_object(h.dtype), &p);
   PyObject* k = y && keep ? new_kept(sh[0], sh[1], halves, type_object(h.dtype), a[1], limit, dev,

@@ -292,6 +292,14 @@ class _Held:
         return t
 
 
+def _limit(limit):
+    """swiglu_limit as a float; one that is not 0 but that fp32 rounds to 0 (no limit) is refused."""
+    limit = float(limit)
+    if limit and C.c_float(limit).value == 0.0:
+        raise ValueError(f"swiglu_limit: {limit} is 0 in fp32")
+    return limit
+
+
 class Checkpoint(_Held):
     """Rows kept in 8 bits: codes [R, halves, W32] and scales [R, halves, W32 / 32] uint8, of
     `cols` values a half.  act: None for checkpoint's, else the activation whose input it is."""
@@ -299,14 +307,14 @@ class Checkpoint(_Held):
 
     def __init__(self, codes, scales, cols, dtype, act=None, swiglu_limit=0.0):
         self.rows, self.cols, self.dtype, self.act = codes.shape[0], cols, dtype, act
-        self.halves, self.swiglu_limit = 2 if act == "swiglu" else 1, float(swiglu_limit)
+        self.halves, self.swiglu_limit = 2 if act == "swiglu" else 1, _limit(swiglu_limit)
         self.c = self._set(codes, scales)
 
     @classmethod
     def empty(cls, rows, cols, dtype, like, act=None, swiglu_limit=0.0, stream=None):
         k = cls.__new__(cls)
         k.rows, k.cols, k.dtype, k.act = rows, cols, dtype, act
-        k.halves, k.swiglu_limit = 2 if act == "swiglu" else 1, float(swiglu_limit)
+        k.halves, k.swiglu_limit = 2 if act == "swiglu" else 1, _limit(swiglu_limit)
         n = rows * k.halves * ((cols + 31) >> 5)
         k.c = k._alloc(32 * n, n, like, stream)
         return k
@@ -378,6 +386,7 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
             return r
     if act not in ACT:
         raise ValueError(f"act: one of {sorted(ACT)}")
+    limit = _limit(swiglu_limit)
     m = _matrix(h, "h")
     R, I = h.shape
     if act == "swiglu":
@@ -386,13 +395,13 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
     codes = scales = None
     if kept is None:
         if checkpoint:
-            kept = Checkpoint.empty(R, I, h.dtype, h, act, swiglu_limit, stream)
+            kept = Checkpoint.empty(R, I, h.dtype, h, act, limit, stream)
             codes, scales = kept.c
     else:
-        if kept.act != act or kept.swiglu_limit != float(swiglu_limit):
+        if kept.act != act or kept.swiglu_limit != limit:
             raise ValueError("kept: made for another activation")
         codes, scales = kept._for(R, I)
-    _check(lib().moe_nvfp4_expert_act(m, ACT[act], swiglu_limit, p, ld, codes, scales,
+    _check(lib().moe_nvfp4_expert_act(m, ACT[act], limit, p, ld, codes, scales,
                                       _n_rows(n_rows, h), _raw(stream)), "moe_nvfp4_expert_act")
     return y if kept is None else (y, kept)
 
@@ -607,7 +616,7 @@ class MxExperts:
         I = N1 // 2 if act == "swiglu" else N1
         if fc2.shape != (E, H, I):
             raise ValueError(f"fc2: expected {(E, H, I)}, got {tuple(fc2.shape)}")
-        self.E, self.H, self.I, self.act, self.limit = E, H, I, act, float(swiglu_limit)
+        self.E, self.H, self.I, self.act, self.limit = E, H, I, act, _limit(swiglu_limit)
         self.fc1, self.fc2 = mx_quantize(fc1, stream=stream), mx_quantize(fc2, stream=stream)
         self.fc1_t = mx_quantize_transposed(fc1, stream=stream)
         self.fc2_t = mx_quantize_transposed(fc2, stream=stream)
