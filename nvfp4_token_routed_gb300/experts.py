@@ -306,6 +306,8 @@ class Checkpoint(_Held):
     __slots__ = ("rows", "halves", "cols", "dtype", "act", "swiglu_limit", "c")
 
     def __init__(self, codes, scales, cols, dtype, act=None, swiglu_limit=0.0):
+        if act is not None and act not in ACT:
+            raise ValueError(f"act: None or one of {sorted(ACT)}")
         self.rows, self.cols, self.dtype, self.act = codes.shape[0], cols, dtype, act
         self.halves, self.swiglu_limit = 2 if act == "swiglu" else 1, _limit(swiglu_limit)
         self.c = self._set(codes, scales)
