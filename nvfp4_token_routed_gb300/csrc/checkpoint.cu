@@ -260,9 +260,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 5) act_grad_kernel(
           uc = pack2(clip(up.v[i], L), clip(up.v[i + 1], L));
         }
         const f32x2 dd = pack2(d.v[i], d.v[i + 1]), s = sigmoid2<DT>(gc), gs = mul2(gc, s);
-        // s (1 + g (1 - s)) = s + g s (1 - s)
+        // s (1 + g (1 - s)) = s + g s (1 - s), times u before dy: dy u may pass fp32's range where
+        // the slope is small or 0
         const f32x2 rest = fma2(s, pack2(-1.0f, -1.0f), pack2(1.0f, 1.0f));
-        const float2 dg = unpack2(mul2(mul2(dd, uc), fma2(gs, rest, s)));
+        const float2 dg = unpack2(mul2(dd, mul2(uc, fma2(gs, rest, s))));
         const float2 du = unpack2(mul2(dd, gs));
         const float2 gf = unpack2(gk), uf = unpack2(uk);
         g.v[i] = LIMIT && gf.x > L ? 0.0f : dg.x;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 5) act_grad_kernel(
       span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + a.W + cu), a.W - cu, stage, up);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * d.v[i] * positive(g.v[i]);
+      for (int i = 0; i < 8; ++i) g.v[i] = 2.0f * (d.v[i] * positive(g.v[i]));  // 2 dy may overflow
     }
     span_store<DT, VB>(elem_ptr<DT>(a.out, r * a.ld_out + cu), a.W - cu, stage, g);
   }
