@@ -247,9 +247,9 @@ class _Held:
         return at
 
     def _moved(self, codes, scales):
-        """Whether the tensors lie elsewhere than at these addresses (a buffer is nobody else's)."""
-        return self._buf is None and (self._codes.data_ptr() != (codes or 0) or
-                                      self._scales.data_ptr() != (scales or 0))
+        """Whether the tensors lie elsewhere than at these addresses."""
+        return (self._codes.data_ptr() != (codes or 0) or
+                self._scales.data_ptr() != (scales or 0))
 
     def _alloc(self, n_codes, n_scales, like, stream):
         at = (n_codes + 255) & -256
@@ -326,7 +326,7 @@ class Checkpoint(_Held):
                             self.swiglu_limit)
 
     def _look(self):
-        if self._moved(*self.c):
+        if self._buf is None and self._moved(*self.c):  # a buffer is nobody else's
             self.c = self._set(self._codes, self._scales)
 
     def _shapes(self):
@@ -454,6 +454,8 @@ class MxTensor(_Held):
         return MxTensor, (self.codes, self.scales, self.shape)
 
     def _look(self):
+        if self._buf is not None:
+            return
         m = moe_mx.from_buffer_copy(self.raw)
         if self._moved(m.codes, m.scales):
             p, q = self._set(self._codes, self._scales)
