@@ -528,9 +528,9 @@ moe_status moe_nvfp4_router_loss_grad(const moe_router_batch* b, const int32_t* 
  *     multiples of 16 bytes are fastest.
  *   - The route rows of a batch are numbered 0 .. T*K-1, experts in ascending order;
  *     empty slots have no row, so a batch with empty slots leaves the last rows unused.
- *     Unused rows are neither read nor written.  Where a call takes n_rows, a DEVICE
- *     int32 (offsets + E of moe_nvfp4_sort_routes), rows from *n_rows on are left alone;
- *     NULL: every row counts.
+ *     Unused rows are not written, and what they hold has no effect.  Where a call takes
+ *     n_rows, a DEVICE int32 (offsets + E of moe_nvfp4_sort_routes), rows from *n_rows on
+ *     are left alone; NULL: every row counts.
  *   - Sums are fp32 in a fixed order, results rounded once: equal inputs give equal bits,
  *     and a row's results do not depend on the other rows.
  *   - Outputs do not overlap inputs unless a call says so. */
@@ -592,7 +592,9 @@ moe_status moe_nvfp4_restore(const uint8_t* codes, const uint8_t* scales, const 
  *   swiglu: y = silu(gate) * up; swiglu_limit L > 0: gate = min(gate, L),
  *           up = min(max(up, -L), L) first;   relu2: y = max(h, 0)^2
  * Where codes is not NULL, h is kept in 8 bits beside it, each half blocked for itself:
- * codes [R][halves][I32], scales [R][halves][I32 / 32]. */
+ * codes [R][halves][I32], scales [R][halves][I32 / 32].  h is kept as it is, before any
+ * limit: an infinity that the limit makes a finite y of still makes its block, and the 32
+ * gradients there, NaN. */
 moe_status moe_nvfp4_expert_act(const moe_rows* h, int32_t act, float swiglu_limit, void* y,
                                 int64_t ld_y, uint8_t* codes, uint8_t* scales,
                                 const int32_t* n_rows, moe_stream_t stream);

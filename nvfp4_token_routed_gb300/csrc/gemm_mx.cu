@@ -28,7 +28,8 @@
 //     TMEM, and writes NaN to the items that it leaves.
 // Measured (bf16 out): 128 rows on 64 experts N2048 D2048 22.2 us (0.97 of the copy rate,
 // 6686 GB/s), on 256 experts N4096 D7168 223 us (1.0); 2048 rows on 32 experts N4096 D7168 83
-// us (0.95).  Where rows bound it, see the pairs below.
+// us (0.95).  One matrix N4096 D7168 has 32 items and is bound by how fast 32 CTAs read: 1 to 16
+// rows 9.3 us (floor 2.4).  Where rows bound it, see the pairs below.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -567,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // them to registers as 16-bit pairs, free them, and store while the next item's MMAs run.
 // Measured: 16384 rows N4096 D7168 on 8 experts 145 us (6.6 PFLOP/s; kind::mxf4 issues 16384
 // products a cycle and SM, 9.6 PFLOP/s at 1.92 GHz), on 32 ragged ones 167 us, one matrix of
-// 4096 rows 40 us; single CTAs 196, 224 and 60.  A stage's MMAs take 512 of its 550 cycles, the
+// 4096 rows 40 us (fp32 results, whose accumulators are held until stored: 203, 224 and 52);
+// single CTAs 196, 224 and 60.  A stage's MMAs take 512 of its 550 cycles, the
 // pause between items 1850 (drain, then refill); copies bring 65 bytes a cycle and SM, and
 // halving the rows' took 6 % off, which sharing them by multicast could gain at most.
 namespace pair {

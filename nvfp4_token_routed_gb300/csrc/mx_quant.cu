@@ -111,7 +111,9 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const MxQuantArgs a, 
 
 // Columns of a stack of matrices as rows: 256 values of 32 columns a block, through
 // shared memory (a column's stride of 261 words keeps a warp's reads of 8 consecutive
-// values at most 8 to a bank, and its writes free of conflicts).
+// values at most 8 to a bank, and its writes free of conflicts).  8 x 4096 x 7168 bf16 in 337
+// us, 0.26 of the copy rate, against 94 for the same stack row by row: loads of 2 bytes a lane
+// and those conflicts.  It runs once for a layer's weights.
 constexpr int kColsT = 32, kStrideT = kMxPanel + 5;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) quantize_t_kernel(const MxQuantArgs a, int C) {

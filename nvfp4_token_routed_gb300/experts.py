@@ -381,7 +381,8 @@ def expert_act(h, act, swiglu_limit=0.0, checkpoint=False, y=None, kept=None, n_
                stream=None):
     """The experts' activation of FC1 rows h: [R, 2I] = [gate | up] ("swiglu") or [R, I]
     ("relu2") -> y [R, I].  With checkpoint (or `kept`, a Checkpoint to fill) h is kept in 8
-    bits for expert_act_grad: (y, kept), else y."""
+    bits for expert_act_grad: (y, kept), else y.  A block of 32 with an infinity or a NaN is kept
+    as NaN, also where the limit makes y finite."""
     if y is None and kept is None and n_rows is None and stream is None:
         r = _fast.expert_act(h, act, swiglu_limit, checkpoint)
         if r is not None:
@@ -611,6 +612,10 @@ class MxExperts:
     fc1 [E, N1, H] ([gate; up] for "swiglu"), fc2 [E, H, I].  backward multiplies with the
     transposed stacks, quantised along their other side (quantisation itself passes gradients
     through unchanged).  y = combine(FC2(act(FC1(x)))).
+
+    The gradients that backward multiplies are rounded to FP4 to nearest, in blocks of 32: below a
+    24th to a 12th of the block's largest they become 0.  A captured backward belongs into the
+    graph of its forward, whose rows it overwrites.
     """
 
     def __init__(self, fc1, fc2, act, swiglu_limit=0.0, stream=None):
