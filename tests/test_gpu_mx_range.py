@@ -42,3 +42,24 @@ def test_values_about_the_largest(dtype, transposed):
     w = torch.eye(64, device=DEV) * 2.0 ** -20
     y = M.mx_product(q, M.mx_quantize(w), dtype=torch.float32)
     assert torch.equal(y.cpu().double(), want * 2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_values_about_the_smallest(dtype):
+    """Blocks of the least exponent, -127: subnormals, held in steps of 2^-128 and taken by
+    products as what they are."""
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+    x = torch.zeros(8, 64, dtype=torch.float64)
+    for i in range(8):
+        x[i, :8] = grid.roll(i) * 2.0 ** -127
+        x[i, 32:40] = -grid.roll(i) * 2.0 ** -127
+    q = M.mx_quantize(x.to(dtype).to(DEV))
+    assert torch.equal(x.to(dtype).double(), x) and not q.scales[0, :8, :2].any()
+    assert torch.equal(M.mx_restore(q, dtype).cpu().double(), x)
+    for up in (30, 100):
+        w = torch.eye(64, device=DEV) * 2.0 ** up
+        y = M.mx_product(q, M.mx_quantize(w), dtype=torch.float32)
+        assert torch.equal(y.cpu().double(), x * 2.0 ** up)
+    # below half the smallest step: zeros
+    tiny = torch.full((1, 32), 2.0 ** -130).to(dtype).to(DEV)
+    assert not M.mx_restore(M.mx_quantize(tiny), torch.float32).any()
